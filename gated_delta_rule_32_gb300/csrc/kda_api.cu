@@ -247,6 +247,8 @@ const char* kda_status_string(kda_status s) {
     case KDA_ERR_CUDA: return "KDA_ERR_CUDA: CUDA runtime error";
     case KDA_ERR_WORKSPACE: return "KDA_ERR_WORKSPACE: workspace too small";
     case KDA_ERR_BOUNDS: return "KDA_ERR_BOUNDS: device-side bounds check failed (debug build)";
+    case KDA_ERR_BAD_PAGES: return "KDA_ERR_BAD_PAGES: page number outside the pool";
+    case KDA_ERR_NO_PAGES: return "KDA_ERR_NO_PAGES: free stack shorter than the step's pages";
   }
   return "KDA_ERR_UNKNOWN";
 }

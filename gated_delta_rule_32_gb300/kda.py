@@ -25,18 +25,23 @@ KDA_ERR_TIMEOUT = 5
 KDA_ERR_CUDA = 6
 KDA_ERR_WORKSPACE = 7
 KDA_ERR_BOUNDS = 8
+KDA_ERR_BAD_PAGES = 9
+KDA_ERR_NO_PAGES = 10
 KDA_BF16 = 0
 KDA_F32 = 1
 KDA_ALGO_AUTO = 0
 KDA_ALGO_SIMT = 1
 KDA_ALGO_TC = 2
 KDA_ALGO_SPLIT = 3
+KDA_I8 = 0
+KDA_E4M3 = 1
 
 _lock = threading.Lock()
 _lib = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_l = ctypes.c_int64
 _SIGS = {
     "kda_status_string": (ctypes.c_char_p, [_i]),
     "kda_build_info": (ctypes.c_char_p, []),
@@ -68,6 +73,13 @@ _SIGS = {
     "kda_summary_floats": (ctypes.c_size_t, [_i] * 4),
     "kda_state_compose": (_i, [_vp, _i, _vp, _vp] + [_i] * 4 + [_vp]),
     "kda_debug_record_capacity": (_i, [ctypes.c_int64]),
+    "kda_page_plan": (_i, [_vp] * 2 + [_i] * 3 + [_vp, _i, _vp, _vp, _i] + [_vp] * 8),
+    "kda_page_runs": (_i, [_i] * 3),
+    "kda_page_release": (_i, [_vp, _i, _i, _vp, _vp, _i, _vp, _vp, _i, _vp, _vp]),
+    "kda_cache_append": (_i, [_vp, _vp, _l, _l, _i, _vp, _i] + [_vp] * 4 + [_i] * 5 + [_vp] * 2),
+    "kda_cache_attn": (_i, [_vp, _l] + [_vp] * 3 + [_i] + [_vp] * 6 + [_i] * 9 +
+                       [ctypes.c_float, _vp, ctypes.c_size_t, _vp, _vp]),
+    "kda_cache_attn_workspace_bytes": (ctypes.c_size_t, [_i] * 6),
 }
 
 
@@ -312,3 +324,46 @@ def kda_state_compose(summaries, m, init_state, state_out, N, H, dk=128, dv=128,
                       stream=None) -> int:
     return load().kda_state_compose(_p(summaries), m, _p(init_state), _p(state_out), N, H,
                                     dk, dv, _stream(stream))
+
+
+def kda_page_plan(new_lens, ctx_lens, R, T, page, block_table, max_pages, free_pages, free_count,
+                  num_pages, cu_seqlens, kv_lens, slots, positions, runs, free_count_out,
+                  dev_status=None, stream=None) -> int:
+    return load().kda_page_plan(_p(new_lens), _p(ctx_lens), R, T, page, _p(block_table), max_pages,
+                                _p(free_pages), _p(free_count), num_pages, _p(cu_seqlens),
+                                _p(kv_lens), _p(slots), _p(positions), _p(runs),
+                                _p(free_count_out), _p(dev_status), _stream(stream))
+
+
+def kda_page_runs(R, T, page) -> int:
+    return load().kda_page_runs(R, T, page)
+
+
+def kda_page_release(release, R, page, kv_lens, block_table, max_pages, free_pages, free_count,
+                     num_pages, dev_status=None, stream=None) -> int:
+    return load().kda_page_release(_p(release), R, page, _p(kv_lens), _p(block_table), max_pages,
+                                   _p(free_pages), _p(free_count), num_pages, _p(dev_status),
+                                   _stream(stream))
+
+
+def kda_cache_append(k, v, k_stride, v_stride, T, runs, num_runs, k_codes, v_codes, k_scale,
+                     v_scale, num_pages, page, Hkv, d, code=KDA_I8, dev_status=None,
+                     stream=None) -> int:
+    return load().kda_cache_append(_p(k), _p(v), k_stride, v_stride, T, _p(runs), num_runs,
+                                   _p(k_codes), _p(v_codes), _p(k_scale), _p(v_scale), num_pages,
+                                   page, Hkv, d, code, _p(dev_status), _stream(stream))
+
+
+def kda_cache_attn(q, q_stride, cu_seqlens, kv_lens, block_table, max_pages, k_codes, v_codes,
+                   k_scale, v_scale, out, lse, R, T, max_new, Hq, Hkv, d, num_pages, page,
+                   code=KDA_I8, scale=1.0, workspace=None, workspace_bytes=0, dev_status=None,
+                   stream=None) -> int:
+    return load().kda_cache_attn(_p(q), q_stride, _p(cu_seqlens), _p(kv_lens), _p(block_table),
+                                 max_pages, _p(k_codes), _p(v_codes), _p(k_scale), _p(v_scale),
+                                 _p(out), _p(lse), R, T, max_new, Hq, Hkv, d, num_pages, page,
+                                 code, float(scale), _p(workspace), workspace_bytes,
+                                 _p(dev_status), _stream(stream))
+
+
+def kda_cache_attn_workspace_bytes(R, T, max_new, Hq, Hkv, d) -> int:
+    return load().kda_cache_attn_workspace_bytes(R, T, max_new, Hq, Hkv, d)

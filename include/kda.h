@@ -73,7 +73,9 @@ typedef enum {
   KDA_ERR_TIMEOUT = 5,      /* a bounded on-chip wait gave up (device-detected) */
   KDA_ERR_CUDA = 6,         /* a CUDA runtime call failed */
   KDA_ERR_WORKSPACE = 7,    /* workspace given but below the path's minimum (see kda_chunk_fwd_ex) */
-  KDA_ERR_BOUNDS = 8        /* a device-side bounds check failed (KDA_DEBUG builds only) */
+  KDA_ERR_BOUNDS = 8,       /* a device-side bounds check failed (KDA_DEBUG builds only) */
+  KDA_ERR_BAD_PAGES = 9,    /* a page number outside the pool, or a run outside its page (device-detected) */
+  KDA_ERR_NO_PAGES = 10     /* the free stack holds fewer pages than a step needs (device-detected) */
 } kda_status;
 
 typedef enum { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype;
@@ -400,6 +402,136 @@ int kda_split_segment_count(int N, int T, int H, size_t workspace_bytes);
  * in normal builds.  Process-wide; not thread-safe against concurrent calls.
  */
 kda_status kda_debug_record_capacity(int64_t items);
+
+/*
+ * The paged 8-bit cache: keys and values of the full-attention layers that a
+ * hybrid model keeps beside its gated delta rule layers.  (No counterpart on
+ * the pages above, which describe the recurrent layers only.)
+ *
+ * One layer's cache is a pool of pages of `page` tokens (16, 32, 64 or 128):
+ *   k_codes, v_codes   [num_pages, Hkv, page, d]  one byte per value
+ *   k_scale, v_scale   [num_pages, Hkv]           fp32
+ * scale is the largest magnitude that the page and head hold; a code c
+ * stands for c * scale / 127 (KDA_I8, c in -127..127) or c * scale / 448
+ * (KDA_E4M3, c the e4m3 value).  d is 64 or 128; Hkv >= 1.
+ *
+ * A batch of R requests is described by device int32 arrays: request r has
+ * kv_lens[r] tokens in the cache, the last cu_seqlens[r + 1] -
+ * cu_seqlens[r] of which are the rows [cu_seqlens[r], cu_seqlens[r + 1]) of
+ * the step's packed token tensors (the same cu_seqlens as a packed
+ * kda_chunk_fwd takes); block_table [R, max_pages] holds the page number of
+ * each request's tokens p * page .. p * page + page - 1 in column p.
+ * Columns past a request's last page are never read.  What a page holds past
+ * its request's length never reaches a result, whatever its bytes.
+ */
+typedef enum { KDA_I8 = 0, KDA_E4M3 = 1 } kda_code;
+
+/*
+ * kda_page_plan -- one step's bookkeeping, from the requests' lengths:
+ * request r brings new_lens[r] tokens to the ctx_lens[r] it has cached.
+ * Pages are taken from the top of the free stack (free_pages[0 ..
+ * free_count[0]) holds the free page numbers, the top last), request by
+ * request, and entered into block_table (in place; columns that were filled
+ * are kept).  Outputs (device int32, none of them overlapping an input):
+ *   cu_seqlens  [R + 1]   packed offsets of the new tokens
+ *   kv_lens     [R]       ctx_lens + new_lens
+ *   slots       [T]       page * page_size + offset of each new token, in
+ *                         the order of the packed rows; -1 past the last
+ *   positions   [T]       each new token's position in its request; -1 past
+ *   runs        [kda_page_runs(R, T, page)][4]  for every page a request's
+ *                         new tokens touch: first packed row, tokens, page
+ *                         number, offset in the page; zeros past the last.
+ *                         16-byte aligned.
+ *   free_count_out [1]    what is left of the stack (free_pages itself is
+ *                         only read)
+ * T is the rows the caller has; the new tokens may be fewer.  R <= 16384.
+ * A negative length, more than T new tokens or a request longer than its
+ * table row is KDA_ERR_BAD_SEQLENS, a stack too short KDA_ERR_NO_PAGES, in
+ * dev_status; then nothing is taken (cu_seqlens all 0, kv_lens = ctx_lens,
+ * no runs, slots -1, the table unchanged), so that the calls below do
+ * nothing.  A page number outside the pool is KDA_ERR_BAD_PAGES; tokens in
+ * it get slot -1 and no run.  dev_status (here and below): as in
+ * kda_chunk_fwd_ex.
+ */
+kda_status kda_page_plan(const int32_t* new_lens, const int32_t* ctx_lens, int R, int T, int page,
+                         int32_t* block_table, int max_pages, const int32_t* free_pages,
+                         const int32_t* free_count, int num_pages, int32_t* cu_seqlens,
+                         int32_t* kv_lens, int32_t* slots, int32_t* positions, int32_t* runs,
+                         int32_t* free_count_out, int32_t* dev_status, kda_stream_t stream);
+
+/* Rows of kda_page_plan's `runs`: max(1, min(T, T / page + 2 R)), the most
+ * that R requests of T new tokens in all can touch. 0 for bad arguments. */
+int kda_page_runs(int R, int T, int page);
+
+/*
+ * kda_page_release -- requests with release[r] != 0 (device int32) give
+ * their pages back: pushed onto the free stack request by request, page by
+ * page; their table columns become -1 and their kv_lens 0.  kv_lens,
+ * block_table, free_pages and free_count are updated in place.  Lengths that
+ * do not fit the table are KDA_ERR_BAD_SEQLENS, a stack that would hold more
+ * than num_pages KDA_ERR_BAD_PAGES; then nothing changes.  R <= 16384.
+ */
+kda_status kda_page_release(const int32_t* release, int R, int page, int32_t* kv_lens,
+                            int32_t* block_table, int max_pages, int32_t* free_pages,
+                            int32_t* free_count, int num_pages, int32_t* dev_status,
+                            kda_stream_t stream);
+
+/*
+ * kda_cache_append -- writes a step's keys and values (bf16, [T, Hkv, d],
+ * token strides k_stride and v_stride in elements, heads and channels
+ * contiguous) into the cache, by the plan's runs.  For every run, head and
+ * tensor, with a0 the scale held (0 if the run starts its page) and a1 =
+ * max(a0, max |x| over the run): codes already in the page become
+ * rn(c * a0 / a1), the new ones rn(x * top / a1) (top 127 or 448; to
+ * nearest, ties to even), and the scale a1.  Both quotients are fp32
+ * divisions whose rounded code equals exact arithmetic's for every bf16
+ * input.  A run with an infinity or NaN makes its page and head's scale NaN:
+ * attention over them is NaN until the page is reused.
+ * Runs outside the pool or the rows are KDA_ERR_BAD_PAGES and skipped.
+ * k, v 16-byte aligned, strides multiples of 8 elements and >= Hkv * d;
+ * codes 16-byte aligned.
+ */
+kda_status kda_cache_append(const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                            int64_t v_stride, int T, const int32_t* runs, int num_runs,
+                            void* k_codes, void* v_codes, float* k_scale, float* v_scale,
+                            int num_pages, int page, int Hkv, int d, kda_code code,
+                            int32_t* dev_status, kda_stream_t stream);
+
+/*
+ * kda_cache_attn -- causal attention of a step's queries over the cache,
+ * the step's own tokens (appended before) among it.  Query row i of request
+ * r, n new tokens of kv_lens[r], sees the first kv_lens[r] - n + i + 1
+ * tokens; head h reads key / value head h / (Hq / Hkv):
+ *   s_j = scale * q . k_j,   out = sum_j softmax(s)_j v_j,
+ *   lse = log sum_j exp(s_j)
+ * A row that sees nothing (kv_lens[r] < n) gives out 0 and lse -infinity.
+ *   q     bf16 [T, Hq, d], token stride q_stride elements (a multiple of 8)
+ *   out   bf16 [T, Hq, d] contiguous;  lse  fp32 [T, Hq], or NULL
+ * Rows past cu_seqlens[R] are not written.  Hq a multiple of Hkv, at most
+ * 64 query heads for each; R <= 16384.  max_new: the most new tokens any
+ * request has, as far as the host knows (T is always right); a larger
+ * request is KDA_ERR_BAD_SEQLENS.  A request whose new tokens make at most
+ * 16 query rows for a key / value head runs on a kernel for few rows (bound
+ * by the cache's bytes), others on the tensor cores in tiles; both split a
+ * long cache over the chip and join the parts.
+ * Malformed cu_seqlens or lengths past the table are KDA_ERR_BAD_SEQLENS, a
+ * page number outside the pool KDA_ERR_BAD_PAGES; the request's outputs are
+ * then unspecified.
+ *   workspace  device scratch of kda_cache_attn_workspace_bytes() bytes,
+ *              256-byte aligned, contents arbitrary; or NULL: taken from the
+ *              stream-ordered allocator.
+ * q, out, codes 16-byte aligned.
+ */
+kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride, const int32_t* cu_seqlens,
+                          const int32_t* kv_lens, const int32_t* block_table, int max_pages,
+                          const void* k_codes, const void* v_codes, const float* k_scale,
+                          const float* v_scale, uint16_t* out, float* lse, int R, int T,
+                          int max_new, int Hq, int Hkv, int d, int num_pages, int page,
+                          kda_code code, float scale, void* workspace, size_t workspace_bytes,
+                          int32_t* dev_status, kda_stream_t stream);
+
+/* Scratch bytes of kda_cache_attn for these sizes on the current device. */
+size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv, int d);
 
 /* The path family kda_chunk_fwd_ex would take for these arguments:
  * KDA_ALGO_SIMT, KDA_ALGO_TC (AUTO on the tensor cores: fused, segmented or
