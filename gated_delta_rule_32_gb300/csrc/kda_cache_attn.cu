@@ -1,23 +1,10 @@
 // kda_cache_attn.cu -- attention of a step's queries over the paged 8-bit
 // cache: argument checks and kernels.
-#include "kda_cache.cuh"
+#include "kda_cache_attn.cuh"
 
 namespace {
 
 using namespace kda_cache;
-
-struct AttnArgs {
-  const uint16_t* q;
-  int64_t q_stride;
-  const int32_t *cu, *kv_lens, *table;
-  const uint8_t *k_codes, *v_codes;
-  const float *k_scale, *v_scale;
-  uint16_t* out;
-  float* lse;
-  int32_t* status;
-  int R, T, max_new, max_pages, Hq, Hkv, G, num_pages, page_log2;
-  float scale;
-};
 
 // The plain form on the GPU: one warp per query row, one key at a time, the
 // running maximum and sum of the softmax in fp32.
@@ -40,6 +27,7 @@ __global__ void __launch_bounds__(128) kda_cache_attn_row_kernel(AttnArgs p) {
     if (lane == 0) report(p.status, KDA_ERR_BAD_SEQLENS);
     return;
   }
+  if ((int64_t)n * p.G <= kFewRows) return;
   constexpr int E = D / 32;
   float q[E], o[E] = {};
   for (int e = 0; e < E; ++e)
@@ -70,11 +58,29 @@ __global__ void __launch_bounds__(128) kda_cache_attn_row_kernel(AttnArgs p) {
   if (p.lse && lane == 0) p.lse[row] = seen > 0 ? m + logf(l) : -INFINITY;
 }
 
+size_t r256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace: the schedule's prefix sums, then the parts of the few-row kernel
+// (two for each of its CTAs).
+struct Layout {
+  int ctas;
+  size_t ml, o, bytes;
+};
+Layout layout(int R, int max_new, int G, int d) {
+  Layout w;
+  w.ctas = kda_device_sms() * ((int64_t)max_new * G <= 8 ? 4 : 3);
+  w.ml = r256((size_t)(R + 1) * 8);
+  w.o = w.ml + r256((size_t)2 * w.ctas * kFewRows * 8);
+  w.bytes = w.o + r256((size_t)2 * w.ctas * kFewRows * d * 4);
+  return w;
+}
+
 }  // namespace
 
 extern "C" size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv,
                                                  int d) {
-  return 0;
+  if (R < 1 || T < 1 || max_new < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || !head_dim_ok(d)) return 0;
+  return layout(R, max_new, Hq / Hkv, d).bytes;
 }
 
 extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
@@ -110,6 +116,11 @@ extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
     if (overlaps(out, out_n, ins[i], in_n[i]) || overlaps(lse, lse_n, ins[i], in_n[i]))
       return KDA_ERR_INVALID_ARG;
   if (overlaps(out, out_n, lse, lse_n)) return KDA_ERR_INVALID_ARG;
+  if (workspace) {
+    if (((uintptr_t)workspace & 255) != 0) return KDA_ERR_MISALIGNED;
+    if (workspace_bytes < kda_cache_attn_workspace_bytes(R, T, max_new, Hq, Hkv, d))
+      return KDA_ERR_WORKSPACE;
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)
     return KDA_ERR_CUDA;
@@ -118,14 +129,29 @@ extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
   while ((1 << lg) < page) ++lg;
   AttnArgs p{q, q_stride, cu_seqlens, kv_lens, block_table, (const uint8_t*)k_codes,
              (const uint8_t*)v_codes, k_scale, v_scale, out, lse, dev_status, R, T, max_new,
-             max_pages, Hq, Hkv, Hq / Hkv, num_pages, lg, scale};
-  const unsigned grid = (unsigned)(((int64_t)T * Hq + 3) / 4);
-  if (code == KDA_I8) {
-    if (d == 64) kda_cache_attn_row_kernel<KDA_I8, 64><<<grid, 128, 0, s>>>(p);
-    else kda_cache_attn_row_kernel<KDA_I8, 128><<<grid, 128, 0, s>>>(p);
-  } else {
-    if (d == 64) kda_cache_attn_row_kernel<KDA_E4M3, 64><<<grid, 128, 0, s>>>(p);
-    else kda_cache_attn_row_kernel<KDA_E4M3, 128><<<grid, 128, 0, s>>>(p);
+             max_pages, Hq, Hkv, Hq / Hkv, num_pages, lg, scale, nullptr, nullptr, nullptr};
+  const Layout w = layout(R, max_new, p.G, d);
+  if (w.ctas < 1) return KDA_ERR_CUDA;
+  const bool own = workspace == nullptr;
+  if (own) {
+    if (cudaMallocAsync(&workspace, w.bytes, s) != cudaSuccess) return KDA_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.prefix = reinterpret_cast<int64_t*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
+  kda_status rc = kda_launch_attn_rows(p, d, code, w.ctas, s);
+  if (rc == KDA_OK && (int64_t)max_new * p.G > kFewRows) {
+    const unsigned grid = (unsigned)(((int64_t)T * Hq + 3) / 4);
+    if (code == KDA_I8) {
+      if (d == 64) kda_cache_attn_row_kernel<KDA_I8, 64><<<grid, 128, 0, s>>>(p);
+      else kda_cache_attn_row_kernel<KDA_I8, 128><<<grid, 128, 0, s>>>(p);
+    } else {
+      if (d == 64) kda_cache_attn_row_kernel<KDA_E4M3, 64><<<grid, 128, 0, s>>>(p);
+      else kda_cache_attn_row_kernel<KDA_E4M3, 128><<<grid, 128, 0, s>>>(p);
+    }
+    if (cudaGetLastError() != cudaSuccess) rc = KDA_ERR_CUDA;
+  }
+  if (own && cudaFreeAsync(workspace, s) != cudaSuccess && rc == KDA_OK) rc = KDA_ERR_CUDA;
+  return rc;
 }

@@ -1,0 +1,164 @@
+// kda_cache_attn.cuh -- what the attention kernels over the paged cache
+// share: arguments, the requests' checks, the schedule and the partial
+// results.
+#pragma once
+
+#include "kda_cache.cuh"
+
+namespace kda_cache {
+
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  const int32_t *cu, *kv_lens, *table;
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
+  uint16_t* out;
+  float* lse;
+  int32_t* status;
+  int R, T, max_new, max_pages, Hq, Hkv, G, num_pages, page_log2;
+  float scale;
+  // workspace of one kernel and its joining kernel
+  int64_t* prefix;  // [R + 1] units of the requests before
+  float* part_ml;   // [2 * CTAs][rows][2] maximum (log2) and sum of a part's rows
+  float* part_o;    // [2 * CTAs][rows][D] a part's sum of weighted values
+};
+
+// Query rows per key / value head up to which a request runs on the few-row
+// kernel.
+constexpr int kFewRows = 16;
+
+struct Req {
+  int c0, n, kv;
+};
+
+// Request r, or n = 0 if it brings nothing or is malformed (`bad`).
+__device__ __forceinline__ Req load_req(const AttnArgs& p, int r, bool& bad) {
+  const int a = p.cu[r], b = p.cu[r + 1], kv = p.kv_lens[r];
+  bad = a < 0 || b < a || b > p.T || b - a > p.max_new || kv < 0 ||
+        kv > ((int64_t)p.max_pages << p.page_log2);
+  return {a, bad ? 0 : b - a, kv};
+}
+
+// The schedule: every request has a number of work units, the CTAs take equal
+// contiguous shares of the sum over requests.  A CTA finds the request its
+// first unit falls in: every thread sums a contiguous range of requests, the
+// block scans the sums, the thread whose range holds the unit walks it.
+// Also writes the prefix sums (one CTA) and reports malformed requests.
+// units(Req) -> int64; NT threads.  Returns the CTA's units [u0, u1) and the
+// request of u0 with the units before it; u0 == u1 if there is nothing to do.
+struct Share {
+  int64_t u0, u1, base;
+  int r;
+};
+
+template <int NT, class Units>
+__device__ __forceinline__ Share find_share(const AttnArgs& p, Units units) {
+  __shared__ int64_t s_warp[NT / 32];
+  __shared__ int64_t s_base;
+  __shared__ int s_r;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.R + NT - 1) / NT;
+  const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    bool bad;
+    const Req q = load_req(p, r, bad);
+    if (bad && blockIdx.x == 0) report(p.status, KDA_ERR_BAD_SEQLENS);
+    if (q.n > 0) mine += units(q);
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  Share s;
+  s.u0 = min(total, (int64_t)blockIdx.x * share);
+  s.u1 = min(total, s.u0 + share);
+  int64_t at = before + inc - mine;
+  const bool here = s.u0 < s.u1 && at <= s.u0 && s.u0 < at + mine;
+  if (here || blockIdx.x == 0) {
+    for (int r = r0; r < r1; ++r) {
+      bool bad;
+      const Req q = load_req(p, r, bad);
+      const int64_t u = q.n > 0 ? units(q) : 0;
+      if (here && at <= s.u0 && s.u0 < at + u) {
+        s_r = r;
+        s_base = at;
+      }
+      if (blockIdx.x == 0) p.prefix[r] = at;
+      at += u;
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) p.prefix[p.R] = total;
+  __syncthreads();
+  s.r = s_r;
+  s.base = s_base;
+  return s;
+}
+
+// The smallest power of two not below x (x > 0 finite), 2^127 at most: its
+// reciprocal is exact.
+__device__ __forceinline__ float pow2_above(float x) {
+  const uint32_t b = __float_as_uint(fmaxf(x, 0x1p-126f)) + 0x007fffffu;
+  return __uint_as_float(min(b & 0x7f800000u, 0x7f000000u));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four codes -> two f16 pairs, exactly.  int8: u = c + 128 in the low byte of
+// 0x6400 is the half 1024 + u.
+template <int CODE>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (CODE == KDA_I8) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
+    __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+    lo = *reinterpret_cast<uint32_t*>(&x);
+    hi = *reinterpret_cast<uint32_t*>(&y);
+  } else {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+        " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A power of two by which a row of bf16 values with largest magnitude `most`
+// (bits, sign off) is divided so that it fits f16: most lands in [1, 2).
+// Elements below 2^-14 of it lose bits: 2^-25 of `most` at worst.  Infinity
+// and NaN stay what they are.  Returns the exponent.
+__device__ __forceinline__ int row_exponent(uint32_t most) {
+  const int e = (int)(most >> 23) - 127;
+  return most == 0 || most >= 0x7f800000u ? 0 : min(max(e, -126), 126);
+}
+__device__ __forceinline__ float exp2i(int e) {  // -126 <= e <= 127
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+}  // namespace kda_cache
+
+kda_status kda_launch_attn_rows(const kda_cache::AttnArgs& p, int d, int code, int ctas,
+                                cudaStream_t s);

@@ -1,0 +1,479 @@
+// kda_cache_rows.cu -- attention over the paged cache for requests with few
+// query rows per key / value head (decode steps, short drafts), and the join
+// of parts.
+//
+// Bound by the cache's bytes: every code is used for at most 16 query rows,
+// 4 * 16 flops per byte.  The work is cut in units of 64 tokens of a (request,
+// head) and every CTA takes an equal share of all units, so ragged batches
+// and single long requests fill the chip alike; a (request, head) that
+// crosses a CTA boundary leaves parts, which kda_attn_join_kernel joins.
+//
+// Warp w of a CTA takes the 16-token blocks 4 u + w.  Products run on
+// mma.m16n8k16 with the tokens (then the channels) on the 16-row side, which
+// leaves 8 columns for query rows: S^T = K Q^T, O^T += V^T P^T.  The codes
+// go from global memory to registers in the very layout that the A operand
+// wants, because the order of the contracted index is free: a lane's 16-byte
+// chunk of a key row holds its channels of all k-steps (queries are loaded in
+// the same order), its chunks of four value rows hold its channels of all
+// m-tiles.  So the asynchronous copies land in lane-private slots of shared
+// memory: no barrier, no bank conflict, no layout change.
+#include "kda_cache_attn.cuh"
+
+namespace {
+
+using namespace kda_cache;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnit = 16 * kWarps;  // tokens
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D>
+struct Ring {
+  static constexpr int kStage = 32 * D;                  // 16 tokens, keys and values
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kWarpBytes = kStage * kStages;    // 12 KiB
+};
+
+// NT: 8-row tiles of query rows.
+template <int CODE, int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+    kda_cache_attn_rows_kernel(AttnArgs p) {
+  constexpr int KS = D / 16;         // k-steps of K Q^T = m-tiles of V^T P^T
+  constexpr int KC = D / 64;         // 16-byte chunks of a key row per lane
+  constexpr int VB = D / 8;          // bytes of a value row per lane
+  constexpr int ROWS = 8 * NT;
+  constexpr int S = Ring<D>::kStages;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i8 = lane >> 2, j = lane & 3;
+  const int lg = p.page_log2, P = 1 << lg, G = p.G;
+  unsigned char* ring = smem + warp * Ring<D>::kWarpBytes;
+  const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
+
+  auto blocks_of = [&](const Req& q) -> int64_t {
+    if ((int64_t)q.n * G > kFewRows) return 0;
+    return max(1, (int)(((int64_t)q.kv + kUnit - 1) / kUnit));
+  };
+  Share sh = find_share<kThreads>(p, [&](const Req& q) { return blocks_of(q) * p.Hkv; });
+  int r = sh.r;
+  int64_t base = sh.base, u = sh.u0;
+
+  while (u < sh.u1) {
+    bool bad;
+    const Req rq = load_req(p, r, bad);
+    const int64_t nb = rq.n > 0 ? blocks_of(rq) : 0;
+    if (u >= base + nb * p.Hkv) {
+      base += nb * p.Hkv;
+      ++r;
+      continue;
+    }
+    const int h = (int)((u - base) / nb);
+    const int64_t seg0 = base + h * nb;               // the (request, head)'s units
+    const int b0 = (int)(u - seg0);
+    const int b1 = (int)(min(sh.u1, seg0 + nb) - seg0);
+    const bool whole = b0 == 0 && b1 == nb;
+    const int rows = rq.n * G, kv = rq.kv;
+
+    // queries, in the k order of the keys' chunks; each row scaled to f16
+    uint32_t qf[NT][KS][2];
+    float qs[NT][2];   // factors of this lane's two columns
+    int lim[NT][2];    // tokens that they see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = 8 * nt + i8;
+      uint4 x[2 * KC];
+      uint32_t most = 0;
+#pragma unroll
+      for (int c = 0; c < 2 * KC; ++c) {
+        x[c] = make_uint4(0, 0, 0, 0);
+        if (row < rows) {
+          const uint16_t* src = p.q + (int64_t)(rq.c0 + row / G) * p.q_stride +
+                                (int64_t)(h * G + row % G) * D + 64 * (c >> 1) + 16 * j +
+                                8 * (c & 1);
+          x[c] = *reinterpret_cast<const uint4*>(src);
+        }
+        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          most = max(most, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fff0000u));
+      }
+      most = max(most, __shfl_xor_sync(~0u, most, 1));
+      most = max(most, __shfl_xor_sync(~0u, most, 2));
+      const int ex = row_exponent(most);
+      const float down = exp2i(min(-ex, 127));
+#pragma unroll
+      for (int c = 0; c < 2 * KC; ++c) {
+        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f[e] = pack_half(__uint_as_float(w[e] << 16) * down,
+                           __uint_as_float(w[e] & 0xffff0000u) * down);
+        // channels 8 (c & 1) .. + 7 of the lane's chunk c / 2: two k-steps
+        const int s0 = 4 * (c >> 1) + 2 * (c & 1);
+        qf[nt][s0][0] = f[0];
+        qf[nt][s0][1] = f[1];
+        qf[nt][s0 + 1][0] = f[2];
+        qf[nt][s0 + 1][1] = f[3];
+      }
+      const float up = exp2i(ex);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = 8 * nt + 2 * j + c;
+        qs[nt][c] = __shfl_sync(~0u, up, (2 * j + c) * 4);
+        lim[nt][c] = col < rows ? kv - rq.n + col / G + 1 : 0;
+      }
+    }
+    const int all_see = kv - rq.n + 1;  // tokens that every row sees
+    const float sm = p.scale * 1.4426950408889634f / code_top(CODE);
+
+    float o[NT][KS][4], m[NT][2], l[NT][2];
+    float vref = 0.0f, vinv = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = -INFINITY;
+        l[nt][c] = 0.0f;
+      }
+    }
+
+    // this warp's 16-token blocks: 4 (b0 + i) + warp, i < count
+    const int all = (kv + 15) >> 4;
+    const int count = max(0, min(b1, (all - warp + kWarps - 1) / kWarps) - b0);
+    const int32_t* table = p.table + (int64_t)r * p.max_pages;
+    // pages and scales of 32 blocks at a time, one per lane, a batch ahead
+    auto page_at = [&](int i) -> int {
+      if (i >= count) return 0;
+      const int pg = table[((4 * (b0 + i) + warp) << 4) >> lg];
+      if (pg >= 0 && pg < p.num_pages) return pg;
+      report(p.status, KDA_ERR_BAD_PAGES);
+      return 0;
+    };
+    int pg_cur = page_at(lane), pg_next = page_at(32 + lane);
+    float ks_cur = p.k_scale[(int64_t)pg_cur * p.Hkv + h];
+    float vs_cur = p.v_scale[(int64_t)pg_cur * p.Hkv + h];
+    float ks_next = 0.0f, vs_next = 0.0f;
+
+    auto issue = [&](int i, int in_batch) {  // (all lanes)
+      const int pa = __shfl_sync(~0u, pg_cur, in_batch & 31);
+      const int pb = __shfl_sync(~0u, pg_next, in_batch & 31);
+      if (i < count) {
+        const int pg = in_batch < 32 ? pa : pb;
+        const int t0 = ((4 * (b0 + i) + warp) << 4) & (P - 1);
+        const int64_t at = ((((int64_t)pg * p.Hkv + h) << lg) + t0) * D;
+        const uint32_t dst = ring_u + (i % S) * Ring<D>::kStage;
+        const uint8_t* k = p.k_codes + at + i8 * D + 16 * j;
+        const uint8_t* v = p.v_codes + at + 2 * j * D + i8 * VB;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int c = 0; c < KC; ++c)
+            copy_async<16>(dst + (half * KC + c) * 512 + lane * 16, k + half * 8 * D + c * 64);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          copy_async<VB>(dst + 16 * D + e * (32 * VB) + lane * VB,
+                         v + ((e & 1) + (e >> 1) * 8) * D);
+      }
+      copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(i, i);
+
+    int bi = 0;  // i within its batch of 32
+    for (int i = 0; i < count; ++i, ++bi) {
+      if (bi == 32) {
+        bi = 0;
+        pg_cur = pg_next;
+        ks_cur = ks_next;
+        vs_cur = vs_next;
+        pg_next = page_at(i + 32 + lane);
+      }
+      if (bi == 8) {
+        ks_next = p.k_scale[(int64_t)pg_next * p.Hkv + h];
+        vs_next = p.v_scale[(int64_t)pg_next * p.Hkv + h];
+      }
+      issue(i + S - 1, bi + S - 1);
+      const float kf = __shfl_sync(~0u, ks_cur, bi) * sm, vs = __shfl_sync(~0u, vs_cur, bi);
+      copy_wait<S - 1>();
+      const unsigned char* st = ring + (i % S) * Ring<D>::kStage;
+      const int tok = (4 * (b0 + i) + warp) << 4;
+
+      // S^T = K Q^T
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const uint4 ka = *reinterpret_cast<const uint4*>(st + c * 512 + lane * 16);
+        const uint4 kb = *reinterpret_cast<const uint4*>(st + (KC + c) * 512 + lane * 16);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_half<CODE>(wa[s], a0, a2);
+          codes_to_half<CODE>(wb[s], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(x[nt], a0, a1, a2, a3, qf[nt][4 * c + s][0], qf[nt][4 * c + s][1]);
+        }
+      }
+      // scores in log2 units; tokens i8 and i8 + 8, columns 2 j and 2 j + 1
+      const bool edge = tok + 16 > all_see;
+      bool grow = vs > vref;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[nt][e] *= kf * qs[nt][e & 1];
+          if (edge && tok + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) x[nt][e] = -INFINITY;
+          grow |= x[nt][e] > m[nt][e & 1] + 8.0f;
+        }
+      }
+      // The reference m of a row need not be its maximum: it moves only when
+      // a score passes it by 8 (weights stay below 2^8, far inside f16).  So
+      // most blocks need one vote here and no shuffles.
+      if (__any_sync(~0u, grow)) {
+        const float vnew = vs > vref ? pow2_above(vs) : vref;
+        const float fv = vnew > 0.0f ? vref / vnew : 0.0f;
+        vref = vnew;
+        vinv = 1.0f / vnew;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(x[nt][c], x[nt][c + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+            const float mn = fmaxf(m[nt][c], mx);
+            f[c] = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - mn);
+            m[nt][c] = mn;
+            l[nt][c] *= f[c];
+            f[c] *= fv;
+          }
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][s][e] *= f[e & 1];
+        }
+      }
+      const float vw = vref > 0.0f ? vs * vinv : vs;  // (a page of zeros first: 0, or its NaN)
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mm = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
+          w[e] = ex2(x[nt][e] - mm);
+          l[nt][e & 1] += w[e];
+        }
+        pb[nt][0] = transpose8x8(pack_half(w[0] * vw, w[1] * vw));
+        pb[nt][1] = transpose8x8(pack_half(w[2] * vw, w[3] * vw));
+      }
+      // O^T += V^T P^T; lane's tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+      uint32_t v[4][VB / 4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned char* at = st + 16 * D + e * (32 * VB) + lane * VB;
+        if (VB == 16) {
+          const uint4 y = *reinterpret_cast<const uint4*>(at);
+          v[e][0] = y.x; v[e][1] = y.y; v[e][VB / 4 - 2] = y.z; v[e][VB / 4 - 1] = y.w;
+        } else {
+          const uint2 y = *reinterpret_cast<const uint2*>(at);
+          v[e][0] = y.x; v[e][1] = y.y;
+        }
+        // what a page holds past the request's end may be a NaN
+        if (CODE == KDA_E4M3 && edge && tok + 2 * j + (e & 1) + 8 * (e >> 1) >= kv) {
+#pragma unroll
+          for (int w = 0; w < VB / 4; ++w) v[e][w] = 0;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const uint32_t sel = (s & 1) ? 0x7362 : 0x5140;
+        uint32_t a0, a1, a2, a3;
+        codes_to_half<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
+        codes_to_half<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816(o[nt][s], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      }
+    }
+    copy_wait<0>();
+
+    // the warps' sums meet in shared memory (each in its own ring)
+    float* so = reinterpret_cast<float*>(ring);
+    const float ov = vref / code_top(CODE);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float y = l[nt][c];
+        y += __shfl_xor_sync(~0u, y, 4);
+        y += __shfl_xor_sync(~0u, y, 8);
+        y += __shfl_xor_sync(~0u, y, 16);
+        const int row = 8 * nt + 2 * j + c;
+        if (i8 == 0) {
+          s_m[warp][row] = m[nt][c];
+          s_l[warp][row] = y;
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          *reinterpret_cast<float2*>(so + row * D + i8 * VB + 2 * s) =
+              make_float2(o[nt][s][c] * ov, o[nt][s][c + 2] * ov);
+      }
+    }
+    __syncthreads();
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (u == sh.u0 && b0 > 0 ? 0 : 1);
+    for (int e = tid; e < rows * D; e += kThreads) {
+      const int row = e / D, ch = e % D;
+      float mx = s_m[0][row];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][row]);
+      const float mm = mx == -INFINITY ? 0.0f : mx;
+      float sum = 0.0f, acc = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_m[w][row] - mm);
+        sum += f * s_l[w][row];
+        acc += f * *reinterpret_cast<float*>(smem + w * Ring<D>::kWarpBytes + e * 4);
+      }
+      if (whole) {
+        const int64_t at = (int64_t)(rq.c0 + row / G) * p.Hq + h * G + row % G;
+        reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + ch] =
+            __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc / sum);
+        if (p.lse && ch == 0)
+          p.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+      } else {
+        p.part_o[(slot * kFewRows + row) * D + ch] = acc;
+        if (ch == 0) {
+          p.part_ml[(slot * kFewRows + row) * 2] = mx;
+          p.part_ml[(slot * kFewRows + row) * 2 + 1] = sum;
+        }
+      }
+    }
+    __syncthreads();
+    u = seg0 + b1;
+  }
+}
+
+// Joins the parts of one (request, head) row, in CTA order: out = sum_c w_c
+// O_c / sum_c w_c l_c with w_c = 2^(m_c - max m).  One CTA per row; warp w
+// takes the parts w, w + 8, ...
+template <int D>
+__global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, int ctas) {
+  constexpr int E = D / 32;
+  __shared__ float s_o[8][D], s_l[8], s_mx[8];
+  const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, row = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t base = p.prefix[r], nu = p.prefix[r + 1] - base, total = p.prefix[p.R];
+  if (nu == 0) return;
+  const int n = p.cu[r + 1] - p.cu[r];
+  if (row >= n * p.G) return;
+  const int64_t nb = nu / p.Hkv, share = (total + ctas - 1) / ctas;
+  const int64_t seg0 = base + h * nb, seg1 = seg0 + nb;
+  const int ca = (int)(seg0 / share), cb = (int)((seg1 - 1) / share);
+  if (ca == cb) return;  // written whole
+  // the first CTA holds it as its last piece, the others as their first
+  auto slot = [&](int c) -> int64_t { return 2 * (int64_t)c + (c == ca ? 1 : 0); };
+  float mx = -INFINITY;
+  for (int c = ca + tid; c <= cb; c += 256)
+    mx = fmaxf(mx, p.part_ml[(slot(c) * kFewRows + row) * 2]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+  if (lane == 0) s_mx[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) mx = fmaxf(mx, s_mx[w]);
+  const float mm = mx == -INFINITY ? 0.0f : mx;
+  float acc[E] = {}, sum = 0.0f;
+#pragma unroll 4
+  for (int c = ca + warp; c <= cb; c += 8) {
+    const int64_t at = slot(c) * kFewRows + row;
+    const float f = ex2(p.part_ml[at * 2] - mm);
+    sum += f * p.part_ml[at * 2 + 1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += f * p.part_o[at * D + e * 32 + lane];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = acc[e];
+  if (lane == 0) s_l[warp] = sum;
+  __syncthreads();
+  if (tid < D) {
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      a += s_o[w][tid];
+      b += s_l[w];
+    }
+    const int64_t at = (int64_t)(p.cu[r] + row / p.G) * p.Hq + h * p.G + row % p.G;
+    reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + tid] =
+        __float2bfloat16_rn(b == 0.0f ? 0.0f : a / b);
+    if (p.lse && tid == 0)
+      p.lse[at] = b == 0.0f ? -INFINITY : (mx + log2f(b)) * 0.6931471805599453f;
+  }
+}
+
+template <int CODE, int D, int NT>
+kda_status launch_rows(const AttnArgs& p, int ctas, cudaStream_t s) {
+  auto kernel = kda_cache_attn_rows_kernel<CODE, D, NT>;
+  const int smem = kWarps * Ring<D>::kWarpBytes;
+  const kda_status rc = kda_smem_attr((const void*)kernel, smem);
+  if (rc != KDA_OK) return rc;
+  kernel<<<ctas, kThreads, smem, s>>>(p);
+  const int64_t rows = (int64_t)p.max_new * p.G;
+  const dim3 grid((unsigned)p.R * p.Hkv, (unsigned)(rows < kFewRows ? rows : kFewRows));
+  kda_attn_join_kernel<D><<<grid, 256, 0, s>>>(p, ctas);
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <int CODE, int D>
+kda_status launch_nt(const AttnArgs& p, int ctas, cudaStream_t s) {
+  // one 8-row tile where no request can have more rows than that
+  if ((int64_t)p.max_new * p.G <= 8) return launch_rows<CODE, D, 1>(p, ctas, s);
+  return launch_rows<CODE, D, 2>(p, ctas, s);
+}
+
+}  // namespace
+
+kda_status kda_launch_attn_rows(const AttnArgs& p, int d, int code, int ctas, cudaStream_t s) {
+  if (code == KDA_I8)
+    return d == 64 ? launch_nt<KDA_I8, 64>(p, ctas, s) : launch_nt<KDA_I8, 128>(p, ctas, s);
+  return d == 64 ? launch_nt<KDA_E4M3, 64>(p, ctas, s) : launch_nt<KDA_E4M3, 128>(p, ctas, s);
+}
