@@ -7,6 +7,13 @@
 
 namespace kda_cache {
 
+// The segment (request, head, row tile) that a CTA's share begins in the
+// middle of: its units, first token, rows (0: none) and head.
+struct PartHead {
+  int64_t seg0, seg1;
+  int32_t tok0, rows, h, pad;
+};
+
 struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
@@ -19,14 +26,19 @@ struct AttnArgs {
   int R, T, max_new, max_pages, Hq, Hkv, G, num_pages, page_log2;
   float scale;
   // workspace of one kernel and its joining kernel
-  int64_t* prefix;  // [R + 1] units of the requests before
-  float* part_ml;   // [2 * CTAs][rows][2] maximum (log2) and sum of a part's rows
-  float* part_o;    // [2 * CTAs][rows][D] a part's sum of weighted values
+  int64_t* total;       // units of the whole batch
+  PartHead* part_head;  // [CTAs]
+  // A CTA leaves at most two parts: of the segment that its share begins in
+  // (slot 2 c) and of the one that it ends in (slot 2 c + 1).
+  float* part_ml;       // [2 * CTAs][rows][2] maximum (log2) and sum of a part's rows
+  float* part_o;        // [2 * CTAs][rows][D] a part's sum of weighted values
 };
 
 // Query rows per key / value head up to which a request runs on the few-row
 // kernel.
 constexpr int kFewRows = 16;
+// Query rows of a segment on the tile kernel.
+constexpr int kTileRows = 256;
 
 struct Req {
   int c0, n, kv;
@@ -44,7 +56,7 @@ __device__ __forceinline__ Req load_req(const AttnArgs& p, int r, bool& bad) {
 // contiguous shares of the sum over requests.  A CTA finds the request its
 // first unit falls in: every thread sums a contiguous range of requests, the
 // block scans the sums, the thread whose range holds the unit walks it.
-// Also writes the prefix sums (one CTA) and reports malformed requests.
+// CTA 0 also writes the sum and reports malformed requests.
 // units(Req) -> int64; NT threads.  Returns the CTA's units [u0, u1) and the
 // request of u0 with the units before it; u0 == u1 if there is nothing to do.
 struct Share {
@@ -87,20 +99,19 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, Units units) {
   s.u1 = min(total, s.u0 + share);
   int64_t at = before + inc - mine;
   const bool here = s.u0 < s.u1 && at <= s.u0 && s.u0 < at + mine;
-  if (here || blockIdx.x == 0) {
+  if (here) {
     for (int r = r0; r < r1; ++r) {
       bool bad;
       const Req q = load_req(p, r, bad);
       const int64_t u = q.n > 0 ? units(q) : 0;
-      if (here && at <= s.u0 && s.u0 < at + u) {
+      if (at <= s.u0 && s.u0 < at + u) {
         s_r = r;
         s_base = at;
       }
-      if (blockIdx.x == 0) p.prefix[r] = at;
       at += u;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) p.prefix[p.R] = total;
+  if (blockIdx.x == 0 && tid == 0) *p.total = total;
   __syncthreads();
   s.r = s_r;
   s.base = s_base;
@@ -160,5 +171,11 @@ __device__ __forceinline__ float exp2i(int e) {  // -126 <= e <= 127
 
 }  // namespace kda_cache
 
+// The kernels for few rows (kFewRows rows in a part) and for tiles of rows
+// (kTileRows), and the join of the parts that one of them has left.
 kda_status kda_launch_attn_rows(const kda_cache::AttnArgs& p, int d, int code, int ctas,
+                                cudaStream_t s);
+kda_status kda_launch_attn_tile(const kda_cache::AttnArgs& p, int d, int code, int ctas,
+                                cudaStream_t s);
+kda_status kda_launch_attn_join(const kda_cache::AttnArgs& p, int d, int part_rows, int ctas,
                                 cudaStream_t s);

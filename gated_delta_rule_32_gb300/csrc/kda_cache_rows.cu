@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   int r = sh.r;
   int64_t base = sh.base, u = sh.u0;
 
+  if (tid == 0) p.part_head[blockIdx.x].rows = 0;
   while (u < sh.u1) {
     bool bad;
     const Req rq = load_req(p, r, bad);
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     const int b1 = (int)(min(sh.u1, seg0 + nb) - seg0);
     const bool whole = b0 == 0 && b1 == nb;
     const int rows = rq.n * G, kv = rq.kv;
+    if (tid == 0 && b0 > 0) p.part_head[blockIdx.x] = {seg0, seg0 + nb, rq.c0, rows, h, 0};
 
     // queries, in the k order of the keys' chunks; each row scaled to f16
     uint32_t qf[NT][KS][2];
@@ -302,9 +304,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
           const float mm = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
           w[e] = ex2(x[nt][e] - mm);
           l[nt][e & 1] += w[e];
+          // (a masked token's weight stays 0 where the page's scale is a NaN)
+          w[e] = x[nt][e] == -INFINITY ? 0.0f : w[e] * vw;
         }
-        pb[nt][0] = transpose8x8(pack_half(w[0] * vw, w[1] * vw));
-        pb[nt][1] = transpose8x8(pack_half(w[2] * vw, w[3] * vw));
+        pb[nt][0] = transpose8x8(pack_half(w[0], w[1]));
+        pb[nt][1] = transpose8x8(pack_half(w[2], w[3]));
       }
       // O^T += V^T P^T; lane's tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9
       uint32_t v[4][VB / 4];
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       }
     }
     __syncthreads();
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (u == sh.u0 && b0 > 0 ? 0 : 1);
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (b0 > 0 ? 0 : 1);
     for (int e = tid; e < rows * D; e += kThreads) {
       const int row = e / D, ch = e % D;
       float mx = s_m[0][row];
@@ -393,60 +397,64 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   }
 }
 
-// Joins the parts of one (request, head) row, in CTA order: out = sum_c w_c
-// O_c / sum_c w_c l_c with w_c = 2^(m_c - max m).  One CTA per row; warp w
-// takes the parts w, w + 8, ...
-template <int D>
-__global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, int ctas) {
+// Joins the parts of the segments that cross CTA boundaries, in CTA order:
+// out = sum_c w_c O_c / sum_c w_c l_c with w_c = 2^(m_c - max m).  Block (c, y)
+// looks at the boundary between CTAs c and c + 1 and works if it is the first
+// inside its segment; WPR warps share a row and take its parts in turn.
+template <int D, int WPR>
+__global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, int ctas, int part_rows) {
   constexpr int E = D / 32;
-  __shared__ float s_o[8][D], s_l[8], s_mx[8];
-  const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, row = blockIdx.y;
+  constexpr int NR = 8 / WPR;  // rows of a block
+  __shared__ float s_o[8][D], s_l[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t base = p.prefix[r], nu = p.prefix[r + 1] - base, total = p.prefix[p.R];
-  if (nu == 0) return;
-  const int n = p.cu[r + 1] - p.cu[r];
-  if (row >= n * p.G) return;
-  const int64_t nb = nu / p.Hkv, share = (total + ctas - 1) / ctas;
-  const int64_t seg0 = base + h * nb, seg1 = seg0 + nb;
-  const int ca = (int)(seg0 / share), cb = (int)((seg1 - 1) / share);
-  if (ca == cb) return;  // written whole
-  // the first CTA holds it as its last piece, the others as their first
-  auto slot = [&](int c) -> int64_t { return 2 * (int64_t)c + (c == ca ? 1 : 0); };
-  float mx = -INFINITY;
-  for (int c = ca + tid; c <= cb; c += 256)
-    mx = fmaxf(mx, p.part_ml[(slot(c) * kFewRows + row) * 2]);
+  const PartHead ph = p.part_head[blockIdx.x + 1];
+  if ((int)blockIdx.y * NR >= ph.rows) return;
+  const int64_t share = (*p.total + ctas - 1) / ctas;
+  const int ca = (int)(ph.seg0 / share), cb = (int)((ph.seg1 - 1) / share);
+  if (ca != (int)blockIdx.x) return;
+  const int row = blockIdx.y * NR + warp / WPR, sub = warp % WPR;
+  const bool live = row < ph.rows;
+  // the first CTA holds it as its last segment, the others as their first
+  auto part = [&](int c) -> int64_t {
+    return (2 * (int64_t)c + (c == ca ? 1 : 0)) * part_rows + row;
+  };
+  float mx = -INFINITY, acc[E] = {}, sum = 0.0f;
+  if (live) {
+    for (int c = ca + lane; c <= cb; c += 32) mx = fmaxf(mx, p.part_ml[part(c) * 2]);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-  if (lane == 0) s_mx[warp] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) mx = fmaxf(mx, s_mx[w]);
-  const float mm = mx == -INFINITY ? 0.0f : mx;
-  float acc[E] = {}, sum = 0.0f;
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+    const float mm = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll 4
-  for (int c = ca + warp; c <= cb; c += 8) {
-    const int64_t at = slot(c) * kFewRows + row;
-    const float f = ex2(p.part_ml[at * 2] - mm);
-    sum += f * p.part_ml[at * 2 + 1];
+    for (int c = ca + sub; c <= cb; c += WPR) {
+      const int64_t at = part(c);
+      const float f = ex2(p.part_ml[at * 2] - mm);
+      sum += f * p.part_ml[at * 2 + 1];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += f * p.part_o[at * D + e * 32 + lane];
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = acc[e];
-  if (lane == 0) s_l[warp] = sum;
-  __syncthreads();
-  if (tid < D) {
-    float a = 0.0f, b = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      a += s_o[w][tid];
-      b += s_l[w];
+      for (int e = 0; e < E; ++e) acc[e] += f * p.part_o[at * D + e * 32 + lane];
     }
-    const int64_t at = (int64_t)(p.cu[r] + row / p.G) * p.Hq + h * p.G + row % p.G;
-    reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + tid] =
-        __float2bfloat16_rn(b == 0.0f ? 0.0f : a / b);
-    if (p.lse && tid == 0)
-      p.lse[at] = b == 0.0f ? -INFINITY : (mx + log2f(b)) * 0.6931471805599453f;
+  }
+  if (WPR > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = acc[e];
+    if (lane == 0) s_l[warp] = sum;
+    __syncthreads();
+    if (sub == 0) {
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) {
+        sum += s_l[warp + w];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += s_o[warp + w][e * 32 + lane];
+      }
+    }
+  }
+  if (live && sub == 0) {
+    const int64_t at = (int64_t)(ph.tok0 + row / p.G) * p.Hq + ph.h * p.G + row % p.G;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + e * 32 + lane] =
+          __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[e] / sum);
+    if (p.lse && lane == 0)
+      p.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
@@ -457,9 +465,6 @@ kda_status launch_rows(const AttnArgs& p, int ctas, cudaStream_t s) {
   const kda_status rc = kda_smem_attr((const void*)kernel, smem);
   if (rc != KDA_OK) return rc;
   kernel<<<ctas, kThreads, smem, s>>>(p);
-  const int64_t rows = (int64_t)p.max_new * p.G;
-  const dim3 grid((unsigned)p.R * p.Hkv, (unsigned)(rows < kFewRows ? rows : kFewRows));
-  kda_attn_join_kernel<D><<<grid, 256, 0, s>>>(p, ctas);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -476,4 +481,22 @@ kda_status kda_launch_attn_rows(const AttnArgs& p, int d, int code, int ctas, cu
   if (code == KDA_I8)
     return d == 64 ? launch_nt<KDA_I8, 64>(p, ctas, s) : launch_nt<KDA_I8, 128>(p, ctas, s);
   return d == 64 ? launch_nt<KDA_E4M3, 64>(p, ctas, s) : launch_nt<KDA_E4M3, 128>(p, ctas, s);
+}
+
+kda_status kda_launch_attn_join(const AttnArgs& p, int d, int part_rows, int ctas,
+                                cudaStream_t s) {
+  if (ctas < 2) return KDA_OK;
+  const int64_t most = (int64_t)p.max_new * p.G;
+  const int rows = (int)(most < part_rows ? most : part_rows);
+  if (part_rows == kFewRows) {
+    // few rows, up to as many parts as CTAs
+    const dim3 grid(ctas - 1, rows);
+    if (d == 64) kda_attn_join_kernel<64, 8><<<grid, 256, 0, s>>>(p, ctas, part_rows);
+    else kda_attn_join_kernel<128, 8><<<grid, 256, 0, s>>>(p, ctas, part_rows);
+  } else {
+    const dim3 grid(ctas - 1, (rows + 7) / 8);
+    if (d == 64) kda_attn_join_kernel<64, 1><<<grid, 256, 0, s>>>(p, ctas, part_rows);
+    else kda_attn_join_kernel<128, 1><<<grid, 256, 0, s>>>(p, ctas, part_rows);
+  }
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -1,0 +1,658 @@
+// kda_cache_tile.cu -- attention over the paged cache for requests with more
+// than a few query rows per key / value head (prompts, pieces of prompts),
+// on the tcgen05 tensor cores.
+//
+// A CTA works on segments: up to 256 query rows of one (request, key / value
+// head) -- rows are (token, head of the group) pairs, so the group shares the
+// keys it reads -- against a range of 128-token key tiles.  Two 128-row
+// tiles alternate: while one's softmax runs, the tensor cores work for the
+// other.  Warps:
+//   0-3, 4-7   softmax of row tile 0 / 1, one thread per row
+//   8-11       keys:   codes -> f16 operand tiles in shared memory
+//   12-15      values: the same
+//   16         issues the products (one thread) and owns tensor memory
+//   17         walks the schedule, a segment or two ahead of the others
+//   18, 19     only give their registers up
+// Tensor memory (512 columns): S of both tiles (the weights P replace S in
+// place, in f16), O of both tiles.
+//
+// Codes are exact in f16, so the only roundings of the products' inputs are
+// those of P (11 bits) and of small query elements next to large ones of the
+// same row.  A page's key scale multiplies its scores after the product; its
+// value scale multiplies its columns of P, relative to a power of two at
+// least as large (vref), which leaves O at the end.
+#include "kda_cache_attn.cuh"
+#include "sm100.cuh"
+
+namespace {
+
+using namespace kda_cache;
+
+// Five warpgroups launched with 96 registers a thread; they share them out
+// anew (setmaxnreg): 2 x 144 + 2 x 56 + 80 = 5 x 96.
+constexpr int kThreads = 640;
+constexpr int kRegsSoftmax = 144, kRegsConvert = 56, kRegsIssue = 80;
+static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue == 5 * 96, "registers at launch");
+constexpr int kTok = 128;    // tokens per key tile
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = 128 * D * 2;     // one f16 operand tile
+  static constexpr int kQ = 0;                  // 2 tiles
+  static constexpr int kK = 2 * kTile;          // 2 stages
+  static constexpr int kV = 4 * kTile;          // 2 stages
+  static constexpr int kBytes = 6 * kTile + 1024;
+};
+
+struct Bars {
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t seg_full[2], seg_empty[2];
+  uint64_t drain;
+};
+
+// A segment as the schedule's warp hands it to the others; rows = 0 ends.
+struct Seg {
+  int r, h, c0, n, kv;     // request and head
+  int tok0, rows;          // first token of the row tile in the request, query rows
+  int b0, b1, nu;          // key tiles [b0, b1) of nu
+};
+constexpr int kReaders = 17;  // warps that read it
+
+// Bounded wait that also gives up when another warp of the CTA has.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (sm100::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = sm100::globaltimer_ns();
+  for (;;) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (sm100::globaltimer_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Instruction descriptor, f16 operands and fp32 accumulation (the formats of
+// A and B are 0).
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+// sum_{i < n} floor((a i + b) / m), a, b >= 0, m > 0: the lattice points under
+// a line, by the steps of Euclid's algorithm (Graham, Knuth and Patashnik,
+// Concrete Mathematics, section 3.5).
+__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// The row tiles of a request: tile i holds tokens [i tt, (i + 1) tt) and sees
+// the first `seen(i)` tokens; its units are key tiles, one at least.
+struct Tiles {
+  int n, kv, tt, count;
+  __device__ Tiles(const Req& q, int G) : n(q.n), kv(q.kv), tt(kTileRows / G) {
+    count = q.n * (int64_t)G > kFewRows ? (q.n + tt - 1) / tt : 0;
+  }
+  __device__ int seen(int i) const { return max(0, kv - n + min(n, (i + 1) * tt)); }
+  __device__ int units(int i) const { return max(1, (int)(((int64_t)seen(i) + kTok - 1) / kTok)); }
+  // units of the tiles before i
+  __device__ int64_t before(int i) const {
+    const int last = min(i, count - 1);        // the full tiles among them
+    const int64_t first = (int64_t)kv - n + tt; // what a full tile 0 sees
+    // tiles that see at most one key tile have one unit
+    int64_t few = first > kTok ? 0 : (kTok - first) / tt + 1;
+    few = few < last ? few : last;
+    int64_t s = few + floor_sum(last - few, kTok, tt, first + few * tt + kTok - 1);
+    if (i > last) s += units(last);
+    return s;
+  }
+};
+
+// Walks a CTA's share, segment by segment.
+struct Walk {
+  const AttnArgs& p;
+  int64_t u, u1, base;  // next unit, end of the share, units before request r
+  int r, h, tile, b0, b1, nu;
+  int64_t per_head, seg0;
+  Req q;
+  Tiles t;
+  __device__ Walk(const AttnArgs& p_, const Share& s)
+      : p(p_), u(s.u0), u1(s.u1), base(s.base), r(s.r), h(0), tile(0), b0(0), b1(0), nu(0),
+        per_head(0), seg0(0), q{0, 0, 0}, t(Req{0, 0, 0}, 1) {
+    if (u >= u1) return;
+    load();
+    const int64_t in = u - base;
+    h = (int)(in / per_head);
+    const int64_t left = in - h * per_head;
+    int lo = 0, hi = t.count;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (t.before(mid) <= left) lo = mid; else hi = mid;
+    }
+    tile = lo;
+    seg0 = base + h * per_head + t.before(tile);
+    nu = t.units(tile);
+    set();
+  }
+  __device__ void load() {
+    bool bad;
+    q = load_req(p, r, bad);
+    t = Tiles(q, p.G);
+    per_head = t.count ? t.before(t.count) : 0;
+  }
+  __device__ void set() {
+    b0 = (int)(u - seg0);
+    b1 = (int)min((int64_t)nu, u1 - seg0);
+  }
+  __device__ bool live() const { return u < u1; }
+  __device__ void next() {
+    u = seg0 + b1;
+    if (u >= u1) return;
+    seg0 += nu;
+    if (++tile == t.count) {
+      tile = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        base += per_head * p.Hkv;
+        do {
+          ++r;
+          load();
+        } while (t.count == 0);
+      }
+    }
+    nu = t.units(tile);
+    set();
+  }
+  __device__ int tokens() const { return min(t.tt, q.n - tile * t.tt); }
+};
+
+template <int CODE, int D>
+__global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnArgs p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ Bars bars;
+  __shared__ Seg s_seg[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  unsigned char* smem = smem_raw + ((1024u - (sm100::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int lg = p.page_log2, P = 1 << lg;
+  volatile int* abort = &s_abort;
+
+  if (warp == 16) {
+    sm100::tmem_alloc(&s_tmem, 512);
+    sm100::tmem_relinquish();
+  }
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&bars.q_full[i], 128);
+      sm100::mbar_init(&bars.s_full[i], 1);
+      sm100::mbar_init(&bars.p_full[i], 128);
+      sm100::mbar_init(&bars.o_full[i], 1);
+      sm100::mbar_init(&bars.k_full[i], 128);
+      sm100::mbar_init(&bars.k_empty[i], 1);
+      sm100::mbar_init(&bars.v_full[i], 128);
+      sm100::mbar_init(&bars.v_empty[i], 1);
+      sm100::mbar_init(&bars.seg_full[i], 1);
+      sm100::mbar_init(&bars.seg_empty[i], kReaders);
+    }
+    sm100::mbar_init(&bars.drain, 1);
+    sm100::fence_mbar_init();
+  }
+  sm100::tc_fence_before();
+  const Share share = find_share<kThreads>(p, [&](const Req& q) {
+    const Tiles t(q, p.G);
+    return t.count ? t.before(t.count) * p.Hkv : 0;
+  });
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  uint32_t nseg = 0;  // segments seen
+  // the next segment, or rows = 0 at the end (or when a wait gave up), for a
+  // whole warp or for one thread of it
+  auto next_seg = [&](bool solo) -> Seg {
+    const uint32_t slot = nseg & 1;
+    Seg g;
+    bool ok = wait(&bars.seg_full[slot], (nseg >> 1) & 1, abort);
+    if (!solo) ok = __all_sync(~0u, ok);
+    if (ok) {
+      g = s_seg[slot];
+      if (!solo) __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&bars.seg_empty[slot]);
+      ++nseg;
+    } else {
+      g.rows = 0;
+    }
+    return g;
+  };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    regs_up<kRegsSoftmax>();
+    const int wg = warp >> 2, row = 128 * wg + 32 * (warp & 3) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + lanes + 128 * wg, tO = tmem + lanes + 256 + D * wg;
+    const float sm = fabsf(p.scale) * 1.4426950408889634f / code_top(CODE);
+    uint32_t seg = 0, it = 0;  // segments and key tiles that this row tile has had
+    for (;;) {
+      const Seg g = next_seg(false);
+      if (g.rows == 0) break;
+      if (128 * wg >= g.rows) continue;
+      const int kv = g.kv, tok = g.tok0 + row / p.G;
+      const bool mine = row < g.rows;
+      // query row: scaled to f16, to shared memory
+      float qs = 0.0f;
+      {
+        uint4 x[D / 8];
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          x[c] = make_uint4(0, 0, 0, 0);
+          if (mine)
+            x[c] = reinterpret_cast<const uint4*>(p.q + (int64_t)(g.c0 + tok) * p.q_stride +
+                                                  (int64_t)(g.h * p.G + row % p.G) * D)[c];
+          const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            most = max(most, max(y[e] & 0x7fff0000u, (y[e] << 16) & 0x7fff0000u));
+        }
+        const int ex = row_exponent(most);
+        const float down = copysignf(exp2i(-ex), p.scale);
+        qs = exp2i(ex) * sm;
+        unsigned char* dst = smem + Smem<D>::kQ + wg * Smem<D>::kTile + (row & 127) * 16;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            f[e] = pack_half(__uint_as_float(y[e] << 16) * down,
+                             __uint_as_float(y[e] & 0xffff0000u) * down);
+          *reinterpret_cast<uint4*>(dst + c * 2048) = make_uint4(f[0], f[1], f[2], f[3]);
+        }
+      }
+      sm100::fence_async_smem();
+      sm100::mbar_arrive(&bars.q_full[wg]);
+
+      const int lim = mine ? kv - g.n + tok + 1 : 0;  // tokens this row sees
+      const int all_see = kv - g.n + g.tok0 + (128 * wg) / p.G + 1;
+      float m = -INFINITY, l = 0.0f, vref = 0.0f, vinv = 0.0f;
+      const int nk = g.b1 - g.b0;
+      // lane i < 8 keeps the scales of tokens 16 i .. 16 i + 15 of a key tile,
+      // loaded a tile ahead, its page two
+      const int32_t* table = p.table + (int64_t)g.r * p.max_pages;
+      auto page_of = [&](int k) -> int {
+        const int64_t t0 = (int64_t)(g.b0 + k) * kTok + 16 * (lane & 7);
+        if (k >= nk || t0 >= kv) return -1;
+        const int pg = table[t0 >> lg];
+        if (pg >= 0 && pg < p.num_pages) return pg;
+        report(p.status, KDA_ERR_BAD_PAGES);
+        return -1;
+      };
+      auto scale_of = [&](const float* s, int pg) {
+        return pg < 0 ? 0.0f : s[(int64_t)pg * p.Hkv + g.h];
+      };
+      int pg = page_of(0);
+      float ks = scale_of(p.k_scale, pg), vs = scale_of(p.v_scale, pg);
+      pg = page_of(1);
+      bool ok = true;
+      for (int k = 0; k < nk; ++k, ++it) {
+        const float ks_next = scale_of(p.k_scale, pg), vs_next = scale_of(p.v_scale, pg);
+        pg = page_of(k + 2);
+        float vmax = vs;
+        vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 1));
+        vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 2));
+        vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 4));
+        const int t0 = (g.b0 + k) * kTok;
+        const bool edge = t0 + kTok > all_see;
+        ok = __all_sync(~0u, wait(&bars.s_full[wg], it & 1, abort));
+        if (!ok) break;
+        sm100::tc_fence_after();
+        // the row's maximum in log2 units
+        float mx = -INFINITY;
+        uint32_t s[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(tS + 32 * c, s);
+          const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs, f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
+          sm100::tmem_wait_ld();
+          if (!edge) {
+            float a = __uint_as_float(s[0]), b = __uint_as_float(s[16]);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) {
+              a = fmaxf(a, __uint_as_float(s[e]));
+              b = fmaxf(b, __uint_as_float(s[16 + e]));
+            }
+            mx = fmaxf(mx, fmaxf(a * f0, b * f1));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (t0 + 32 * c + e < lim) mx = fmaxf(mx, __uint_as_float(s[e]) * (e < 16 ? f0 : f1));
+          }
+        }
+        // as in the few-row kernel, the reference moves only when passed by 8
+        const bool grow = mx > m + 8.0f;
+        if (__any_sync(~0u, grow) || vmax > vref) {
+          const float vnew = vmax > vref ? pow2_above(vmax) : vref;
+          float f = vnew > 0.0f ? vref / vnew : 0.0f;
+          vref = vnew;
+          vinv = 1.0f / vnew;
+          if (grow) {
+            const float fm = m == -INFINITY ? 0.0f : ex2(m - mx);
+            l *= fm;
+            f *= fm;
+            m = mx;
+          }
+          if (k > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              float y[16];
+              uint32_t z[16];
+              __syncwarp();
+              sm100::tmem_ld16(tO + 16 * c, y);
+              sm100::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(y[e] * f);
+              sm100::tmem_st16(tO + 16 * c, z);
+            }
+          }
+        }
+        const float mm = m == -INFINITY ? 0.0f : m;
+        const float vrel = vref > 0.0f ? vs * vinv : vs;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(tS + 32 * c, s);
+          const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs, f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
+          const float v0 = __shfl_sync(~0u, vrel, 2 * c), v1 = __shfl_sync(~0u, vrel, 2 * c + 1);
+          sm100::tmem_wait_ld();
+          uint32_t z[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float f = e < 16 ? f0 : f1, v = e < 16 ? v0 : v1;
+            float a = ex2(fmaf(__uint_as_float(s[e]), f, -mm));
+            float b = ex2(fmaf(__uint_as_float(s[e + 1]), f, -mm));
+            float av = a * v, bv = b * v;
+            if (edge) {  // (the scales of masked tokens may be NaN)
+              if (t0 + 32 * c + e >= lim) a = av = 0.0f;
+              if (t0 + 32 * c + e + 1 >= lim) b = bv = 0.0f;
+            }
+            l += a + b;
+            z[e / 2] = pack_half(av, bv);
+          }
+          sm100::tmem_st16(tS + 16 * c, z);
+        }
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        sm100::mbar_arrive(&bars.p_full[wg]);
+        ks = ks_next;
+        vs = vs_next;
+      }
+      if (!ok || !__all_sync(~0u, wait(&bars.o_full[wg], seg & 1, abort))) break;
+      ++seg;
+      sm100::tc_fence_after();
+      const float ov = vref / code_top(CODE);
+      const bool whole = g.b0 == 0 && g.b1 == g.nu;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (g.b0 > 0 ? 0 : 1);
+      const int64_t at = (int64_t)(g.c0 + tok) * p.Hq + g.h * p.G + row % p.G;
+      const float f = whole ? (l == 0.0f ? 0.0f : ov / l) : ov;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        float y[16];
+        __syncwarp();
+        sm100::tmem_ld16(tO + 16 * c, y);
+        sm100::tmem_wait_ld();
+        // (a row that has seen nothing: its weights are zeros, so is its sum)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] *= f;
+        if (mine && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + 16 * c);
+          dst[0] = make_uint4(sm100::pack_bf16x2(y[0], y[1]), sm100::pack_bf16x2(y[2], y[3]),
+                              sm100::pack_bf16x2(y[4], y[5]), sm100::pack_bf16x2(y[6], y[7]));
+          dst[1] = make_uint4(sm100::pack_bf16x2(y[8], y[9]), sm100::pack_bf16x2(y[10], y[11]),
+                              sm100::pack_bf16x2(y[12], y[13]), sm100::pack_bf16x2(y[14], y[15]));
+        } else if (mine) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * kTileRows + row) * D + 16 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        }
+      }
+      sm100::tc_fence_before();
+      if (mine) {
+        if (!whole) {
+          p.part_ml[(slot * kTileRows + row) * 2] = m;
+          p.part_ml[(slot * kTileRows + row) * 2 + 1] = l;
+        } else if (p.lse) {
+          p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+    }
+  } else if (warp < 16) {
+    // ---------------------------------------------- codes -> f16 operands
+    // Both operands are laid out [8-channel chunk][token][16 bytes]: core
+    // matrices of 8 tokens x 16 bytes, K-major for the keys (contracted over
+    // channels), MN-major for the values (contracted over tokens).  Lanes 8 c
+    // .. 8 c + 7 of a warp take the same 16 codes of 8 tokens, so the global
+    // reads are whole sectors and the shared writes free of conflicts.
+    regs_down<kRegsConvert>();
+    const bool is_v = warp >= 12;
+    const int wq = warp & 3, t8 = lane & 7, c4 = lane >> 3;
+    const uint8_t* codes = is_v ? p.v_codes : p.k_codes;
+    uint64_t* full = is_v ? bars.v_full : bars.k_full;
+    uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
+    unsigned char* tiles = smem + (is_v ? Smem<D>::kV : Smem<D>::kK);
+    constexpr int NC = D / 64;  // 64-byte column blocks
+    uint32_t cnt = 0;
+    bool ok = true;
+    while (ok) {
+      const Seg sg = next_seg(false);
+      if (sg.rows == 0) break;
+      const int nk = sg.b1 - sg.b0, kv = sg.kv;
+      const int32_t* table = p.table + (int64_t)sg.r * p.max_pages;
+      // this warp's 32 tokens of a tile lie in two 16-token groups
+      auto page_of = [&](int k, int g) -> int {
+        const int64_t t0 = (int64_t)(sg.b0 + k) * kTok + 32 * wq + 16 * g;
+        if (k >= nk || t0 >= kv) return -1;
+        const int pg = table[t0 >> lg];
+        return pg >= 0 && pg < p.num_pages ? pg : -1;
+      };
+      uint4 x[4][NC];
+      auto fetch = [&](int k, int pa, int pb) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int pg = g < 2 ? pa : pb;
+          const int64_t t = (int64_t)(sg.b0 + k) * kTok + 32 * wq + 8 * g + t8;
+          const uint8_t* src =
+              codes + ((((int64_t)pg * p.Hkv + sg.h) << lg) + (t & (P - 1))) * D + 16 * c4;
+          // (what a page holds past the request's end may be a NaN)
+          const bool use = pg >= 0 && (!is_v || t < kv);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            x[g][c] = use ? *reinterpret_cast<const uint4*>(src + 64 * c) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      int pa = page_of(0, 0), pb = page_of(0, 1);
+      fetch(0, pa, pb);
+      pa = page_of(1, 0);
+      pb = page_of(1, 1);
+      for (int k = 0; k < nk; ++k, ++cnt) {
+        const int st = cnt & 1;
+        if (cnt >= 2) {
+          ok = __all_sync(~0u, wait(&empty[st], ((cnt >> 1) - 1) & 1, abort));
+          if (!ok) break;
+        }
+        unsigned char* dst = tiles + st * Smem<D>::kTile + (32 * wq + t8) * 16;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const uint32_t y[4] = {x[g][c].x, x[g][c].y, x[g][c].z, x[g][c].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) codes_to_half<CODE>(y[e], f[2 * e], f[2 * e + 1]);
+            unsigned char* d = dst + g * 128 + (8 * c + 2 * c4) * 2048;
+            *reinterpret_cast<uint4*>(d) = make_uint4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint4*>(d + 2048) = make_uint4(f[4], f[5], f[6], f[7]);
+          }
+        if (k + 1 < nk) fetch(k + 1, pa, pb);
+        pa = page_of(k + 2, 0);
+        pb = page_of(k + 2, 1);
+        sm100::fence_async_smem();
+        sm100::mbar_arrive(&full[st]);
+      }
+    }
+  } else {
+    regs_down<kRegsIssue>();
+    if (warp == 17) {
+      // ---------------------------------------------------------- schedule
+      if (lane == 0) {
+        Walk w(p, share);
+        // what the join of parts needs to know of the segment that this CTA
+        // enters in its middle
+        PartHead ph{0, 0, 0, 0, 0, 0};
+        if (w.live() && w.b0 > 0)
+          ph = {w.seg0, w.seg0 + w.nu, w.q.c0 + w.tile * w.t.tt, w.tokens() * p.G, w.h, 0};
+        p.part_head[blockIdx.x] = ph;
+        for (uint32_t i = 0;; ++i) {
+          if (i >= 2 && !wait(&bars.seg_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
+          Seg g{};
+          if (w.live())
+            g = {w.r, w.h, w.q.c0, w.q.n, w.q.kv, w.tile * w.t.tt, w.tokens() * p.G, w.b0, w.b1,
+                 w.nu};
+          s_seg[i & 1] = g;
+          sm100::mbar_arrive(&bars.seg_full[i & 1]);
+          if (g.rows == 0) break;
+          w.next();
+        }
+      }
+    } else if (warp == 16 && lane == 0) {
+    // ----------------------------------------------------------- products
+    const uint32_t id_s = idesc_f16(128, kTok, 0), id_o = idesc_f16(128, D, 1);
+    const uint32_t sQ = sm100::smem_u32(smem + Smem<D>::kQ);
+    const uint32_t sK = sm100::smem_u32(smem + Smem<D>::kK);
+    const uint32_t sV = sm100::smem_u32(smem + Smem<D>::kV);
+    auto scores = [&](int t, int st) {  // S_t = Q_t K^T
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+        sm100::mma_ss(tmem + 128 * t,
+                      sm100::smem_desc(sQ + t * Smem<D>::kTile + s * 4096, 2048, 128),
+                      sm100::smem_desc(sK + st * Smem<D>::kTile + s * 4096, 2048, 128), id_s, s > 0);
+      sm100::mma_commit(&bars.s_full[t]);
+    };
+    auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
+#pragma unroll
+      for (int s = 0; s < kTok / 16; ++s)
+        sm100::mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * s,
+                      sm100::smem_desc(sV + st * Smem<D>::kTile + s * 256, 128, 2048), id_o,
+                      !first || s > 0);
+    };
+    uint32_t seg[2] = {0, 0}, it[2] = {0, 0}, kc = 0, vc = 0;
+    bool ok = true;
+    for (;;) {
+      const Seg g = next_seg(true);
+      if (g.rows == 0) break;
+      const bool two = g.rows > 128;
+      const int nk = g.b1 - g.b0;
+      ok = wait(&bars.q_full[0], seg[0]++ & 1, abort) &&
+           (!two || wait(&bars.q_full[1], seg[1]++ & 1, abort)) &&
+           wait(&bars.k_full[kc & 1], (kc >> 1) & 1, abort);
+      if (!ok) break;
+      sm100::tc_fence_after();
+      scores(0, kc & 1);
+      if (two) scores(1, kc & 1);
+      sm100::mma_commit(&bars.k_empty[kc & 1]);
+      ++kc;
+      for (int k = 0; k < nk; ++k, ++vc) {
+        const bool last = k + 1 == nk;
+        ok = wait(&bars.v_full[vc & 1], (vc >> 1) & 1, abort) &&
+             wait(&bars.p_full[0], it[0]++ & 1, abort);
+        if (!ok) break;
+        sm100::tc_fence_after();
+        values(0, vc & 1, k == 0);
+        if (last) {
+          sm100::mma_commit(&bars.o_full[0]);
+        } else {
+          ok = wait(&bars.k_full[kc & 1], (kc >> 1) & 1, abort);
+          if (!ok) break;
+          sm100::tc_fence_after();
+          scores(0, kc & 1);
+        }
+        if (two) {
+          ok = wait(&bars.p_full[1], it[1]++ & 1, abort);
+          if (!ok) break;
+          sm100::tc_fence_after();
+          values(1, vc & 1, k == 0);
+          if (last) sm100::mma_commit(&bars.o_full[1]);
+        }
+        sm100::mma_commit(&bars.v_empty[vc & 1]);
+        if (!last) {
+          if (two) scores(1, kc & 1);
+          sm100::mma_commit(&bars.k_empty[kc & 1]);
+          ++kc;
+        }
+      }
+    }
+    // the last commits (of k_empty, v_empty) must land before the CTA leaves
+    sm100::mma_commit(&bars.drain);
+    sm100::mbar_wait(&bars.drain, 0, 200000000ull);
+    }
+  }
+  __syncwarp();
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && s_abort) report(p.status, KDA_ERR_TIMEOUT);
+  if (warp == 16) sm100::tmem_dealloc(tmem, 512);
+}
+
+template <int CODE, int D>
+kda_status launch_tile(const AttnArgs& p, int ctas, cudaStream_t s) {
+  auto kernel = kda_cache_attn_tile_kernel<CODE, D>;
+  const kda_status rc = kda_smem_attr((const void*)kernel, Smem<D>::kBytes);
+  if (rc != KDA_OK) return rc;
+  kernel<<<ctas, kThreads, Smem<D>::kBytes, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace
+
+kda_status kda_launch_attn_tile(const AttnArgs& p, int d, int code, int ctas, cudaStream_t s) {
+  if (code == KDA_I8)
+    return d == 64 ? launch_tile<KDA_I8, 64>(p, ctas, s) : launch_tile<KDA_I8, 128>(p, ctas, s);
+  return d == 64 ? launch_tile<KDA_E4M3, 64>(p, ctas, s) : launch_tile<KDA_E4M3, 128>(p, ctas, s);
+}

@@ -401,6 +401,22 @@ def test_marked_page_reaches_only_those_who_see_it(new):
     assert out[n:].isfinite().all()
 
 
+@pytest.mark.parametrize("n,G", [(4, 4), (90, 2), (90, 8)])
+@pytest.mark.parametrize("dtype", [I8, F8])
+def test_marked_page_of_later_tokens_stays_unseen(n, G, dtype):
+    # the last page, of new tokens only, is marked: queries before it are untouched
+    page, ctx = 16, 48 - n % 16 + 2
+    b = batch([n], [ctx], page, 1, G, 64, dtype, seed=53)
+    clean, clean_lse = call(b)
+    first = (ctx + n - 1) // page * page - ctx      # the first new token in the last page
+    pg = b["table"][0][(ctx + n - 1) // page]
+    b["vs"][pg] = float("nan")
+    b["ks"][pg] = float("nan")
+    out, lse = call(b)
+    assert torch.equal(out[:first], clean[:first]) and torch.equal(lse[:first], clean_lse[:first])
+    assert out[first:].isnan().all() and lse[first:].isnan().all()
+
+
 @pytest.mark.parametrize("new", [[1] * 7, [30, 1, 70]])
 def test_token_stride_other_stream_and_no_lse(new):
     b = batch(new, [50 + 60 * i for i in range(len(new))], 64, 2, 4, 128, I8, seed=23)
