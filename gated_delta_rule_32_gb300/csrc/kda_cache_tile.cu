@@ -86,6 +86,49 @@ __device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&r)[32]) {
       : "r"(ta));
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t ta, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(ta),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Pairs of fp32 values in one 64-bit register, two results an instruction.
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -312,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
 
       const int lim = mine ? kv - g.n + tok + 1 : 0;  // tokens this row sees
       const int all_see = kv - g.n + g.tok0 + (128 * wg) / p.G + 1;
-      float m = -INFINITY, l = 0.0f, vref = 0.0f, vinv = 0.0f;
+      float m = -INFINITY, l = 0.0f, vref = 0.0f, vrel_of = 1.0f;
       const int nk = g.b1 - g.b0;
       // lane i < 8 keeps the scales of tokens 16 i .. 16 i + 15 of a key tile,
       // loaded a tile ahead, its page two
@@ -344,79 +387,116 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         ok = __all_sync(~0u, wait(&bars.s_full[wg], it & 1, abort));
         if (!ok) break;
         sm100::tc_fence_after();
-        // the row's maximum in log2 units
-        float mx = -INFINITY;
-        uint32_t s[32];
+        // Weights with the reference m of the tiles before; only where a row
+        // passes it by 8 (its weight by 2^8: f16 has room for that), in the
+        // first tile, or when a page's value scale passes vref, is the
+        // maximum sought, O rescaled and the tile's weights made again.  So
+        // S is read once, and O almost never.
+        uint32_t z[64];
+        float lt;
+        bool fresh = k == 0 || vmax > vref;
+        for (;;) {
+          if (fresh) {
+            float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(tS + 32 * c, s);
-          const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs, f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
-          sm100::tmem_wait_ld();
-          if (!edge) {
-            float a = __uint_as_float(s[0]), b = __uint_as_float(s[16]);
-#pragma unroll
-            for (int e = 1; e < 16; ++e) {
-              a = fmaxf(a, __uint_as_float(s[e]));
-              b = fmaxf(b, __uint_as_float(s[16 + e]));
-            }
-            mx = fmaxf(mx, fmaxf(a * f0, b * f1));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (t0 + 32 * c + e < lim) mx = fmaxf(mx, __uint_as_float(s[e]) * (e < 16 ? f0 : f1));
-          }
-        }
-        // as in the few-row kernel, the reference moves only when passed by 8
-        const bool grow = mx > m + 8.0f;
-        if (__any_sync(~0u, grow) || vmax > vref) {
-          const float vnew = vmax > vref ? pow2_above(vmax) : vref;
-          float f = vnew > 0.0f ? vref / vnew : 0.0f;
-          vref = vnew;
-          vinv = 1.0f / vnew;
-          if (grow) {
-            const float fm = m == -INFINITY ? 0.0f : ex2(m - mx);
-            l *= fm;
-            f *= fm;
-            m = mx;
-          }
-          if (k > 0) {
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              float y[16];
-              uint32_t z[16];
-              __syncwarp();
-              sm100::tmem_ld16(tO + 16 * c, y);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs;
+              const float f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
+              tmem_ld32(tS + 32 * c, s);
               sm100::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(y[e] * f);
-              sm100::tmem_st16(tO + 16 * c, z);
+              for (int e = 0; e < 32; ++e)
+                if (t0 + 32 * c + e < lim)
+                  mx = fmaxf(mx, __uint_as_float(s[e]) * (e < 16 ? f0 : f1));
+            }
+            // (a row that sees nothing here sees nothing further on: 0 serves)
+            const float mn = fmaxf(m, mx) == -INFINITY ? 0.0f : fmaxf(m, mx);
+            const float vnew = vmax > vref ? pow2_above(vmax) : vref;
+            const float fm = k == 0 ? 0.0f : ex2(m - mn);
+            const float f = vnew > 0.0f ? vref / vnew * fm : fm;
+            m = mn;
+            l *= fm;
+            vref = vnew;
+            vrel_of = vnew > 0.0f ? 1.0f / vnew : 1.0f;
+            if (k > 0) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                float y[16];
+                uint32_t o[16];
+                __syncwarp();
+                sm100::tmem_ld16(tO + 16 * c, y);
+                sm100::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(y[e] * f);
+                sm100::tmem_st16(tO + 16 * c, o);
+              }
             }
           }
-        }
-        const float mm = m == -INFINITY ? 0.0f : m;
-        const float vrel = vref > 0.0f ? vs * vinv : vs;
+          const float vrel = vs * vrel_of;
+          uint32_t zmax = 0;
+          f32x2 l2 = pack2(0.0f, 0.0f), m2 = pack2(-m, -m);
+          if (!edge) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(tS + 32 * c, s);
-          const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs, f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
-          const float v0 = __shfl_sync(~0u, vrel, 2 * c), v1 = __shfl_sync(~0u, vrel, 2 * c + 1);
-          sm100::tmem_wait_ld();
-          uint32_t z[16];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              tmem_ld32(tS + 32 * c, s);
+              const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs;
+              const float f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
+              const float v0 = __shfl_sync(~0u, vrel, 2 * c);
+              const float v1 = __shfl_sync(~0u, vrel, 2 * c + 1);
+              sm100::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float f = e < 16 ? f0 : f1, v = e < 16 ? v0 : v1;
-            float a = ex2(fmaf(__uint_as_float(s[e]), f, -mm));
-            float b = ex2(fmaf(__uint_as_float(s[e + 1]), f, -mm));
-            float av = a * v, bv = b * v;
-            if (edge) {  // (the scales of masked tokens may be NaN)
-              if (t0 + 32 * c + e >= lim) a = av = 0.0f;
-              if (t0 + 32 * c + e + 1 >= lim) b = bv = 0.0f;
+              for (int e = 0; e < 32; e += 2) {
+                const float f = e < 16 ? f0 : f1, v = e < 16 ? v0 : v1;
+                float a, b;
+                unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pack2(f, f),
+                             m2), a, b);
+                const f32x2 w = pack2(ex2(a), ex2(b));
+                l2 = add2(l2, w);
+                unpack2(mul2(w, pack2(v, v)), a, b);
+                z[16 * c + e / 2] = pack_half(a, b);
+                zmax = max_half2(zmax, z[16 * c + e / 2]);
+              }
             }
-            l += a + b;
-            z[e / 2] = pack_half(av, bv);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              tmem_ld32(tS + 32 * c, s);
+              const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs;
+              const float f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
+              const float v0 = __shfl_sync(~0u, vrel, 2 * c);
+              const float v1 = __shfl_sync(~0u, vrel, 2 * c + 1);
+              sm100::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float f = e < 16 ? f0 : f1, v = e < 16 ? v0 : v1;
+                float a = ex2(fmaf(__uint_as_float(s[e]), f, -m));
+                float b = ex2(fmaf(__uint_as_float(s[e + 1]), f, -m));
+                float av = a * v, bv = b * v;
+                // (the scales of masked tokens may be NaN)
+                if (t0 + 32 * c + e >= lim) a = av = 0.0f;
+                if (t0 + 32 * c + e + 1 >= lim) b = bv = 0.0f;
+                l2 = add2(l2, pack2(a, b));
+                z[16 * c + e / 2] = pack_half(av, bv);
+                zmax = max_half2(zmax, z[16 * c + e / 2]);
+              }
+            }
           }
-          sm100::tmem_st16(tS + 16 * c, z);
+          float la, lb;
+          unpack2(l2, la, lb);
+          lt = la + lb;
+          // (!<=: an infinity or NaN counts too)
+          const __half2 zm = *reinterpret_cast<__half2*>(&zmax);
+          const bool over = !(__low2float(zm) <= 256.0f && __high2float(zm) <= 256.0f);
+          if (fresh || !__any_sync(~0u, over)) break;
+          fresh = true;
         }
+        l += lt;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_st32(tS + 32 * c, z + 32 * c);
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
         sm100::mbar_arrive(&bars.p_full[wg]);
@@ -456,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       sm100::tc_fence_before();
       if (mine) {
         if (!whole) {
-          p.part_ml[(slot * kTileRows + row) * 2] = m;
+          p.part_ml[(slot * kTileRows + row) * 2] = l == 0.0f ? -INFINITY : m;
           p.part_ml[(slot * kTileRows + row) * 2 + 1] = l;
         } else if (p.lse) {
           p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -564,22 +644,22 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     } else if (warp == 16 && lane == 0) {
     // ----------------------------------------------------------- products
     const uint32_t id_s = idesc_f16(128, kTok, 0), id_o = idesc_f16(128, D, 1);
-    const uint32_t sQ = sm100::smem_u32(smem + Smem<D>::kQ);
-    const uint32_t sK = sm100::smem_u32(smem + Smem<D>::kK);
-    const uint32_t sV = sm100::smem_u32(smem + Smem<D>::kV);
+    // (a descriptor's address field counts 16-byte units)
+    const uint64_t dQ = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kQ), 2048, 128);
+    const uint64_t dK = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kK), 2048, 128);
+    const uint64_t dV = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kV), 128, 2048);
+    constexpr int kTile16 = Smem<D>::kTile / 16;
     auto scores = [&](int t, int st) {  // S_t = Q_t K^T
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
-        sm100::mma_ss(tmem + 128 * t,
-                      sm100::smem_desc(sQ + t * Smem<D>::kTile + s * 4096, 2048, 128),
-                      sm100::smem_desc(sK + st * Smem<D>::kTile + s * 4096, 2048, 128), id_s, s > 0);
+        sm100::mma_ss(tmem + 128 * t, dQ + t * kTile16 + s * 256, dK + st * kTile16 + s * 256, id_s,
+                      s > 0);
       sm100::mma_commit(&bars.s_full[t]);
     };
     auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
 #pragma unroll
       for (int s = 0; s < kTok / 16; ++s)
-        sm100::mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * s,
-                      sm100::smem_desc(sV + st * Smem<D>::kTile + s * 256, 128, 2048), id_o,
+        sm100::mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * s, dV + st * kTile16 + s * 16, id_o,
                       !first || s > 0);
     };
     uint32_t seg[2] = {0, 0}, it[2] = {0, 0}, kc = 0, vc = 0;
