@@ -129,6 +129,40 @@ __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// The products, issued by a whole warp that runs in step, of which one thread
+// (`one`) carries them out.  In a branch of one thread the operands are not
+// known to be uniform, and each product cost 97-105 cycles to issue; so it is
+// the tensor cores' own 64 (128 x 128 x 16, f16).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::"
+      "arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(sm100::smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -285,18 +319,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   });
   __syncthreads();
   sm100::tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(~0u, s_tmem, 0);
   uint32_t nseg = 0;  // segments seen
-  // the next segment, or rows = 0 at the end (or when a wait gave up), for a
-  // whole warp or for one thread of it
-  auto next_seg = [&](bool solo) -> Seg {
+  // a wait of a whole warp; the next segment, or rows = 0 at the end (or when a
+  // wait gave up)
+  auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(~0u, wait(bar, parity, abort));
+  };
+  auto next_seg = [&]() -> Seg {
     const uint32_t slot = nseg & 1;
     Seg g;
-    bool ok = wait(&bars.seg_full[slot], (nseg >> 1) & 1, abort);
-    if (!solo) ok = __all_sync(~0u, ok);
-    if (ok) {
+    if (all_wait(&bars.seg_full[slot], (nseg >> 1) & 1)) {
       g = s_seg[slot];
-      if (!solo) __syncwarp();
+      __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&bars.seg_empty[slot]);
       ++nseg;
     } else {
@@ -314,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     const float sm = fabsf(p.scale) * 1.4426950408889634f / code_top(CODE);
     uint32_t seg = 0, it = 0;  // segments and key tiles that this row tile has had
     for (;;) {
-      const Seg g = next_seg(false);
+      const Seg g = next_seg();
       if (g.rows == 0) break;
       if (128 * wg >= g.rows) continue;
       const int kv = g.kv, tok = g.tok0 + row / p.G;
@@ -384,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 4));
         const int t0 = (g.b0 + k) * kTok;
         const bool edge = t0 + kTok > all_see;
-        ok = __all_sync(~0u, wait(&bars.s_full[wg], it & 1, abort));
+        ok = all_wait(&bars.s_full[wg], it & 1);
         if (!ok) break;
         sm100::tc_fence_after();
         // Weights with the reference m of the tiles before; only where a row
@@ -503,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         ks = ks_next;
         vs = vs_next;
       }
-      if (!ok || !__all_sync(~0u, wait(&bars.o_full[wg], seg & 1, abort))) break;
+      if (!ok || !all_wait(&bars.o_full[wg], seg & 1)) break;
       ++seg;
       sm100::tc_fence_after();
       const float ov = vref / code_top(CODE);
@@ -561,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     uint32_t cnt = 0;
     bool ok = true;
     while (ok) {
-      const Seg sg = next_seg(false);
+      const Seg sg = next_seg();
       if (sg.rows == 0) break;
       const int nk = sg.b1 - sg.b0, kv = sg.kv;
       const int32_t* table = p.table + (int64_t)sg.r * p.max_pages;
@@ -594,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       for (int k = 0; k < nk; ++k, ++cnt) {
         const int st = cnt & 1;
         if (cnt >= 2) {
-          ok = __all_sync(~0u, wait(&empty[st], ((cnt >> 1) - 1) & 1, abort));
+          ok = all_wait(&empty[st], ((cnt >> 1) - 1) & 1);
           if (!ok) break;
         }
         unsigned char* dst = tiles + st * Smem<D>::kTile + (32 * wq + t8) * 16;
@@ -641,9 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
           w.next();
         }
       }
-    } else if (warp == 16 && lane == 0) {
+    } else if (warp == 16) {
     // ----------------------------------------------------------- products
     const uint32_t id_s = idesc_f16(128, kTok, 0), id_o = idesc_f16(128, D, 1);
+    const uint32_t one = elect_one();
     // (a descriptor's address field counts 16-byte units)
     const uint64_t dQ = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kQ), 2048, 128);
     const uint64_t dK = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kK), 2048, 128);
@@ -652,64 +688,63 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     auto scores = [&](int t, int st) {  // S_t = Q_t K^T
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
-        sm100::mma_ss(tmem + 128 * t, dQ + t * kTile16 + s * 256, dK + st * kTile16 + s * 256, id_s,
-                      s > 0);
-      sm100::mma_commit(&bars.s_full[t]);
+        mma_ss(tmem + 128 * t, dQ + t * kTile16 + s * 256, dK + st * kTile16 + s * 256, id_s, s > 0, one);
+      mma_commit(&bars.s_full[t], one);
     };
     auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
 #pragma unroll
       for (int s = 0; s < kTok / 16; ++s)
-        sm100::mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * s, dV + st * kTile16 + s * 16, id_o,
-                      !first || s > 0);
+        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * s, dV + st * kTile16 + s * 16, id_o,
+               !first || s > 0, one);
     };
     uint32_t seg[2] = {0, 0}, it[2] = {0, 0}, kc = 0, vc = 0;
     bool ok = true;
     for (;;) {
-      const Seg g = next_seg(true);
+      const Seg g = next_seg();
       if (g.rows == 0) break;
       const bool two = g.rows > 128;
       const int nk = g.b1 - g.b0;
-      ok = wait(&bars.q_full[0], seg[0]++ & 1, abort) &&
-           (!two || wait(&bars.q_full[1], seg[1]++ & 1, abort)) &&
-           wait(&bars.k_full[kc & 1], (kc >> 1) & 1, abort);
+      ok = all_wait(&bars.q_full[0], seg[0]++ & 1) &&
+           (!two || all_wait(&bars.q_full[1], seg[1]++ & 1)) &&
+           all_wait(&bars.k_full[kc & 1], (kc >> 1) & 1);
       if (!ok) break;
       sm100::tc_fence_after();
       scores(0, kc & 1);
       if (two) scores(1, kc & 1);
-      sm100::mma_commit(&bars.k_empty[kc & 1]);
+      mma_commit(&bars.k_empty[kc & 1], one);
       ++kc;
       for (int k = 0; k < nk; ++k, ++vc) {
         const bool last = k + 1 == nk;
-        ok = wait(&bars.v_full[vc & 1], (vc >> 1) & 1, abort) &&
-             wait(&bars.p_full[0], it[0]++ & 1, abort);
+        ok = all_wait(&bars.v_full[vc & 1], (vc >> 1) & 1) &&
+             all_wait(&bars.p_full[0], it[0]++ & 1);
         if (!ok) break;
         sm100::tc_fence_after();
         values(0, vc & 1, k == 0);
         if (last) {
-          sm100::mma_commit(&bars.o_full[0]);
+          mma_commit(&bars.o_full[0], one);
         } else {
-          ok = wait(&bars.k_full[kc & 1], (kc >> 1) & 1, abort);
+          ok = all_wait(&bars.k_full[kc & 1], (kc >> 1) & 1);
           if (!ok) break;
           sm100::tc_fence_after();
           scores(0, kc & 1);
         }
         if (two) {
-          ok = wait(&bars.p_full[1], it[1]++ & 1, abort);
+          ok = all_wait(&bars.p_full[1], it[1]++ & 1);
           if (!ok) break;
           sm100::tc_fence_after();
           values(1, vc & 1, k == 0);
-          if (last) sm100::mma_commit(&bars.o_full[1]);
+          if (last) mma_commit(&bars.o_full[1], one);
         }
-        sm100::mma_commit(&bars.v_empty[vc & 1]);
+        mma_commit(&bars.v_empty[vc & 1], one);
         if (!last) {
           if (two) scores(1, kc & 1);
-          sm100::mma_commit(&bars.k_empty[kc & 1]);
+          mma_commit(&bars.k_empty[kc & 1], one);
           ++kc;
         }
       }
     }
     // the last commits (of k_empty, v_empty) must land before the CTA leaves
-    sm100::mma_commit(&bars.drain);
+    mma_commit(&bars.drain, one);
     sm100::mbar_wait(&bars.drain, 0, 200000000ull);
     }
   }
