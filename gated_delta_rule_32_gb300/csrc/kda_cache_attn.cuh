@@ -118,6 +118,34 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, Units units) {
   return s;
 }
 
+// Loads that are zero (or -1) where `use` is false: predicated, so that
+// nothing waits for them before their value is used.
+__device__ __forceinline__ uint4 load16_if(const void* src, bool use) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n"
+      " mov.b32 %2, 0;\n mov.b32 %3, 0;\n @p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(src), "r"((int)use));
+  return v;
+}
+__device__ __forceinline__ int load_page_if(const int32_t* src, bool use) {
+  int v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, -1;\n"
+               " @p ld.global.nc.u32 %0, [%1];\n}"
+               : "=&r"(v)
+               : "l"(src), "r"((int)use));
+  return v;
+}
+__device__ __forceinline__ float load_scale_if(const float* src, bool use) {
+  float v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, 0;\n"
+               " @p ld.global.nc.f32 %0, [%1];\n}"
+               : "=&f"(v)
+               : "l"(src), "r"((int)use));
+  return v;
+}
+
 // The smallest power of two not below x (x > 0 finite), 2^127 at most: its
 // reciprocal is exact.
 __device__ __forceinline__ float pow2_above(float x) {

@@ -395,23 +395,23 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       // lane i < 8 keeps the scales of tokens 16 i .. 16 i + 15 of a key tile,
       // loaded a tile ahead, its page two
       const int32_t* table = p.table + (int64_t)g.r * p.max_pages;
-      auto page_of = [&](int k) -> int {
-        const int64_t t0 = (int64_t)(g.b0 + k) * kTok + 16 * (lane & 7);
-        if (k >= nk || t0 >= kv) return -1;
-        const int pg = table[t0 >> lg];
-        if (pg >= 0 && pg < p.num_pages) return pg;
-        report(p.status, KDA_ERR_BAD_PAGES);
-        return -1;
+      auto has = [&](int k) {
+        return k < nk && (int64_t)(g.b0 + k) * kTok + 16 * (lane & 7) < kv;
+      };
+      auto page_of = [&](int k) -> int {  // (checked when it is used, a tile later)
+        return load_page_if(table + (((int64_t)(g.b0 + k) * kTok + 16 * (lane & 7)) >> lg), has(k));
       };
       auto scale_of = [&](const float* s, int pg) {
-        return pg < 0 ? 0.0f : s[(int64_t)pg * p.Hkv + g.h];
+        return load_scale_if(s + (int64_t)pg * p.Hkv + g.h, (uint32_t)pg < (uint32_t)p.num_pages);
       };
       int pg = page_of(0);
       float ks = scale_of(p.k_scale, pg), vs = scale_of(p.v_scale, pg);
+      if ((uint32_t)pg >= (uint32_t)p.num_pages && has(0)) report(p.status, KDA_ERR_BAD_PAGES);
       pg = page_of(1);
       bool ok = true;
       for (int k = 0; k < nk; ++k, ++it) {
         const float ks_next = scale_of(p.k_scale, pg), vs_next = scale_of(p.v_scale, pg);
+        if ((uint32_t)pg >= (uint32_t)p.num_pages && has(k + 1)) report(p.status, KDA_ERR_BAD_PAGES);
         pg = page_of(k + 2);
         float vmax = vs;
         vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 1));
@@ -603,9 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       // this warp's 32 tokens of a tile lie in two 16-token groups
       auto page_of = [&](int k, int g) -> int {
         const int64_t t0 = (int64_t)(sg.b0 + k) * kTok + 32 * wq + 16 * g;
-        if (k >= nk || t0 >= kv) return -1;
-        const int pg = table[t0 >> lg];
-        return pg >= 0 && pg < p.num_pages ? pg : -1;
+        return load_page_if(table + (t0 >> lg), k < nk && t0 < kv);
       };
       uint4 x[4][NC];
       auto fetch = [&](int k, int pa, int pb) {
@@ -616,10 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
           const uint8_t* src =
               codes + ((((int64_t)pg * p.Hkv + sg.h) << lg) + (t & (P - 1))) * D + 16 * c4;
           // (what a page holds past the request's end may be a NaN)
-          const bool use = pg >= 0 && (!is_v || t < kv);
+          const bool use = (uint32_t)pg < (uint32_t)p.num_pages && (!is_v || t < kv);
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-            x[g][c] = use ? *reinterpret_cast<const uint4*>(src + 64 * c) : make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < NC; ++c) x[g][c] = load16_if(src + 64 * c, use);
         }
       };
       int pa = page_of(0, 0), pb = page_of(0, 1);
