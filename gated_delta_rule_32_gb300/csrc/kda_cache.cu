@@ -355,7 +355,8 @@ extern "C" kda_status kda_page_plan(const int32_t* new_lens, const int32_t* ctx_
     return KDA_ERR_INVALID_ARG;
   if (T > 0 && (!slots || !positions)) return KDA_ERR_INVALID_ARG;
   if (R > kMaxRequests || !page_ok(page)) return KDA_ERR_UNSUPPORTED;
-  if ((int64_t)num_pages * page > INT32_MAX || (int64_t)max_pages * page > INT32_MAX)
+  if ((int64_t)num_pages * page > INT32_MAX || (int64_t)max_pages * page > (1 << 30) ||
+      T > (1 << 26))
     return KDA_ERR_UNSUPPORTED;  // slots and lengths are int32
   if (((uintptr_t)runs & 15) != 0) return KDA_ERR_MISALIGNED;
   const int max_runs = kda_page_runs(R, T, page);

@@ -62,7 +62,7 @@ extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
   if (!page_ok(page) || !head_dim_ok(d) || (code != KDA_I8 && code != KDA_E4M3) ||
       Hq / Hkv > 64 || R > kMaxRequests)
     return KDA_ERR_UNSUPPORTED;
-  if ((int64_t)max_pages * page > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)max_pages * page > (1 << 30) || T > (1 << 26)) return KDA_ERR_UNSUPPORTED;
   const int64_t width = (int64_t)Hq * d;
   if (q_stride < width) return KDA_ERR_INVALID_ARG;
   if (q_stride % 8 || (((uintptr_t)q | (uintptr_t)out | (uintptr_t)k_codes |

@@ -11,10 +11,15 @@
 //   8-11       keys:   codes -> f16 operand tiles in shared memory
 //   12-15      values: the same
 //   16         issues the products (one thread) and owns tensor memory
-//   17         walks the schedule, a segment or two ahead of the others
-//   18, 19     only give their registers up
+//   17         walks the schedule and looks up the pages' scales, some key
+//              tiles ahead of the softmax
+//   18, 19     queries of the next segment -> f16 operand tiles, while the
+//              softmax of this one ends
 // Tensor memory (512 columns): S of both tiles (the weights P replace S in
-// place, in f16), O of both tiles.
+// place, in f16), O of both tiles.  A row tile's S comes in halves of 64
+// tokens, each a buffer of its own: while the softmax works on one, the other
+// half's weights meet the values and its place gets the next scores, so no
+// softmax waits for products.
 //
 // Codes are exact in f16, so the only roundings of the products' inputs are
 // those of P (11 bits) and of small query elements next to large ones of the
@@ -29,9 +34,9 @@ namespace {
 using namespace kda_cache;
 
 // Five warpgroups launched with 96 registers a thread; they share them out
-// anew (setmaxnreg): 2 x 144 + 2 x 56 + 80 = 5 x 96.
+// anew (setmaxnreg): 2 x 128 + 2 x 80 + 64 = 5 x 96.
 constexpr int kThreads = 640;
-constexpr int kRegsSoftmax = 144, kRegsConvert = 56, kRegsIssue = 80;
+constexpr int kRegsSoftmax = 128, kRegsConvert = 80, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue == 5 * 96, "registers at launch");
 constexpr int kTok = 128;    // tokens per key tile
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -42,13 +47,19 @@ struct Smem {
   static constexpr int kQ = 0;                  // 2 tiles
   static constexpr int kK = 2 * kTile;          // 2 stages
   static constexpr int kV = 4 * kTile;          // 2 stages
-  static constexpr int kBytes = 6 * kTile + 1024;
+  static constexpr int kStage = 6 * kTile;      // 64 bytes of 32 rows for each softmax warp
+  static constexpr int kStageRow = 80;          // (a row's 64 bytes, padded against conflicts)
+  static constexpr int kStageWarp = 32 * kStageRow;
+  static constexpr int kBytes = kStage + 8 * kStageWarp + 1024;
 };
 
 struct Bars {
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2][2], q_empty[2];  // row tile, and parity of its segments
+  uint64_t s_full[2][2], p_full[2][2];   // row tile, half
+  uint64_t pv_done[2][2];                // row tile, half: O holds that half's share
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t seg_full[2], seg_empty[2];
+  uint64_t sc_full[4], sc_empty[4];
   uint64_t drain;
 };
 
@@ -57,8 +68,18 @@ struct Seg {
   int r, h, c0, n, kv;     // request and head
   int tok0, rows;          // first token of the row tile in the request, query rows
   int b0, b1, nu;          // key tiles [b0, b1) of nu
+  int halves;              // 64-token halves of them that hold a token that is seen
 };
-constexpr int kReaders = 17;  // warps that read it
+constexpr int kReaders = 19;  // warps that read it
+
+// The scales of a key tile: of tokens 16 i .. 16 i + 15, the factor from a
+// product of codes to log2 units (without the query row's) and the value
+// scale, and the largest value scale.
+struct Scales {
+  float4 k[2], v[2];
+  float vmax, pad[3];
+};
+constexpr int kRing = 4;
 
 // Bounded wait that also gives up when another warp of the CTA has.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -86,6 +107,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&r)[32]) {
       : "r"(ta));
 }
 
+// Waits for this thread's loads; the registers pass through it, so that no
+// use of them is moved before it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t ta, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
@@ -179,56 +213,67 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
          ((uint32_t)(M >> 4) << 24);
 }
 
-// sum_{i < n} floor((a i + b) / m), a, b >= 0, m > 0: the lattice points under
-// a line, by the steps of Euclid's algorithm (Graham, Knuth and Patashnik,
-// Concrete Mathematics, section 3.5).
-__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t sum = 0;
-  while (n > 0) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t y = a * n + b;
-    if (y < m) break;
+// sum_{i < n} floor((a i + b) / 128), n < 2^24: the lattice points under a
+// line, by the steps of Euclid's algorithm (Graham, Knuth and Patashnik,
+// Concrete Mathematics, section 3.5); a is below 128 after the first step, so
+// everything but the sum fits 32 bits.
+__device__ inline int64_t sum_tiles(uint32_t n, uint32_t a, uint32_t b) {
+  int64_t sum = (int64_t)n * (n - 1) / 2 * (a >> 7) + (int64_t)n * (b >> 7);
+  if (n == 0) return 0;
+  uint32_t m = 128;
+  a &= 127;
+  b &= 127;
+  for (;;) {
+    const uint32_t y = a * n + b;
+    if (y < m) return sum;
     n = y / m;
     b = y % m;
-    const int64_t t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
+    sum += (int64_t)n * (n - 1) / 2 * (a / m) + (int64_t)n * (b / m);
+    a %= m;
+    b %= m;
   }
-  return sum;
 }
 
+// What a segment costs beside its key tiles (queries in, O out, the first
+// tile's maximum), in key tiles: the schedule counts it as so many units that
+// hold no work.
+constexpr int kLead = 2;
+
 // The row tiles of a request: tile i holds tokens [i tt, (i + 1) tt) and sees
-// the first `seen(i)` tokens; its units are key tiles, one at least.
+// the first `seen(i)` tokens, in key tiles of which it has one at least.
 struct Tiles {
   int n, kv, tt, count;
   __device__ Tiles(const Req& q, int G) : n(q.n), kv(q.kv), tt(kTileRows / G) {
     count = q.n * (int64_t)G > kFewRows ? (q.n + tt - 1) / tt : 0;
   }
   __device__ int seen(int i) const { return max(0, kv - n + min(n, (i + 1) * tt)); }
-  __device__ int units(int i) const { return max(1, (int)(((int64_t)seen(i) + kTok - 1) / kTok)); }
+  __device__ int keys(int i) const { return max(1, (int)(((uint32_t)seen(i) + kTok - 1) / kTok)); }
   // units of the tiles before i
   __device__ int64_t before(int i) const {
-    const int last = min(i, count - 1);        // the full tiles among them
-    const int64_t first = (int64_t)kv - n + tt; // what a full tile 0 sees
-    // tiles that see at most one key tile have one unit
-    int64_t few = first > kTok ? 0 : (kTok - first) / tt + 1;
+    const int last = min(i, count - 1);  // the full tiles among them
+    const int first = kv - n + tt;       // what a full tile 0 sees
+    // tiles that see at most one key tile
+    int few = first > kTok ? 0 : (int)((uint32_t)(kTok - first) / (uint32_t)tt) + 1;
     few = few < last ? few : last;
-    int64_t s = few + floor_sum(last - few, kTok, tt, first + few * tt + kTok - 1);
-    if (i > last) s += units(last);
+    int64_t s = (int64_t)kLead * i + few +
+                sum_tiles(last - few, tt, (uint32_t)first + (uint32_t)few * tt + kTok - 1);
+    if (i > last) s += keys(last);
     return s;
   }
 };
 
-// Walks a CTA's share, segment by segment.
+// Walks a CTA's share, segment by segment: key tiles [b0, b1) of nu.
 struct Walk {
   const AttnArgs& p;
   int64_t u, u1, base;  // next unit, end of the share, units before request r
   int r, h, tile, b0, b1, nu;
-  int64_t per_head, seg0;
+  int64_t per_head, seg0;  // units of a head, units before the segment
   Req q;
   Tiles t;
+  // (a whole warp, every lane with the same values)
   __device__ Walk(const AttnArgs& p_, const Share& s)
       : p(p_), u(s.u0), u1(s.u1), base(s.base), r(s.r), h(0), tile(0), b0(0), b1(0), nu(0),
         per_head(0), seg0(0), q{0, 0, 0}, t(Req{0, 0, 0}, 1) {
@@ -238,14 +283,16 @@ struct Walk {
     h = (int)(in / per_head);
     const int64_t left = in - h * per_head;
     int lo = 0, hi = t.count;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (t.before(mid) <= left) lo = mid; else hi = mid;
+    while (hi - lo > 1) {  // the last tile with at most `left` units before it
+      const int step = (hi - lo + 31) >> 5, mid = lo + step * (threadIdx.x & 31);
+      const uint32_t yes = __ballot_sync(~0u, mid < hi && t.before(min(mid, t.count)) <= left);
+      lo += step * (31 - __clz(yes));
+      hi = min(hi, lo + step);
     }
     tile = lo;
     seg0 = base + h * per_head + t.before(tile);
-    nu = t.units(tile);
     set();
+    if (b0 == b1) next();
   }
   __device__ void load() {
     bool bad;
@@ -254,29 +301,35 @@ struct Walk {
     per_head = t.count ? t.before(t.count) : 0;
   }
   __device__ void set() {
-    b0 = (int)(u - seg0);
-    b1 = (int)min((int64_t)nu, u1 - seg0);
+    nu = t.keys(tile);
+    b0 = max(0, (int)(u - seg0) - kLead);
+    b1 = max(0, (int)min((int64_t)nu, u1 - seg0 - kLead));
   }
   __device__ bool live() const { return u < u1; }
   __device__ void next() {
-    u = seg0 + b1;
-    if (u >= u1) return;
-    seg0 += nu;
-    if (++tile == t.count) {
-      tile = 0;
-      if (++h == p.Hkv) {
-        h = 0;
-        base += per_head * p.Hkv;
-        do {
-          ++r;
-          load();
-        } while (t.count == 0);
+    do {
+      seg0 += kLead + nu;
+      u = seg0;
+      if (u >= u1) return;
+      if (++tile == t.count) {
+        tile = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          base += per_head * p.Hkv;
+          do {
+            ++r;
+            load();
+          } while (t.count == 0);
+        }
       }
-    }
-    nu = t.units(tile);
-    set();
+      set();
+    } while (b0 == b1);
   }
   __device__ int tokens() const { return min(t.tt, q.n - tile * t.tt); }
+  __device__ int halves() const {
+    const int all = 2 * (b1 - b0);
+    return b1 == nu ? min(all, max(1, (t.seen(tile) - b0 * kTok + 63) / 64)) : all;
+  }
 };
 
 template <int CODE, int D>
@@ -284,6 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ Bars bars;
   __shared__ Seg s_seg[2];
+  __shared__ Scales s_scales[kRing];
+  __shared__ float s_qscale[2][kTileRows];  // what a query row was divided by
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   unsigned char* smem = smem_raw + ((1024u - (sm100::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -298,16 +353,24 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&bars.q_full[i], 128);
-      sm100::mbar_init(&bars.s_full[i], 1);
-      sm100::mbar_init(&bars.p_full[i], 128);
-      sm100::mbar_init(&bars.o_full[i], 1);
+      sm100::mbar_init(&bars.q_full[i][0], 64);
+      sm100::mbar_init(&bars.q_full[i][1], 64);
+      sm100::mbar_init(&bars.q_empty[i], 1);
+      for (int x = 0; x < 2; ++x) {
+        sm100::mbar_init(&bars.s_full[i][x], 1);
+        sm100::mbar_init(&bars.p_full[i][x], 128);
+        sm100::mbar_init(&bars.pv_done[i][x], 1);
+      }
       sm100::mbar_init(&bars.k_full[i], 128);
       sm100::mbar_init(&bars.k_empty[i], 1);
       sm100::mbar_init(&bars.v_full[i], 128);
       sm100::mbar_init(&bars.v_empty[i], 1);
       sm100::mbar_init(&bars.seg_full[i], 1);
       sm100::mbar_init(&bars.seg_empty[i], kReaders);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      sm100::mbar_init(&bars.sc_full[i], 1);
+      sm100::mbar_init(&bars.sc_empty[i], 8);
     }
     sm100::mbar_init(&bars.drain, 1);
     sm100::fence_mbar_init();
@@ -346,147 +409,140 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     const int wg = warp >> 2, row = 128 * wg + 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + 128 * wg, tO = tmem + lanes + 256 + D * wg;
-    const float sm = fabsf(p.scale) * 1.4426950408889634f / code_top(CODE);
-    uint32_t seg = 0, it = 0;  // segments and key tiles that this row tile has had
+    uint32_t tiles = 0;  // key tiles had (of every segment)
+    // the next key tile's scales
+    auto next_scales = [&](Scales& sc) -> bool {
+      const uint32_t e = tiles % kRing;
+      if (!all_wait(&bars.sc_full[e], (tiles / kRing) & 1)) return false;
+      sc.k[0] = s_scales[e].k[0];
+      sc.k[1] = s_scales[e].k[1];
+      sc.v[0] = s_scales[e].v[0];
+      sc.v[1] = s_scales[e].v[1];
+      sc.vmax = s_scales[e].vmax;
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&bars.sc_empty[e]);
+      ++tiles;
+      return true;
+    };
+    uint32_t seg = 0, it0 = 0, it1 = 0;  // segments, first and second halves had
     for (;;) {
       const Seg g = next_seg();
       if (g.rows == 0) break;
-      if (128 * wg >= g.rows) continue;
+      if (128 * wg >= g.rows) {  // (no rows here: only the scales pass by)
+        Scales sc;
+        bool ok = true;
+        for (int k = g.b0; ok && k < g.b1; ++k) ok = next_scales(sc);
+        if (!ok) break;
+        continue;
+      }
       const int kv = g.kv, tok = g.tok0 + row / p.G;
       const bool mine = row < g.rows;
-      // query row: scaled to f16, to shared memory
-      float qs = 0.0f;
-      {
-        uint4 x[D / 8];
-        uint32_t most = 0;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          x[c] = make_uint4(0, 0, 0, 0);
-          if (mine)
-            x[c] = reinterpret_cast<const uint4*>(p.q + (int64_t)(g.c0 + tok) * p.q_stride +
-                                                  (int64_t)(g.h * p.G + row % p.G) * D)[c];
-          const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            most = max(most, max(y[e] & 0x7fff0000u, (y[e] << 16) & 0x7fff0000u));
-        }
-        const int ex = row_exponent(most);
-        const float down = copysignf(exp2i(-ex), p.scale);
-        qs = exp2i(ex) * sm;
-        unsigned char* dst = smem + Smem<D>::kQ + wg * Smem<D>::kTile + (row & 127) * 16;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-          uint32_t f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            f[e] = pack_half(__uint_as_float(y[e] << 16) * down,
-                             __uint_as_float(y[e] & 0xffff0000u) * down);
-          *reinterpret_cast<uint4*>(dst + c * 2048) = make_uint4(f[0], f[1], f[2], f[3]);
-        }
-      }
-      sm100::fence_async_smem();
-      sm100::mbar_arrive(&bars.q_full[wg]);
-
-      const int lim = mine ? kv - g.n + tok + 1 : 0;  // tokens this row sees
-      const int all_see = kv - g.n + g.tok0 + (128 * wg) / p.G + 1;
+      // tokens this row sees, and the fewest and most that a row of the warp does
+      int lim = mine ? kv - g.n + tok + 1 : 0;
+      const int lim_hi = __reduce_max_sync(~0u, lim);
+      if (!mine) lim = lim_hi;
+      const int lim_lo = __reduce_min_sync(~0u, lim);
       float m = -INFINITY, l = 0.0f, vref = 0.0f, vrel_of = 1.0f;
-      const int nk = g.b1 - g.b0;
-      // lane i < 8 keeps the scales of tokens 16 i .. 16 i + 15 of a key tile,
-      // loaded a tile ahead, its page two
-      const int32_t* table = p.table + (int64_t)g.r * p.max_pages;
-      auto has = [&](int k) {
-        return k < nk && (int64_t)(g.b0 + k) * kTok + 16 * (lane & 7) < kv;
-      };
-      auto page_of = [&](int k) -> int {  // (checked when it is used, a tile later)
-        return load_page_if(table + (((int64_t)(g.b0 + k) * kTok + 16 * (lane & 7)) >> lg), has(k));
-      };
-      auto scale_of = [&](const float* s, int pg) {
-        return load_scale_if(s + (int64_t)pg * p.Hkv + g.h, (uint32_t)pg < (uint32_t)p.num_pages);
-      };
-      int pg = page_of(0);
-      float ks = scale_of(p.k_scale, pg), vs = scale_of(p.v_scale, pg);
-      if ((uint32_t)pg >= (uint32_t)p.num_pages && has(0)) report(p.status, KDA_ERR_BAD_PAGES);
-      pg = page_of(1);
-      bool ok = true;
-      for (int k = 0; k < nk; ++k, ++it) {
-        const float ks_next = scale_of(p.k_scale, pg), vs_next = scale_of(p.v_scale, pg);
-        if ((uint32_t)pg >= (uint32_t)p.num_pages && has(k + 1)) report(p.status, KDA_ERR_BAD_PAGES);
-        pg = page_of(k + 2);
-        float vmax = vs;
-        vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 1));
-        vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 2));
-        vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 4));
-        const int t0 = (g.b0 + k) * kTok;
-        const bool edge = t0 + kTok > all_see;
-        ok = all_wait(&bars.s_full[wg], it & 1);
+      bool ok = all_wait(&bars.q_full[wg][seg & 1], (seg >> 1) & 1);
+      const float qs = s_qscale[seg & 1][row];
+      Scales sc;
+      for (int j = 0; ok && j < g.halves; ++j) {
+        const int x = j & 1;
+        if (x == 0) {
+          ok = next_scales(sc);
+          if (!ok) break;
+        }
+        const float vmax = sc.vmax;
+        const float4 ks = x ? sc.k[1] : sc.k[0], vs = x ? sc.v[1] : sc.v[0];
+        const float kf[4] = {ks.x * qs, ks.y * qs, ks.z * qs, ks.w * qs};
+        const int t0 = g.b0 * kTok + 64 * j;
+        const uint32_t tSx = tS + 64 * x;
+        // (A parity tells two phases apart, so every phase of a barrier is
+        // waited for: here the products of half j - 2, which came before these
+        // scores.)
+        ok = all_wait(&bars.s_full[wg][x], (x ? it1++ : it0++) & 1) &&
+             (j < 2 || all_wait(&bars.pv_done[wg][x], (x ? it1 : it0) & 1));
         if (!ok) break;
         sm100::tc_fence_after();
-        // Weights with the reference m of the tiles before; only where a row
+        // Weights with the reference m of the halves before; only where a row
         // passes it by 8 (its weight by 2^8: f16 has room for that), in the
-        // first tile, or when a page's value scale passes vref, is the
-        // maximum sought, O rescaled and the tile's weights made again.  So
+        // first half, or when a page's value scale passes vref, is the
+        // maximum sought, O rescaled and the half's weights made again.  So
         // S is read once, and O almost never.
-        uint32_t z[64];
+        uint32_t z[32];
         float lt;
-        bool fresh = k == 0 || vmax > vref;
+        bool fresh = j == 0 || vmax > vref;
         for (;;) {
           if (fresh) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
+              const int c0 = t0 + 32 * c;
+              if (c0 >= lim_hi) break;
               uint32_t s[32];
-              const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs;
-              const float f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
-              tmem_ld32(tS + 32 * c, s);
-              sm100::tmem_wait_ld();
+              const float f0 = kf[2 * c], f1 = kf[2 * c + 1];
+              tmem_ld32(tSx + 32 * c, s);
+              tmem_wait_ld32(s);
+              float a = -INFINITY, b = -INFINITY;
+              if (c0 + 32 <= lim_lo) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (t0 + 32 * c + e < lim)
-                  mx = fmaxf(mx, __uint_as_float(s[e]) * (e < 16 ? f0 : f1));
+                for (int e = 0; e < 16; ++e) {
+                  a = fmaxf(a, __uint_as_float(s[e]));
+                  b = fmaxf(b, __uint_as_float(s[16 + e]));
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  if (c0 + e < lim) a = fmaxf(a, __uint_as_float(s[e]));
+                  if (c0 + 16 + e < lim) b = fmaxf(b, __uint_as_float(s[16 + e]));
+                }
+              }
+              // (a group of which the row sees nothing: its scale may be 0)
+              if (c0 < lim) mx = fmaxf(mx, a * f0);
+              if (c0 + 16 < lim) mx = fmaxf(mx, b * f1);
             }
             // (a row that sees nothing here sees nothing further on: 0 serves)
             const float mn = fmaxf(m, mx) == -INFINITY ? 0.0f : fmaxf(m, mx);
             const float vnew = vmax > vref ? pow2_above(vmax) : vref;
-            const float fm = k == 0 ? 0.0f : ex2(m - mn);
+            const float fm = j == 0 ? 0.0f : ex2(m - mn);
             const float f = vnew > 0.0f ? vref / vnew * fm : fm;
             m = mn;
             l *= fm;
             vref = vnew;
             vrel_of = vnew > 0.0f ? 1.0f / vnew : 1.0f;
-            if (k > 0) {
+            if (j > 0) {
+              ok = all_wait(&bars.pv_done[wg][x ^ 1], ((x ? it0 : it1) + 1) & 1);
+              if (!ok) break;
+              sm100::tc_fence_after();
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                float y[16];
-                uint32_t o[16];
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
                 __syncwarp();
-                sm100::tmem_ld16(tO + 16 * c, y);
-                sm100::tmem_wait_ld();
+                tmem_ld32(tO + 32 * c, o);
+                tmem_wait_ld32(o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(y[e] * f);
-                sm100::tmem_st16(tO + 16 * c, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(tO + 32 * c, o);
               }
             }
           }
-          const float vrel = vs * vrel_of;
+          const float vf[4] = {vs.x * vrel_of, vs.y * vrel_of, vs.z * vrel_of, vs.w * vrel_of};
           uint32_t zmax = 0;
           f32x2 l2 = pack2(0.0f, 0.0f), m2 = pack2(-m, -m);
-          if (!edge) {
+          if (t0 + 64 <= lim_lo) {  // every row of the warp sees the whole half
+            uint32_t s[2][32];
+            tmem_ld32(tSx, s[0]);
+            tmem_wait_ld32(s[0]);
+            tmem_ld32(tSx + 32, s[1]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              tmem_ld32(tS + 32 * c, s);
-              const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs;
-              const float f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
-              const float v0 = __shfl_sync(~0u, vrel, 2 * c);
-              const float v1 = __shfl_sync(~0u, vrel, 2 * c + 1);
-              sm100::tmem_wait_ld();
+            for (int c = 0; c < 2; ++c) {
+              if (c == 1) tmem_wait_ld32(s[1]);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                const float f = e < 16 ? f0 : f1, v = e < 16 ? v0 : v1;
+                const float f = kf[2 * c + e / 16], v = vf[2 * c + e / 16];
                 float a, b;
-                unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pack2(f, f),
-                             m2), a, b);
+                unpack2(fma2(pack2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                             pack2(f, f), m2), a, b);
                 const f32x2 w = pack2(ex2(a), ex2(b));
                 l2 = add2(l2, w);
                 unpack2(mul2(w, pack2(v, v)), a, b);
@@ -496,25 +552,30 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
+              const int c0 = t0 + 32 * c;
+              if (c0 >= lim_hi) {  // no row of the warp sees these 32 tokens
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[16 * c + e] = 0;
+                continue;
+              }
               uint32_t s[32];
-              tmem_ld32(tS + 32 * c, s);
-              const float f0 = __shfl_sync(~0u, ks, 2 * c) * qs;
-              const float f1 = __shfl_sync(~0u, ks, 2 * c + 1) * qs;
-              const float v0 = __shfl_sync(~0u, vrel, 2 * c);
-              const float v1 = __shfl_sync(~0u, vrel, 2 * c + 1);
-              sm100::tmem_wait_ld();
+              tmem_ld32(tSx + 32 * c, s);
+              tmem_wait_ld32(s);
+              // (where the row sees nothing of a group its scale may be a NaN)
+              const float v0 = c0 < lim ? vf[2 * c] : 0.0f;
+              const float v1 = c0 + 16 < lim ? vf[2 * c + 1] : 0.0f;
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                const float f = e < 16 ? f0 : f1, v = e < 16 ? v0 : v1;
-                float a = ex2(fmaf(__uint_as_float(s[e]), f, -m));
-                float b = ex2(fmaf(__uint_as_float(s[e + 1]), f, -m));
-                float av = a * v, bv = b * v;
-                // (the scales of masked tokens may be NaN)
-                if (t0 + 32 * c + e >= lim) a = av = 0.0f;
-                if (t0 + 32 * c + e + 1 >= lim) b = bv = 0.0f;
-                l2 = add2(l2, pack2(a, b));
-                z[16 * c + e / 2] = pack_half(av, bv);
+                const float f = kf[2 * c + e / 16], v = e < 16 ? v0 : v1;
+                float a = fmaf(__uint_as_float(s[e]), f, -m);
+                float b = fmaf(__uint_as_float(s[e + 1]), f, -m);
+                if (c0 + e >= lim) a = -INFINITY;
+                if (c0 + e + 1 >= lim) b = -INFINITY;
+                const f32x2 w = pack2(ex2(a), ex2(b));
+                l2 = add2(l2, w);
+                unpack2(mul2(w, pack2(v, v)), a, b);
+                z[16 * c + e / 2] = pack_half(a, b);
                 zmax = max_half2(zmax, z[16 * c + e / 2]);
               }
             }
@@ -528,17 +589,17 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
           if (fresh || !__any_sync(~0u, over)) break;
           fresh = true;
         }
+        if (!ok) break;
         l += lt;
         __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_st32(tS + 32 * c, z + 32 * c);
+        tmem_st32(tSx, z);
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
-        sm100::mbar_arrive(&bars.p_full[wg]);
-        ks = ks_next;
-        vs = vs_next;
+        sm100::mbar_arrive(&bars.p_full[wg][x]);
       }
-      if (!ok || !all_wait(&bars.o_full[wg], seg & 1)) break;
+      if (!ok || !all_wait(&bars.pv_done[wg][0], (it0 + 1) & 1) ||
+          (g.halves > 1 && !all_wait(&bars.pv_done[wg][1], (it1 + 1) & 1)))
+        break;
       ++seg;
       sm100::tc_fence_after();
       const float ov = vref / code_top(CODE);
@@ -546,26 +607,54 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       const int64_t slot = 2 * (int64_t)blockIdx.x + (g.b0 > 0 ? 0 : 1);
       const int64_t at = (int64_t)(g.c0 + tok) * p.Hq + g.h * p.G + row % p.G;
       const float f = whole ? (l == 0.0f ? 0.0f : ov / l) : ov;
+      // O leaves through 64-byte row pieces in shared memory, so that a store
+      // writes 8 rows' whole sectors and not 32 rows' halves.
+      unsigned char* dst_row = whole
+                                   ? reinterpret_cast<unsigned char*>(p.out + at * D)
+                                   : reinterpret_cast<unsigned char*>(
+                                         p.part_o + (slot * kTileRows + row) * D);
+      const uint64_t dst_u = mine ? reinterpret_cast<uint64_t>(dst_row) : 0;
+      uint64_t dst[4];
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        float y[16];
+      for (int i = 0; i < 4; ++i) {
+        dst[i] = __shfl_sync(~0u, dst_u, 8 * i + (lane >> 2));
+        if (dst[i]) dst[i] += 16 * (lane & 3);
+      }
+      unsigned char* stage = smem + Smem<D>::kStage + warp * Smem<D>::kStageWarp;
+      auto put = [&](const uint32_t (&y)[16], int piece) {
+        uint4* mine_at = reinterpret_cast<uint4*>(stage + lane * Smem<D>::kStageRow);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mine_at[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         __syncwarp();
-        sm100::tmem_ld16(tO + 16 * c, y);
-        sm100::tmem_wait_ld();
-        // (a row that has seen nothing: its weights are zeros, so is its sum)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] *= f;
-        if (mine && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + 16 * c);
-          dst[0] = make_uint4(sm100::pack_bf16x2(y[0], y[1]), sm100::pack_bf16x2(y[2], y[3]),
-                              sm100::pack_bf16x2(y[4], y[5]), sm100::pack_bf16x2(y[6], y[7]));
-          dst[1] = make_uint4(sm100::pack_bf16x2(y[8], y[9]), sm100::pack_bf16x2(y[10], y[11]),
-                              sm100::pack_bf16x2(y[12], y[13]), sm100::pack_bf16x2(y[14], y[15]));
-        } else if (mine) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * kTileRows + row) * D + 16 * c);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              stage + (8 * i + (lane >> 2)) * Smem<D>::kStageRow + 16 * (lane & 3));
+          if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + 64 * piece) = v;
+        }
+        __syncwarp();
+      };
+      // (a row that has seen nothing: its weights are zeros, so is its sum)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t y[32], z[16];
+        __syncwarp();
+        tmem_ld32(tO + 32 * c, y);
+        tmem_wait_ld32(y);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            z[e] = sm100::pack_bf16x2(__uint_as_float(y[2 * e]) * f,
+                                      __uint_as_float(y[2 * e + 1]) * f);
+          put(z, c);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+          put(z, 2 * c);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(__uint_as_float(y[16 + e]) * f);
+          put(z, 2 * c + 1);
         }
       }
       sm100::tc_fence_before();
@@ -652,93 +741,210 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   } else {
     regs_down<kRegsIssue>();
     if (warp == 17) {
-      // ---------------------------------------------------------- schedule
+      // ------------------------------------------------ schedule and scales
+      const float sm = fabsf(p.scale) * 1.4426950408889634f / code_top(CODE);
+      Walk w(p, share);
       if (lane == 0) {
-        Walk w(p, share);
         // what the join of parts needs to know of the segment that this CTA
         // enters in its middle
         PartHead ph{0, 0, 0, 0, 0, 0};
         if (w.live() && w.b0 > 0)
-          ph = {w.seg0, w.seg0 + w.nu, w.q.c0 + w.tile * w.t.tt, w.tokens() * p.G, w.h, 0};
+          ph = {w.seg0 + kLead, w.seg0 + kLead + w.nu, w.q.c0 + w.tile * w.t.tt,
+                w.tokens() * p.G, w.h, 0};
         p.part_head[blockIdx.x] = ph;
-        for (uint32_t i = 0;; ++i) {
-          if (i >= 2 && !wait(&bars.seg_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
+      }
+      uint32_t tiles = 0;
+      bool ok = true;
+      for (uint32_t i = 0; ok; ++i) {
+        ok = i < 2 || all_wait(&bars.seg_empty[i & 1], ((i >> 1) - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
           Seg g{};
           if (w.live())
             g = {w.r, w.h, w.q.c0, w.q.n, w.q.kv, w.tile * w.t.tt, w.tokens() * p.G, w.b0, w.b1,
-                 w.nu};
+                 w.nu, w.halves()};
           s_seg[i & 1] = g;
           sm100::mbar_arrive(&bars.seg_full[i & 1]);
-          if (g.rows == 0) break;
-          w.next();
+        }
+        if (!w.live()) break;
+        // lane i < 8 looks up tokens 16 i .. 16 i + 15, a page a tile ahead
+        const int32_t* table = p.table + (int64_t)w.r * p.max_pages;
+        auto has = [&](int k) {
+          return k < w.b1 && (int64_t)k * kTok + 16 * (lane & 7) < w.q.kv;
+        };
+        auto page_of = [&](int k) -> int {
+          return load_page_if(table + (((int64_t)k * kTok + 16 * (lane & 7)) >> lg), has(k));
+        };
+        int pg = page_of(w.b0);
+        for (int k = w.b0; k < w.b1; ++k, ++tiles) {
+          const bool in = (uint32_t)pg < (uint32_t)p.num_pages;
+          if (!in && has(k)) report(p.status, KDA_ERR_BAD_PAGES);
+          const float ks = load_scale_if(p.k_scale + (int64_t)pg * p.Hkv + w.h, in);
+          const float vs = load_scale_if(p.v_scale + (int64_t)pg * p.Hkv + w.h, in);
+          pg = page_of(k + 1);
+          const uint32_t e = tiles % kRing;
+          ok = tiles < kRing || all_wait(&bars.sc_empty[e], (tiles / kRing - 1) & 1);
+          if (!ok) break;
+          float vmax = vs;
+          vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 1));
+          vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 2));
+          vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, 4));
+          if (lane < 8) {
+            reinterpret_cast<float*>(s_scales[e].k)[lane] = ks * sm;
+            reinterpret_cast<float*>(s_scales[e].v)[lane] = vs;
+          }
+          if (lane == 0) s_scales[e].vmax = vmax;
+          __syncwarp();
+          if (lane == 0) sm100::mbar_arrive(&bars.sc_full[e]);
+        }
+        w.next();
+      }
+    } else if (warp >= 18) {
+      // ----------------------------------------------------------- queries
+      // Lanes 8 c .. 8 c + 7 take the same 8 channels of 8 rows, as the
+      // converting warps do.  A row is divided by a power of two so that it
+      // fits f16; its sign carries the sign of the score's scale.
+      constexpr int C = D / 32;  // 16-byte pieces of a row per lane
+      const int r8 = lane & 7, c4 = lane >> 3;
+      uint32_t seg[2] = {0, 0};
+      bool ok = true;
+      while (ok) {
+        const Seg g = next_seg();
+        if (g.rows == 0) break;
+        for (int t = 0; ok && 128 * t < g.rows; ++t) {
+          const uint32_t i = seg[t]++;
+          for (int g8 = warp - 18; g8 < 16; g8 += 4) {
+            uint4 x[2][C];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              const int row = 128 * t + 8 * (g8 + 2 * a) + r8;
+              const uint16_t* src = p.q + (int64_t)(g.c0 + g.tok0 + row / p.G) * p.q_stride +
+                                    (int64_t)(g.h * p.G + row % p.G) * D + 8 * c4;
+#pragma unroll
+              for (int c = 0; c < C; ++c) x[a][c] = load16_if(src + 32 * c, row < g.rows);
+            }
+            if (g8 == warp - 18 && i > 0) {  // (the first loads are on their way)
+              ok = all_wait(&bars.q_empty[t], (i - 1) & 1);
+              if (!ok) break;
+            }
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              const int row = 8 * (g8 + 2 * a) + r8;
+              uint32_t most = 0;
+#pragma unroll
+              for (int c = 0; c < C; ++c) {
+                const uint32_t y[4] = {x[a][c].x, x[a][c].y, x[a][c].z, x[a][c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  most = max(most, max(y[e] & 0x7fff0000u, (y[e] << 16) & 0x7fff0000u));
+              }
+              most = max(most, __shfl_xor_sync(~0u, most, 8));
+              most = max(most, __shfl_xor_sync(~0u, most, 16));
+              const int ex = row_exponent(most);
+              const float down = copysignf(exp2i(-ex), p.scale);
+              if (c4 == 0) s_qscale[i & 1][128 * t + row] = exp2i(ex);
+              unsigned char* d = smem + Smem<D>::kQ + t * Smem<D>::kTile + row * 16 + c4 * 2048;
+#pragma unroll
+              for (int c = 0; c < C; ++c) {
+                const uint32_t y[4] = {x[a][c].x, x[a][c].y, x[a][c].z, x[a][c].w};
+                uint32_t f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  f[e] = pack_half(__uint_as_float(y[e] << 16) * down,
+                                   __uint_as_float(y[e] & 0xffff0000u) * down);
+                *reinterpret_cast<uint4*>(d + c * 8192) = make_uint4(f[0], f[1], f[2], f[3]);
+              }
+            }
+          }
+          if (!ok) break;
+          sm100::fence_async_smem();
+          sm100::mbar_arrive(&bars.q_full[t][i & 1]);
         }
       }
     } else if (warp == 16) {
     // ----------------------------------------------------------- products
-    const uint32_t id_s = idesc_f16(128, kTok, 0), id_o = idesc_f16(128, D, 1);
+    const uint32_t id_s = idesc_f16(128, 64, 0), id_o = idesc_f16(128, D, 1);
     const uint32_t one = elect_one();
     // (a descriptor's address field counts 16-byte units)
     const uint64_t dQ = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kQ), 2048, 128);
     const uint64_t dK = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kK), 2048, 128);
     const uint64_t dV = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kV), 128, 2048);
     constexpr int kTile16 = Smem<D>::kTile / 16;
-    auto scores = [&](int t, int st) {  // S_t = Q_t K^T
+    auto scores = [&](int t, int x, int st) {  // S_t = Q_t K^T, half x of the key tile
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
-        mma_ss(tmem + 128 * t, dQ + t * kTile16 + s * 256, dK + st * kTile16 + s * 256, id_s, s > 0, one);
-      mma_commit(&bars.s_full[t], one);
+        mma_ss(tmem + 128 * t + 64 * x, dQ + t * kTile16 + s * 256,
+               dK + st * kTile16 + 64 * x + s * 256, id_s, s > 0, one);
+      mma_commit(&bars.s_full[t][x], one);
     };
-    auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
+    auto values = [&](int t, int x, int st, bool first) {  // O_t (+)= P_t V
 #pragma unroll
-      for (int s = 0; s < kTok / 16; ++s)
-        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * s, dV + st * kTile16 + s * 16, id_o,
-               !first || s > 0, one);
+      for (int s = 0; s < 4; ++s)
+        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 64 * x + 8 * s,
+               dV + st * kTile16 + 64 * x + s * 16, id_o, !first || s > 0, one);
+      mma_commit(&bars.pv_done[t][x], one);
     };
-    uint32_t seg[2] = {0, 0}, it[2] = {0, 0}, kc = 0, vc = 0;
+    uint32_t seg0 = 0, seg1 = 0, kc = 0, vc = 0, pa = 0, pb = 0;  // pa, pb: halves 0 and 1 had
+    uint32_t qa = 0, qb = 0;                                      // (row tile 1's)
     bool ok = true;
     for (;;) {
       const Seg g = next_seg();
       if (g.rows == 0) break;
       const bool two = g.rows > 128;
-      const int nk = g.b1 - g.b0;
-      ok = all_wait(&bars.q_full[0], seg[0]++ & 1) &&
-           (!two || all_wait(&bars.q_full[1], seg[1]++ & 1)) &&
+      const int nh = g.halves;
+      ok = all_wait(&bars.q_full[0][seg0 & 1], (seg0 >> 1) & 1) &&
            all_wait(&bars.k_full[kc & 1], (kc >> 1) & 1);
       if (!ok) break;
+      ++seg0;
       sm100::tc_fence_after();
-      scores(0, kc & 1);
-      if (two) scores(1, kc & 1);
+      scores(0, 0, kc & 1);
+      if (nh > 1) scores(0, 1, kc & 1);
+      if (nh <= 2) mma_commit(&bars.q_empty[0], one);
+      if (two) {
+        ok = all_wait(&bars.q_full[1][seg1 & 1], (seg1 >> 1) & 1);
+        if (!ok) break;
+        ++seg1;
+        sm100::tc_fence_after();
+        scores(1, 0, kc & 1);
+        if (nh > 1) scores(1, 1, kc & 1);
+        if (nh <= 2) mma_commit(&bars.q_empty[1], one);
+      }
       mma_commit(&bars.k_empty[kc & 1], one);
       ++kc;
-      for (int k = 0; k < nk; ++k, ++vc) {
-        const bool last = k + 1 == nk;
-        ok = all_wait(&bars.v_full[vc & 1], (vc >> 1) & 1) &&
-             all_wait(&bars.p_full[0], it[0]++ & 1);
+      for (int j = 0; j < nh; ++j) {
+        const int x = j & 1;
+        if (x == 0) {
+          ok = all_wait(&bars.v_full[vc & 1], (vc >> 1) & 1);
+          if (!ok) break;
+        }
+        ok = all_wait(&bars.p_full[0][x], (x ? pb++ : pa++) & 1);
         if (!ok) break;
         sm100::tc_fence_after();
-        values(0, vc & 1, k == 0);
-        if (last) {
-          mma_commit(&bars.o_full[0], one);
-        } else {
-          ok = all_wait(&bars.k_full[kc & 1], (kc >> 1) & 1);
-          if (!ok) break;
-          sm100::tc_fence_after();
-          scores(0, kc & 1);
+        values(0, x, vc & 1, j == 0);
+        if (j + 2 < nh) {
+          if (x == 0) {
+            ok = all_wait(&bars.k_full[kc & 1], (kc >> 1) & 1);
+            if (!ok) break;
+            sm100::tc_fence_after();
+          }
+          scores(0, x, kc & 1);
+          if (j + 3 == nh) mma_commit(&bars.q_empty[0], one);
         }
         if (two) {
-          ok = all_wait(&bars.p_full[1], it[1]++ & 1);
+          ok = all_wait(&bars.p_full[1][x], (x ? qb++ : qa++) & 1);
           if (!ok) break;
           sm100::tc_fence_after();
-          values(1, vc & 1, k == 0);
-          if (last) mma_commit(&bars.o_full[1], one);
+          values(1, x, vc & 1, j == 0);
+          if (j + 2 < nh) {
+            scores(1, x, kc & 1);
+            if (j + 3 == nh) mma_commit(&bars.q_empty[1], one);
+          }
         }
-        mma_commit(&bars.v_empty[vc & 1], one);
-        if (!last) {
-          if (two) scores(1, kc & 1);
-          mma_commit(&bars.k_empty[kc & 1], one);
-          ++kc;
-        }
+        if (x == 1 || j + 1 == nh) mma_commit(&bars.v_empty[vc++ & 1], one);
+        // (the next key tile's scores are all issued)
+        if (j + 2 < nh && (x == 1 || j + 3 == nh)) mma_commit(&bars.k_empty[kc++ & 1], one);
       }
+      if (!ok) break;
     }
     // the last commits (of k_empty, v_empty) must land before the CTA leaves
     mma_commit(&bars.drain, one);

@@ -421,7 +421,8 @@ kda_status kda_debug_record_capacity(int64_t items);
  * the step's packed token tensors (the same cu_seqlens as a packed
  * kda_chunk_fwd takes); block_table [R, max_pages] holds the page number of
  * each request's tokens p * page .. p * page + page - 1 in column p.
- * Columns past a request's last page are never read.  What a page holds past
+ * Columns past a request's last page are never read.  Limits: R <= 16384,
+ * max_pages * page <= 2^30, T <= 2^26.  What a page holds past
  * its request's length never reaches a result, whatever its bytes.
  */
 typedef enum { KDA_I8 = 0, KDA_E4M3 = 1 } kda_code;
