@@ -9,23 +9,21 @@
 // other.  Warps:
 //   0-3, 4-7   softmax of row tile 0 / 1, one thread per row
 //   8-11       keys:   codes -> f16 operand tiles in shared memory
-//   12-15      values: the same
+//   12-15      values: the same; between segments 8-15 convert the queries
 //   16         issues the products (one thread) and owns tensor memory
 //   17         walks the schedule and looks up the pages' scales, some key
 //              tiles ahead of the softmax
-//   18, 19     queries of the next segment -> f16 operand tiles, while the
-//              softmax of this one ends
+//   18, 19     bring the next segment's queries into L2
 // Tensor memory (512 columns): S of both tiles (the weights P replace S in
-// place, in f16), O of both tiles.  A row tile's S comes in halves of 64
-// tokens, each a buffer of its own: while the softmax works on one, the other
-// half's weights meet the values and its place gets the next scores, so no
-// softmax waits for products.
+// place, in f16), O of both tiles.
 //
 // Codes are exact in f16, so the only roundings of the products' inputs are
 // those of P (11 bits) and of small query elements next to large ones of the
 // same row.  A page's key scale multiplies its scores after the product; its
 // value scale multiplies its columns of P, relative to a power of two at
 // least as large (vref), which leaves O at the end.
+#include <type_traits>
+
 #include "kda_cache_attn.cuh"
 #include "sm100.cuh"
 
@@ -55,8 +53,7 @@ struct Smem {
 
 struct Bars {
   uint64_t q_full[2][2], q_empty[2];  // row tile, and parity of its segments
-  uint64_t s_full[2][2], p_full[2][2];   // row tile, half
-  uint64_t pv_done[2][2];                // row tile, half: O holds that half's share
+  uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t seg_full[2], seg_empty[2];
   uint64_t sc_full[4], sc_empty[4];
@@ -68,7 +65,6 @@ struct Seg {
   int r, h, c0, n, kv;     // request and head
   int tok0, rows;          // first token of the row tile in the request, query rows
   int b0, b1, nu;          // key tiles [b0, b1) of nu
-  int halves;              // 64-token halves of them that hold a token that is seen
 };
 constexpr int kReaders = 19;  // warps that read it
 
@@ -76,17 +72,30 @@ constexpr int kReaders = 19;  // warps that read it
 // product of codes to log2 units (without the query row's) and the value
 // scale, and the largest value scale.
 struct Scales {
-  float4 k[2], v[2];
+  float2 k[4], v[4];
   float vmax, pad[3];
 };
 constexpr int kRing = 4;
 
-// Bounded wait that also gives up when another warp of the CTA has.
+// Bounded wait that also gives up when another warp of the CTA has.  The hint
+// lets the hardware suspend the warp for up to 1 ms at a time: a warp that
+// polls takes issue slots from the one that issues the products.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (sm100::mbar_try_wait(bar, parity)) return true;
+  auto poll = [&]() -> bool {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(1000000)
+        : "memory");
+    return ok != 0;
+  };
+  if (poll()) return true;
   const uint64_t t0 = sm100::globaltimer_ns();
   for (;;) {
-    if (sm100::mbar_try_wait(bar, parity)) return true;
+    if (poll()) return true;
     if (*abort) return false;
     if (sm100::globaltimer_ns() - t0 > kWaitNs) {
       *abort = 1;
@@ -164,29 +173,52 @@ __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
 }
 
 // The products, issued by a whole warp that runs in step, of which one thread
-// (`one`) carries them out.  In a branch of one thread the operands are not
-// known to be uniform, and each product cost 97-105 cycles to issue; so it is
-// the tensor cores' own 64 (128 x 128 x 16, f16).
+// (`one`) carries them out; four k-steps an asm block.  Issue slots are what
+// this warp must not lack, its scheduler serving four busy warps beside it: in
+// a branch of one thread the operands are not known to be uniform, and a
+// 128 x 128 x 16 product took 97-105 cycles to issue; in step it takes the
+// tensor cores' own 64.  With the other warps issuing all the time it took
+// 141 with 64-bit descriptor arithmetic for each product, 100 in this form.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
                : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t one) {
+// D (+)= A B^T, A and B in shared memory, both [chunk][row][16 bytes] with 128
+// rows: the low words of their descriptors go up by two chunks a k-step.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                        uint32_t idesc, uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+      "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n .reg .b32 x, y;\n"
+      " setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+      " add.u32 x, %1, 256;\n add.u32 y, %2, 256;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 512;\n add.u32 y, %2, 512;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 768;\n add.u32 y, %2, 768;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t one) {
+// The same with A in tensor memory, 8 columns a k-step, and B's rows the
+// contracted index: 16 of them a k-step.
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                        uint32_t idesc, uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+      "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 x, y;\n"
+      " setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
+      " add.u32 x, %1, 8;\n add.u32 y, %2, 16;\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      " add.u32 x, %1, 16;\n add.u32 y, %2, 32;\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      " add.u32 x, %1, 24;\n add.u32 y, %2, 48;\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t one) {
@@ -326,10 +358,6 @@ struct Walk {
     } while (b0 == b1);
   }
   __device__ int tokens() const { return min(t.tt, q.n - tile * t.tt); }
-  __device__ int halves() const {
-    const int all = 2 * (b1 - b0);
-    return b1 == nu ? min(all, max(1, (t.seen(tile) - b0 * kTok + 63) / 64)) : all;
-  }
 };
 
 template <int CODE, int D>
@@ -353,14 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&bars.q_full[i][0], 64);
-      sm100::mbar_init(&bars.q_full[i][1], 64);
+      sm100::mbar_init(&bars.q_full[i][0], 256);
+      sm100::mbar_init(&bars.q_full[i][1], 256);
       sm100::mbar_init(&bars.q_empty[i], 1);
-      for (int x = 0; x < 2; ++x) {
-        sm100::mbar_init(&bars.s_full[i][x], 1);
-        sm100::mbar_init(&bars.p_full[i][x], 128);
-        sm100::mbar_init(&bars.pv_done[i][x], 1);
-      }
+      sm100::mbar_init(&bars.s_full[i], 1);
+      sm100::mbar_init(&bars.p_full[i], 128);
+      sm100::mbar_init(&bars.o_full[i], 1);
       sm100::mbar_init(&bars.k_full[i], 128);
       sm100::mbar_init(&bars.k_empty[i], 1);
       sm100::mbar_init(&bars.v_full[i], 128);
@@ -382,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   });
   __syncthreads();
   sm100::tc_fence_after();
-  const uint32_t tmem = __shfl_sync(~0u, s_tmem, 0);
+  constexpr uint32_t tmem = 0;  // (all 512 columns are this CTA's)
   uint32_t nseg = 0;  // segments seen
   // a wait of a whole warp; the next segment, or rows = 0 at the end (or when a
   // wait gave up)
@@ -409,29 +435,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     const int wg = warp >> 2, row = 128 * wg + 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + 128 * wg, tO = tmem + lanes + 256 + D * wg;
-    uint32_t tiles = 0;  // key tiles had (of every segment)
-    // the next key tile's scales
-    auto next_scales = [&](Scales& sc) -> bool {
-      const uint32_t e = tiles % kRing;
-      if (!all_wait(&bars.sc_full[e], (tiles / kRing) & 1)) return false;
-      sc.k[0] = s_scales[e].k[0];
-      sc.k[1] = s_scales[e].k[1];
-      sc.v[0] = s_scales[e].v[0];
-      sc.v[1] = s_scales[e].v[1];
-      sc.vmax = s_scales[e].vmax;
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&bars.sc_empty[e]);
-      ++tiles;
-      return true;
-    };
-    uint32_t seg = 0, it0 = 0, it1 = 0;  // segments, first and second halves had
+    uint32_t seg = 0, it = 0;  // segments and key tiles that this row tile has had
+    uint32_t tiles = 0;        // key tiles of every segment
     for (;;) {
       const Seg g = next_seg();
       if (g.rows == 0) break;
+      const int nk = g.b1 - g.b0;
       if (128 * wg >= g.rows) {  // (no rows here: only the scales pass by)
-        Scales sc;
         bool ok = true;
-        for (int k = g.b0; ok && k < g.b1; ++k) ok = next_scales(sc);
+        for (int k = 0; ok && k < nk; ++k, ++tiles) {
+          ok = all_wait(&bars.sc_full[tiles % kRing], (tiles / kRing) & 1);
+          if (ok && lane == 0) sm100::mbar_arrive(&bars.sc_empty[tiles % kRing]);
+        }
         if (!ok) break;
         continue;
       }
@@ -445,43 +460,33 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       float m = -INFINITY, l = 0.0f, vref = 0.0f, vrel_of = 1.0f;
       bool ok = all_wait(&bars.q_full[wg][seg & 1], (seg >> 1) & 1);
       const float qs = s_qscale[seg & 1][row];
-      Scales sc;
-      for (int j = 0; ok && j < g.halves; ++j) {
-        const int x = j & 1;
-        if (x == 0) {
-          ok = next_scales(sc);
-          if (!ok) break;
-        }
+      for (int k = 0; ok && k < nk; ++k, ++it, ++tiles) {
+        const Scales& sc = s_scales[tiles % kRing];
+        const int t0 = (g.b0 + k) * kTok;
+        ok = all_wait(&bars.sc_full[tiles % kRing], (tiles / kRing) & 1);
+        if (!ok) break;
         const float vmax = sc.vmax;
-        const float4 ks = x ? sc.k[1] : sc.k[0], vs = x ? sc.v[1] : sc.v[0];
-        const float kf[4] = {ks.x * qs, ks.y * qs, ks.z * qs, ks.w * qs};
-        const int t0 = g.b0 * kTok + 64 * j;
-        const uint32_t tSx = tS + 64 * x;
-        // (A parity tells two phases apart, so every phase of a barrier is
-        // waited for: here the products of half j - 2, which came before these
-        // scores.)
-        ok = all_wait(&bars.s_full[wg][x], (x ? it1++ : it0++) & 1) &&
-             (j < 2 || all_wait(&bars.pv_done[wg][x], (x ? it1 : it0) & 1));
+        ok = all_wait(&bars.s_full[wg], it & 1);
         if (!ok) break;
         sm100::tc_fence_after();
-        // Weights with the reference m of the halves before; only where a row
+        // Weights with the reference m of the tiles before; only where a row
         // passes it by 8 (its weight by 2^8: f16 has room for that), in the
-        // first half, or when a page's value scale passes vref, is the
-        // maximum sought, O rescaled and the half's weights made again.  So
+        // first tile, or when a page's value scale passes vref, is the
+        // maximum sought, O rescaled and the tile's weights made again.  So
         // S is read once, and O almost never.
-        uint32_t z[32];
+        uint32_t z[64];
         float lt;
-        bool fresh = j == 0 || vmax > vref;
+        bool fresh = k == 0 || vmax > vref;
         for (;;) {
           if (fresh) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 4; ++c) {
               const int c0 = t0 + 32 * c;
               if (c0 >= lim_hi) break;
+              const float2 ks = sc.k[c];
               uint32_t s[32];
-              const float f0 = kf[2 * c], f1 = kf[2 * c + 1];
-              tmem_ld32(tSx + 32 * c, s);
+              tmem_ld32(tS + 32 * c, s);
               tmem_wait_ld32(s);
               float a = -INFINITY, b = -INFINITY;
               if (c0 + 32 <= lim_lo) {
@@ -498,22 +503,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
                 }
               }
               // (a group of which the row sees nothing: its scale may be 0)
-              if (c0 < lim) mx = fmaxf(mx, a * f0);
-              if (c0 + 16 < lim) mx = fmaxf(mx, b * f1);
+              if (c0 < lim) mx = fmaxf(mx, a * (ks.x * qs));
+              if (c0 + 16 < lim) mx = fmaxf(mx, b * (ks.y * qs));
             }
             // (a row that sees nothing here sees nothing further on: 0 serves)
             const float mn = fmaxf(m, mx) == -INFINITY ? 0.0f : fmaxf(m, mx);
             const float vnew = vmax > vref ? pow2_above(vmax) : vref;
-            const float fm = j == 0 ? 0.0f : ex2(m - mn);
+            const float fm = k == 0 ? 0.0f : ex2(m - mn);
             const float f = vnew > 0.0f ? vref / vnew * fm : fm;
             m = mn;
             l *= fm;
             vref = vnew;
             vrel_of = vnew > 0.0f ? 1.0f / vnew : 1.0f;
-            if (j > 0) {
-              ok = all_wait(&bars.pv_done[wg][x ^ 1], ((x ? it0 : it1) + 1) & 1);
-              if (!ok) break;
-              sm100::tc_fence_after();
+            if (k > 0) {
 #pragma unroll
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -526,23 +528,23 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
               }
             }
           }
-          const float vf[4] = {vs.x * vrel_of, vs.y * vrel_of, vs.z * vrel_of, vs.w * vrel_of};
           uint32_t zmax = 0;
           f32x2 l2 = pack2(0.0f, 0.0f), m2 = pack2(-m, -m);
-          if (t0 + 64 <= lim_lo) {  // every row of the warp sees the whole half
-            uint32_t s[2][32];
-            tmem_ld32(tSx, s[0]);
-            tmem_wait_ld32(s[0]);
-            tmem_ld32(tSx + 32, s[1]);
+          if (t0 + kTok <= lim_lo) {  // every row of the warp sees the whole tile
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (c == 1) tmem_wait_ld32(s[1]);
+            for (int c = 0; c < 4; ++c) {
+              const float2 ks = sc.k[c], vs = sc.v[c];
+              uint32_t s[32];
+              tmem_ld32(tS + 32 * c, s);
+              const float f0 = ks.x * qs, f1 = ks.y * qs;
+              const float v0 = vs.x * vrel_of, v1 = vs.y * vrel_of;
+              tmem_wait_ld32(s);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                const float f = kf[2 * c + e / 16], v = vf[2 * c + e / 16];
+                const float f = e < 16 ? f0 : f1, v = e < 16 ? v0 : v1;
                 float a, b;
-                unpack2(fma2(pack2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
-                             pack2(f, f), m2), a, b);
+                unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pack2(f, f),
+                             m2), a, b);
                 const f32x2 w = pack2(ex2(a), ex2(b));
                 l2 = add2(l2, w);
                 unpack2(mul2(w, pack2(v, v)), a, b);
@@ -552,22 +554,24 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 4; ++c) {
               const int c0 = t0 + 32 * c;
               if (c0 >= lim_hi) {  // no row of the warp sees these 32 tokens
 #pragma unroll
                 for (int e = 0; e < 16; ++e) z[16 * c + e] = 0;
                 continue;
               }
+              const float2 ks = sc.k[c], vs = sc.v[c];
               uint32_t s[32];
-              tmem_ld32(tSx + 32 * c, s);
-              tmem_wait_ld32(s);
+              tmem_ld32(tS + 32 * c, s);
+              const float f0 = ks.x * qs, f1 = ks.y * qs;
               // (where the row sees nothing of a group its scale may be a NaN)
-              const float v0 = c0 < lim ? vf[2 * c] : 0.0f;
-              const float v1 = c0 + 16 < lim ? vf[2 * c + 1] : 0.0f;
+              const float v0 = c0 < lim ? vs.x * vrel_of : 0.0f;
+              const float v1 = c0 + 16 < lim ? vs.y * vrel_of : 0.0f;
+              tmem_wait_ld32(s);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                const float f = kf[2 * c + e / 16], v = e < 16 ? v0 : v1;
+                const float f = e < 16 ? f0 : f1, v = e < 16 ? v0 : v1;
                 float a = fmaf(__uint_as_float(s[e]), f, -m);
                 float b = fmaf(__uint_as_float(s[e + 1]), f, -m);
                 if (c0 + e >= lim) a = -INFINITY;
@@ -589,17 +593,16 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
           if (fresh || !__any_sync(~0u, over)) break;
           fresh = true;
         }
-        if (!ok) break;
         l += lt;
         __syncwarp();
-        tmem_st32(tSx, z);
+        tmem_st32(tS, z);
+        tmem_st32(tS + 32, z + 32);
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
-        sm100::mbar_arrive(&bars.p_full[wg][x]);
+        sm100::mbar_arrive(&bars.p_full[wg]);
+        if (lane == 0) sm100::mbar_arrive(&bars.sc_empty[tiles % kRing]);
       }
-      if (!ok || !all_wait(&bars.pv_done[wg][0], (it0 + 1) & 1) ||
-          (g.halves > 1 && !all_wait(&bars.pv_done[wg][1], (it1 + 1) & 1)))
-        break;
+      if (!ok || !all_wait(&bars.o_full[wg], seg & 1)) break;
       ++seg;
       sm100::tc_fence_after();
       const float ov = vref / code_top(CODE);
@@ -682,8 +685,52 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
     unsigned char* tiles = smem + (is_v ? Smem<D>::kV : Smem<D>::kK);
     constexpr int NC = D / 64;  // 64-byte column blocks
-    uint32_t cnt = 0;
+    uint32_t cnt = 0, n0 = 0, n1 = 0;
     bool ok = true;
+    // The queries of a segment, 8 rows of each row tile for a warp at a time:
+    // a row is divided by a power of two so that it fits f16, its sign carries
+    // the sign of the score's scale.
+    auto queries = [&](const Seg& g, int t) -> bool {
+      constexpr int C = D / 32;  // 16-byte pieces of a row per lane
+      const uint32_t i = t ? n1++ : n0++;
+#pragma unroll 1
+      for (int g8 = warp - 8; g8 < 16; g8 += 8) {
+        const int row = 8 * g8 + t8, of = 128 * t + row;
+        const uint16_t* src = p.q + (int64_t)(g.c0 + g.tok0 + of / p.G) * p.q_stride +
+                              (int64_t)(g.h * p.G + of % p.G) * D + 8 * c4;
+        uint4 y[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) y[c] = load16_if(src + 32 * c, of < g.rows);
+        if (g8 == warp - 8 && i > 0 && !all_wait(&bars.q_empty[t], (i - 1) & 1)) return false;
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const uint32_t a[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            most = max(most, max(a[e] & 0x7fff0000u, (a[e] << 16) & 0x7fff0000u));
+        }
+        most = max(most, __shfl_xor_sync(~0u, most, 8));
+        most = max(most, __shfl_xor_sync(~0u, most, 16));
+        const int ex = row_exponent(most);
+        const float down = copysignf(exp2i(-ex), p.scale);
+        if (c4 == 0) s_qscale[i & 1][of] = exp2i(ex);
+        unsigned char* d = smem + Smem<D>::kQ + t * Smem<D>::kTile + row * 16 + c4 * 2048;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const uint32_t a[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            f[e] = pack_half(__uint_as_float(a[e] << 16) * down,
+                             __uint_as_float(a[e] & 0xffff0000u) * down);
+          *reinterpret_cast<uint4*>(d + c * 8192) = make_uint4(f[0], f[1], f[2], f[3]);
+        }
+      }
+      sm100::fence_async_smem();
+      sm100::mbar_arrive(&bars.q_full[t][i & 1]);
+      return true;
+    };
     while (ok) {
       const Seg sg = next_seg();
       if (sg.rows == 0) break;
@@ -708,16 +755,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
           for (int c = 0; c < NC; ++c) x[g][c] = load16_if(src + 64 * c, use);
         }
       };
-      int pa = page_of(0, 0), pb = page_of(0, 1);
-      fetch(0, pa, pb);
-      pa = page_of(1, 0);
-      pb = page_of(1, 1);
-      for (int k = 0; k < nk; ++k, ++cnt) {
+      auto place = [&]() -> bool {  // x -> the next stage
         const int st = cnt & 1;
-        if (cnt >= 2) {
-          ok = all_wait(&empty[st], ((cnt >> 1) - 1) & 1);
-          if (!ok) break;
-        }
+        if (cnt >= 2 && !all_wait(&empty[st], ((cnt >> 1) - 1) & 1)) return false;
         unsigned char* dst = tiles + st * Smem<D>::kTile + (32 * wq + t8) * 16;
 #pragma unroll
         for (int g = 0; g < 4; ++g)
@@ -731,11 +771,26 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
             *reinterpret_cast<uint4*>(d) = make_uint4(f[0], f[1], f[2], f[3]);
             *reinterpret_cast<uint4*>(d + 2048) = make_uint4(f[4], f[5], f[6], f[7]);
           }
+        return true;
+      };
+      fetch(0, page_of(0, 0), page_of(0, 1));
+      ok = place();
+      if (!ok) break;
+      sm100::fence_async_smem();
+      sm100::mbar_arrive(&full[cnt++ & 1]);
+      // (the queries while no codes are held in registers)
+      ok = queries(sg, 0) && (sg.rows <= 128 || queries(sg, 1));
+      if (!ok || nk == 1) continue;
+      fetch(1, page_of(1, 0), page_of(1, 1));
+      int pa = page_of(2, 0), pb = page_of(2, 1);
+      for (int k = 1; k < nk; ++k, ++cnt) {
+        ok = place();
+        if (!ok) break;
         if (k + 1 < nk) fetch(k + 1, pa, pb);
         pa = page_of(k + 2, 0);
         pb = page_of(k + 2, 1);
         sm100::fence_async_smem();
-        sm100::mbar_arrive(&full[st]);
+        sm100::mbar_arrive(&full[cnt & 1]);
       }
     }
   } else {
@@ -762,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
           Seg g{};
           if (w.live())
             g = {w.r, w.h, w.q.c0, w.q.n, w.q.kv, w.tile * w.t.tt, w.tokens() * p.G, w.b0, w.b1,
-                 w.nu, w.halves()};
+                 w.nu};
           s_seg[i & 1] = g;
           sm100::mbar_arrive(&bars.seg_full[i & 1]);
         }
@@ -800,149 +855,103 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         w.next();
       }
     } else if (warp >= 18) {
-      // ----------------------------------------------------------- queries
-      // Lanes 8 c .. 8 c + 7 take the same 8 channels of 8 rows, as the
-      // converting warps do.  A row is divided by a power of two so that it
-      // fits f16; its sign carries the sign of the score's scale.
-      constexpr int C = D / 32;  // 16-byte pieces of a row per lane
-      const int r8 = lane & 7, c4 = lane >> 3;
-      uint32_t seg[2] = {0, 0};
-      bool ok = true;
-      while (ok) {
+      // ---------------------------------------------- queries ahead into L2
+      for (;;) {
         const Seg g = next_seg();
         if (g.rows == 0) break;
-        for (int t = 0; ok && 128 * t < g.rows; ++t) {
-          const uint32_t i = seg[t]++;
-          for (int g8 = warp - 18; g8 < 16; g8 += 4) {
-            uint4 x[2][C];
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              const int row = 128 * t + 8 * (g8 + 2 * a) + r8;
-              const uint16_t* src = p.q + (int64_t)(g.c0 + g.tok0 + row / p.G) * p.q_stride +
-                                    (int64_t)(g.h * p.G + row % p.G) * D + 8 * c4;
-#pragma unroll
-              for (int c = 0; c < C; ++c) x[a][c] = load16_if(src + 32 * c, row < g.rows);
-            }
-            if (g8 == warp - 18 && i > 0) {  // (the first loads are on their way)
-              ok = all_wait(&bars.q_empty[t], (i - 1) & 1);
-              if (!ok) break;
-            }
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              const int row = 8 * (g8 + 2 * a) + r8;
-              uint32_t most = 0;
-#pragma unroll
-              for (int c = 0; c < C; ++c) {
-                const uint32_t y[4] = {x[a][c].x, x[a][c].y, x[a][c].z, x[a][c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  most = max(most, max(y[e] & 0x7fff0000u, (y[e] << 16) & 0x7fff0000u));
-              }
-              most = max(most, __shfl_xor_sync(~0u, most, 8));
-              most = max(most, __shfl_xor_sync(~0u, most, 16));
-              const int ex = row_exponent(most);
-              const float down = copysignf(exp2i(-ex), p.scale);
-              if (c4 == 0) s_qscale[i & 1][128 * t + row] = exp2i(ex);
-              unsigned char* d = smem + Smem<D>::kQ + t * Smem<D>::kTile + row * 16 + c4 * 2048;
-#pragma unroll
-              for (int c = 0; c < C; ++c) {
-                const uint32_t y[4] = {x[a][c].x, x[a][c].y, x[a][c].z, x[a][c].w};
-                uint32_t f[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  f[e] = pack_half(__uint_as_float(y[e] << 16) * down,
-                                   __uint_as_float(y[e] & 0xffff0000u) * down);
-                *reinterpret_cast<uint4*>(d + c * 8192) = make_uint4(f[0], f[1], f[2], f[3]);
-              }
-            }
-          }
-          if (!ok) break;
-          sm100::fence_async_smem();
-          sm100::mbar_arrive(&bars.q_full[t][i & 1]);
+        for (int e = threadIdx.x - 18 * 32; e < g.rows * (D / 64); e += 64) {
+          const int row = e / (D / 64);
+          const uint16_t* src = p.q + (int64_t)(g.c0 + g.tok0 + row / p.G) * p.q_stride +
+                                (int64_t)(g.h * p.G + row % p.G) * D + 64 * (e % (D / 64));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
         }
       }
     } else if (warp == 16) {
     // ----------------------------------------------------------- products
-    const uint32_t id_s = idesc_f16(128, 64, 0), id_o = idesc_f16(128, D, 1);
+    const uint32_t id_s = idesc_f16(128, kTok, 0), id_o = idesc_f16(128, D, 1);
     const uint32_t one = elect_one();
     // (a descriptor's address field counts 16-byte units)
-    const uint64_t dQ = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kQ), 2048, 128);
-    const uint64_t dK = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kK), 2048, 128);
-    const uint64_t dV = sm100::smem_desc(sm100::smem_u32(smem + Smem<D>::kV), 128, 2048);
+    const uint64_t dk = sm100::smem_desc(sm100::smem_u32(smem), 2048, 128);
+    const uint64_t dv = sm100::smem_desc(sm100::smem_u32(smem), 128, 2048);
+    const uint32_t q_lo = (uint32_t)dk + Smem<D>::kQ / 16, k_lo = (uint32_t)dk + Smem<D>::kK / 16;
+    const uint32_t v_lo = (uint32_t)dv + Smem<D>::kV / 16;
+    const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
     constexpr int kTile16 = Smem<D>::kTile / 16;
-    auto scores = [&](int t, int x, int st) {  // S_t = Q_t K^T, half x of the key tile
+    auto scores = [&](int t, int st, bool last) {  // S_t = Q_t K^T
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        mma_ss(tmem + 128 * t + 64 * x, dQ + t * kTile16 + s * 256,
-               dK + st * kTile16 + 64 * x + s * 256, id_s, s > 0, one);
-      mma_commit(&bars.s_full[t][x], one);
+      for (int s = 0; s < D / 64; ++s)
+        mma4_ss(128 * t, q_lo + t * kTile16 + s * 1024, k_lo + st * kTile16 + s * 1024, k_hi, id_s, s,
+                one);
+      mma_commit(&bars.s_full[t], one);
+      if (last) mma_commit(&bars.q_empty[t], one);
     };
-    auto values = [&](int t, int x, int st, bool first) {  // O_t (+)= P_t V
+    auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 64 * x + 8 * s,
-               dV + st * kTile16 + 64 * x + s * 16, id_o, !first || s > 0, one);
-      mma_commit(&bars.pv_done[t][x], one);
+      for (int s = 0; s < 2; ++s)
+        mma4_ts(256 + D * t, 128 * t + 32 * s, v_lo + st * kTile16 + 64 * s, v_hi, id_o,
+                !first || s > 0, one);
     };
-    uint32_t seg0 = 0, seg1 = 0, kc = 0, vc = 0, pa = 0, pb = 0;  // pa, pb: halves 0 and 1 had
-    uint32_t qa = 0, qb = 0;                                      // (row tile 1's)
-    bool ok = true;
+    uint32_t n0 = 0, n1 = 0, t0 = 0, t1 = 0;  // segments and key tiles of the row tiles
+    uint32_t kc = 0;                          // key tiles before this one
+    bool two = false, ok = true;
+    int nk = 0;
+    // Key tile k of a segment, in stage ST: its weights meet the values, and
+    // the next key tile's scores follow as soon as their place is free.
+    auto step = [&](auto stage, int k) {
+      constexpr int ST = decltype(stage)::value;
+      const bool last = k + 1 == nk, before_last = k + 2 == nk;
+      const uint32_t kp = (kc >> 1) & 1, np = ((kc + 1) >> 1) & 1;
+      ok = all_wait(&bars.v_full[ST], kp) && all_wait(&bars.p_full[0], t0++ & 1);
+      if (!ok) return;
+      sm100::tc_fence_after();
+      values(0, ST, k == 0);
+      if (last) {
+        mma_commit(&bars.o_full[0], one);
+      } else {
+        ok = all_wait(&bars.k_full[1 - ST], np);
+        if (!ok) return;
+        sm100::tc_fence_after();
+        scores(0, 1 - ST, before_last);
+      }
+      if (two) {
+        ok = all_wait(&bars.p_full[1], t1++ & 1);
+        if (!ok) return;
+        sm100::tc_fence_after();
+        values(1, ST, k == 0);
+        if (last) mma_commit(&bars.o_full[1], one);
+        else scores(1, 1 - ST, before_last);
+      }
+      mma_commit(&bars.v_empty[ST], one);
+      if (!last) mma_commit(&bars.k_empty[1 - ST], one);
+    };
+    auto first_scores = [&](auto stage) {
+      constexpr int ST = decltype(stage)::value;
+      ok = all_wait(&bars.q_full[0][n0 & 1], (n0 >> 1) & 1) &&
+           all_wait(&bars.k_full[ST], (kc >> 1) & 1);
+      if (!ok) return;
+      ++n0;
+      sm100::tc_fence_after();
+      scores(0, ST, nk == 1);
+      if (two) {
+        ok = all_wait(&bars.q_full[1][n1 & 1], (n1 >> 1) & 1);
+        if (!ok) return;
+        ++n1;
+        sm100::tc_fence_after();
+        scores(1, ST, nk == 1);
+      }
+      mma_commit(&bars.k_empty[ST], one);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
     for (;;) {
       const Seg g = next_seg();
       if (g.rows == 0) break;
-      const bool two = g.rows > 128;
-      const int nh = g.halves;
-      ok = all_wait(&bars.q_full[0][seg0 & 1], (seg0 >> 1) & 1) &&
-           all_wait(&bars.k_full[kc & 1], (kc >> 1) & 1);
-      if (!ok) break;
-      ++seg0;
-      sm100::tc_fence_after();
-      scores(0, 0, kc & 1);
-      if (nh > 1) scores(0, 1, kc & 1);
-      if (nh <= 2) mma_commit(&bars.q_empty[0], one);
-      if (two) {
-        ok = all_wait(&bars.q_full[1][seg1 & 1], (seg1 >> 1) & 1);
-        if (!ok) break;
-        ++seg1;
-        sm100::tc_fence_after();
-        scores(1, 0, kc & 1);
-        if (nh > 1) scores(1, 1, kc & 1);
-        if (nh <= 2) mma_commit(&bars.q_empty[1], one);
-      }
-      mma_commit(&bars.k_empty[kc & 1], one);
-      ++kc;
-      for (int j = 0; j < nh; ++j) {
-        const int x = j & 1;
-        if (x == 0) {
-          ok = all_wait(&bars.v_full[vc & 1], (vc >> 1) & 1);
-          if (!ok) break;
-        }
-        ok = all_wait(&bars.p_full[0][x], (x ? pb++ : pa++) & 1);
-        if (!ok) break;
-        sm100::tc_fence_after();
-        values(0, x, vc & 1, j == 0);
-        if (j + 2 < nh) {
-          if (x == 0) {
-            ok = all_wait(&bars.k_full[kc & 1], (kc >> 1) & 1);
-            if (!ok) break;
-            sm100::tc_fence_after();
-          }
-          scores(0, x, kc & 1);
-          if (j + 3 == nh) mma_commit(&bars.q_empty[0], one);
-        }
-        if (two) {
-          ok = all_wait(&bars.p_full[1][x], (x ? qb++ : qa++) & 1);
-          if (!ok) break;
-          sm100::tc_fence_after();
-          values(1, x, vc & 1, j == 0);
-          if (j + 2 < nh) {
-            scores(1, x, kc & 1);
-            if (j + 3 == nh) mma_commit(&bars.q_empty[1], one);
-          }
-        }
-        if (x == 1 || j + 1 == nh) mma_commit(&bars.v_empty[vc++ & 1], one);
-        // (the next key tile's scores are all issued)
-        if (j + 2 < nh && (x == 1 || j + 3 == nh)) mma_commit(&bars.k_empty[kc++ & 1], one);
+      // (a reduction's result is known to be uniform)
+      two = __reduce_max_sync(~0u, g.rows) > 128;
+      nk = __reduce_max_sync(~0u, g.b1 - g.b0);
+      if (kc & 1) first_scores(S1{}); else first_scores(S0{});
+      for (int k = 0; ok && k < nk; ++k, ++kc) {
+        if (kc & 1) step(S1{}, k); else step(S0{}, k);
       }
       if (!ok) break;
     }
@@ -955,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   sm100::tc_fence_before();
   __syncthreads();
   if (tid == 0 && s_abort) report(p.status, KDA_ERR_TIMEOUT);
-  if (warp == 16) sm100::tmem_dealloc(tmem, 512);
+  if (warp == 16) sm100::tmem_dealloc(s_tmem, 512);
 }
 
 template <int CODE, int D>
