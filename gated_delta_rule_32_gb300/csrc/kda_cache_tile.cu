@@ -166,12 +166,6 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // The products, issued by a whole warp that runs in step, of which one thread
 // (`one`) carries them out; four k-steps an asm block.  Issue slots are what
 // this warp must not lack, its scheduler serving four busy warps beside it: in
@@ -469,11 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         ok = all_wait(&bars.s_full[wg], it & 1);
         if (!ok) break;
         sm100::tc_fence_after();
-        // Weights with the reference m of the tiles before; only where a row
-        // passes it by 8 (its weight by 2^8: f16 has room for that), in the
-        // first tile, or when a page's value scale passes vref, is the
-        // maximum sought, O rescaled and the tile's weights made again.  So
-        // S is read once, and O almost never.
+        // Weights with the reference m of the tiles before; only where a row's
+        // weights sum to more than 2^15 (f16 ends at 65504), in the first
+        // tile, or when a page's value scale passes vref, is the maximum
+        // sought, O rescaled and the tile's weights made again.  So S is read
+        // once, and O almost never.
         uint32_t z[64];
         float lt;
         bool fresh = k == 0 || vmax > vref;
@@ -528,7 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
               }
             }
           }
-          uint32_t zmax = 0;
           f32x2 l2 = pack2(0.0f, 0.0f), m2 = pack2(-m, -m);
           if (t0 + kTok <= lim_lo) {  // every row of the warp sees the whole tile
 #pragma unroll
@@ -549,7 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
                 l2 = add2(l2, w);
                 unpack2(mul2(w, pack2(v, v)), a, b);
                 z[16 * c + e / 2] = pack_half(a, b);
-                zmax = max_half2(zmax, z[16 * c + e / 2]);
               }
             }
           } else {
@@ -580,16 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
                 l2 = add2(l2, w);
                 unpack2(mul2(w, pack2(v, v)), a, b);
                 z[16 * c + e / 2] = pack_half(a, b);
-                zmax = max_half2(zmax, z[16 * c + e / 2]);
               }
             }
           }
           float la, lb;
           unpack2(l2, la, lb);
           lt = la + lb;
-          // (!<=: an infinity or NaN counts too)
-          const __half2 zm = *reinterpret_cast<__half2*>(&zmax);
-          const bool over = !(__low2float(zm) <= 256.0f && __high2float(zm) <= 256.0f);
+          // no weight above the sum; an infinity or NaN is seen too
+          const bool over = !(lt <= 32768.0f);
           if (fresh || !__any_sync(~0u, over)) break;
           fresh = true;
         }
