@@ -3,12 +3,12 @@
 // of parts.
 //
 // Bound by the cache's bytes: every code is used for at most 16 query rows,
-// 4 * 16 flops per byte.  The work is cut in units of 64 tokens of a (request,
+// 4 * 16 flops per byte.  The work is cut in units of 64 NB tokens of a (request,
 // head) and every CTA takes an equal share of all units, so ragged batches
 // and single long requests fill the chip alike; a (request, head) that
 // crosses a CTA boundary leaves parts, which kda_attn_join_kernel joins.
 //
-// Warp w of a CTA takes the 16-token blocks 4 u + w.  Products run on
+// Warp w of a CTA takes every fourth run of NB 16-token blocks.  Products run on
 // mma.m16n8k16 with the tokens (then the channels) on the 16-row side, which
 // leaves 8 columns for query rows: S^T = K Q^T, O^T += V^T P^T.  The codes
 // go from global memory to registers in the very layout that the A operand
@@ -25,7 +25,6 @@ using namespace kda_cache;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 16 * kWarps;  // tokens
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -53,33 +52,37 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D>
-struct Ring {
-  static constexpr int kStage = 32 * D;                  // 16 tokens, keys and values
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kWarpBytes = kStage * kStages;    // 12 KiB
+// NT: 8-row tiles of query rows.  NB: 16-token blocks that a warp takes at a
+// time: two where the registers allow it, so that one's products overlap the
+// other's conversion.
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kBlocks = NT == 1 ? 2 : 1;
+  static constexpr int kUnit = 16 * kBlocks * kWarps;      // tokens
+  static constexpr int kBlockBytes = 32 * D;               // keys and values of a block
+  static constexpr int kStage = kBlocks * kBlockBytes;
+  static constexpr int kStages = (D == 128 ? 4 : 8) / kBlocks - (NT == 2 ? 1 : 0);
+  static constexpr int kWarpBytes = kStage * kStages;      // 12 or 16 KiB
 };
 
-// NT: 8-row tiles of query rows.
 template <int CODE, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
-    kda_cache_attn_rows_kernel(AttnArgs p) {
+__global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnArgs p) {
+  using C = Cfg<D, NT>;
   constexpr int KS = D / 16;         // k-steps of K Q^T = m-tiles of V^T P^T
   constexpr int KC = D / 64;         // 16-byte chunks of a key row per lane
   constexpr int VB = D / 8;          // bytes of a value row per lane
-  constexpr int ROWS = 8 * NT;
-  constexpr int S = Ring<D>::kStages;
+  constexpr int ROWS = 8 * NT, NB = C::kBlocks, S = C::kStages;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i8 = lane >> 2, j = lane & 3;
   const int lg = p.page_log2, P = 1 << lg, G = p.G;
-  unsigned char* ring = smem + warp * Ring<D>::kWarpBytes;
+  unsigned char* ring = smem + warp * C::kWarpBytes;
   const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
 
   auto blocks_of = [&](const Req& q) -> int64_t {
     if ((int64_t)q.n * G > kFewRows) return 0;
-    return max(1, (int)(((int64_t)q.kv + kUnit - 1) / kUnit));
+    return max(1, (int)(((int64_t)q.kv + C::kUnit - 1) / C::kUnit));
   };
   Share sh = find_share<kThreads>(p, [&](const Req& q) { return blocks_of(q) * p.Hkv; });
   int r = sh.r;
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     const float sm = p.scale * 1.4426950408889634f / code_top(CODE);
 
     float o[NT][KS][4], m[NT][2], l[NT][2];
-    float vref = 0.0f, vinv = 0.0f;
+    float vref = 0.0f, vinv = 1.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -165,178 +168,233 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        m[nt][c] = -INFINITY;
-        l[nt][c] = 0.0f;
-      }
+      for (int c = 0; c < 2; ++c) m[nt][c] = l[nt][c] = 0.0f;
     }
 
-    // this warp's 16-token blocks: 4 (b0 + i) + warp, i < count
-    const int all = (kv + 15) >> 4;
+    // this warp's runs of NB blocks: 4 (b0 + i) + warp, i < count
+    const int all = (int)(((int64_t)kv + 16 * NB - 1) / (16 * NB));
     const int count = max(0, min(b1, (all - warp + kWarps - 1) / kWarps) - b0);
     const int32_t* table = p.table + (int64_t)r * p.max_pages;
     // pages and scales of 32 blocks at a time, one per lane, a batch ahead
-    auto page_at = [&](int i) -> int {
-      if (i >= count) return 0;
-      const int pg = table[((4 * (b0 + i) + warp) << 4) >> lg];
-      if (pg >= 0 && pg < p.num_pages) return pg;
-      report(p.status, KDA_ERR_BAD_PAGES);
+    // (checked when they are used)
+    auto token_of = [&](int x) { return ((4 * (b0 + x / NB) + warp) * NB + x % NB) << 4; };
+    auto has = [&](int x) { return x < count * NB && token_of(x) < kv; };
+    auto page_at = [&](int x) { return load_page_if(table + (token_of(x) >> lg), has(x)); };
+    auto checked = [&](int pg, int x) -> int {
+      if ((uint32_t)pg < (uint32_t)p.num_pages) return pg;
+      if (has(x)) report(p.status, KDA_ERR_BAD_PAGES);
       return 0;
     };
-    int pg_cur = page_at(lane), pg_next = page_at(32 + lane);
+    int pg_cur = checked(page_at(lane), lane), pg_next = page_at(32 + lane);
     float ks_cur = p.k_scale[(int64_t)pg_cur * p.Hkv + h];
     float vs_cur = p.v_scale[(int64_t)pg_cur * p.Hkv + h];
     float ks_next = 0.0f, vs_next = 0.0f;
 
-    auto issue = [&](int i, int in_batch) {  // (all lanes)
-      const int pa = __shfl_sync(~0u, pg_cur, in_batch & 31);
-      const int pb = __shfl_sync(~0u, pg_next, in_batch & 31);
-      if (i < count) {
-        const int pg = in_batch < 32 ? pa : pb;
-        const int t0 = ((4 * (b0 + i) + warp) << 4) & (P - 1);
-        const int64_t at = ((((int64_t)pg * p.Hkv + h) << lg) + t0) * D;
-        const uint32_t dst = ring_u + (i % S) * Ring<D>::kStage;
-        const uint8_t* k = p.k_codes + at + i8 * D + 16 * j;
-        const uint8_t* v = p.v_codes + at + 2 * j * D + i8 * VB;
+    // block x of this warp -> its place in the ring (all lanes); in_batch
+    // counts from the current batch's start
+    const int64_t lane_k = (int64_t)i8 * D + 16 * j, lane_v = (int64_t)2 * j * D + i8 * VB;
+    auto issue = [&](int i, int in_batch, int slot) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+      for (int b = 0; b < NB; ++b) {
+        const int pa = __shfl_sync(~0u, pg_cur, (in_batch + b) & 31);
+        const int pb = __shfl_sync(~0u, pg_next, (in_batch + b) & 31);
+        if (has(i * NB + b)) {
+          const int pg = in_batch + b < 32 ? pa : pb;
+          const int t0 = token_of(i * NB + b) & (P - 1);
+          const int64_t at = ((((int64_t)pg * p.Hkv + h) << lg) + t0) * D;
+          const uint32_t dst = ring_u + slot * C::kStage + b * C::kBlockBytes;
+          const uint8_t* k = p.k_codes + at + lane_k;
+          const uint8_t* v = p.v_codes + at + lane_v;
 #pragma unroll
-          for (int c = 0; c < KC; ++c)
-            copy_async<16>(dst + (half * KC + c) * 512 + lane * 16, k + half * 8 * D + c * 64);
+          for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          copy_async<VB>(dst + 16 * D + e * (32 * VB) + lane * VB,
-                         v + ((e & 1) + (e >> 1) * 8) * D);
+            for (int c = 0; c < KC; ++c)
+              copy_async<16>(dst + (half * KC + c) * 512 + lane * 16, k + half * 8 * D + c * 64);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            copy_async<VB>(dst + 16 * D + e * (32 * VB) + lane * VB,
+                           v + ((e & 1) + (e >> 1) * 8) * D);
+        }
       }
       copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) issue(i, i);
+    for (int i = 0; i < S - 1; ++i) issue(i, i * NB, i);
 
-    int bi = 0;  // i within its batch of 32
-    for (int i = 0; i < count; ++i, ++bi) {
+    int bi = 0;             // blocks since the batch's start
+    int slot = 0, fill = S - 1;  // ring places of this run and of the one that is fetched
+    for (int i = 0; i < count; ++i, bi += NB) {
       if (bi == 32) {
         bi = 0;
         pg_cur = pg_next;
         ks_cur = ks_next;
         vs_cur = vs_next;
-        pg_next = page_at(i + 32 + lane);
+        pg_next = page_at((i * NB + 32) + lane);
       }
       if (bi == 8) {
+        pg_next = checked(pg_next, i * NB - 8 + 32 + lane);
         ks_next = p.k_scale[(int64_t)pg_next * p.Hkv + h];
         vs_next = p.v_scale[(int64_t)pg_next * p.Hkv + h];
       }
-      issue(i + S - 1, bi + S - 1);
-      const float kf = __shfl_sync(~0u, ks_cur, bi) * sm, vs = __shfl_sync(~0u, vs_cur, bi);
+      issue(i + S - 1, bi + (S - 1) * NB, fill);
+      fill = fill + 1 == S ? 0 : fill + 1;
+      float kf[NB], vs[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        kf[b] = __shfl_sync(~0u, ks_cur, bi + b) * sm;
+        vs[b] = __shfl_sync(~0u, vs_cur, bi + b);
+      }
       copy_wait<S - 1>();
-      const unsigned char* st = ring + (i % S) * Ring<D>::kStage;
-      const int tok = (4 * (b0 + i) + warp) << 4;
+      const unsigned char* st = ring + slot * C::kStage;
+      slot = slot + 1 == S ? 0 : slot + 1;
+      const int tok = token_of(i * NB);
+      const bool edge = tok + 16 * NB > all_see;
+      float vmax = vs[0];
+      if (NB == 2) {
+        // (a last run's second block may lie past the end: no page, no copy)
+        if (tok + 16 >= kv) vs[NB - 1] = kf[NB - 1] = 0.0f;
+        vmax = fmaxf(vmax, vs[NB - 1]);
+      }
 
       // S^T = K Q^T
-      float x[NT][4];
+      float x[NB][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const uint4 ka = *reinterpret_cast<const uint4*>(st + c * 512 + lane * 16);
-        const uint4 kb = *reinterpret_cast<const uint4*>(st + (KC + c) * 512 + lane * 16);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          uint32_t a0, a1, a2, a3;
-          codes_to_half<CODE>(wa[s], a0, a2);
-          codes_to_half<CODE>(wb[s], a1, a3);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(x[nt], a0, a1, a2, a3, qf[nt][4 * c + s][0], qf[nt][4 * c + s][1]);
-        }
-      }
-      // scores in log2 units; tokens i8 and i8 + 8, columns 2 j and 2 j + 1
-      const bool edge = tok + 16 > all_see;
-      bool grow = vs > vref;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[nt][e] *= kf * qs[nt][e & 1];
-          if (edge && tok + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) x[nt][e] = -INFINITY;
-          grow |= x[nt][e] > m[nt][e & 1] + 8.0f;
-        }
-      }
-      // The reference m of a row need not be its maximum: it moves only when
-      // a score passes it by 8 (weights stay below 2^8, far inside f16).  So
-      // most blocks need one vote here and no shuffles.
-      if (__any_sync(~0u, grow)) {
-        const float vnew = vs > vref ? pow2_above(vs) : vref;
-        const float fv = vnew > 0.0f ? vref / vnew : 0.0f;
-        vref = vnew;
-        vinv = 1.0f / vnew;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float f[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(x[nt][c], x[nt][c + 2]);
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-            const float mn = fmaxf(m[nt][c], mx);
-            f[c] = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - mn);
-            m[nt][c] = mn;
-            l[nt][c] *= f[c];
-            f[c] *= fv;
-          }
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][s][e] *= f[e & 1];
-        }
-      }
-      const float vw = vref > 0.0f ? vs * vinv : vs;  // (a page of zeros first: 0, or its NaN)
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float mm = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
-          w[e] = ex2(x[nt][e] - mm);
-          l[nt][e & 1] += w[e];
-          // (a masked token's weight stays 0 where the page's scale is a NaN)
-          w[e] = x[nt][e] == -INFINITY ? 0.0f : w[e] * vw;
-        }
-        pb[nt][0] = transpose8x8(pack_half(w[0], w[1]));
-        pb[nt][1] = transpose8x8(pack_half(w[2], w[3]));
-      }
-      // O^T += V^T P^T; lane's tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9
-      uint32_t v[4][VB / 4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const unsigned char* at = st + 16 * D + e * (32 * VB) + lane * VB;
-        if (VB == 16) {
-          const uint4 y = *reinterpret_cast<const uint4*>(at);
-          v[e][0] = y.x; v[e][1] = y.y; v[e][VB / 4 - 2] = y.z; v[e][VB / 4 - 1] = y.w;
-        } else {
-          const uint2 y = *reinterpret_cast<const uint2*>(at);
-          v[e][0] = y.x; v[e][1] = y.y;
-        }
-        // what a page holds past the request's end may be a NaN
-        if (CODE == KDA_E4M3 && edge && tok + 2 * j + (e & 1) + 8 * (e >> 1) >= kv) {
-#pragma unroll
-          for (int w = 0; w < VB / 4; ++w) v[e][w] = 0;
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const uint32_t sel = (s & 1) ? 0x7362 : 0x5140;
-        uint32_t a0, a1, a2, a3;
-        codes_to_half<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
-        codes_to_half<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
+      for (int b = 0; b < NB; ++b) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          mma16816(o[nt][s], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const unsigned char* sk = st + b * C::kBlockBytes + lane * 16;
+          const uint4 ka = *reinterpret_cast<const uint4*>(sk + c * 512);
+          const uint4 kb = *reinterpret_cast<const uint4*>(sk + (KC + c) * 512);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t a0, a1, a2, a3;
+            codes_to_half<CODE>(wa[s], a0, a2);
+            codes_to_half<CODE>(wb[s], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(x[b][nt], a0, a1, a2, a3, qf[nt][4 * c + s][0], qf[nt][4 * c + s][1]);
+          }
+        }
+        if (edge) {  // tokens i8 and i8 + 8, columns 2 j and 2 j + 1
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) x[b][nt][e] = NAN;
+        }
+      }
+      // Weights with the standing reference m of each row, which need not be
+      // the maximum: it is sought, with shuffles, only in the first run, when
+      // weights sum to more than 2^15 (f16 ends at 65504), or when a page's
+      // value scale passes vref.  Most runs need one vote.  (A masked score is
+      // a NaN until here, a masked weight 0.)
+      float w[NB][NT][4], lt[NT][2];
+      bool fresh = i == 0 || vmax > vref;
+      for (;;) {
+        if (fresh) {
+          const float vnew = vmax > vref ? pow2_above(vmax) : vref;
+          const float fv = vnew > 0.0f ? vref / vnew : 1.0f;
+          vref = vnew;
+          vinv = vnew > 0.0f ? 1.0f / vnew : 1.0f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float mx = -INFINITY;  // (fmaxf passes over NaN)
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                mx = fmaxf(mx, fmaxf(x[b][nt][c] * (kf[b] * qs[nt][c]),
+                                     x[b][nt][c + 2] * (kf[b] * qs[nt][c])));
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+              // (a row that sees nothing in the first run sees nothing at all)
+              const float mn = i == 0 ? (mx == -INFINITY ? 0.0f : mx) : fmaxf(m[nt][c], mx);
+              f[c] = i == 0 ? 0.0f : ex2(m[nt][c] - mn);
+              m[nt][c] = mn;
+              l[nt][c] *= f[c];
+              f[c] *= fv;
+            }
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][s][e] *= f[e & 1];
+          }
+        }
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          lt[nt][0] = lt[nt][1] = 0.0f;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              w[b][nt][e] = ex2(fmaf(x[b][nt][e], kf[b] * qs[nt][e & 1], -m[nt][e & 1]));
+              if (edge && tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) w[b][nt][e] = 0.0f;
+              lt[nt][e & 1] += w[b][nt][e];
+            }
+          // (columns without a row see no token; a NaN counts as over)
+          over |= !(lt[nt][0] <= 32768.0f && lt[nt][1] <= 32768.0f);
+        }
+        if (fresh || !__any_sync(~0u, over)) break;
+        fresh = true;
+      }
+      uint32_t pb[NB][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        l[nt][0] += lt[nt][0];
+        l[nt][1] += lt[nt][1];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float vw = vs[b] * vinv;
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = w[b][nt][e] * vw;
+            // (0 times a scale that may be NaN)
+            if (edge && tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) y[e] = 0.0f;
+          }
+          pb[b][nt][0] = transpose8x8(pack_half(y[0], y[1]));
+          pb[b][nt][1] = transpose8x8(pack_half(y[2], y[3]));
+        }
+      }
+      // O^T += V^T P^T; lane's tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t v[4][VB / 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const unsigned char* at =
+              st + b * C::kBlockBytes + 16 * D + e * (32 * VB) + lane * VB;
+          if (VB == 16) {
+            const uint4 y = *reinterpret_cast<const uint4*>(at);
+            v[e][0] = y.x; v[e][1] = y.y; v[e][VB / 4 - 2] = y.z; v[e][VB / 4 - 1] = y.w;
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(at);
+            v[e][0] = y.x; v[e][1] = y.y;
+          }
+          // what lies past the request's end may be a NaN
+          if (CODE == KDA_E4M3 && edge && tok + 16 * b + 2 * j + (e & 1) + 8 * (e >> 1) >= kv) {
+#pragma unroll
+            for (int w = 0; w < VB / 4; ++w) v[e][w] = 0;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint32_t sel = (s & 1) ? 0x7362 : 0x5140;
+          uint32_t a0, a1, a2, a3;
+          codes_to_half<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
+          codes_to_half<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(o[nt][s], a0, a1, a2, a3, pb[b][nt][0], pb[b][nt][1]);
+        }
       }
     }
     copy_wait<0>();
@@ -354,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         y += __shfl_xor_sync(~0u, y, 16);
         const int row = 8 * nt + 2 * j + c;
         if (i8 == 0) {
-          s_m[warp][row] = m[nt][c];
+          s_m[warp][row] = y == 0.0f ? -INFINITY : m[nt][c];
           s_l[warp][row] = y;
         }
 #pragma unroll
@@ -364,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       }
     }
     __syncthreads();
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (b0 > 0 ? 0 : 1);
+    const int64_t part = 2 * (int64_t)blockIdx.x + (b0 > 0 ? 0 : 1);
     for (int e = tid; e < rows * D; e += kThreads) {
       const int row = e / D, ch = e % D;
       float mx = s_m[0][row];
@@ -376,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(s_m[w][row] - mm);
         sum += f * s_l[w][row];
-        acc += f * *reinterpret_cast<float*>(smem + w * Ring<D>::kWarpBytes + e * 4);
+        acc += f * *reinterpret_cast<float*>(smem + w * C::kWarpBytes + e * 4);
       }
       if (whole) {
         const int64_t at = (int64_t)(rq.c0 + row / G) * p.Hq + h * G + row % G;
@@ -385,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         if (p.lse && ch == 0)
           p.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
       } else {
-        p.part_o[(slot * kFewRows + row) * D + ch] = acc;
+        p.part_o[(part * kFewRows + row) * D + ch] = acc;
         if (ch == 0) {
-          p.part_ml[(slot * kFewRows + row) * 2] = mx;
-          p.part_ml[(slot * kFewRows + row) * 2 + 1] = sum;
+          p.part_ml[(part * kFewRows + row) * 2] = mx;
+          p.part_ml[(part * kFewRows + row) * 2 + 1] = sum;
         }
       }
     }
@@ -461,7 +519,7 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, int ctas
 template <int CODE, int D, int NT>
 kda_status launch_rows(const AttnArgs& p, int ctas, cudaStream_t s) {
   auto kernel = kda_cache_attn_rows_kernel<CODE, D, NT>;
-  const int smem = kWarps * Ring<D>::kWarpBytes;
+  const int smem = kWarps * Cfg<D, NT>::kWarpBytes;
   const kda_status rc = kda_smem_attr((const void*)kernel, smem);
   if (rc != KDA_OK) return rc;
   kernel<<<ctas, kThreads, smem, s>>>(p);
