@@ -10,13 +10,14 @@
 //
 // Warp w of a CTA takes every fourth run of NB 16-token blocks.  Products run on
 // mma.m16n8k16 with the tokens (then the channels) on the 16-row side, which
-// leaves 8 columns for query rows: S^T = K Q^T, O^T += V^T P^T.  The codes
-// go from global memory to registers in the very layout that the A operand
-// wants, because the order of the contracted index is free: a lane's 16-byte
-// chunk of a key row holds its channels of all k-steps (queries are loaded in
-// the same order), its chunks of four value rows hold its channels of all
-// m-tiles.  So the asynchronous copies land in lane-private slots of shared
-// memory: no barrier, no bank conflict, no layout change.
+// leaves 8 columns for query rows: S^T = K Q^T, O^T += V^T P^T.  The order of
+// the contracted index is free, so a lane's 16-byte chunk of a key row holds
+// its channels of all k-steps (queries are loaded in the same order), and its
+// chunks of four value rows its channels of all m-tiles: the codes need no
+// change of layout.  They come by asynchronous copies into a ring of each
+// warp's own -- eight lanes fetch a whole 128-byte row; in a first form, whose
+// lanes fetched what they use themselves, L2 sent every byte twice -- with the
+// chunks permuted so that neither side meets bank conflicts.
 #include "kda_cache_attn.cuh"
 
 namespace {
@@ -39,13 +40,23 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+
+// Byte offsets of 16-byte chunk c of token t in a block's keys and values.  A
+// quarter of a warp reads the chunks of two tokens of keys, and two chunks of
+// every second token of four pairs of values; each set covers all banks.
+template <int D>
+__device__ __forceinline__ int key_at(int t, int c) {
+  return D == 128 ? t * 128 + ((c ^ ((t & 1) << 2)) << 4) : t * 64 + (c << 4);
+}
+template <int D>
+__device__ __forceinline__ int value_at(int t, int c) {
+  return D == 128 ? t * 128 + ((c ^ (t & 6)) << 4)
+                  : (t ^ ((t >> 1) & 1)) * 64 + ((c ^ ((t >> 1) & 2)) << 4);
+}
+
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -192,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
 
     // block x of this warp -> its place in the ring (all lanes); in_batch
     // counts from the current batch's start
-    const int64_t lane_k = (int64_t)i8 * D + 16 * j, lane_v = (int64_t)2 * j * D + i8 * VB;
+    constexpr int ROWL = D / 16;         // lanes a row
+    constexpr int ROWS_I = 32 / ROWL;    // rows an instruction
+    const int rl = lane / ROWL, cl = lane % ROWL;
     auto issue = [&](int i, int in_batch, int slot) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -203,17 +216,14 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
           const int t0 = token_of(i * NB + b) & (P - 1);
           const int64_t at = ((((int64_t)pg * p.Hkv + h) << lg) + t0) * D;
           const uint32_t dst = ring_u + slot * C::kStage + b * C::kBlockBytes;
-          const uint8_t* k = p.k_codes + at + lane_k;
-          const uint8_t* v = p.v_codes + at + lane_v;
+          const uint8_t* k = p.k_codes + at + lane * 16;
+          const uint8_t* v = p.v_codes + at + lane * 16;
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+          for (int e = 0; e < 16 / ROWS_I; ++e)
+            copy_async16(dst + key_at<D>(e * ROWS_I + rl, cl), k + e * 512);
 #pragma unroll
-            for (int c = 0; c < KC; ++c)
-              copy_async<16>(dst + (half * KC + c) * 512 + lane * 16, k + half * 8 * D + c * 64);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            copy_async<VB>(dst + 16 * D + e * (32 * VB) + lane * VB,
-                           v + ((e & 1) + (e >> 1) * 8) * D);
+          for (int e = 0; e < 16 / ROWS_I; ++e)
+            copy_async16(dst + 16 * D + value_at<D>(e * ROWS_I + rl, cl), v + e * 512);
         }
       }
       copy_commit();
@@ -224,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
     int bi = 0;             // blocks since the batch's start
     int slot = 0, fill = S - 1;  // ring places of this run and of the one that is fetched
     for (int i = 0; i < count; ++i, bi += NB) {
+      __syncwarp();  // (the place that is filled next has been read)
       if (bi == 32) {
         bi = 0;
         pg_cur = pg_next;
@@ -245,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
         vs[b] = __shfl_sync(~0u, vs_cur, bi + b);
       }
       copy_wait<S - 1>();
+      __syncwarp();
       const unsigned char* st = ring + slot * C::kStage;
       slot = slot + 1 == S ? 0 : slot + 1;
       const int tok = token_of(i * NB);
@@ -266,9 +278,9 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
           for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.0f;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-          const unsigned char* sk = st + b * C::kBlockBytes + lane * 16;
-          const uint4 ka = *reinterpret_cast<const uint4*>(sk + c * 512);
-          const uint4 kb = *reinterpret_cast<const uint4*>(sk + (KC + c) * 512);
+          const unsigned char* sk = st + b * C::kBlockBytes;
+          const uint4 ka = *reinterpret_cast<const uint4*>(sk + key_at<D>(i8, 4 * c + j));
+          const uint4 kb = *reinterpret_cast<const uint4*>(sk + key_at<D>(i8 + 8, 4 * c + j));
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
@@ -370,8 +382,9 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
         uint32_t v[4][VB / 4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const unsigned char* at =
-              st + b * C::kBlockBytes + 16 * D + e * (32 * VB) + lane * VB;
+          const unsigned char* at = st + b * C::kBlockBytes + 16 * D +
+                                    value_at<D>(2 * j + (e & 1) + 8 * (e >> 1), i8 * VB / 16) +
+                                    (i8 * VB) % 16;
           if (VB == 16) {
             const uint4 y = *reinterpret_cast<const uint4*>(at);
             v[e][0] = y.x; v[e][1] = y.y; v[e][VB / 4 - 2] = y.z; v[e][VB / 4 - 1] = y.w;
@@ -398,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
       }
     }
     copy_wait<0>();
+    __syncwarp();
 
     // the warps' sums meet in shared memory (each in its own ring)
     float* so = reinterpret_cast<float*>(ring);
