@@ -60,7 +60,7 @@ extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
   if (T > 0 && (!q || !out)) return KDA_ERR_INVALID_ARG;
   if (Hq % Hkv) return KDA_ERR_INVALID_ARG;
   if (!page_ok(page) || !head_dim_ok(d) || (code != KDA_I8 && code != KDA_E4M3) ||
-      Hq / Hkv > 64 || R > kMaxRequests)
+      Hq / Hkv > 64 || Hkv > 4096 || R > kMaxRequests)
     return KDA_ERR_UNSUPPORTED;
   if ((int64_t)max_pages * page > (1 << 30) || T > (1 << 26)) return KDA_ERR_UNSUPPORTED;
   const int64_t width = (int64_t)Hq * d;
@@ -90,24 +90,25 @@ extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
   while ((1 << lg) < page) ++lg;
   AttnArgs p{q, q_stride, cu_seqlens, kv_lens, block_table, (const uint8_t*)k_codes,
              (const uint8_t*)v_codes, k_scale, v_scale, out, lse, dev_status, R, T, max_new,
-             max_pages, Hq, Hkv, Hq / Hkv, num_pages, lg, scale, nullptr, nullptr, nullptr,
-             nullptr};
+             max_pages, Hq, Hkv, Hq / Hkv, num_pages, lg, scale, {}};
   const Layout w = layout(max_new, p.G, d);
   if (w.ctas[0] < 1) return KDA_ERR_CUDA;
   const bool own = workspace == nullptr;
   if (own && cudaMallocAsync(&workspace, w.bytes, s) != cudaSuccess) return KDA_ERR_CUDA;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  kda_status rc = KDA_OK;
-  for (int i = 0; i < 2 && rc == KDA_OK; ++i) {
-    if (w.ctas[i] == 0) continue;
-    p.total = reinterpret_cast<int64_t*>(ws + w.total[i]);
-    p.part_head = reinterpret_cast<PartHead*>(ws + w.head[i]);
-    p.part_ml = reinterpret_cast<float*>(ws + w.ml[i]);
-    p.part_o = reinterpret_cast<float*>(ws + w.o[i]);
-    rc = i == 0 ? kda_launch_attn_rows(p, d, code, w.ctas[i], s)
-                : kda_launch_attn_tile(p, d, code, w.ctas[i], s);
-    if (rc == KDA_OK) rc = kda_launch_attn_join(p, d, kPartRows[i], w.ctas[i], s);
+  Parts parts[2];
+  for (int i = 0; i < 2; ++i)
+    parts[i] = {w.ctas[i], kPartRows[i], reinterpret_cast<int64_t*>(ws + w.total[i]),
+                reinterpret_cast<PartHead*>(ws + w.head[i]), reinterpret_cast<float*>(ws + w.ml[i]),
+                reinterpret_cast<float*>(ws + w.o[i])};
+  p.parts = parts[0];
+  kda_status rc = kda_launch_attn_rows(p, d, code, s);
+  if (rc == KDA_OK && parts[1].ctas) {
+    p.parts = parts[1];
+    rc = kda_launch_attn_tile(p, d, code, s);
   }
+  p.parts = parts[0];
+  if (rc == KDA_OK) rc = kda_launch_attn_join(p, parts[1], d, s);
   if (own && cudaFreeAsync(workspace, s) != cudaSuccess && rc == KDA_OK) rc = KDA_ERR_CUDA;
   return rc;
 }

@@ -14,6 +14,17 @@ struct PartHead {
   int32_t tok0, rows, h, pad;
 };
 
+// What a kernel leaves for the join, in the workspace.  A CTA leaves at most
+// two parts: of the segment that its share begins in (slot 2 c) and of the one
+// that it ends in (slot 2 c + 1).
+struct Parts {
+  int ctas, rows;    // of the kernel; a part's rows
+  int64_t* total;    // units of the whole batch
+  PartHead* head;    // [ctas]
+  float* ml;         // [2 ctas][rows][2] maximum (log2) and sum of a part's rows
+  float* o;          // [2 ctas][rows][D] a part's sum of weighted values
+};
+
 struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
@@ -25,13 +36,7 @@ struct AttnArgs {
   int32_t* status;
   int R, T, max_new, max_pages, Hq, Hkv, G, num_pages, page_log2;
   float scale;
-  // workspace of one kernel and its joining kernel
-  int64_t* total;       // units of the whole batch
-  PartHead* part_head;  // [CTAs]
-  // A CTA leaves at most two parts: of the segment that its share begins in
-  // (slot 2 c) and of the one that it ends in (slot 2 c + 1).
-  float* part_ml;       // [2 * CTAs][rows][2] maximum (log2) and sum of a part's rows
-  float* part_o;        // [2 * CTAs][rows][D] a part's sum of weighted values
+  Parts parts;  // of the kernel that the arguments are for
 };
 
 // Query rows per key / value head up to which a request runs on the few-row
@@ -111,7 +116,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, Units units) {
       at += u;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) *p.total = total;
+  if (blockIdx.x == 0 && tid == 0) *p.parts.total = total;
   __syncthreads();
   s.r = s_r;
   s.base = s_base;
@@ -199,11 +204,41 @@ __device__ __forceinline__ float exp2i(int e) {  // -126 <= e <= 127
 
 }  // namespace kda_cache
 
-// The kernels for few rows (kFewRows rows in a part) and for tiles of rows
-// (kTileRows), and the join of the parts that one of them has left.
-kda_status kda_launch_attn_rows(const kda_cache::AttnArgs& p, int d, int code, int ctas,
+// The kernels for few rows and for tiles of rows, and the join of the parts
+// that both have left (`tile`.ctas 0: the tile kernel has not run).  The later
+// ones are launched so that their start overlaps the end of the one before.
+kda_status kda_launch_attn_rows(const kda_cache::AttnArgs& p, int d, int code, cudaStream_t s);
+kda_status kda_launch_attn_tile(const kda_cache::AttnArgs& p, int d, int code, cudaStream_t s);
+kda_status kda_launch_attn_join(const kda_cache::AttnArgs& p, const kda_cache::Parts& tile, int d,
                                 cudaStream_t s);
-kda_status kda_launch_attn_tile(const kda_cache::AttnArgs& p, int d, int code, int ctas,
-                                cudaStream_t s);
-kda_status kda_launch_attn_join(const kda_cache::AttnArgs& p, int d, int part_rows, int ctas,
-                                cudaStream_t s);
+
+namespace kda_cache {
+
+// Programmatic dependent launch: the kernel may start when the one before it
+// in the stream has let it (kernel_may_follow), and must call
+// wait_for_kernel_before at a point after which it needs, or before it ends
+// and so lets others need, what that one wrote.
+__device__ __forceinline__ void kernel_may_follow() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_kernel_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class... Params, class... Args>
+inline kda_status launch_following(void (*kernel)(Params...), dim3 grid, dim3 block, int smem,
+                                   cudaStream_t s, Args... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace kda_cache

@@ -18,6 +18,14 @@
 // warp's own -- eight lanes fetch a whole 128-byte row; in a first form, whose
 // lanes fetched what they use themselves, L2 sent every byte twice -- with the
 // chunks permuted so that neither side meets bank conflicts.
+//
+// An int8 code enters a product as the f16 subnormal u 2^-24, u = c + 128 its
+// byte with the top bit flipped: two logic operations for four codes and no
+// arithmetic.  Q K^T is then 2^-24 (Q C^T + 128 sum_d Q), V^T P^T the same with
+// the sum of the weights, which one more product with ones gives; both are
+// taken out in fp32 (a bias of the codes' own size costs no accuracy).
+#include <type_traits>
+
 #include "kda_cache_attn.cuh"
 
 namespace {
@@ -43,6 +51,23 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+
+// Codes as factors of the products.  int8: two pairs (0, 2), (1, 3) of a word;
+// e4m3: pairs (0, 1), (2, 3).
+template <int CODE>
+__device__ __forceinline__ void factors(uint32_t w, uint32_t& a, uint32_t& b) {
+  if (CODE == KDA_I8) {
+    a = (w ^ 0x00800080u) & 0x00ff00ffu;
+    b = ((w >> 8) ^ 0x00800080u) & 0x00ff00ffu;
+  } else {
+    codes_to_half<CODE>(w, a, b);
+  }
+}
+// (of int8) what a factor must be multiplied by, and the bias of a code
+template <int CODE>
+__device__ __forceinline__ constexpr float unit_of() { return CODE == KDA_I8 ? 0x1p24f : 1.0f; }
+template <int CODE>
+__device__ __forceinline__ constexpr float bias_of() { return CODE == KDA_I8 ? 128.0f : 0.0f; }
 
 // Byte offsets of 16-byte chunk c of token t in a block's keys and values.  A
 // quarter of a warp reads the chunks of two tokens of keys, and two chunks of
@@ -95,11 +120,12 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
     if ((int64_t)q.n * G > kFewRows) return 0;
     return max(1, (int)(((int64_t)q.kv + C::kUnit - 1) / C::kUnit));
   };
+  kernel_may_follow();
   Share sh = find_share<kThreads>(p, [&](const Req& q) { return blocks_of(q) * p.Hkv; });
   int r = sh.r;
   int64_t base = sh.base, u = sh.u0;
 
-  if (tid == 0) p.part_head[blockIdx.x].rows = 0;
+  if (tid == 0) p.parts.head[blockIdx.x].rows = 0;
   while (u < sh.u1) {
     bool bad;
     const Req rq = load_req(p, r, bad);
@@ -115,11 +141,12 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
     const int b1 = (int)(min(sh.u1, seg0 + nb) - seg0);
     const bool whole = b0 == 0 && b1 == nb;
     const int rows = rq.n * G, kv = rq.kv;
-    if (tid == 0 && b0 > 0) p.part_head[blockIdx.x] = {seg0, seg0 + nb, rq.c0, rows, h, 0};
+    if (tid == 0 && b0 > 0) p.parts.head[blockIdx.x] = {seg0, seg0 + nb, rq.c0, rows, h, 0};
 
     // queries, in the k order of the keys' chunks; each row scaled to f16
     uint32_t qf[NT][KS][2];
     float qs[NT][2];   // factors of this lane's two columns
+    float qb[NT][2];   // and their bias: bias_of times the sum of the query row
     int lim[NT][2];    // tokens that they see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -143,39 +170,55 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
       most = max(most, __shfl_xor_sync(~0u, most, 1));
       most = max(most, __shfl_xor_sync(~0u, most, 2));
       const int ex = row_exponent(most);
-      const float down = exp2i(min(-ex, 127));
+      const float down = exp2i(-ex);
+      float sum = 0.0f;
 #pragma unroll
       for (int c = 0; c < 2 * KC; ++c) {
         const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-        uint32_t f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          f[e] = pack_half(__uint_as_float(w[e] << 16) * down,
-                           __uint_as_float(w[e] & 0xffff0000u) * down);
-        // channels 8 (c & 1) .. + 7 of the lane's chunk c / 2: two k-steps
+        // channels 8 (c & 1) .. + 7 of the lane's chunk c / 2: two k-steps, in
+        // the order of factors()
         const int s0 = 4 * (c >> 1) + 2 * (c & 1);
-        qf[nt][s0][0] = f[0];
-        qf[nt][s0][1] = f[1];
-        qf[nt][s0 + 1][0] = f[2];
-        qf[nt][s0 + 1][1] = f[3];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float y[4] = {__uint_as_float(w[2 * e] << 16) * down,
+                              __uint_as_float(w[2 * e] & 0xffff0000u) * down,
+                              __uint_as_float(w[2 * e + 1] << 16) * down,
+                              __uint_as_float(w[2 * e + 1] & 0xffff0000u) * down};
+          constexpr int B = CODE == KDA_I8 ? 2 : 1, A = CODE == KDA_I8 ? 1 : 2;
+          qf[nt][s0 + e][0] = pack_half(y[0], y[B]);
+          qf[nt][s0 + e][1] = pack_half(y[A], y[3]);
+          if (CODE == KDA_I8) {  // of what the products will see
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 z = __half22float2(*reinterpret_cast<__half2*>(&qf[nt][s0 + e][i]));
+              sum += z.x + z.y;
+            }
+          }
+        }
       }
-      const float up = exp2i(ex);
+      const float up = exp2i(ex) * unit_of<CODE>();
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+      sum *= -bias_of<CODE>() / unit_of<CODE>();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int col = 8 * nt + 2 * j + c;
         qs[nt][c] = __shfl_sync(~0u, up, (2 * j + c) * 4);
+        qb[nt][c] = __shfl_sync(~0u, sum, (2 * j + c) * 4);
         lim[nt][c] = col < rows ? kv - rq.n + col / G + 1 : 0;
       }
     }
     const int all_see = kv - rq.n + 1;  // tokens that every row sees
     const float sm = p.scale * 1.4426950408889634f / code_top(CODE);
 
-    float o[NT][KS][4], m[NT][2], l[NT][2];
+    // (int8: o[.][KS] is the sum of the weights as the products see them)
+    constexpr int KO = CODE == KDA_I8 ? KS + 1 : KS;
+    float o[NT][KO][4], m[NT][2], l[NT][2];
     float vref = 0.0f, vinv = 1.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+      for (int s = 0; s < KO; ++s)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.0f;
 #pragma unroll
@@ -203,18 +246,18 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
 
     // block x of this warp -> its place in the ring (all lanes); in_batch
     // counts from the current batch's start
+    const uint32_t page_bytes = (uint32_t)(p.Hkv << lg) * D;
     constexpr int ROWL = D / 16;         // lanes a row
     constexpr int ROWS_I = 32 / ROWL;    // rows an instruction
     const int rl = lane / ROWL, cl = lane % ROWL;
     auto issue = [&](int i, int in_batch, int slot) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int pa = __shfl_sync(~0u, pg_cur, (in_batch + b) & 31);
-        const int pb = __shfl_sync(~0u, pg_next, (in_batch + b) & 31);
+        const int pg =
+            __shfl_sync(~0u, in_batch + b < 32 ? pg_cur : pg_next, (in_batch + b) & 31);
         if (has(i * NB + b)) {
-          const int pg = in_batch + b < 32 ? pa : pb;
           const int t0 = token_of(i * NB + b) & (P - 1);
-          const int64_t at = ((((int64_t)pg * p.Hkv + h) << lg) + t0) * D;
+          const uint64_t at = (uint64_t)(uint32_t)pg * page_bytes + (uint32_t)((h << lg) + t0) * D;
           const uint32_t dst = ring_u + slot * C::kStage + b * C::kBlockBytes;
           const uint8_t* k = p.k_codes + at + lane * 16;
           const uint8_t* v = p.v_codes + at + lane * 16;
@@ -268,147 +311,163 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
         vmax = fmaxf(vmax, vs[NB - 1]);
       }
 
-      // S^T = K Q^T
-      float x[NB][NT][4];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const unsigned char* sk = st + b * C::kBlockBytes;
-          const uint4 ka = *reinterpret_cast<const uint4*>(sk + key_at<D>(i8, 4 * c + j));
-          const uint4 kb = *reinterpret_cast<const uint4*>(sk + key_at<D>(i8 + 8, 4 * c + j));
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            uint32_t a0, a1, a2, a3;
-            codes_to_half<CODE>(wa[s], a0, a2);
-            codes_to_half<CODE>(wb[s], a1, a3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(x[b][nt], a0, a1, a2, a3, qf[nt][4 * c + s][0], qf[nt][4 * c + s][1]);
-          }
-        }
-        if (edge) {  // tokens i8 and i8 + 8, columns 2 j and 2 j + 1
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) x[b][nt][e] = NAN;
-        }
-      }
-      // Weights with the standing reference m of each row, which need not be
-      // the maximum: it is sought, with shuffles, only in the first run, when
-      // weights sum to more than 2^15 (f16 ends at 65504), or when a page's
-      // value scale passes vref.  Most runs need one vote.  (A masked score is
-      // a NaN until here, a masked weight 0.)
-      float w[NB][NT][4], lt[NT][2];
-      bool fresh = i == 0 || vmax > vref;
-      for (;;) {
-        if (fresh) {
-          const float vnew = vmax > vref ? pow2_above(vmax) : vref;
-          const float fv = vnew > 0.0f ? vref / vnew : 1.0f;
-          vref = vnew;
-          vinv = vnew > 0.0f ? 1.0f / vnew : 1.0f;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float f[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float mx = -INFINITY;  // (fmaxf passes over NaN)
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-                mx = fmaxf(mx, fmaxf(x[b][nt][c] * (kf[b] * qs[nt][c]),
-                                     x[b][nt][c + 2] * (kf[b] * qs[nt][c])));
-              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-              // (a row that sees nothing in the first run sees nothing at all)
-              const float mn = i == 0 ? (mx == -INFINITY ? 0.0f : mx) : fmaxf(m[nt][c], mx);
-              f[c] = i == 0 ? 0.0f : ex2(m[nt][c] - mn);
-              m[nt][c] = mn;
-              l[nt][c] *= f[c];
-              f[c] *= fv;
-            }
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[nt][s][e] *= f[e & 1];
-          }
-        }
-        bool over = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          lt[nt][0] = lt[nt][1] = 0.0f;
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[b][nt][e] = ex2(fmaf(x[b][nt][e], kf[b] * qs[nt][e & 1], -m[nt][e & 1]));
-              if (edge && tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) w[b][nt][e] = 0.0f;
-              lt[nt][e & 1] += w[b][nt][e];
-            }
-          // (columns without a row see no token; a NaN counts as over)
-          over |= !(lt[nt][0] <= 32768.0f && lt[nt][1] <= 32768.0f);
-        }
-        if (fresh || !__any_sync(~0u, over)) break;
-        fresh = true;
-      }
-      uint32_t pb[NB][NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        l[nt][0] += lt[nt][0];
-        l[nt][1] += lt[nt][1];
+      // (the tests of single tokens only where a run has tokens to hide)
+      auto take = [&](auto at_edge) {
+        constexpr bool EDGE = decltype(at_edge)::value;
+        // S^T = K Q^T
+        float x[NB][NT][4];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float vw = vs[b] * vinv;
-          float y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[e] = w[b][nt][e] * vw;
-            // (0 times a scale that may be NaN)
-            if (edge && tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) y[e] = 0.0f;
-          }
-          pb[b][nt][0] = transpose8x8(pack_half(y[0], y[1]));
-          pb[b][nt][1] = transpose8x8(pack_half(y[2], y[3]));
-        }
-      }
-      // O^T += V^T P^T; lane's tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t v[4][VB / 4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const unsigned char* at = st + b * C::kBlockBytes + 16 * D +
-                                    value_at<D>(2 * j + (e & 1) + 8 * (e >> 1), i8 * VB / 16) +
-                                    (i8 * VB) % 16;
-          if (VB == 16) {
-            const uint4 y = *reinterpret_cast<const uint4*>(at);
-            v[e][0] = y.x; v[e][1] = y.y; v[e][VB / 4 - 2] = y.z; v[e][VB / 4 - 1] = y.w;
-          } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(at);
-            v[e][0] = y.x; v[e][1] = y.y;
-          }
-          // what lies past the request's end may be a NaN
-          if (CODE == KDA_E4M3 && edge && tok + 16 * b + 2 * j + (e & 1) + 8 * (e >> 1) >= kv) {
-#pragma unroll
-            for (int w = 0; w < VB / 4; ++w) v[e][w] = 0;
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const uint32_t sel = (s & 1) ? 0x7362 : 0x5140;
-          uint32_t a0, a1, a2, a3;
-          codes_to_half<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
-          codes_to_half<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma16816(o[nt][s], a0, a1, a2, a3, pb[b][nt][0], pb[b][nt][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[b][nt][e] = qb[nt][e & 1];
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            const unsigned char* sk = st + b * C::kBlockBytes;
+            const uint4 ka = *reinterpret_cast<const uint4*>(sk + key_at<D>(i8, 4 * c + j));
+            const uint4 kb = *reinterpret_cast<const uint4*>(sk + key_at<D>(i8 + 8, 4 * c + j));
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              uint32_t a0, a1, a2, a3;
+              factors<CODE>(wa[s], a0, a2);
+              factors<CODE>(wb[s], a1, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(x[b][nt], a0, a1, a2, a3, qf[nt][4 * c + s][0], qf[nt][4 * c + s][1]);
+            }
+          }
+          if (EDGE) {  // tokens i8 and i8 + 8, columns 2 j and 2 j + 1
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) x[b][nt][e] = NAN;
+          }
         }
-      }
+        // Weights with the standing reference m of each row, which need not be
+        // the maximum: it is sought, with shuffles, only in the first run, when
+        // weights sum to more than 2^15 (f16 ends at 65504), or when a page's
+        // value scale passes vref.  Most runs need one vote.  (A masked score is
+        // a NaN until here, a masked weight 0.)
+        float w[NB][NT][4], lt[NT][2];
+        bool fresh = i == 0 || vmax > vref;
+        for (;;) {
+          if (fresh) {
+            const float vnew = vmax > vref ? pow2_above(vmax) : vref;
+            const float fv = vnew > 0.0f ? vref / vnew : 1.0f;
+            vref = vnew;
+            vinv = vnew > 0.0f ? 1.0f / vnew : 1.0f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float f[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float mx = -INFINITY;  // (fmaxf passes over NaN)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                  mx = fmaxf(mx, fmaxf(x[b][nt][c] * (kf[b] * qs[nt][c]),
+                                       x[b][nt][c + 2] * (kf[b] * qs[nt][c])));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+                // (a row that sees nothing in the first run sees nothing at all)
+                const float mn = i == 0 ? (mx == -INFINITY ? 0.0f : mx) : fmaxf(m[nt][c], mx);
+                f[c] = i == 0 ? 0.0f : ex2(m[nt][c] - mn);
+                m[nt][c] = mn;
+                l[nt][c] *= f[c];
+                f[c] *= fv;
+              }
+#pragma unroll
+              for (int s = 0; s < KO; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][s][e] *= f[e & 1];
+            }
+          }
+          bool over = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            lt[nt][0] = lt[nt][1] = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                w[b][nt][e] = ex2(fmaf(x[b][nt][e], kf[b] * qs[nt][e & 1], -m[nt][e & 1]));
+                if (EDGE && tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) w[b][nt][e] = 0.0f;
+                lt[nt][e & 1] += w[b][nt][e];
+              }
+            // (columns without a row see no token; a NaN counts as over)
+            over |= !(lt[nt][0] <= 32768.0f && lt[nt][1] <= 32768.0f);
+          }
+          if (fresh || !__any_sync(~0u, over)) break;
+          fresh = true;
+        }
+        uint32_t pb[NB][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          l[nt][0] += lt[nt][0];
+          l[nt][1] += lt[nt][1];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const float vw = vs[b] * vinv;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[e] = w[b][nt][e] * vw;
+              // (0 times a scale that may be NaN)
+              if (EDGE && tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) y[e] = 0.0f;
+            }
+            pb[b][nt][0] = transpose8x8(pack_half(y[0], y[1]));
+            pb[b][nt][1] = transpose8x8(pack_half(y[2], y[3]));
+          }
+        }
+        // O^T += V^T P^T; lane's tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t v[4][VB / 4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const unsigned char* at = st + b * C::kBlockBytes + 16 * D +
+                                      value_at<D>(2 * j + (e & 1) + 8 * (e >> 1), i8 * VB / 16) +
+                                      (i8 * VB) % 16;
+            if (VB == 16) {
+              const uint4 y = *reinterpret_cast<const uint4*>(at);
+              v[e][0] = y.x; v[e][1] = y.y; v[e][VB / 4 - 2] = y.z; v[e][VB / 4 - 1] = y.w;
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(at);
+              v[e][0] = y.x; v[e][1] = y.y;
+            }
+            // what lies past the request's end may be a NaN
+            if (CODE == KDA_E4M3 && EDGE && tok + 16 * b + 2 * j + (e & 1) + 8 * (e >> 1) >= kv) {
+#pragma unroll
+              for (int w = 0; w < VB / 4; ++w) v[e][w] = 0;
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            // channels 2 s and 2 s + 1 of two tokens, in the order of factors()
+            const uint32_t sel = CODE == KDA_I8 ? ((s & 1) ? 0x7632 : 0x5410)
+                                                : ((s & 1) ? 0x7362 : 0x5140);
+            uint32_t a0, a1, a2, a3;
+            factors<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
+            factors<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(o[nt][s], a0, a1, a2, a3, pb[b][nt][0], pb[b][nt][1]);
+          }
+          if (CODE == KDA_I8) {
+            const uint32_t ones = 0x3c003c00u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(o[nt][KO - 1], ones, ones, ones, ones, pb[b][nt][0], pb[b][nt][1]);
+          }
+        }
+      };
+      if (edge)
+        take(std::true_type{});
+      else
+        take(std::false_type{});
     }
     copy_wait<0>();
     __syncwarp();
@@ -420,6 +479,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        const float ob =
+            CODE == KDA_I8 ? o[nt][KO - 1][c] * (bias_of<CODE>() / unit_of<CODE>()) : 0.0f;
         float y = l[nt][c];
         y += __shfl_xor_sync(~0u, y, 4);
         y += __shfl_xor_sync(~0u, y, 8);
@@ -432,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
 #pragma unroll
         for (int s = 0; s < KS; ++s)
           *reinterpret_cast<float2*>(so + row * D + i8 * VB + 2 * s) =
-              make_float2(o[nt][s][c] * ov, o[nt][s][c + 2] * ov);
+              make_float2((o[nt][s][c] - ob) * unit_of<CODE>() * ov,
+                          (o[nt][s][c + 2] - ob) * unit_of<CODE>() * ov);
       }
     }
     __syncthreads();
@@ -457,10 +519,10 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
         if (p.lse && ch == 0)
           p.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
       } else {
-        p.part_o[(part * kFewRows + row) * D + ch] = acc;
+        p.parts.o[(part * kFewRows + row) * D + ch] = acc;
         if (ch == 0) {
-          p.part_ml[(part * kFewRows + row) * 2] = mx;
-          p.part_ml[(part * kFewRows + row) * 2 + 1] = sum;
+          p.parts.ml[(part * kFewRows + row) * 2] = mx;
+          p.parts.ml[(part * kFewRows + row) * 2 + 1] = sum;
         }
       }
     }
@@ -470,105 +532,115 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
 }
 
 // Joins the parts of the segments that cross CTA boundaries, in CTA order:
-// out = sum_c w_c O_c / sum_c w_c l_c with w_c = 2^(m_c - max m).  Block (c, y)
-// looks at the boundary between CTAs c and c + 1 and works if it is the first
-// inside its segment; WPR warps share a row and take its parts in turn.
-template <int D, int WPR>
-__global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, int ctas, int part_rows) {
+// out = sum_c w_c O_c / sum_c w_c l_c with w_c = 2^(m_c - max m).  A block looks
+// at the boundary between CTAs c and c + 1 of a kernel and works if it is the
+// first inside its segment, on up to 4 rows of the few-row kernel (a long cache
+// leaves as many parts as there are CTAs) or 32 of the tile kernel (two or
+// three parts).  Where the rows are fewer than its 8 warps, several warps
+// share a row's parts.
+template <int D>
+__global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, Parts rows_kernel,
+                                                            Parts tile_kernel,
+                                                            int few_blocks) {
   constexpr int E = D / 32;
-  constexpr int NR = 8 / WPR;  // rows of a block
   __shared__ float s_o[8][D], s_l[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const PartHead ph = p.part_head[blockIdx.x + 1];
-  if ((int)blockIdx.y * NR >= ph.rows) return;
-  const int64_t share = (*p.total + ctas - 1) / ctas;
+  const bool few = (int)blockIdx.x < few_blocks;
+  const Parts q = few ? rows_kernel : tile_kernel;
+  const int of = few ? blockIdx.x : (int)blockIdx.x - few_blocks, group = few ? 4 : 32;
+  const int c0 = of % (q.ctas - 1), row0 = group * (of / (q.ctas - 1));
+  wait_for_kernel_before();
+  const PartHead ph = q.head[c0 + 1];
+  const int n = min(ph.rows - row0, group);
+  if (n <= 0) return;
+  const int64_t share = (*q.total + q.ctas - 1) / q.ctas;
   const int ca = (int)(ph.seg0 / share), cb = (int)((ph.seg1 - 1) / share);
-  if (ca != (int)blockIdx.x) return;
-  const int row = blockIdx.y * NR + warp / WPR, sub = warp % WPR;
-  const bool live = row < ph.rows;
-  // the first CTA holds it as its last segment, the others as their first
-  auto part = [&](int c) -> int64_t {
-    return (2 * (int64_t)c + (c == ca ? 1 : 0)) * part_rows + row;
-  };
-  float mx = -INFINITY, acc[E] = {}, sum = 0.0f;
-  if (live) {
-    for (int c = ca + lane; c <= cb; c += 32) mx = fmaxf(mx, p.part_ml[part(c) * 2]);
+  if (ca != c0) return;
+  const int wpr = n > 4 ? 1 : n > 2 ? 2 : n > 1 ? 4 : 8;  // warps a row
+  const int sub = warp % wpr;
+  for (int i = warp / wpr; i < n; i += 8 / wpr) {
+    const int row = row0 + i;
+    // the first CTA holds it as its last segment, the others as their first
+    auto part = [&](int c) -> int64_t { return (2 * (int64_t)c + (c == ca ? 1 : 0)) * q.rows + row; };
+    float mx = -INFINITY, acc[E] = {}, sum = 0.0f;
+    for (int c = ca + lane; c <= cb; c += 32) mx = fmaxf(mx, q.ml[part(c) * 2]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
     const float mm = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll 4
-    for (int c = ca + sub; c <= cb; c += WPR) {
+#pragma unroll 8
+    for (int c = ca + sub; c <= cb; c += wpr) {
       const int64_t at = part(c);
-      const float f = ex2(p.part_ml[at * 2] - mm);
-      sum += f * p.part_ml[at * 2 + 1];
+      const float2 ml = *reinterpret_cast<const float2*>(q.ml + at * 2);
+      const float f = ex2(ml.x - mm);
+      sum += f * ml.y;
+      float v[E];
+      if constexpr (E == 4)
+        *reinterpret_cast<float4*>(v) = reinterpret_cast<const float4*>(q.o + at * D)[lane];
+      else
+        *reinterpret_cast<float2*>(v) = reinterpret_cast<const float2*>(q.o + at * D)[lane];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += f * p.part_o[at * D + e * 32 + lane];
+      for (int e = 0; e < E; ++e) acc[e] += f * v[e];
     }
-  }
-  if (WPR > 1) {
+    if (wpr > 1) {  // (then each warp has one row at most)
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = acc[e];
-    if (lane == 0) s_l[warp] = sum;
-    __syncthreads();
-    if (sub == 0) {
-#pragma unroll
-      for (int w = 1; w < WPR; ++w) {
+      for (int e = 0; e < E; ++e) s_o[warp][E * lane + e] = acc[e];
+      if (lane == 0) s_l[warp] = sum;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpr), "r"(32 * wpr) : "memory");
+      if (sub) break;
+      for (int w = 1; w < wpr; ++w) {
         sum += s_l[warp + w];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += s_o[warp + w][e * 32 + lane];
+        for (int e = 0; e < E; ++e) acc[e] += s_o[warp + w][E * lane + e];
       }
     }
-  }
-  if (live && sub == 0) {
     const int64_t at = (int64_t)(ph.tok0 + row / p.G) * p.Hq + ph.h * p.G + row % p.G;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint32_t y[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + e * 32 + lane] =
-          __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[e] / sum);
+    for (int e = 0; e < E; e += 2) {
+      const __nv_bfloat162 z = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+      y[e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+    }
+    if constexpr (E == 4)
+      reinterpret_cast<uint2*>(p.out + at * D)[lane] = make_uint2(y[0], y[1]);
+    else
+      reinterpret_cast<uint32_t*>(p.out + at * D)[lane] = y[0];
     if (p.lse && lane == 0)
       p.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
 template <int CODE, int D, int NT>
-kda_status launch_rows(const AttnArgs& p, int ctas, cudaStream_t s) {
+kda_status launch_rows(const AttnArgs& p, cudaStream_t s) {
   auto kernel = kda_cache_attn_rows_kernel<CODE, D, NT>;
   const int smem = kWarps * Cfg<D, NT>::kWarpBytes;
   const kda_status rc = kda_smem_attr((const void*)kernel, smem);
   if (rc != KDA_OK) return rc;
-  kernel<<<ctas, kThreads, smem, s>>>(p);
+  kernel<<<p.parts.ctas, kThreads, smem, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 template <int CODE, int D>
-kda_status launch_nt(const AttnArgs& p, int ctas, cudaStream_t s) {
+kda_status launch_nt(const AttnArgs& p, cudaStream_t s) {
   // one 8-row tile where no request can have more rows than that
-  if ((int64_t)p.max_new * p.G <= 8) return launch_rows<CODE, D, 1>(p, ctas, s);
-  return launch_rows<CODE, D, 2>(p, ctas, s);
+  if ((int64_t)p.max_new * p.G <= 8) return launch_rows<CODE, D, 1>(p, s);
+  return launch_rows<CODE, D, 2>(p, s);
 }
 
 }  // namespace
 
-kda_status kda_launch_attn_rows(const AttnArgs& p, int d, int code, int ctas, cudaStream_t s) {
-  if (code == KDA_I8)
-    return d == 64 ? launch_nt<KDA_I8, 64>(p, ctas, s) : launch_nt<KDA_I8, 128>(p, ctas, s);
-  return d == 64 ? launch_nt<KDA_E4M3, 64>(p, ctas, s) : launch_nt<KDA_E4M3, 128>(p, ctas, s);
+kda_status kda_launch_attn_rows(const AttnArgs& p, int d, int code, cudaStream_t s) {
+  if (code == KDA_I8) return d == 64 ? launch_nt<KDA_I8, 64>(p, s) : launch_nt<KDA_I8, 128>(p, s);
+  return d == 64 ? launch_nt<KDA_E4M3, 64>(p, s) : launch_nt<KDA_E4M3, 128>(p, s);
 }
 
-kda_status kda_launch_attn_join(const AttnArgs& p, int d, int part_rows, int ctas,
-                                cudaStream_t s) {
-  if (ctas < 2) return KDA_OK;
+kda_status kda_launch_attn_join(const AttnArgs& p, const Parts& tile, int d, cudaStream_t s) {
   const int64_t most = (int64_t)p.max_new * p.G;
-  const int rows = (int)(most < part_rows ? most : part_rows);
-  if (part_rows == kFewRows) {
-    // few rows, up to as many parts as CTAs
-    const dim3 grid(ctas - 1, rows);
-    if (d == 64) kda_attn_join_kernel<64, 8><<<grid, 256, 0, s>>>(p, ctas, part_rows);
-    else kda_attn_join_kernel<128, 8><<<grid, 256, 0, s>>>(p, ctas, part_rows);
-  } else {
-    const dim3 grid(ctas - 1, (rows + 7) / 8);
-    if (d == 64) kda_attn_join_kernel<64, 1><<<grid, 256, 0, s>>>(p, ctas, part_rows);
-    else kda_attn_join_kernel<128, 1><<<grid, 256, 0, s>>>(p, ctas, part_rows);
-  }
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  const int few_rows = most < kFewRows ? (int)most : kFewRows;
+  const int tile_rows = most < kTileRows ? (int)most : kTileRows;
+  const int few_blocks = (p.parts.ctas - 1) * ((few_rows + 3) / 4);
+  const int tile_blocks = tile.ctas > 1 ? (tile.ctas - 1) * ((tile_rows + 31) / 32) : 0;
+  if (few_blocks + tile_blocks == 0) return KDA_OK;
+  return launch_following(d == 64 ? kda_attn_join_kernel<64> : kda_attn_join_kernel<128>,
+                          few_blocks + tile_blocks, 256, 0, s, p, p.parts, tile, few_blocks);
 }

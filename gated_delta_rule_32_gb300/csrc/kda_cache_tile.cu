@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     sm100::fence_mbar_init();
   }
   sm100::tc_fence_before();
+  kernel_may_follow();
   const Share share = find_share<kThreads>(p, [&](const Req& q) {
     const Tiles t(q, p.G);
     return t.count ? t.before(t.count) * p.Hkv : 0;
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       unsigned char* dst_row = whole
                                    ? reinterpret_cast<unsigned char*>(p.out + at * D)
                                    : reinterpret_cast<unsigned char*>(
-                                         p.part_o + (slot * kTileRows + row) * D);
+                                         p.parts.o + (slot * kTileRows + row) * D);
       const uint64_t dst_u = mine ? reinterpret_cast<uint64_t>(dst_row) : 0;
       uint64_t dst[4];
 #pragma unroll
@@ -653,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       sm100::tc_fence_before();
       if (mine) {
         if (!whole) {
-          p.part_ml[(slot * kTileRows + row) * 2] = l == 0.0f ? -INFINITY : m;
-          p.part_ml[(slot * kTileRows + row) * 2 + 1] = l;
+          p.parts.ml[(slot * kTileRows + row) * 2] = l == 0.0f ? -INFINITY : m;
+          p.parts.ml[(slot * kTileRows + row) * 2 + 1] = l;
         } else if (p.lse) {
           p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         if (w.live() && w.b0 > 0)
           ph = {w.seg0 + kLead, w.seg0 + kLead + w.nu, w.q.c0 + w.tile * w.t.tt,
                 w.tokens() * p.G, w.h, 0};
-        p.part_head[blockIdx.x] = ph;
+        p.parts.head[blockIdx.x] = ph;
       }
       uint32_t tiles = 0;
       bool ok = true;
@@ -954,22 +955,22 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   sm100::tc_fence_before();
   __syncthreads();
   if (tid == 0 && s_abort) report(p.status, KDA_ERR_TIMEOUT);
+  wait_for_kernel_before();  // (this one needs nothing of it, what follows may)
   if (warp == 16) sm100::tmem_dealloc(s_tmem, 512);
 }
 
 template <int CODE, int D>
-kda_status launch_tile(const AttnArgs& p, int ctas, cudaStream_t s) {
+kda_status launch_tile(const AttnArgs& p, cudaStream_t s) {
   auto kernel = kda_cache_attn_tile_kernel<CODE, D>;
   const kda_status rc = kda_smem_attr((const void*)kernel, Smem<D>::kBytes);
   if (rc != KDA_OK) return rc;
-  kernel<<<ctas, kThreads, Smem<D>::kBytes, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  return launch_following(kernel, p.parts.ctas, kThreads, Smem<D>::kBytes, s, p);
 }
 
 }  // namespace
 
-kda_status kda_launch_attn_tile(const AttnArgs& p, int d, int code, int ctas, cudaStream_t s) {
+kda_status kda_launch_attn_tile(const AttnArgs& p, int d, int code, cudaStream_t s) {
   if (code == KDA_I8)
-    return d == 64 ? launch_tile<KDA_I8, 64>(p, ctas, s) : launch_tile<KDA_I8, 128>(p, ctas, s);
-  return d == 64 ? launch_tile<KDA_E4M3, 64>(p, ctas, s) : launch_tile<KDA_E4M3, 128>(p, ctas, s);
+    return d == 64 ? launch_tile<KDA_I8, 64>(p, s) : launch_tile<KDA_I8, 128>(p, s);
+  return d == 64 ? launch_tile<KDA_E4M3, 64>(p, s) : launch_tile<KDA_E4M3, 128>(p, s);
 }

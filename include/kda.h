@@ -413,7 +413,7 @@ kda_status kda_debug_record_capacity(int64_t items);
  *   k_scale, v_scale   [num_pages, Hkv]           fp32
  * scale is the largest magnitude that the page and head hold; a code c
  * stands for c * scale / 127 (KDA_I8, c in -127..127) or c * scale / 448
- * (KDA_E4M3, c the e4m3 value).  d is 64 or 128; Hkv >= 1.
+ * (KDA_E4M3, c the e4m3 value).  d is 64 or 128; Hkv in 1..4096.
  *
  * A batch of R requests is described by device int32 arrays: request r has
  * kv_lens[r] tokens in the cache, the last cu_seqlens[r + 1] -
