@@ -231,6 +231,63 @@ struct AppendArgs {
 
 constexpr int kAppendThreads = 128;
 
+// Codes of 8 bf16 values (as 4 words): rn(x * pre * TOP / den), exactly.  The
+// quotient is bracketed: t = x * (TOP / den) is within 2^-23 of it (two
+// roundings), so it lies between t (1 - 2^-22) and t (1 + 2^-22); rounding to a
+// code is monotonic, and where both ends give the same code that is the one.
+// Where they differ (a tie or next to one) the fp32 division decides, which is
+// exact enough: x * TOP has at most 15 bits, den 8, so no quotient comes
+// within half an ulp of a tie without being one.
+template <int CODE>
+__device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float pre, float inv, float den) {
+  constexpr float TOP = code_top(CODE);
+  float lo[8], hi[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float f = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    const float t = f * inv;
+    lo[e] = t * (1.0f - 0x1p-22f);
+    hi[e] = t * (1.0f + 0x1p-22f);
+  }
+  uint32_t a[2], b[2];
+  if (CODE == KDA_I8) {
+    // (adding 1.5 * 2^23 rounds to an integer, ties to even, in the low bits)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __float_as_uint(lo[4 * i + e] + 12582912.0f);
+        y[e] = __float_as_uint(hi[4 * i + e] + 12582912.0f);
+      }
+      a[i] = __byte_perm(__byte_perm(x[0], x[1], 0x0040), __byte_perm(x[2], x[3], 0x0040), 0x5410);
+      b[i] = __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t x[2], y[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int at = 4 * i + 2 * e;
+        x[e] = __nv_cvt_float2_to_fp8x2(make_float2(lo[at], lo[at + 1]), __NV_SATFINITE, __NV_E4M3);
+        y[e] = __nv_cvt_float2_to_fp8x2(make_float2(hi[at], hi[at + 1]), __NV_SATFINITE, __NV_E4M3);
+      }
+      a[i] = x[0] | x[1] << 16;
+      b[i] = y[0] | y[1] << 16;
+    }
+  }
+  if (a[0] != b[0] || a[1] != b[1] || pre != 1.0f) {  // (inv is only right for pre = 1)
+    a[0] = a[1] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float f = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+      a[e >> 2] |= encode1<CODE>(__fdiv_rn((f * pre) * TOP, den)) << (8 * (e & 3));
+    }
+  }
+  return make_uint2(a[0], a[1]);
+}
+
 // One CTA per (run, head, tensor).  The run's values are read once, into
 // registers (at most page * d = 128 per thread), their largest magnitude is
 // found by an unsigned maximum of the bit patterns without the sign (which
@@ -288,6 +345,7 @@ __global__ void __launch_bounds__(kAppendThreads) kda_cache_append_kernel(Append
   // normal; it changes no quotient
   const float pre = now >= 0x5f800000u ? 0x1p-64f : now < 0x1f800000u ? 0x1p64f : 1.0f;
   const float den = a1 * pre;
+  const float inv = TOP / den;
   if (now != had && had != 0 && !poisoned) {
     for (int t = t0; t < off; t += RPP) {
       uint2 c = *reinterpret_cast<uint2*>(codes + t * D);
@@ -305,15 +363,9 @@ __global__ void __launch_bounds__(kAppendThreads) kda_cache_append_kernel(Append
     const int t = t0 + i * RPP;
     if (t >= count) break;
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint32_t r[2] = {0, 0};
-    if (now != 0 && !poisoned) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-        r[e >> 2] |= encode1<CODE>(__fdiv_rn((f * pre) * TOP, den)) << (8 * (e & 3));
-      }
-    }
-    *reinterpret_cast<uint2*>(codes + (int64_t)(off + t) * D) = make_uint2(r[0], r[1]);
+    uint2 r = make_uint2(0, 0);
+    if (now != 0 && !poisoned) r = encode8<CODE>(w, pre, inv, den);
+    *reinterpret_cast<uint2*>(codes + (int64_t)(off + t) * D) = r;
   }
 }
 
