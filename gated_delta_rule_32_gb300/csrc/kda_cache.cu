@@ -229,23 +229,29 @@ struct AppendArgs {
   int T, num_pages, H;
 };
 
-constexpr int kAppendThreads = 128;
+// Threads: kAppendPasses 16-byte pieces each where the page has so many.
+constexpr int kAppendPasses = 8;
+__host__ __device__ constexpr int append_threads(int page, int d) {
+  const int n = page * d / 8 / kAppendPasses;
+  return n < 64 ? 64 : n > 512 ? 512 : n;
+}
 
-// Codes of 8 bf16 values (as 4 words): rn(x * pre * TOP / den), exactly.  The
-// quotient is bracketed: t = x * (TOP / den) is within 2^-23 of it (two
-// roundings), so it lies between t (1 - 2^-22) and t (1 + 2^-22); rounding to a
-// code is monotonic, and where both ends give the same code that is the one.
-// Where they differ (a tie or next to one) the fp32 division decides, which is
-// exact enough: x * TOP has at most 15 bits, den 8, so no quotient comes
-// within half an ulp of a tie without being one.
+// Codes of 8 bf16 values (as 4 words): rn(x TOP / a), exactly and without a
+// division; inv = TOP / (a pre).  t = (x pre) inv is within 2^-23 of the
+// quotient (two roundings), which so lies between t (1 - 2^-22) and
+// t (1 + 2^-22); rounding to a code is monotonic, and where both ends give the
+// same code that is the one.  Where they differ the quotient is a tie, and the
+// even code is taken: x and a have 8 significant bits, so a quotient that is
+// no tie keeps a relative distance of 2^-16 (int8: |127 X 2^k - (2 n + 1) A| is
+// a whole multiple of the smaller unit, against at most 2 A 127) or 2^-13
+// (e4m3: the same with 7 X and M A, M at most 31) from every tie.
 template <int CODE>
-__device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float pre, float inv, float den) {
-  constexpr float TOP = code_top(CODE);
+__device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float pre, float inv) {
   float lo[8], hi[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float f = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-    const float t = f * inv;
+    const float t = f * pre * inv;
     lo[e] = t * (1.0f - 0x1p-22f);
     hi[e] = t * (1.0f + 0x1p-22f);
   }
@@ -277,13 +283,10 @@ __device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float pre, floa
       b[i] = y[0] | y[1] << 16;
     }
   }
-  if (a[0] != b[0] || a[1] != b[1] || pre != 1.0f) {  // (inv is only right for pre = 1)
-    a[0] = a[1] = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float f = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-      a[e >> 2] |= encode1<CODE>(__fdiv_rn((f * pre) * TOP, den)) << (8 * (e & 3));
-    }
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t odd = (a[i] & 0x01010101u) * 0xffu;
+    a[i] ^= (a[i] ^ b[i]) & odd;
   }
   return make_uint2(a[0], a[1]);
 }
@@ -294,12 +297,13 @@ __device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float pre, floa
 // orders finite < infinity < NaN), and the codes are written from the
 // registers.
 template <int CODE, int D, int PAGE>
-__global__ void __launch_bounds__(kAppendThreads) kda_cache_append_kernel(AppendArgs p) {
+__global__ void __launch_bounds__(append_threads(PAGE, D)) kda_cache_append_kernel(AppendArgs p) {
+  constexpr int NT = append_threads(PAGE, D);
   constexpr int TPR = D / 8;                     // threads per token, 8 values each
-  constexpr int RPP = kAppendThreads / TPR;      // tokens per pass
+  constexpr int RPP = NT / TPR;      // tokens per pass
   constexpr int PASSES = PAGE / RPP;
   constexpr float TOP = code_top(CODE);
-  __shared__ uint32_t s_max[kAppendThreads / 32];
+  __shared__ uint32_t s_max[NT / 32];
   const int tid = threadIdx.x;
   const int which = blockIdx.x % (2 * p.H), j = blockIdx.x / (2 * p.H);
   const int h = which >> 1, kv = which & 1;
@@ -336,12 +340,12 @@ __global__ void __launch_bounds__(kAppendThreads) kda_cache_append_kernel(Append
   if ((tid & 31) == 0) s_max[tid >> 5] = most;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) most = max(most, s_max[w]);
+  for (int w = 0; w < NT / 32; ++w) most = max(most, s_max[w]);
   const uint32_t now = max(most, had);
   const bool poisoned = now >= 0x7f800000u;
   if (tid == 0) *scale = poisoned ? __uint_as_float(0x7fc00000u) : __uint_as_float(now);
   const float a1 = __uint_as_float(now), a0 = __uint_as_float(had);
-  // a power of two on both sides of the quotient keeps x * top finite and
+  // a power of two on both sides of a quotient keeps its terms finite and
   // normal; it changes no quotient
   const float pre = now >= 0x5f800000u ? 0x1p-64f : now < 0x1f800000u ? 0x1p64f : 1.0f;
   const float den = a1 * pre;
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(kAppendThreads) kda_cache_append_kernel(Append
     if (t >= count) break;
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint2 r = make_uint2(0, 0);
-    if (now != 0 && !poisoned) r = encode8<CODE>(w, pre, inv, den);
+    if (now != 0 && !poisoned) r = encode8<CODE>(w, pre, inv);
     *reinterpret_cast<uint2*>(codes + (int64_t)(off + t) * D) = r;
   }
 }
@@ -372,10 +376,10 @@ __global__ void __launch_bounds__(kAppendThreads) kda_cache_append_kernel(Append
 template <int CODE, int D>
 void launch_append(const AppendArgs& p, int page, unsigned grid, cudaStream_t s) {
   switch (page) {
-    case 16: kda_cache_append_kernel<CODE, D, 16><<<grid, kAppendThreads, 0, s>>>(p); break;
-    case 32: kda_cache_append_kernel<CODE, D, 32><<<grid, kAppendThreads, 0, s>>>(p); break;
-    case 64: kda_cache_append_kernel<CODE, D, 64><<<grid, kAppendThreads, 0, s>>>(p); break;
-    default: kda_cache_append_kernel<CODE, D, 128><<<grid, kAppendThreads, 0, s>>>(p); break;
+    case 16: kda_cache_append_kernel<CODE, D, 16><<<grid, append_threads(16, D), 0, s>>>(p); break;
+    case 32: kda_cache_append_kernel<CODE, D, 32><<<grid, append_threads(32, D), 0, s>>>(p); break;
+    case 64: kda_cache_append_kernel<CODE, D, 64><<<grid, append_threads(64, D), 0, s>>>(p); break;
+    default: kda_cache_append_kernel<CODE, D, 128><<<grid, append_threads(128, D), 0, s>>>(p); break;
   }
 }
 
