@@ -14,11 +14,11 @@ struct PartHead {
   int32_t tok0, rows, h, pad;
 };
 
-// What a kernel leaves for the join, in the workspace.  A CTA leaves at most
+// What a kernel leaves for the join, in the workspace.  A worker leaves at most
 // two parts: of the segment that its share begins in (slot 2 c) and of the one
 // that it ends in (slot 2 c + 1).
 struct Parts {
-  int ctas, rows;    // of the kernel; a part's rows
+  int ctas, rows;    // workers of the kernel (CTAs, or pairs); a part's rows
   int64_t* total;    // units of the whole batch
   PartHead* head;    // [ctas]
   float* ml;         // [2 ctas][rows][2] maximum (log2) and sum of a part's rows
@@ -43,7 +43,7 @@ struct AttnArgs {
 // kernel.
 constexpr int kFewRows = 16;
 // Query rows of a segment on the tile kernel.
-constexpr int kTileRows = 256;
+constexpr int kTileRows = 512;
 
 struct Req {
   int c0, n, kv;
@@ -57,20 +57,21 @@ __device__ __forceinline__ Req load_req(const AttnArgs& p, int r, bool& bad) {
   return {a, bad ? 0 : b - a, kv};
 }
 
-// The schedule: every request has a number of work units, the CTAs take equal
-// contiguous shares of the sum over requests.  A CTA finds the request its
-// first unit falls in: every thread sums a contiguous range of requests, the
-// block scans the sums, the thread whose range holds the unit walks it.
-// CTA 0 also writes the sum and reports malformed requests.
-// units(Req) -> int64; NT threads.  Returns the CTA's units [u0, u1) and the
-// request of u0 with the units before it; u0 == u1 if there is nothing to do.
+// The schedule: every request has a number of work units, the workers (CTAs, or
+// pairs of them) take equal contiguous shares of the sum over requests.  A CTA
+// finds the request its first unit falls in: every thread sums a contiguous
+// range of requests, the block scans the sums, the thread whose range holds
+// the unit walks it.  Worker 0 also writes the sum and reports malformed
+// requests.  units(Req) -> int64; NT threads.  Returns the worker's units
+// [u0, u1) and the request of u0 with the units before it; u0 == u1 if there
+// is nothing to do.
 struct Share {
   int64_t u0, u1, base;
   int r;
 };
 
 template <int NT, class Units>
-__device__ __forceinline__ Share find_share(const AttnArgs& p, Units units) {
+__device__ __forceinline__ Share find_share(const AttnArgs& p, int worker, Units units) {
   __shared__ int64_t s_warp[NT / 32];
   __shared__ int64_t s_base;
   __shared__ int s_r;
@@ -81,7 +82,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, Units units) {
   for (int r = r0; r < r1; ++r) {
     bool bad;
     const Req q = load_req(p, r, bad);
-    if (bad && blockIdx.x == 0) report(p.status, KDA_ERR_BAD_SEQLENS);
+    if (bad && worker == 0) report(p.status, KDA_ERR_BAD_SEQLENS);
     if (q.n > 0) mine += units(q);
   }
   int64_t inc = mine;
@@ -98,9 +99,9 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, Units units) {
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
-  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t share = (total + p.parts.ctas - 1) / p.parts.ctas;
   Share s;
-  s.u0 = min(total, (int64_t)blockIdx.x * share);
+  s.u0 = min(total, (int64_t)worker * share);
   s.u1 = min(total, s.u0 + share);
   int64_t at = before + inc - mine;
   const bool here = s.u0 < s.u1 && at <= s.u0 && s.u0 < at + mine;
@@ -116,7 +117,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, Units units) {
       at += u;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) *p.parts.total = total;
+  if (worker == 0 && tid == 0) *p.parts.total = total;
   __syncthreads();
   s.r = s_r;
   s.base = s_base;

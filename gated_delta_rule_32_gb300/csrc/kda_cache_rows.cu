@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
     return max(1, (int)(((int64_t)q.kv + C::kUnit - 1) / C::kUnit));
   };
   kernel_may_follow();
-  Share sh = find_share<kThreads>(p, [&](const Req& q) { return blocks_of(q) * p.Hkv; });
+  Share sh = find_share<kThreads>(p, blockIdx.x, [&](const Req& q) { return blocks_of(q) * p.Hkv; });
   int r = sh.r;
   int64_t base = sh.base, u = sh.u0;
 

@@ -2,15 +2,21 @@
 // than a few query rows per key / value head (prompts, pieces of prompts),
 // on the tcgen05 tensor cores.
 //
-// A CTA works on segments: up to 256 query rows of one (request, key / value
-// head) -- rows are (token, head of the group) pairs, so the group shares the
-// keys it reads -- against a range of 128-token key tiles.  Two 128-row
-// tiles alternate: while one's softmax runs, the tensor cores work for the
-// other.  Warps:
+// A pair of CTAs (a cluster of two SMs) works on segments: up to 512 query rows
+// of one (request, key / value head) -- rows are (token, head of the group)
+// pairs, so the group shares the keys it reads -- against a range of 128-token
+// key tiles.  Two row tiles of 256 rows, 128 in each CTA, alternate: while one's
+// softmax runs, the tensor cores work for the other.  Each CTA converts and
+// holds half of a key tile (64 tokens) and of a value tile (half the channels);
+// a product reads both halves (cta_group::2).  With one CTA a tile, shared
+// memory was what bound this kernel: its operands, 128 bytes a cycle of the
+// scores' products, left none for the other warps' traffic.
+// Warps of a CTA:
 //   0-3, 4-7   softmax of row tile 0 / 1, one thread per row
 //   8-11       keys:   codes -> f16 operand tiles in shared memory
 //   12-15      values: the same; between segments 8-15 convert the queries
-//   16         issues the products (one thread) and owns tensor memory
+//   16         owns tensor memory; of the first CTA: issues all products (one
+//              thread)
 //   17         walks the schedule and looks up the pages' scales, some key
 //              tiles ahead of the softmax
 //   18, 19     bring the next segment's queries into L2
@@ -32,29 +38,37 @@ namespace {
 using namespace kda_cache;
 
 // Five warpgroups launched with 96 registers a thread; they share them out
-// anew (setmaxnreg): 2 x 128 + 2 x 80 + 64 = 5 x 96.
+// anew (setmaxnreg): 2 x 136 + 2 x 72 + 64 = 5 x 96.
 constexpr int kThreads = 640;
-constexpr int kRegsSoftmax = 128, kRegsConvert = 80, kRegsIssue = 64;
+constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue == 5 * 96, "registers at launch");
 constexpr int kTok = 128;    // tokens per key tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+constexpr int kStages = 4;   // key and value tiles in shared memory
+
 template <int D>
 struct Smem {
-  static constexpr int kTile = 128 * D * 2;     // one f16 operand tile
-  static constexpr int kQ = 0;                  // 2 tiles
-  static constexpr int kK = 2 * kTile;          // 2 stages
-  static constexpr int kV = 4 * kTile;          // 2 stages
-  static constexpr int kStage = 6 * kTile;      // 64 bytes of 32 rows for each softmax warp
-  static constexpr int kStageRow = 80;          // (a row's 64 bytes, padded against conflicts)
+  static constexpr int kQTile = 128 * D * 2;         // a row tile's queries
+  static constexpr int kTile = 64 * D * 2;           // this CTA's half of a key or value tile
+  static constexpr int kQ = 0;                       // 2 tiles
+  static constexpr int kK = 2 * kQTile;              // kStages
+  static constexpr int kV = kK + kStages * kTile;    // kStages
+  static constexpr int kStage = kV + kStages * kTile;  // 64 bytes of 32 rows for each softmax warp
+  static constexpr int kStageRow = 80;               // (a row's 64 bytes, padded against conflicts)
   static constexpr int kStageWarp = 32 * kStageRow;
   static constexpr int kBytes = kStage + 8 * kStageWarp + 1024;
 };
 
+// "leader": only the first CTA's is used, both arrive there.  The others are
+// each CTA's own; those that products complete are completed in both.
 struct Bars {
-  uint64_t q_full[2][2], q_empty[2];  // row tile, and parity of its segments
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2][2];              // leader; row tile, and parity of its segments
+  uint64_t qs_full[2][2], q_empty[2];
+  uint64_t s_full[2], o_full[2];
+  uint64_t p_full[2];                 // leader
+  uint64_t k_full[kStages], v_full[kStages];  // leader
+  uint64_t k_empty[kStages], v_empty[kStages];
   uint64_t seg_full[2], seg_empty[2];
   uint64_t sc_full[4], sc_empty[4];
   uint64_t drain;
@@ -85,7 +99,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(1000000)
@@ -102,6 +116,23 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
       return false;
     }
   }
+}
+
+// Arrives at the first CTA's copy of a barrier.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(sm100::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&r)[32]) {
@@ -179,22 +210,23 @@ __device__ __forceinline__ uint32_t elect_one() {
                : "=r"(r));
   return r;
 }
-// D (+)= A B^T, A and B in shared memory, both [chunk][row][16 bytes] with 128
+// D (+)= A B^T, A and B in shared memory, [chunk][row][16 bytes] with 128 and 64
 // rows: the low words of their descriptors go up by two chunks a k-step.
-__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
-                                        uint32_t idesc, uint32_t accumulate, uint32_t one) {
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t a_hi,
+                                        uint32_t b_hi, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t one) {
   asm volatile(
       "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n .reg .b32 x, y;\n"
-      " setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n"
-      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
-      " add.u32 x, %1, 256;\n add.u32 y, %2, 256;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 512;\n add.u32 y, %2, 512;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 768;\n add.u32 y, %2, 768;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
+      " setp.ne.b32 q, %7, 0;\n setp.ne.b32 p, %6, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %4};\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n"
+      " add.u32 x, %1, 256;\n add.u32 y, %2, 128;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %4};\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+      " add.u32 x, %1, 512;\n add.u32 y, %2, 256;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %4};\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+      " add.u32 x, %1, 768;\n add.u32 y, %2, 384;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %4};\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
 // The same with A in tensor memory, 8 columns a k-step, and B's rows the
@@ -205,21 +237,22 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b, uint
       "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 x, y;\n"
       " setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n"
       " mov.b64 b, {%2, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n"
       " add.u32 x, %1, 8;\n add.u32 y, %2, 16;\n mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [x], b, %4, t;\n"
       " add.u32 x, %1, 16;\n add.u32 y, %2, 32;\n mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [x], b, %4, t;\n"
       " add.u32 x, %1, 24;\n add.u32 y, %2, 48;\n mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n}" ::"r"(d),
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [x], b, %4, t;\n}" ::"r"(d),
       "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
+// Arrives at a barrier of both CTAs when the products so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::"
-      "arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(sm100::smem_u32(bar)),
-      "r"(one)
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::2.mbarrier::"
+      "arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}" ::"r"(sm100::smem_u32(bar)),
+      "r"(one), "h"((uint16_t)3)
       : "memory");
 }
 
@@ -355,38 +388,46 @@ struct Walk {
 };
 
 template <int CODE, int D>
-__global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnArgs p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    kda_cache_attn_tile_kernel(AttnArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ Bars bars;
   __shared__ Seg s_seg[2];
   __shared__ Scales s_scales[kRing];
-  __shared__ float s_qscale[2][kTileRows];  // what a query row was divided by
+  __shared__ float s_qscale[2][256];  // what a query row was divided by
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   unsigned char* smem = smem_raw + ((1024u - (sm100::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int lg = p.page_log2, P = 1 << lg;
   volatile int* abort = &s_abort;
+  const int rank = cluster_rank(), pair = blockIdx.x >> 1;
 
   if (warp == 16) {
-    sm100::tmem_alloc(&s_tmem, 512);
-    sm100::tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     sm100::smem_u32(&s_tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&bars.q_full[i][0], 256);
-      sm100::mbar_init(&bars.q_full[i][1], 256);
+      for (int x = 0; x < 2; ++x) {
+        sm100::mbar_init(&bars.q_full[i][x], 16);   // (a warp's arrival is one)
+        sm100::mbar_init(&bars.qs_full[i][x], 8);
+      }
       sm100::mbar_init(&bars.q_empty[i], 1);
       sm100::mbar_init(&bars.s_full[i], 1);
-      sm100::mbar_init(&bars.p_full[i], 128);
       sm100::mbar_init(&bars.o_full[i], 1);
-      sm100::mbar_init(&bars.k_full[i], 128);
-      sm100::mbar_init(&bars.k_empty[i], 1);
-      sm100::mbar_init(&bars.v_full[i], 128);
-      sm100::mbar_init(&bars.v_empty[i], 1);
+      sm100::mbar_init(&bars.p_full[i], 8);
       sm100::mbar_init(&bars.seg_full[i], 1);
       sm100::mbar_init(&bars.seg_empty[i], kReaders);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      sm100::mbar_init(&bars.k_full[i], 8);
+      sm100::mbar_init(&bars.v_full[i], 8);
+      sm100::mbar_init(&bars.k_empty[i], 1);
+      sm100::mbar_init(&bars.v_empty[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
       sm100::mbar_init(&bars.sc_full[i], 1);
@@ -397,11 +438,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   }
   sm100::tc_fence_before();
   kernel_may_follow();
-  const Share share = find_share<kThreads>(p, [&](const Req& q) {
+  const Share share = find_share<kThreads>(p, pair, [&](const Req& q) {
     const Tiles t(q, p.G);
     return t.count ? t.before(t.count) * p.Hkv : 0;
   });
-  __syncthreads();
+  cluster_sync();  // (both CTAs' barriers are there)
   sm100::tc_fence_after();
   constexpr uint32_t tmem = 0;  // (all 512 columns are this CTA's)
   uint32_t nseg = 0;  // segments seen
@@ -427,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
     regs_up<kRegsSoftmax>();
-    const int wg = warp >> 2, row = 128 * wg + 32 * (warp & 3) + lane;
+    const int wg = warp >> 2, row = 256 * wg + 128 * rank + 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + 128 * wg, tO = tmem + lanes + 256 + D * wg;
     uint32_t seg = 0, it = 0;  // segments and key tiles that this row tile has had
@@ -436,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       const Seg g = next_seg();
       if (g.rows == 0) break;
       const int nk = g.b1 - g.b0;
-      if (128 * wg >= g.rows) {  // (no rows here: only the scales pass by)
+      if (256 * wg >= g.rows) {  // (no rows here: only the scales pass by)
         bool ok = true;
         for (int k = 0; ok && k < nk; ++k, ++tiles) {
           ok = all_wait(&bars.sc_full[tiles % kRing], (tiles / kRing) & 1);
@@ -453,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       if (!mine) lim = lim_hi;
       const int lim_lo = __reduce_min_sync(~0u, lim);
       float m = -INFINITY, l = 0.0f, vref = 0.0f, vrel_of = 1.0f;
-      bool ok = all_wait(&bars.q_full[wg][seg & 1], (seg >> 1) & 1);
-      const float qs = s_qscale[seg & 1][row];
+      bool ok = all_wait(&bars.qs_full[wg][seg & 1], (seg >> 1) & 1);
+      const float qs = s_qscale[seg & 1][128 * wg + 32 * (warp & 3) + lane];
       for (int k = 0; ok && k < nk; ++k, ++it, ++tiles) {
         const Scales& sc = s_scales[tiles % kRing];
         const int t0 = (g.b0 + k) * kTok;
@@ -590,15 +631,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         tmem_st32(tS + 32, z + 32);
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
-        sm100::mbar_arrive(&bars.p_full[wg]);
-        if (lane == 0) sm100::mbar_arrive(&bars.sc_empty[tiles % kRing]);
+        __syncwarp();
+        if (lane == 0) {
+          arrive_leader(&bars.p_full[wg]);
+          sm100::mbar_arrive(&bars.sc_empty[tiles % kRing]);
+        }
       }
       if (!ok || !all_wait(&bars.o_full[wg], seg & 1)) break;
       ++seg;
       sm100::tc_fence_after();
       const float ov = vref / code_top(CODE);
       const bool whole = g.b0 == 0 && g.b1 == g.nu;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (g.b0 > 0 ? 0 : 1);
+      const int64_t slot = 2 * (int64_t)pair + (g.b0 > 0 ? 0 : 1);
       const int64_t at = (int64_t)(g.c0 + tok) * p.Hq + g.h * p.G + row % p.G;
       const float f = whole ? (l == 0.0f ? 0.0f : ov / l) : ov;
       // O leaves through 64-byte row pieces in shared memory, so that a store
@@ -663,19 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     }
   } else if (warp < 16) {
     // ---------------------------------------------- codes -> f16 operands
-    // Both operands are laid out [8-channel chunk][token][16 bytes]: core
-    // matrices of 8 tokens x 16 bytes, K-major for the keys (contracted over
-    // channels), MN-major for the values (contracted over tokens).  Lanes 8 c
-    // .. 8 c + 7 of a warp take the same 16 codes of 8 tokens, so the global
-    // reads are whole sectors and the shared writes free of conflicts.
     regs_down<kRegsConvert>();
-    const bool is_v = warp >= 12;
     const int wq = warp & 3, t8 = lane & 7, c4 = lane >> 3;
-    const uint8_t* codes = is_v ? p.v_codes : p.k_codes;
-    uint64_t* full = is_v ? bars.v_full : bars.k_full;
-    uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
-    unsigned char* tiles = smem + (is_v ? Smem<D>::kV : Smem<D>::kK);
-    constexpr int NC = D / 64;  // 64-byte column blocks
     uint32_t cnt = 0, n0 = 0, n1 = 0;
     bool ok = true;
     // The queries of a segment, 8 rows of each row tile for a warp at a time:
@@ -686,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       const uint32_t i = t ? n1++ : n0++;
 #pragma unroll 1
       for (int g8 = warp - 8; g8 < 16; g8 += 8) {
-        const int row = 8 * g8 + t8, of = 128 * t + row;
+        const int row = 8 * g8 + t8, of = 256 * t + 128 * rank + row;
         const uint16_t* src = p.q + (int64_t)(g.c0 + g.tok0 + of / p.G) * p.q_stride +
                               (int64_t)(g.h * p.G + of % p.G) * D + 8 * c4;
         uint4 y[C];
@@ -705,8 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         most = max(most, __shfl_xor_sync(~0u, most, 16));
         const int ex = row_exponent(most);
         const float down = copysignf(exp2i(-ex), p.scale);
-        if (c4 == 0) s_qscale[i & 1][of] = exp2i(ex);
-        unsigned char* d = smem + Smem<D>::kQ + t * Smem<D>::kTile + row * 16 + c4 * 2048;
+        if (c4 == 0) s_qscale[i & 1][128 * t + row] = exp2i(ex);
+        unsigned char* d = smem + Smem<D>::kQ + t * Smem<D>::kQTile + row * 16 + c4 * 2048;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const uint32_t a[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
@@ -719,71 +752,107 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         }
       }
       sm100::fence_async_smem();
-      sm100::mbar_arrive(&bars.q_full[t][i & 1]);
+      __syncwarp();
+      if (lane == 0) {
+        sm100::mbar_arrive(&bars.qs_full[t][i & 1]);
+        arrive_leader(&bars.q_full[t][i & 1]);
+      }
       return true;
     };
-    while (ok) {
-      const Seg sg = next_seg();
-      if (sg.rows == 0) break;
-      const int nk = sg.b1 - sg.b0, kv = sg.kv;
-      const int32_t* table = p.table + (int64_t)sg.r * p.max_pages;
-      // this warp's 32 tokens of a tile lie in two 16-token groups
-      auto page_of = [&](int k, int g) -> int {
-        const int64_t t0 = (int64_t)(sg.b0 + k) * kTok + 32 * wq + 16 * g;
-        return load_page_if(table + (t0 >> lg), k < nk && t0 < kv);
+    auto convert = [&](auto which) {
+      constexpr bool V = decltype(which)::value;
+      const uint8_t* codes = V ? p.v_codes : p.k_codes;
+      uint64_t* full = V ? bars.v_full : bars.k_full;
+      uint64_t* empty = V ? bars.v_empty : bars.k_empty;
+      // A piece is 16 codes of a token.  Keys: a warp's 16 tokens, whole rows;
+      // values: its 32 tokens, half rows.  N pieces a lane: its token (past the
+      // warp's first) and byte of the row of piece i, and where its two
+      // 16-byte chunks go.
+      constexpr int N = D / 32;
+      auto token = [&](int i) {
+        return !V ? 8 * (i & 1) + t8 : D == 128 ? 8 * i + t8 : 16 * i + 8 * (c4 >> 1) + t8;
       };
-      uint4 x[4][NC];
-      auto fetch = [&](int k, int pa, int pb) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int pg = g < 2 ? pa : pb;
-          const int64_t t = (int64_t)(sg.b0 + k) * kTok + 32 * wq + 8 * g + t8;
-          const uint8_t* src =
-              codes + ((((int64_t)pg * p.Hkv + sg.h) << lg) + (t & (P - 1))) * D + 16 * c4;
-          // (what a page holds past the request's end may be a NaN)
-          const bool use = (uint32_t)pg < (uint32_t)p.num_pages && (!is_v || t < kv);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) x[g][c] = load16_if(src + 64 * c, use);
-        }
+      auto byte = [&](int i) {
+        return !V ? 64 * (i >> 1) + 16 * c4 : D == 128 ? 64 * rank + 16 * c4
+                                                       : 32 * rank + 16 * (c4 & 1);
       };
-      auto place = [&]() -> bool {  // x -> the next stage
-        const int st = cnt & 1;
-        if (cnt >= 2 && !all_wait(&empty[st], ((cnt >> 1) - 1) & 1)) return false;
-        unsigned char* dst = tiles + st * Smem<D>::kTile + (32 * wq + t8) * 16;
+      auto chunk = [&](int i) { return !V ? 8 * (i >> 1) + 2 * c4 : D == 128 ? 2 * c4 : 2 * (c4 & 1); };
+      const int first = V ? 32 * wq : 64 * rank + 16 * wq;  // token of a key tile
+      unsigned char* tiles = smem + (V ? Smem<D>::kV + first * 16 : Smem<D>::kK + 16 * wq * 16);
+      constexpr int kChunk = V ? 2048 : 1024;
+      while (ok) {
+        const Seg sg = next_seg();
+        if (sg.rows == 0) break;
+        const int nk = sg.b1 - sg.b0, kv = sg.kv;
+        const int32_t* table = p.table + (int64_t)sg.r * p.max_pages;
+        // the pages of the warp's tokens 0-15 and (values) 16-31
+        auto page_of = [&](int k, int g) -> int {
+          const int64_t t0 = (int64_t)(sg.b0 + k) * kTok + first + 16 * g;
+          return load_page_if(table + (t0 >> lg), k < nk && t0 < kv);
+        };
+        uint4 x[N];
+        auto fetch = [&](int k, int pa, int pb) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+          for (int i = 0; i < N; ++i) {
+            const int tk = token(i);
+            const int pg = V && (D == 128 ? i >= 2 : i >= 1) ? pb : pa;
+            const int64_t t = (int64_t)(sg.b0 + k) * kTok + first + tk;
+            const uint8_t* src =
+                codes + ((((int64_t)pg * p.Hkv + sg.h) << lg) + (t & (P - 1))) * D + byte(i);
+            // (what a page holds past the request's end may be a NaN)
+            x[i] = load16_if(src, (uint32_t)pg < (uint32_t)p.num_pages && (!V || t < kv));
+          }
+        };
+        auto place = [&]() -> bool {  // x -> the next stage
+          const int st = cnt % kStages;
+          if (cnt >= kStages && !all_wait(&empty[st], (cnt / kStages - 1) & 1)) return false;
+          unsigned char* dst = tiles + st * Smem<D>::kTile;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const uint32_t y[4] = {x[g][c].x, x[g][c].y, x[g][c].z, x[g][c].w};
+          for (int i = 0; i < N; ++i) {
+            const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             uint32_t f[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) codes_to_half<CODE>(y[e], f[2 * e], f[2 * e + 1]);
-            unsigned char* d = dst + g * 128 + (8 * c + 2 * c4) * 2048;
+            unsigned char* d = dst + token(i) * 16 + chunk(i) * kChunk;
             *reinterpret_cast<uint4*>(d) = make_uint4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint4*>(d + 2048) = make_uint4(f[4], f[5], f[6], f[7]);
+            *reinterpret_cast<uint4*>(d + kChunk) = make_uint4(f[4], f[5], f[6], f[7]);
           }
-        return true;
-      };
-      fetch(0, page_of(0, 0), page_of(0, 1));
-      ok = place();
-      if (!ok) break;
-      sm100::fence_async_smem();
-      sm100::mbar_arrive(&full[cnt++ & 1]);
-      // (the queries while no codes are held in registers)
-      ok = queries(sg, 0) && (sg.rows <= 128 || queries(sg, 1));
-      if (!ok || nk == 1) continue;
-      fetch(1, page_of(1, 0), page_of(1, 1));
-      int pa = page_of(2, 0), pb = page_of(2, 1);
-      for (int k = 1; k < nk; ++k, ++cnt) {
+          return true;
+        };
+        auto placed = [&]() {
+          sm100::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_leader(&full[cnt % kStages]);
+          ++cnt;
+        };
+        fetch(0, page_of(0, 0), V ? page_of(0, 1) : -1);
         ok = place();
         if (!ok) break;
-        if (k + 1 < nk) fetch(k + 1, pa, pb);
-        pa = page_of(k + 2, 0);
-        pb = page_of(k + 2, 1);
-        sm100::fence_async_smem();
-        sm100::mbar_arrive(&full[cnt & 1]);
+        placed();
+        // (the queries while no codes are held in registers)
+        ok = queries(sg, 0) && (sg.rows <= 256 || queries(sg, 1));
+        if (!ok || nk == 1) continue;
+        fetch(1, page_of(1, 0), V ? page_of(1, 1) : -1);
+        int pa = page_of(2, 0), pb = V ? page_of(2, 1) : -1;
+        for (int k = 1; k < nk; ++k) {
+          ok = place();
+          if (!ok) break;
+          if (k + 1 < nk) fetch(k + 1, pa, pb);
+          pa = page_of(k + 2, 0);
+          pb = V ? page_of(k + 2, 1) : -1;
+          placed();
+        }
       }
-    }
+    };
+    // Both operands are laid out [8-channel chunk][token][16 bytes]: core
+    // matrices of 8 tokens x 16 bytes, K-major for the keys (contracted over
+    // channels), MN-major for the values (contracted over tokens).  Lanes 8 c
+    // .. 8 c + 7 of a warp take the same 16 codes of 8 tokens, so the global
+    // reads are whole sectors and the shared writes free of conflicts.
+    if (warp < 12)
+      convert(std::false_type{});
+    else
+      convert(std::true_type{});
   } else {
     regs_down<kRegsIssue>();
     if (warp == 17) {
@@ -797,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
         if (w.live() && w.b0 > 0)
           ph = {w.seg0 + kLead, w.seg0 + kLead + w.nu, w.q.c0 + w.tile * w.t.tt,
                 w.tokens() * p.G, w.h, 0};
-        p.parts.head[blockIdx.x] = ph;
+        p.parts.head[pair] = ph;
       }
       uint32_t tiles = 0;
       bool ok = true;
@@ -850,8 +919,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       for (;;) {
         const Seg g = next_seg();
         if (g.rows == 0) break;
-        for (int e = threadIdx.x - 18 * 32; e < g.rows * (D / 64); e += 64) {
-          const int row = e / (D / 64);
+        for (int e = threadIdx.x - 18 * 32; e < 256 * (D / 64); e += 64) {
+          const int at = e / (D / 64), row = 256 * (at >> 7) + 128 * rank + (at & 127);
+          if (row >= g.rows) continue;
           const uint16_t* src = p.q + (int64_t)(g.c0 + g.tok0 + row / p.G) * p.q_stride +
                                 (int64_t)(g.h * p.G + row % p.G) * D + 64 * (e % (D / 64));
           asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
@@ -859,20 +929,23 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
       }
     } else if (warp == 16) {
     // ----------------------------------------------------------- products
-    const uint32_t id_s = idesc_f16(128, kTok, 0), id_o = idesc_f16(128, D, 1);
+    // (of the second CTA this warp only lets the segments pass)
+    const uint32_t id_s = idesc_f16(256, kTok, 0), id_o = idesc_f16(256, D, 1);
     const uint32_t one = elect_one();
     // (a descriptor's address field counts 16-byte units)
-    const uint64_t dk = sm100::smem_desc(sm100::smem_u32(smem), 2048, 128);
+    const uint64_t dq = sm100::smem_desc(sm100::smem_u32(smem), 2048, 128);
+    const uint64_t dk = sm100::smem_desc(sm100::smem_u32(smem), 1024, 128);
     const uint64_t dv = sm100::smem_desc(sm100::smem_u32(smem), 128, 2048);
-    const uint32_t q_lo = (uint32_t)dk + Smem<D>::kQ / 16, k_lo = (uint32_t)dk + Smem<D>::kK / 16;
+    const uint32_t q_lo = (uint32_t)dq + Smem<D>::kQ / 16, k_lo = (uint32_t)dk + Smem<D>::kK / 16;
     const uint32_t v_lo = (uint32_t)dv + Smem<D>::kV / 16;
-    const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
-    constexpr int kTile16 = Smem<D>::kTile / 16;
+    const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32);
+    const uint32_t v_hi = (uint32_t)(dv >> 32);
+    constexpr int kTile16 = Smem<D>::kTile / 16, kQTile16 = Smem<D>::kQTile / 16;
     auto scores = [&](int t, int st, bool last) {  // S_t = Q_t K^T
 #pragma unroll
       for (int s = 0; s < D / 64; ++s)
-        mma4_ss(128 * t, q_lo + t * kTile16 + s * 1024, k_lo + st * kTile16 + s * 1024, k_hi, id_s, s,
-                one);
+        mma4_ss(128 * t, q_lo + t * kQTile16 + s * 1024, k_lo + st * kTile16 + s * 512, q_hi, k_hi,
+                id_s, s, one);
       mma_commit(&bars.s_full[t], one);
       if (last) mma_commit(&bars.q_empty[t], one);
     };
@@ -884,79 +957,69 @@ __global__ void __launch_bounds__(kThreads, 1) kda_cache_attn_tile_kernel(AttnAr
     };
     uint32_t n0 = 0, n1 = 0, t0 = 0, t1 = 0;  // segments and key tiles of the row tiles
     uint32_t kc = 0;                          // key tiles before this one
-    bool two = false, ok = true;
-    int nk = 0;
-    // Key tile k of a segment, in stage ST: its weights meet the values, and
-    // the next key tile's scores follow as soon as their place is free.
-    auto step = [&](auto stage, int k) {
-      constexpr int ST = decltype(stage)::value;
-      const bool last = k + 1 == nk, before_last = k + 2 == nk;
-      const uint32_t kp = (kc >> 1) & 1, np = ((kc + 1) >> 1) & 1;
-      ok = all_wait(&bars.v_full[ST], kp) && all_wait(&bars.p_full[0], t0++ & 1);
-      if (!ok) return;
-      sm100::tc_fence_after();
-      values(0, ST, k == 0);
-      if (last) {
-        mma_commit(&bars.o_full[0], one);
-      } else {
-        ok = all_wait(&bars.k_full[1 - ST], np);
-        if (!ok) return;
-        sm100::tc_fence_after();
-        scores(0, 1 - ST, before_last);
-      }
-      if (two) {
-        ok = all_wait(&bars.p_full[1], t1++ & 1);
-        if (!ok) return;
-        sm100::tc_fence_after();
-        values(1, ST, k == 0);
-        if (last) mma_commit(&bars.o_full[1], one);
-        else scores(1, 1 - ST, before_last);
-      }
-      mma_commit(&bars.v_empty[ST], one);
-      if (!last) mma_commit(&bars.k_empty[1 - ST], one);
-    };
-    auto first_scores = [&](auto stage) {
-      constexpr int ST = decltype(stage)::value;
-      ok = all_wait(&bars.q_full[0][n0 & 1], (n0 >> 1) & 1) &&
-           all_wait(&bars.k_full[ST], (kc >> 1) & 1);
-      if (!ok) return;
-      ++n0;
-      sm100::tc_fence_after();
-      scores(0, ST, nk == 1);
-      if (two) {
-        ok = all_wait(&bars.q_full[1][n1 & 1], (n1 >> 1) & 1);
-        if (!ok) return;
-        ++n1;
-        sm100::tc_fence_after();
-        scores(1, ST, nk == 1);
-      }
-      mma_commit(&bars.k_empty[ST], one);
-    };
-    using S0 = std::integral_constant<int, 0>;
-    using S1 = std::integral_constant<int, 1>;
+    bool ok = true;
     for (;;) {
       const Seg g = next_seg();
       if (g.rows == 0) break;
+      if (rank != 0) continue;
       // (a reduction's result is known to be uniform)
-      two = __reduce_max_sync(~0u, g.rows) > 128;
-      nk = __reduce_max_sync(~0u, g.b1 - g.b0);
-      if (kc & 1) first_scores(S1{}); else first_scores(S0{});
-      for (int k = 0; ok && k < nk; ++k, ++kc) {
-        if (kc & 1) step(S1{}, k); else step(S0{}, k);
+      const bool two = __reduce_max_sync(~0u, g.rows) > 256;
+      const int nk = __reduce_max_sync(~0u, g.b1 - g.b0);
+      {
+        const uint32_t st = kc % kStages;
+        ok = all_wait(&bars.k_full[st], (kc / kStages) & 1) &&
+             all_wait(&bars.q_full[0][n0 & 1], (n0 >> 1) & 1);
+        if (!ok) break;
+        ++n0;
+        sm100::tc_fence_after();
+        scores(0, st, nk == 1);
+        if (two) {
+          ok = all_wait(&bars.q_full[1][n1 & 1], (n1 >> 1) & 1);
+          if (!ok) break;
+          ++n1;
+          sm100::tc_fence_after();
+          scores(1, st, nk == 1);
+        }
+        mma_commit(&bars.k_empty[st], one);
+      }
+      // A key tile's weights meet the values, and the next key tile's scores
+      // follow as soon as their place is free.
+      for (int k = 0; k < nk; ++k, ++kc) {
+        const bool last = k + 1 == nk, before_last = k + 2 == nk;
+        const uint32_t st = kc % kStages, nt = (kc + 1) % kStages;
+        ok = all_wait(&bars.v_full[st], (kc / kStages) & 1) &&
+             (last || all_wait(&bars.k_full[nt], ((kc + 1) / kStages) & 1)) &&
+             all_wait(&bars.p_full[0], t0++ & 1);
+        if (!ok) break;
+        sm100::tc_fence_after();
+        values(0, st, k == 0);
+        if (last) mma_commit(&bars.o_full[0], one);
+        else scores(0, nt, before_last);
+        if (two) {
+          ok = all_wait(&bars.p_full[1], t1++ & 1);
+          if (!ok) break;
+          sm100::tc_fence_after();
+          values(1, st, k == 0);
+          if (last) mma_commit(&bars.o_full[1], one);
+          else scores(1, nt, before_last);
+        }
+        mma_commit(&bars.v_empty[st], one);
+        if (!last) mma_commit(&bars.k_empty[nt], one);
       }
       if (!ok) break;
     }
     // the last commits (of k_empty, v_empty) must land before the CTA leaves
-    mma_commit(&bars.drain, one);
-    sm100::mbar_wait(&bars.drain, 0, 200000000ull);
+    if (rank == 0) mma_commit(&bars.drain, one);
+    sm100::mbar_wait(&bars.drain, 0);
     }
   }
   __syncwarp();
   sm100::tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // (nobody's barriers or tensor memory are used any more)
   if (tid == 0 && s_abort) report(p.status, KDA_ERR_TIMEOUT);
   wait_for_kernel_before();  // (this one needs nothing of it, what follows may)
-  if (warp == 16) sm100::tmem_dealloc(s_tmem, 512);
+  if (warp == 16)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(s_tmem) : "memory");
 }
 
 template <int CODE, int D>
@@ -964,7 +1027,7 @@ kda_status launch_tile(const AttnArgs& p, cudaStream_t s) {
   auto kernel = kda_cache_attn_tile_kernel<CODE, D>;
   const kda_status rc = kda_smem_attr((const void*)kernel, Smem<D>::kBytes);
   if (rc != KDA_OK) return rc;
-  return launch_following(kernel, p.parts.ctas, kThreads, Smem<D>::kBytes, s, p);
+  return launch_following(kernel, 2 * p.parts.ctas, kThreads, Smem<D>::kBytes, s, p);
 }
 
 }  // namespace
