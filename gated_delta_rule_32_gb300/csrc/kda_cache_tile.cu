@@ -99,7 +99,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(1000000)
@@ -118,11 +118,14 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
-// Arrives at the first CTA's copy of a barrier.
+// Arrives at the first CTA's copy of a barrier.  What it announces is this CTA's
+// own shared and tensor memory, which only products read, after the fences to
+// their proxy that come before: it needs no release of the generic writes to
+// the cluster (which took 1000 cycles a time).
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(sm100::smem_u32(bar))
+      " mbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(sm100::smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
