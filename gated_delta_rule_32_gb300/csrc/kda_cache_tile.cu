@@ -986,18 +986,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mma_commit(&bars.k_empty[st], one);
       }
       // A key tile's weights meet the values, and the next key tile's scores
-      // follow as soon as their place is free.
-      for (int k = 0; k < nk; ++k, ++kc) {
+      // follow as soon as their place is free.  What the next step needs of
+      // values and keys is waited for while row tile 1's softmax is awaited (it
+      // is there as a rule): a wait takes a few hundred cycles even so.
+      auto tiles_there = [&](int k) -> bool {
+        const uint32_t at = kc + k;
+        return all_wait(&bars.v_full[at % kStages], (at / kStages) & 1) &&
+               (k + 1 == nk ||
+                all_wait(&bars.k_full[(at + 1) % kStages], ((at + 1) / kStages) & 1));
+      };
+      ok = tiles_there(0);
+      for (int k = 0; ok && k < nk; ++k) {
         const bool last = k + 1 == nk, before_last = k + 2 == nk;
-        const uint32_t st = kc % kStages, nt = (kc + 1) % kStages;
-        ok = all_wait(&bars.v_full[st], (kc / kStages) & 1) &&
-             (last || all_wait(&bars.k_full[nt], ((kc + 1) / kStages) & 1)) &&
-             all_wait(&bars.p_full[0], t0++ & 1);
+        const uint32_t st = (kc + k) % kStages, nt = (kc + k + 1) % kStages;
+        ok = all_wait(&bars.p_full[0], t0++ & 1);
         if (!ok) break;
         sm100::tc_fence_after();
         values(0, st, k == 0);
         if (last) mma_commit(&bars.o_full[0], one);
         else scores(0, nt, before_last);
+        if (!last && kStages > 2) {
+          ok = tiles_there(k + 1);
+          if (!ok) break;
+        }
         if (two) {
           ok = all_wait(&bars.p_full[1], t1++ & 1);
           if (!ok) break;
@@ -1009,6 +1020,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mma_commit(&bars.v_empty[st], one);
         if (!last) mma_commit(&bars.k_empty[nt], one);
       }
+      kc += nk;
       if (!ok) break;
     }
     // the last commits (of k_empty, v_empty) must land before the CTA leaves
