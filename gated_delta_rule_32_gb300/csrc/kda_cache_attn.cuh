@@ -49,6 +49,12 @@ struct Req {
   int c0, n, kv;
 };
 
+// a / b of non-negative numbers, by the much shorter 32-bit division where it will do.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // Request r, or n = 0 if it brings nothing or is malformed (`bad`).
 __device__ __forceinline__ Req load_req(const AttnArgs& p, int r, bool& bad) {
   const int a = p.cu[r], b = p.cu[r + 1], kv = p.kv_lens[r];
@@ -99,7 +105,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, int worker, Units
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
-  const int64_t share = (total + p.parts.ctas - 1) / p.parts.ctas;
+  const int64_t share = quotient(total + p.parts.ctas - 1, p.parts.ctas);
   Share s;
   s.u0 = min(total, (int64_t)worker * share);
   s.u1 = min(total, s.u0 + share);

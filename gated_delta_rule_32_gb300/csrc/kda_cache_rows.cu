@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
       ++r;
       continue;
     }
-    const int h = (int)((u - base) / nb);
+    const int h = (int)quotient(u - base, nb);
     const int64_t seg0 = base + h * nb;               // the (request, head)'s units
     const int b0 = (int)(u - seg0);
     const int b1 = (int)(min(sh.u1, seg0 + nb) - seg0);
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, Parts ro
   const PartHead ph = q.head[c0 + 1];
   const int n = min(ph.rows - row0, group);
   if (n <= 0) return;
-  const int64_t share = (*q.total + q.ctas - 1) / q.ctas;
-  const int ca = (int)(ph.seg0 / share), cb = (int)((ph.seg1 - 1) / share);
+  const int64_t share = quotient(*q.total + q.ctas - 1, q.ctas);
+  const int ca = (int)quotient(ph.seg0, share), cb = (int)quotient(ph.seg1 - 1, share);
   if (ca != c0) return;
   const int wpr = n > 4 ? 1 : n > 2 ? 2 : n > 1 ? 4 : 8;  // warps a row
   const int sub = warp % wpr;

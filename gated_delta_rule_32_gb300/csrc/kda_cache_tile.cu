@@ -342,7 +342,7 @@ struct Walk {
     if (u >= u1) return;
     load();
     const int64_t in = u - base;
-    h = (int)(in / per_head);
+    h = (int)quotient(in, per_head);
     const int64_t left = in - h * per_head;
     int lo = 0, hi = t.count;
     while (hi - lo > 1) {  // the last tile with at most `left` units before it
