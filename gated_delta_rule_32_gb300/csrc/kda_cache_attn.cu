@@ -22,7 +22,7 @@ Layout layout(int max_new, int G, int d) {
   const int sms = kda_device_sms();
   const int64_t rows = (int64_t)max_new * G;
   w.ctas[0] = sms * 3;  // as many as the kernel's registers let an SM hold
-  w.ctas[1] = rows > kFewRows ? sms / 2 : 0;  // (pairs of CTAs)
+  w.ctas[1] = rows > kFewMax ? sms / 2 : 0;  // (pairs of CTAs)
   size_t at = 0;
   for (int i = 0; i < 2; ++i) {
     const size_t parts = (size_t)2 * w.ctas[i] * kPartRows[i];

@@ -11,7 +11,7 @@ namespace kda_cache {
 // middle of: its units, first token, rows (0: none) and head.
 struct PartHead {
   int64_t seg0, seg1;
-  int32_t tok0, rows, h, pad;
+  int32_t tok0, rows, h, row0;  // (row0: its first row, counted from tok0)
 };
 
 // What a kernel leaves for the join, in the workspace.  A worker leaves at most
@@ -39,9 +39,12 @@ struct AttnArgs {
   Parts parts;  // of the kernel that the arguments are for
 };
 
-// Query rows per key / value head up to which a request runs on the few-row
-// kernel.
-constexpr int kFewRows = 16;
+// A request with at most kFewMax query rows per key / value head runs on the
+// few-row kernel, in groups of kFewRows.  With 64 rows (32 requests of 4 tokens
+// over 2 300 cached ones on average, 2 heads of 16, d = 64) that kernel took
+// 42 us and the tile kernel 53; a group costs it as much as the first one,
+// so past 64 rows the tile kernel's 512-row segments win.
+constexpr int kFewRows = 16, kFewMax = 64;
 // Query rows of a segment on the tile kernel.
 constexpr int kTileRows = 512;
 

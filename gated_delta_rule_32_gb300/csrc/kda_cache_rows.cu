@@ -2,8 +2,8 @@
 // query rows per key / value head (decode steps, short drafts), and the join
 // of parts.
 //
-// Bound by the cache's bytes: every code is used for at most 16 query rows,
-// 4 * 16 flops per byte.  The work is cut in units of 64 NB tokens of a (request,
+// Bound by the cache's bytes: every code is used for at most 16 query rows
+// at a time, 2 * 16 flops per byte (up to 64 rows of a request run as groups).  The work is cut in units of 64 NB tokens of a (request,
 // head) and every CTA takes an equal share of all units, so ragged batches
 // and single long requests fill the chip alike; a (request, head) that
 // crosses a CTA boundary leaves parts, which kda_attn_join_kernel joins.
@@ -117,11 +117,15 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
   const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
 
   auto blocks_of = [&](const Req& q) -> int64_t {
-    if ((int64_t)q.n * G > kFewRows) return 0;
+    if ((int64_t)q.n * G > kFewMax) return 0;
     return max(1, (int)(((int64_t)q.kv + C::kUnit - 1) / C::kUnit));
   };
   kernel_may_follow();
-  Share sh = find_share<kThreads>(p, blockIdx.x, [&](const Req& q) { return blocks_of(q) * p.Hkv; });
+  auto groups_of = [&](const Req& q) { return (q.n * G + kFewRows - 1) / kFewRows; };
+  Share sh = find_share<kThreads>(p, blockIdx.x, [&](const Req& q) {
+    const int64_t nb = blocks_of(q);
+    return nb ? nb * (p.Hkv * groups_of(q)) : 0;
+  });
   int r = sh.r;
   int64_t base = sh.base, u = sh.u0;
 
@@ -130,18 +134,20 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
     bool bad;
     const Req rq = load_req(p, r, bad);
     const int64_t nb = rq.n > 0 ? blocks_of(rq) : 0;
-    if (u >= base + nb * p.Hkv) {
-      base += nb * p.Hkv;
+    const int groups = nb ? groups_of(rq) : 0;
+    if (u >= base + nb * (p.Hkv * groups)) {
+      base += nb * (p.Hkv * groups);
       ++r;
       continue;
     }
-    const int h = (int)quotient(u - base, nb);
-    const int64_t seg0 = base + h * nb;               // the (request, head)'s units
+    const int hg = (int)quotient(u - base, nb), h = hg / groups;
+    const int64_t seg0 = base + hg * nb;              // the (request, head, group)'s units
     const int b0 = (int)(u - seg0);
     const int b1 = (int)(min(sh.u1, seg0 + nb) - seg0);
     const bool whole = b0 == 0 && b1 == nb;
-    const int rows = rq.n * G, kv = rq.kv;
-    if (tid == 0 && b0 > 0) p.parts.head[blockIdx.x] = {seg0, seg0 + nb, rq.c0, rows, h, 0};
+    const int row0 = kFewRows * (hg % groups);
+    const int rows = min(kFewRows, rq.n * G - row0), kv = rq.kv;
+    if (tid == 0 && b0 > 0) p.parts.head[blockIdx.x] = {seg0, seg0 + nb, rq.c0, rows, h, row0};
 
     // queries, in the k order of the keys' chunks; each row scaled to f16
     uint32_t qf[NT][KS][2];
@@ -157,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
       for (int c = 0; c < 2 * KC; ++c) {
         x[c] = make_uint4(0, 0, 0, 0);
         if (row < rows) {
-          const uint16_t* src = p.q + (int64_t)(rq.c0 + row / G) * p.q_stride +
-                                (int64_t)(h * G + row % G) * D + 64 * (c >> 1) + 16 * j +
+          const uint16_t* src = p.q + (int64_t)(rq.c0 + (row0 + row) / G) * p.q_stride +
+                                (int64_t)(h * G + (row0 + row) % G) * D + 64 * (c >> 1) + 16 * j +
                                 8 * (c & 1);
           x[c] = *reinterpret_cast<const uint4*>(src);
         }
@@ -205,10 +211,10 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
         const int col = 8 * nt + 2 * j + c;
         qs[nt][c] = __shfl_sync(~0u, up, (2 * j + c) * 4);
         qb[nt][c] = __shfl_sync(~0u, sum, (2 * j + c) * 4);
-        lim[nt][c] = col < rows ? kv - rq.n + col / G + 1 : 0;
+        lim[nt][c] = col < rows ? kv - rq.n + (row0 + col) / G + 1 : 0;
       }
     }
-    const int all_see = kv - rq.n + 1;  // tokens that every row sees
+    const int all_see = kv - rq.n + row0 / G + 1;  // tokens that every row sees
     const float sm = p.scale * 1.4426950408889634f / code_top(CODE);
 
     // (int8: o[.][KS] is the sum of the weights as the products see them)
@@ -513,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
         acc += f * *reinterpret_cast<float*>(smem + w * C::kWarpBytes + e * 4);
       }
       if (whole) {
-        const int64_t at = (int64_t)(rq.c0 + row / G) * p.Hq + h * G + row % G;
+        const int64_t at =
+            (int64_t)(rq.c0 + (row0 + row) / G) * p.Hq + h * G + (row0 + row) % G;
         reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + ch] =
             __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc / sum);
         if (p.lse && ch == 0)
@@ -593,7 +600,8 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, Parts ro
         for (int e = 0; e < E; ++e) acc[e] += s_o[warp + w][E * lane + e];
       }
     }
-    const int64_t at = (int64_t)(ph.tok0 + row / p.G) * p.Hq + ph.h * p.G + row % p.G;
+    const int of_seg = ph.row0 + row;
+    const int64_t at = (int64_t)(ph.tok0 + of_seg / p.G) * p.Hq + ph.h * p.G + of_seg % p.G;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint32_t y[E / 2];
 #pragma unroll

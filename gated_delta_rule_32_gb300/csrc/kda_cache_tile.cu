@@ -309,7 +309,7 @@ constexpr int kLead = 2;
 struct Tiles {
   int n, kv, tt, count;
   __device__ Tiles(const Req& q, int G) : n(q.n), kv(q.kv), tt(kTileRows / G) {
-    count = q.n * (int64_t)G > kFewRows ? (q.n + tt - 1) / tt : 0;
+    count = q.n * (int64_t)G > kFewMax ? (q.n + tt - 1) / tt : 0;
   }
   __device__ int seen(int i) const { return max(0, kv - n + min(n, (i + 1) * tt)); }
   __device__ int keys(int i) const { return max(1, (int)(((uint32_t)seen(i) + kTok - 1) / kTok)); }

@@ -512,7 +512,7 @@ kda_status kda_cache_append(const uint16_t* k, const uint16_t* v, int64_t k_stri
  * 64 query heads for each; R <= 16384.  max_new: the most new tokens any
  * request has, as far as the host knows (T is always right); a larger
  * request is KDA_ERR_BAD_SEQLENS.  A request whose new tokens make at most
- * 16 query rows for a key / value head runs on a kernel for few rows (bound
+ * 64 query rows for a key / value head runs on a kernel for few rows (bound
  * by the cache's bytes), others on the tensor cores in tiles; both split a
  * long cache over the chip and join the parts.
  * Malformed cu_seqlens or lengths past the table are KDA_ERR_BAD_SEQLENS, a
