@@ -19,7 +19,8 @@ def __getattr__(name):
     # (cache.py needs torch, which the C-level binding does not: imported when asked for)
     if name in _CACHE:
         from . import cache
-        return getattr(cache, name)
+        globals()[name] = getattr(cache, name)
+        return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 

@@ -63,10 +63,10 @@ def _call(dev, dev_status, name, *args):
     """The library's function `name`(*args, dev_status, stream) with device
     `dev` and its current stream.  (A decode step's calls are short: no
     context manager where the device is current, no Stream object.)"""
-    fn = getattr(kda.load(), name)
+    fn = getattr(kda._lib or kda.load(), name)
     status = None if dev_status is None else dev_status.data_ptr()
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, status, stream)
     else:
         with torch.cuda.device(dev):
@@ -78,14 +78,17 @@ def _call(dev, dev_status, name, *args):
 def _pool(dev, k_codes, v_codes, k_scale, v_scale):
     """(num_pages, Hkv, page, d, code) of one layer's cache."""
     shape, dtype = k_codes.shape, k_codes.dtype
-    _need(len(shape) == 4 and shape == v_codes.shape, "codes must be [pages, Hkv, page, d]")
-    _need(dtype in _CODES and v_codes.dtype == dtype, "codes must be int8 or float8_e4m3fn")
-    for x in (k_codes, v_codes):
-        _need(x.is_contiguous() and x.get_device() == dev, "codes must be contiguous, on one device")
+    code = _CODES.get(dtype)
+    _need(len(shape) == 4 and v_codes.shape == shape, "codes must be [pages, Hkv, page, d]")
+    _need(code is not None and v_codes.dtype is dtype, "codes must be int8 or float8_e4m3fn")
+    _need(k_codes.is_contiguous() and v_codes.is_contiguous() and v_codes.get_device() == dev,
+          "codes must be contiguous, on one device")
+    scales = shape[:2]
     for x in (k_scale, v_scale):
-        _need(x.dtype is torch.float32 and x.shape == shape[:2] and x.is_contiguous()
-              and x.get_device() == dev, "scales must be contiguous float32 [pages, Hkv]")
-    return (*shape, _CODES[dtype])
+        if x.dtype is not torch.float32 or x.shape != scales or not x.is_contiguous() or \
+                x.get_device() != dev:
+            raise ValueError("scales must be contiguous float32 [pages, Hkv]")
+    return (*shape, code)
 
 
 def _stride(x, name, dev):
@@ -115,15 +118,18 @@ def page_plan(new_lens, ctx_lens, block_table, free_pages, free_count, T, page, 
     R = new_lens.numel()
     _need(ctx_lens.numel() == R and block_table.dim() == 2 and block_table.shape[0] == R,
           "ctx_lens must be [R] and block_table [R, max_pages]")
-    n = kda.load().kda_page_runs(R, T, page)
+    n = (kda._lib or kda.load()).kda_page_runs(R, T, page)
     _need(n > 0, "no requests, a negative T or a page size that is not 16, 32, 64 or 128")
-    empty, kw = torch.empty, {"dtype": torch.int32, "device": new_lens.device}
-    plan = PagePlan(empty(R + 1, **kw), empty(R, **kw), empty(T, **kw), empty(T, **kw),
-                    empty((n, 4), **kw), empty(1, **kw))
-    cu, kv, slots, positions, runs, left = (x.data_ptr() for x in plan)
+    kw = {"dtype": torch.int32, "device": new_lens.device}
+    runs = torch.empty((n, 4), **kw)
+    # (one allocation for the others, pieces of it)
+    cu, kv, slots, positions, left = torch.empty(2 * R + 2 * T + 2, **kw).unsafe_split_with_sizes(
+        (R + 1, R, T, T, 1))
+    plan = PagePlan(cu, kv, slots, positions, runs, left)
     _call(dev, dev_status, "kda_page_plan", new_lens.data_ptr(), ctx_lens.data_ptr(), R, T,
           page, block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(),
-          free_count.data_ptr(), free_pages.numel(), cu, kv, slots, positions, runs, left)
+          free_count.data_ptr(), free_pages.numel(), cu.data_ptr(), kv.data_ptr(),
+          slots.data_ptr(), positions.data_ptr(), runs.data_ptr(), left.data_ptr())
     return plan
 
 
