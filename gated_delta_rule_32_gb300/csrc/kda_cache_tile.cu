@@ -302,7 +302,7 @@ __device__ inline int64_t sum_tiles(uint32_t n, uint32_t a, uint32_t b) {
 // What a segment costs beside its key tiles (queries in, O out, the first
 // tile's maximum), in key tiles: the schedule counts it as so many units that
 // hold no work.
-constexpr int kLead = 2;
+constexpr int kLead = 4;
 
 // The row tiles of a request: tile i holds tokens [i tt, (i + 1) tt) and sees
 // the first `seen(i)` tokens, in key tiles of which it has one at least.
@@ -508,21 +508,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = all_wait(&bars.s_full[wg], it & 1);
         if (!ok) break;
         sm100::tc_fence_after();
-        // Weights with the reference m of the tiles before; only where a row's
-        // weights sum to more than 2^15 (f16 ends at 65504), in the first
-        // tile, or when a page's value scale passes vref, is the maximum
-        // sought, O rescaled and the tile's weights made again.  So S is read
-        // once, and O almost never.
+        // Weights with the reference m of the tiles before, in the first tile
+        // with the maximum over its first 32 tokens.  Only where a row's
+        // weights sum to more than 2^15 (f16 ends at 65504), or when a page's
+        // value scale passes vref, is the tile's maximum sought, O rescaled
+        // and the tile's weights made again.  So S is read once, and O almost
+        // never.
         uint32_t z[64];
         float lt;
-        bool fresh = k == 0 || vmax > vref;
+        int fresh = k == 0 ? 32 : vmax > vref ? kTok : 0;  // tokens of the maximum that is sought
         for (;;) {
           if (fresh) {
             float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int c0 = t0 + 32 * c;
-              if (c0 >= lim_hi) break;
+              if (c0 >= lim_hi || 32 * c >= fresh) break;
               const float2 ks = sc.k[c];
               uint32_t s[32];
               tmem_ld32(tS + 32 * c, s);
@@ -625,8 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           lt = la + lb;
           // no weight above the sum; an infinity or NaN is seen too
           const bool over = !(lt <= 32768.0f);
-          if (fresh || !__any_sync(~0u, over)) break;
-          fresh = true;
+          if (fresh == kTok || !__any_sync(~0u, over)) break;
+          fresh = kTok;
         }
         l += lt;
         __syncwarp();
