@@ -69,6 +69,8 @@ constexpr int kPlanThreads = 512;
 // is one launch and no CTA waits for another; CTA 0 writes what is per
 // request.  Nothing that another CTA reads is written: fresh table columns
 // are computed from the stack by whoever needs them, not read back.
+// Bound by latency (a chain of dependent loads and two barriers): 4.1 us for 64
+// requests' decode step, 4.7 us for 17 prompts with 37 000 tokens.
 __global__ void __launch_bounds__(kPlanThreads) kda_page_plan_kernel(PlanArgs p) {
   extern __shared__ int32_t sm[];
   int32_t* s_tok = sm;                 // [R] first packed row
@@ -171,7 +173,7 @@ struct ReleaseArgs {
 };
 
 // One CTA: the pages of finished requests are few, and one CTA needs no
-// order among others to update the stack in place.
+// order among others to update the stack in place.  Bound by latency.
 __global__ void __launch_bounds__(kPlanThreads) kda_page_release_kernel(ReleaseArgs p) {
   extern __shared__ int32_t s_first[];  // [R] pages pushed by the requests before
   __shared__ Sums s_warp[kPlanThreads / 32];
@@ -229,7 +231,9 @@ struct AppendArgs {
   int T, num_pages, H;
 };
 
-// Threads: kAppendPasses 16-byte pieces each where the page has so many.
+// Threads: kAppendPasses 16-byte pieces each where the page has so many.  More
+// pieces a thread are more bytes in flight an SM until registers run out: the
+// prompts' append took 51.6 / 43.6 / 85 us with 4 / 8 / 16.
 constexpr int kAppendPasses = 8;
 __host__ __device__ constexpr int append_threads(int page, int d) {
   const int n = page * d / 8 / kAppendPasses;
@@ -292,15 +296,16 @@ __device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float pre, floa
 }
 
 // One CTA per (run, head, tensor).  The run's values are read once, into
-// registers (at most page * d = 128 per thread), their largest magnitude is
-// found by an unsigned maximum of the bit patterns without the sign (which
-// orders finite < infinity < NaN), and the codes are written from the
-// registers.
+// registers, their largest magnitude is found by an unsigned maximum of the bit
+// patterns without the sign (which orders finite < infinity < NaN), and the
+// codes are written from the registers.  A stream of 3 bytes a value: 17 prompts
+// with 37 000 tokens of 8 heads (230 MB) take 43.6 us, 5.27 TB/s; one token of
+// each of 64 requests 4.0 us, which is latency.
 template <int CODE, int D, int PAGE>
 __global__ void __launch_bounds__(append_threads(PAGE, D)) kda_cache_append_kernel(AppendArgs p) {
   constexpr int NT = append_threads(PAGE, D);
-  constexpr int TPR = D / 8;                     // threads per token, 8 values each
-  constexpr int RPP = NT / TPR;      // tokens per pass
+  constexpr int TPR = D / 8;     // threads per token, 8 values each
+  constexpr int RPP = NT / TPR;  // tokens per pass
   constexpr int PASSES = PAGE / RPP;
   constexpr float TOP = code_top(CODE);
   __shared__ uint32_t s_max[NT / 32];
@@ -476,7 +481,8 @@ extern "C" kda_status kda_cache_append(const uint16_t* k, const uint16_t* v, int
   if (T < 0 || num_runs < 0 || num_pages < 1 || Hkv < 1) return KDA_ERR_INVALID_ARG;
   if (!runs || !k_codes || !v_codes || !k_scale || !v_scale) return KDA_ERR_INVALID_ARG;
   if (T > 0 && (!k || !v)) return KDA_ERR_INVALID_ARG;
-  if (!page_ok(page) || !head_dim_ok(d) || (code != KDA_I8 && code != KDA_E4M3))
+  if (!page_ok(page) || !head_dim_ok(d) || (code != KDA_I8 && code != KDA_E4M3) || Hkv > 4096 ||
+      T > (1 << 26))
     return KDA_ERR_UNSUPPORTED;
   const int64_t width = (int64_t)Hkv * d;
   if (k_stride < width || v_stride < width) return KDA_ERR_INVALID_ARG;

@@ -22,7 +22,7 @@ Layout layout(int max_new, int G, int d) {
   const int sms = kda_device_sms();
   const int64_t rows = (int64_t)max_new * G;
   w.ctas[0] = sms * 3;  // as many as the kernel's registers let an SM hold
-  w.ctas[1] = rows > kFewMax ? sms / 2 : 0;  // (pairs of CTAs)
+  w.ctas[1] = rows > few_max(d) ? sms / 2 : 0;  // (pairs of CTAs)
   size_t at = 0;
   for (int i = 0; i < 2; ++i) {
     const size_t parts = (size_t)2 * w.ctas[i] * kPartRows[i];
@@ -90,7 +90,7 @@ extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
   while ((1 << lg) < page) ++lg;
   AttnArgs p{q, q_stride, cu_seqlens, kv_lens, block_table, (const uint8_t*)k_codes,
              (const uint8_t*)v_codes, k_scale, v_scale, out, lse, dev_status, R, T, max_new,
-             max_pages, Hq, Hkv, Hq / Hkv, num_pages, lg, scale, {}};
+             max_pages, Hq, Hkv, Hq / Hkv, num_pages, lg, few_max(d), scale, {}};
   const Layout w = layout(max_new, p.G, d);
   if (w.ctas[0] < 1) return KDA_ERR_CUDA;
   const bool own = workspace == nullptr;

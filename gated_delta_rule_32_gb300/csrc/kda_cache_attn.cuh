@@ -34,17 +34,19 @@ struct AttnArgs {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int R, T, max_new, max_pages, Hq, Hkv, G, num_pages, page_log2;
+  int R, T, max_new, max_pages, Hq, Hkv, G, num_pages, page_log2, few_max;
   float scale;
   Parts parts;  // of the kernel that the arguments are for
 };
 
-// A request with at most kFewMax query rows per key / value head runs on the
-// few-row kernel, in groups of kFewRows.  With 64 rows (32 requests of 4 tokens
-// over 2 300 cached ones on average, 2 heads of 16, d = 64) that kernel took
-// 42 us and the tile kernel 53; a group costs it as much as the first one,
-// so past 64 rows the tile kernel's 512-row segments win.
-constexpr int kFewRows = 16, kFewMax = 64;
+// A request with at most few_max(d) query rows per key / value head runs on the
+// few-row kernel, in groups of kFewRows.  Every group converts all codes once
+// more, so its time grows with rows times d, the tile kernel's hardly up to its
+// 512-row segments.  Few-row against tile kernel: d = 64 (32 requests, 2400
+// cached tokens on average, 2 heads) 64 rows 41 : 55 us, 128 rows 68 : 56; d =
+// 128 (48 requests, 1700 tokens, 4 heads) 32 rows 84 : 105, 64 rows 144 : 107.
+constexpr int kFewRows = 16;
+__host__ __device__ constexpr int few_max(int d) { return 4096 / d; }
 // Query rows of a segment on the tile kernel.
 constexpr int kTileRows = 512;
 
@@ -135,13 +137,14 @@ __device__ __forceinline__ Share find_share(const AttnArgs& p, int worker, Units
 
 // Loads that are zero (or -1) where `use` is false: predicated, so that
 // nothing waits for them before their value is used.
+template <int OFFSET>
 __device__ __forceinline__ uint4 load16_if(const void* src, bool use) {
   uint4 v;
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n"
-      " mov.b32 %2, 0;\n mov.b32 %3, 0;\n @p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      " mov.b32 %2, 0;\n mov.b32 %3, 0;\n @p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4 + %6];\n}"
       : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(src), "r"((int)use));
+      : "l"(src), "r"((int)use), "n"(OFFSET));
   return v;
 }
 __device__ __forceinline__ int load_page_if(const int32_t* src, bool use) {
@@ -161,12 +164,19 @@ __device__ __forceinline__ float load_scale_if(const float* src, bool use) {
   return v;
 }
 
-// The smallest power of two not below x (x > 0 finite), 2^127 at most: its
-// reciprocal is exact.
+// The smallest power of two not below x, from 2^-126 to 2^126 (of which x may so
+// be up to four times as much), and the reciprocal of such a power (a division
+// takes its slow path at the range's ends).
 __device__ __forceinline__ float pow2_above(float x) {
   const uint32_t b = __float_as_uint(fmaxf(x, 0x1p-126f)) + 0x007fffffu;
-  return __uint_as_float(min(b & 0x7f800000u, 0x7f000000u));
+  return __uint_as_float(min(b & 0x7f800000u, 0x7e800000u));
 }
+__device__ __forceinline__ float pow2_inverse(float x) {
+  return __uint_as_float(0x7f000000u - __float_as_uint(x));
+}
+// The largest sum of weights with which a tile's weights, times up to four, fit
+// f16, which ends at 65504.
+constexpr float kMaxWeights = 8192.0f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

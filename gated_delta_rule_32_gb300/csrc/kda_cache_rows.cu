@@ -3,10 +3,19 @@
 // of parts.
 //
 // Bound by the cache's bytes: every code is used for at most 16 query rows
-// at a time, 2 * 16 flops per byte (up to 64 rows of a request run as groups).  The work is cut in units of 64 NB tokens of a (request,
-// head) and every CTA takes an equal share of all units, so ragged batches
-// and single long requests fill the chip alike; a (request, head) that
-// crosses a CTA boundary leaves parts, which kda_attn_join_kernel joins.
+// at a time, 2 * 16 flops per byte (more rows of a request run as groups).
+// The work is cut in units of 64 NB tokens of a (request, head, group) and every
+// CTA takes an equal share of all units, so ragged batches and single long
+// requests fill the chip alike; a segment that crosses a CTA boundary leaves
+// parts, which kda_attn_join_kernel joins.
+//
+// 64 requests' decode step on up to 8192 cached tokens (8 heads, d = 128, 654 MB
+// of codes): 140 us with the join, 4.7 TB/s; a kernel that only reads as many
+// bytes takes 108-118 us, and the SMs' times for equal shares differ by half.
+// Two contexts of up to 262144 tokens (4 heads): 86 us.  One request of 700
+// tokens: 11 us, of which the schedule, the chain of one CTA and the join take
+// about equal parts.  Three CTAs an SM, as many as the registers allow; shares
+// half as long (six an SM) took 141 us, four CTAs an SM with NB = 1 142 us.
 //
 // Warp w of a CTA takes every fourth run of NB 16-token blocks.  Products run on
 // mma.m16n8k16 with the tokens (then the channels) on the 16-row side, which
@@ -82,7 +91,9 @@ __device__ __forceinline__ int value_at(int t, int c) {
                   : (t ^ ((t >> 1) & 1)) * 64 + ((c ^ ((t >> 1) & 2)) << 4);
 }
 
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -117,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
   const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
 
   auto blocks_of = [&](const Req& q) -> int64_t {
-    if ((int64_t)q.n * G > kFewMax) return 0;
+    if ((int64_t)q.n * G > few_max(D)) return 0;
     return max(1, (int)(((int64_t)q.kv + C::kUnit - 1) / C::kUnit));
   };
   kernel_may_follow();
@@ -220,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
     // (int8: o[.][KS] is the sum of the weights as the products see them)
     constexpr int KO = CODE == KDA_I8 ? KS + 1 : KS;
     float o[NT][KO][4], m[NT][2], l[NT][2];
-    float vref = 0.0f, vinv = 1.0f;
+    float vinv[NT][2];  // 1 / vref, a power of two not below the value scales seen
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -228,7 +239,10 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) m[nt][c] = l[nt][c] = 0.0f;
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = l[nt][c] = 0.0f;
+        vinv[nt][c] = 0x1p126f;
+      }
     }
 
     // this warp's runs of NB blocks: 4 (b0 + i) + warp, i < count
@@ -354,17 +368,20 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
         }
         // Weights with the standing reference m of each row, which need not be
         // the maximum: it is sought, with shuffles, only in the first run, when
-        // weights sum to more than 2^15 (f16 ends at 65504), or when a page's
-        // value scale passes vref.  Most runs need one vote.  (A masked score is
-        // a NaN until here, a masked weight 0.)
+        // weights sum to more than f16 holds, or when the value scale of a page
+        // that the row sees passes vref.  Most runs need one vote.  (A masked
+        // score is a NaN until here, a masked weight 0.)
         float w[NB][NT][4], lt[NT][2];
-        bool fresh = i == 0 || vmax > vref;
+        // the largest value scale that a column's row sees
+        auto scales_seen = [&](int nt, int c) {
+          if (!EDGE) return vmax;
+          const float a = tok < lim[nt][c] ? vs[0] : 0.0f;
+          return NB == 2 && tok + 16 < lim[nt][c] ? fmaxf(a, vs[NB - 1]) : a;
+        };
+        // (rows' scales part only where not all see the same pages)
+        bool fresh = i == 0 || (!EDGE && vmax * vinv[0][0] > 1.0f);
         for (;;) {
           if (fresh) {
-            const float vnew = vmax > vref ? pow2_above(vmax) : vref;
-            const float fv = vnew > 0.0f ? vref / vnew : 1.0f;
-            vref = vnew;
-            vinv = vnew > 0.0f ? 1.0f / vnew : 1.0f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float f[2];
@@ -383,7 +400,12 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
                 f[c] = i == 0 ? 0.0f : ex2(m[nt][c] - mn);
                 m[nt][c] = mn;
                 l[nt][c] *= f[c];
-                f[c] *= fv;
+                const float vm = scales_seen(nt, c);
+                if (vm * vinv[nt][c] > 1.0f) {
+                  const float vnew = pow2_inverse(pow2_above(vm));
+                  f[c] = f[c] * pow2_inverse(vinv[nt][c]) * vnew;
+                  vinv[nt][c] = vnew;
+                }
               }
 #pragma unroll
               for (int s = 0; s < KO; ++s)
@@ -404,7 +426,11 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
                 lt[nt][e & 1] += w[b][nt][e];
               }
             // (columns without a row see no token; a NaN counts as over)
-            over |= !(lt[nt][0] <= 32768.0f && lt[nt][1] <= 32768.0f);
+            over |= !(lt[nt][0] <= kMaxWeights && lt[nt][1] <= kMaxWeights);
+            if (EDGE) {
+              over |= scales_seen(nt, 0) * vinv[nt][0] > 1.0f;
+              over |= scales_seen(nt, 1) * vinv[nt][1] > 1.0f;
+            }
           }
           if (fresh || !__any_sync(~0u, over)) break;
           fresh = true;
@@ -416,11 +442,10 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
           l[nt][1] += lt[nt][1];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const float vw = vs[b] * vinv;
             float y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              y[e] = w[b][nt][e] * vw;
+              y[e] = w[b][nt][e] * (vs[b] * (EDGE ? vinv[nt][e & 1] : vinv[0][0]));
               // (0 times a scale that may be NaN)
               if (EDGE && tok + 16 * b + i8 + 8 * (e >> 1) >= lim[nt][e & 1]) y[e] = 0.0f;
             }
@@ -480,11 +505,11 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
 
     // the warps' sums meet in shared memory (each in its own ring)
     float* so = reinterpret_cast<float*>(ring);
-    const float ov = vref / code_top(CODE);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        const float ov = pow2_inverse(vinv[nt][c]) * (1.0f / code_top(CODE));
         const float ob =
             CODE == KDA_I8 ? o[nt][KO - 1][c] * (bias_of<CODE>() / unit_of<CODE>()) : 0.0f;
         float y = l[nt][c];
@@ -541,20 +566,23 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
 // Joins the parts of the segments that cross CTA boundaries, in CTA order:
 // out = sum_c w_c O_c / sum_c w_c l_c with w_c = 2^(m_c - max m).  A block looks
 // at the boundary between CTAs c and c + 1 of a kernel and works if it is the
-// first inside its segment, on up to 4 rows of the few-row kernel (a long cache
-// leaves as many parts as there are CTAs) or 32 of the tile kernel (two or
-// three parts).  Where the rows are fewer than its 8 warps, several warps
-// share a row's parts.
+// first inside its segment, on up to `group` rows.  The tile kernel leaves two or
+// three parts a segment: 32 rows (8 or 128 took 110 and 125 us where 32 take
+// 104, a prompt's piece among decode steps).  The few-row kernel leaves as many
+// as there are CTAs for its segments: 16 rows where four or fewer are to be
+// expected (drafts of 32 requests: 38.6 us, 41.7 with 4 rows), else 4 (two long
+// contexts: 86.6 us, 97.7 with 16 rows).  Where the rows are fewer than its 8
+// warps, several warps share a row's parts.
 template <int D>
 __global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, Parts rows_kernel,
                                                             Parts tile_kernel,
-                                                            int few_blocks) {
+                                                            int few_blocks, int few_group) {
   constexpr int E = D / 32;
   __shared__ float s_o[8][D], s_l[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool few = (int)blockIdx.x < few_blocks;
   const Parts q = few ? rows_kernel : tile_kernel;
-  const int of = few ? blockIdx.x : (int)blockIdx.x - few_blocks, group = few ? 4 : 32;
+  const int of = few ? blockIdx.x : (int)blockIdx.x - few_blocks, group = few ? few_group : 32;
   const int c0 = of % (q.ctas - 1), row0 = group * (of / (q.ctas - 1));
   wait_for_kernel_before();
   const PartHead ph = q.head[c0 + 1];
@@ -568,7 +596,9 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, Parts ro
   for (int i = warp / wpr; i < n; i += 8 / wpr) {
     const int row = row0 + i;
     // the first CTA holds it as its last segment, the others as their first
-    auto part = [&](int c) -> int64_t { return (2 * (int64_t)c + (c == ca ? 1 : 0)) * q.rows + row; };
+    auto part = [&](int c) -> int64_t {
+      return (2 * (int64_t)c + (c == ca ? 1 : 0)) * q.rows + row;
+    };
     float mx = -INFINITY, acc[E] = {}, sum = 0.0f;
     for (int c = ca + lane; c <= cb; c += 32) mx = fmaxf(mx, q.ml[part(c) * 2]);
 #pragma unroll
@@ -630,7 +660,8 @@ kda_status launch_rows(const AttnArgs& p, cudaStream_t s) {
 
 template <int CODE, int D>
 kda_status launch_nt(const AttnArgs& p, cudaStream_t s) {
-  // one 8-row tile where no request can have more rows than that
+  // one 8-row tile where no request can have more rows than that: two, the
+  // second empty, took 160 us where one takes 142 (64 decode steps of 4 rows)
   if ((int64_t)p.max_new * p.G <= 8) return launch_rows<CODE, D, 1>(p, s);
   return launch_rows<CODE, D, 2>(p, s);
 }
@@ -646,9 +677,13 @@ kda_status kda_launch_attn_join(const AttnArgs& p, const Parts& tile, int d, cud
   const int64_t most = (int64_t)p.max_new * p.G;
   const int few_rows = most < kFewRows ? (int)most : kFewRows;
   const int tile_rows = most < kTileRows ? (int)most : kTileRows;
-  const int few_blocks = (p.parts.ctas - 1) * ((few_rows + 3) / 4);
+  const int64_t groups = ((most < p.few_max ? most : p.few_max) + kFewRows - 1) / kFewRows;
+  const int64_t segments = groups * p.R * p.Hkv;
+  const int few_group = 4 * segments >= p.parts.ctas ? kFewRows : 4;
+  const int few_blocks = (p.parts.ctas - 1) * ((few_rows + few_group - 1) / few_group);
   const int tile_blocks = tile.ctas > 1 ? (tile.ctas - 1) * ((tile_rows + 31) / 32) : 0;
   if (few_blocks + tile_blocks == 0) return KDA_OK;
   return launch_following(d == 64 ? kda_attn_join_kernel<64> : kda_attn_join_kernel<128>,
-                          few_blocks + tile_blocks, 256, 0, s, p, p.parts, tile, few_blocks);
+                          few_blocks + tile_blocks, 256, 0, s, p, p.parts, tile, few_blocks,
+                          few_group);
 }

@@ -15,8 +15,8 @@
 //   0-3, 4-7   softmax of row tile 0 / 1, one thread per row
 //   8-11       keys:   codes -> f16 operand tiles in shared memory
 //   12-15      values: the same; between segments 8-15 convert the queries
-//   16         owns tensor memory; of the first CTA: issues all products (one
-//              thread)
+//   16         owns tensor memory; of the first CTA: issues all products (in
+//              step, one thread carrying them out)
 //   17         walks the schedule and looks up the pages' scales, some key
 //              tiles ahead of the softmax
 //   18, 19     bring the next segment's queries into L2
@@ -24,10 +24,24 @@
 // place, in f16), O of both tiles.
 //
 // Codes are exact in f16, so the only roundings of the products' inputs are
-// those of P (11 bits) and of small query elements next to large ones of the
-// same row.  A page's key scale multiplies its scores after the product; its
-// value scale multiplies its columns of P, relative to a power of two at
+// those of P (11 bits, and 2^-25 of the reference's weight and the largest
+// value scale at the small end) and of small query elements next to large ones
+// of the same row.  A page's key scale multiplies its scores after the product;
+// its value scale multiplies its columns of P, relative to a power of two at
 // least as large (vref), which leaves O at the end.
+//
+// Bound by the products where rows are many: 4 D flops for each row and token,
+// at 2048 tokens on 32768 cached (32 heads on 4, d = 128) 842 us, 1347 TFLOP/s;
+// the tensor cores work 2 x 1024 of the 2.6-2.9k cycles that a key tile of both
+// row tiles takes, and the rest is the chain of one row tile, which the other's
+// products cover in part only: products 1024 -> softmax 1480-1900 (exponentials
+// at 32 a cycle an SM) -> store and arrivals about 420.  Measured against it:
+// one CTA a tile 1026 us; S in two halves, so that a row tile's products and
+// softmax overlap, 914-1040 us (products of 64 tokens take 48 cycles, not 32:
+// shared memory); a second warp issuing products 950-987 us.  Prompts without a
+// cache, 9 of up to 4096 tokens (32 heads on 8): 466 us, 916 TFLOP/s; half of
+// a tile on the diagonal is masked, and a segment's own cost (queries in, O out)
+// weighs more where its keys are few.
 #include <type_traits>
 
 #include "kda_cache_attn.cuh"
@@ -38,14 +52,19 @@ namespace {
 using namespace kda_cache;
 
 // Five warpgroups launched with 96 registers a thread; they share them out
-// anew (setmaxnreg): 2 x 136 + 2 x 72 + 64 = 5 x 96.
+// anew (setmaxnreg): 2 x 152 + 2 x 64 + 48 = 5 x 96.  Prompts of up to 4096
+// tokens and 2048 tokens on 32768 cached took 466 and 842 us so, 502 and 878
+// with 136 / 72 / 64, 481 and 880 with 144 / 72 / 48, 479 and 894 with
+// 160 / 56 / 48, where the converters spill in their loop.
 constexpr int kThreads = 640;
-constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 64;
+constexpr int kRegsSoftmax = 152, kRegsConvert = 64, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue == 5 * 96, "registers at launch");
 constexpr int kTok = 128;    // tokens per key tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-constexpr int kStages = 4;   // key and value tiles in shared memory
+// Key and value tiles in shared memory: what 227 KB hold beside the queries at
+// D = 128.
+constexpr int kStages = 4;
 
 template <int D>
 struct Smem {
@@ -87,7 +106,7 @@ constexpr int kReaders = 19;  // warps that read it
 // scale, and the largest value scale.
 struct Scales {
   float2 k[4], v[4];
-  float vmax, pad[3];
+  float vmax;
 };
 constexpr int kRing = 4;
 
@@ -259,6 +278,15 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t one) {
       : "memory");
 }
 
+// f(0), ..., f(N - 1), the argument a constant
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void for_each_of(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    for_each_of<N, I + 1>(f);
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -301,15 +329,16 @@ __device__ inline int64_t sum_tiles(uint32_t n, uint32_t a, uint32_t b) {
 
 // What a segment costs beside its key tiles (queries in, O out, the first
 // tile's maximum), in key tiles: the schedule counts it as so many units that
-// hold no work.
+// hold no work.  Prompts of up to 4096 tokens took 531 / 505 / 501 / 528 us with
+// 2 / 3 / 4 / 6 of them.
 constexpr int kLead = 4;
 
 // The row tiles of a request: tile i holds tokens [i tt, (i + 1) tt) and sees
 // the first `seen(i)` tokens, in key tiles of which it has one at least.
 struct Tiles {
   int n, kv, tt, count;
-  __device__ Tiles(const Req& q, int G) : n(q.n), kv(q.kv), tt(kTileRows / G) {
-    count = q.n * (int64_t)G > kFewMax ? (q.n + tt - 1) / tt : 0;
+  __device__ Tiles(const Req& q, const AttnArgs& p) : n(q.n), kv(q.kv), tt(kTileRows / p.G) {
+    count = q.n * (int64_t)p.G > p.few_max ? (q.n + tt - 1) / tt : 0;
   }
   __device__ int seen(int i) const { return max(0, kv - n + min(n, (i + 1) * tt)); }
   __device__ int keys(int i) const { return max(1, (int)(((uint32_t)seen(i) + kTok - 1) / kTok)); }
@@ -338,7 +367,7 @@ struct Walk {
   // (a whole warp, every lane with the same values)
   __device__ Walk(const AttnArgs& p_, const Share& s)
       : p(p_), u(s.u0), u1(s.u1), base(s.base), r(s.r), h(0), tile(0), b0(0), b1(0), nu(0),
-        per_head(0), seg0(0), q{0, 0, 0}, t(Req{0, 0, 0}, 1) {
+        per_head(0), seg0(0), q{0, 0, 0}, t(Req{0, 0, 0}, p_) {
     if (u >= u1) return;
     load();
     const int64_t in = u - base;
@@ -359,7 +388,7 @@ struct Walk {
   __device__ void load() {
     bool bad;
     q = load_req(p, r, bad);
-    t = Tiles(q, p.G);
+    t = Tiles(q, p);
     per_head = t.count ? t.before(t.count) : 0;
   }
   __device__ void set() {
@@ -442,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   sm100::tc_fence_before();
   kernel_may_follow();
   const Share share = find_share<kThreads>(p, pair, [&](const Req& q) {
-    const Tiles t(q, p.G);
+    const Tiles t(q, p);
     return t.count ? t.before(t.count) * p.Hkv : 0;
   });
   cluster_sync();  // (both CTAs' barriers are there)
@@ -496,7 +525,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int lim_hi = __reduce_max_sync(~0u, lim);
       if (!mine) lim = lim_hi;
       const int lim_lo = __reduce_min_sync(~0u, lim);
-      float m = -INFINITY, l = 0.0f, vref = 0.0f, vrel_of = 1.0f;
+      float m = -INFINITY, l = 0.0f;
+      // 1 / vref, a power of two not below the value scales seen; the warp's vref
+      float vrel = 0x1p126f, vtop = 0.0f;
       bool ok = all_wait(&bars.qs_full[wg][seg & 1], (seg >> 1) & 1);
       const float qs = s_qscale[seg & 1][128 * wg + 32 * (warp & 3) + lane];
       for (int k = 0; ok && k < nk; ++k, ++it, ++tiles) {
@@ -510,17 +541,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sm100::tc_fence_after();
         // Weights with the reference m of the tiles before, in the first tile
         // with the maximum over its first 32 tokens.  Only where a row's
-        // weights sum to more than 2^15 (f16 ends at 65504), or when a page's
-        // value scale passes vref, is the tile's maximum sought, O rescaled
-        // and the tile's weights made again.  So S is read once, and O almost
-        // never.
+        // weights sum to more than f16 holds, or when a page's value scale passes
+        // those before, is the tile's maximum sought, O rescaled and the tile's
+        // weights made again.  So S is read once, and O almost never.  (vtop is
+        // the warp's: it equals 1 / vrel of the rows that have seen all pages so
+        // far, and the others see nothing any more.)
         uint32_t z[64];
         float lt;
-        int fresh = k == 0 ? 32 : vmax > vref ? kTok : 0;  // tokens of the maximum that is sought
+        int fresh = k == 0 ? 32 : vmax > vtop ? kTok : 0;  // tokens of the maximum that is sought
         for (;;) {
-          if (fresh) {
+          if (fresh) {  // (rare: kept short, the loop's code must fit the caches)
             float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const int c0 = t0 + 32 * c;
               if (c0 >= lim_hi || 32 * c >= fresh) break;
@@ -548,15 +580,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // (a row that sees nothing here sees nothing further on: 0 serves)
             const float mn = fmaxf(m, mx) == -INFINITY ? 0.0f : fmaxf(m, mx);
-            const float vnew = vmax > vref ? pow2_above(vmax) : vref;
-            const float fm = k == 0 ? 0.0f : ex2(m - mn);
-            const float f = vnew > 0.0f ? vref / vnew * fm : fm;
+            float f = k == 0 ? 0.0f : ex2(m - mn);
             m = mn;
-            l *= fm;
-            vref = vnew;
-            vrel_of = vnew > 0.0f ? 1.0f / vnew : 1.0f;
+            l *= f;
+            float vm = vmax;  // the largest value scale that the row sees
+            if (t0 + kTok > lim_lo) {
+              vm = 0.0f;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                if (t0 + 32 * c < lim) vm = fmaxf(vm, sc.v[c].x);
+                if (t0 + 32 * c + 16 < lim) vm = fmaxf(vm, sc.v[c].y);
+              }
+            }
+            if (vm * vrel > 1.0f) {
+              const float vnew = pow2_inverse(pow2_above(vm));
+              f = f * pow2_inverse(vrel) * vnew;
+              vrel = vnew;
+            }
+            if (vmax > vtop) vtop = pow2_above(vmax);
             if (k > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 __syncwarp();
@@ -576,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint32_t s[32];
               tmem_ld32(tS + 32 * c, s);
               const float f0 = ks.x * qs, f1 = ks.y * qs;
-              const float v0 = vs.x * vrel_of, v1 = vs.y * vrel_of;
+              const float v0 = vs.x * vrel, v1 = vs.y * vrel;
               tmem_wait_ld32(s);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -604,8 +647,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tmem_ld32(tS + 32 * c, s);
               const float f0 = ks.x * qs, f1 = ks.y * qs;
               // (where the row sees nothing of a group its scale may be a NaN)
-              const float v0 = c0 < lim ? vs.x * vrel_of : 0.0f;
-              const float v1 = c0 + 16 < lim ? vs.y * vrel_of : 0.0f;
+              const float v0 = c0 < lim ? vs.x * vrel : 0.0f;
+              const float v1 = c0 + 16 < lim ? vs.y * vrel : 0.0f;
               tmem_wait_ld32(s);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -625,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           unpack2(l2, la, lb);
           lt = la + lb;
           // no weight above the sum; an infinity or NaN is seen too
-          const bool over = !(lt <= 32768.0f);
+          const bool over = !(lt <= kMaxWeights);
           if (fresh == kTok || !__any_sync(~0u, over)) break;
           fresh = kTok;
         }
@@ -644,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok || !all_wait(&bars.o_full[wg], seg & 1)) break;
       ++seg;
       sm100::tc_fence_after();
-      const float ov = vref / code_top(CODE);
+      const float ov = pow2_inverse(vrel) * (1.0f / code_top(CODE));
       const bool whole = g.b0 == 0 && g.b1 == g.nu;
       const int64_t slot = 2 * (int64_t)pair + (g.b0 > 0 ? 0 : 1);
       const int64_t at = (int64_t)(g.c0 + tok) * p.Hq + g.h * p.G + row % p.G;
@@ -678,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       // (a row that has seen nothing: its weights are zeros, so is its sum)
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t y[32], z[16];
         __syncwarp();
@@ -728,7 +771,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               (int64_t)(g.h * p.G + of % p.G) * D + 8 * c4;
         uint4 y[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) y[c] = load16_if(src + 32 * c, of < g.rows);
+        for (int c = 0; c < C; ++c) y[c] = load16_if<0>(src + 32 * c, of < g.rows);
         if (g8 == warp - 8 && i > 0 && !all_wait(&bars.q_empty[t], (i - 1) & 1)) return false;
         uint32_t most = 0;
 #pragma unroll
@@ -780,7 +823,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return !V ? 64 * (i >> 1) + 16 * c4 : D == 128 ? 64 * rank + 16 * c4
                                                        : 32 * rank + 16 * (c4 & 1);
       };
-      auto chunk = [&](int i) { return !V ? 8 * (i >> 1) + 2 * c4 : D == 128 ? 2 * c4 : 2 * (c4 & 1); };
+      auto chunk = [&](int i) {
+        return !V ? 8 * (i >> 1) + 2 * c4 : D == 128 ? 2 * c4 : 2 * (c4 & 1);
+      };
       const int first = V ? 32 * wq : 64 * rank + 16 * wq;  // token of a key tile
       unsigned char* tiles = smem + (V ? Smem<D>::kV + first * 16 : Smem<D>::kK + 16 * wq * 16);
       constexpr int kChunk = V ? 2048 : 1024;
@@ -789,6 +834,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (sg.rows == 0) break;
         const int nk = sg.b1 - sg.b0, kv = sg.kv;
         const int32_t* table = p.table + (int64_t)sg.r * p.max_pages;
+        // A page holds a divisor of a key tile's tokens, so a token's place in
+        // its page is the same in every key tile.
+        const uint32_t page_bytes = (uint32_t)(p.Hkv << lg) * D;
+        auto place_of = [&](int g) {
+          const int at = (sg.h << lg) + ((first + 16 * g) & (P - 1)) + token(0);
+          return codes + (int64_t)at * D + byte(0);
+        };
+        const uint8_t* const at_a = place_of(0);
+        const uint8_t* const at_b = place_of(V ? 1 : 0);
         // the pages of the warp's tokens 0-15 and (values) 16-31
         auto page_of = [&](int k, int g) -> int {
           const int64_t t0 = (int64_t)(sg.b0 + k) * kTok + first + 16 * g;
@@ -796,16 +850,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         uint4 x[N];
         auto fetch = [&](int k, int pa, int pb) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int tk = token(i);
-            const int pg = V && (D == 128 ? i >= 2 : i >= 1) ? pb : pa;
-            const int64_t t = (int64_t)(sg.b0 + k) * kTok + first + tk;
-            const uint8_t* src =
-                codes + ((((int64_t)pg * p.Hkv + sg.h) << lg) + (t & (P - 1))) * D + byte(i);
+          const bool in_a = (uint32_t)pa < (uint32_t)p.num_pages;
+          const bool in_b = (uint32_t)pb < (uint32_t)p.num_pages;
+          const uint8_t* a = at_a + (uint64_t)(uint32_t)pa * page_bytes;
+          const uint8_t* b = at_b + (uint64_t)(uint32_t)pb * page_bytes;
+          const int left = kv - (sg.b0 + k) * kTok - first - token(0);
+          for_each_of<N>([&](auto piece) {
+            constexpr int i = decltype(piece)::value;
+            constexpr int g = !V ? 0 : D == 128 ? i >> 1 : i;  // which 16 tokens
+            constexpr int off = !V         ? 8 * (i & 1) * D + 64 * (i >> 1)
+                                : D == 128 ? 8 * (i & 1) * D
+                                           : 0;
             // (what a page holds past the request's end may be a NaN)
-            x[i] = load16_if(src, (uint32_t)pg < (uint32_t)p.num_pages && (!V || t < kv));
-          }
+            x[i] = load16_if<off>(g ? b : a,
+                                  (g ? in_b : in_a) && (!V || token(i) - token(0) < left));
+          });
         };
         auto place = [&]() -> bool {  // x -> the next stage
           const int st = cnt % kStages;
@@ -931,102 +990,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
         }
       }
-    } else if (warp == 16) {
-    // ----------------------------------------------------------- products
-    // (of the second CTA this warp only lets the segments pass)
-    const uint32_t id_s = idesc_f16(256, kTok, 0), id_o = idesc_f16(256, D, 1);
-    const uint32_t one = elect_one();
-    // (a descriptor's address field counts 16-byte units)
-    const uint64_t dq = sm100::smem_desc(sm100::smem_u32(smem), 2048, 128);
-    const uint64_t dk = sm100::smem_desc(sm100::smem_u32(smem), 1024, 128);
-    const uint64_t dv = sm100::smem_desc(sm100::smem_u32(smem), 128, 2048);
-    const uint32_t q_lo = (uint32_t)dq + Smem<D>::kQ / 16, k_lo = (uint32_t)dk + Smem<D>::kK / 16;
-    const uint32_t v_lo = (uint32_t)dv + Smem<D>::kV / 16;
-    const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32);
-    const uint32_t v_hi = (uint32_t)(dv >> 32);
-    constexpr int kTile16 = Smem<D>::kTile / 16, kQTile16 = Smem<D>::kQTile / 16;
-    auto scores = [&](int t, int st, bool last) {  // S_t = Q_t K^T
-#pragma unroll
-      for (int s = 0; s < D / 64; ++s)
-        mma4_ss(128 * t, q_lo + t * kQTile16 + s * 1024, k_lo + st * kTile16 + s * 512, q_hi, k_hi,
-                id_s, s, one);
-      mma_commit(&bars.s_full[t], one);
-      if (last) mma_commit(&bars.q_empty[t], one);
-    };
-    auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        mma4_ts(256 + D * t, 128 * t + 32 * s, v_lo + st * kTile16 + 64 * s, v_hi, id_o,
-                !first || s > 0, one);
-    };
-    uint32_t n0 = 0, n1 = 0, t0 = 0, t1 = 0;  // segments and key tiles of the row tiles
-    uint32_t kc = 0;                          // key tiles before this one
-    bool ok = true;
-    for (;;) {
-      const Seg g = next_seg();
-      if (g.rows == 0) break;
-      if (rank != 0) continue;
-      // (a reduction's result is known to be uniform)
-      const bool two = __reduce_max_sync(~0u, g.rows) > 256;
-      const int nk = __reduce_max_sync(~0u, g.b1 - g.b0);
-      {
-        const uint32_t st = kc % kStages;
-        ok = all_wait(&bars.k_full[st], (kc / kStages) & 1) &&
-             all_wait(&bars.q_full[0][n0 & 1], (n0 >> 1) & 1);
-        if (!ok) break;
-        ++n0;
-        sm100::tc_fence_after();
-        scores(0, st, nk == 1);
-        if (two) {
-          ok = all_wait(&bars.q_full[1][n1 & 1], (n1 >> 1) & 1);
-          if (!ok) break;
-          ++n1;
-          sm100::tc_fence_after();
-          scores(1, st, nk == 1);
-        }
-        mma_commit(&bars.k_empty[st], one);
-      }
-      // A key tile's weights meet the values, and the next key tile's scores
-      // follow as soon as their place is free.  What the next step needs of
-      // values and keys is waited for while row tile 1's softmax is awaited (it
-      // is there as a rule): a wait takes a few hundred cycles even so.
-      auto tiles_there = [&](int k) -> bool {
-        const uint32_t at = kc + k;
-        return all_wait(&bars.v_full[at % kStages], (at / kStages) & 1) &&
-               (k + 1 == nk ||
-                all_wait(&bars.k_full[(at + 1) % kStages], ((at + 1) / kStages) & 1));
+    } else {
+      // ----------------------------------------------------------- products
+      // (of the second CTA this warp only lets the segments pass)
+      const uint32_t id_s = idesc_f16(256, kTok, 0), id_o = idesc_f16(256, D, 1);
+      const uint32_t one = elect_one();
+      // (a descriptor's address field counts 16-byte units)
+      const uint64_t dq = sm100::smem_desc(sm100::smem_u32(smem), 2048, 128);
+      const uint64_t dk = sm100::smem_desc(sm100::smem_u32(smem), 1024, 128);
+      const uint64_t dv = sm100::smem_desc(sm100::smem_u32(smem), 128, 2048);
+      const uint32_t q_lo = (uint32_t)dq + Smem<D>::kQ / 16, k_lo = (uint32_t)dk + Smem<D>::kK / 16;
+      const uint32_t v_lo = (uint32_t)dv + Smem<D>::kV / 16;
+      const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32);
+      const uint32_t v_hi = (uint32_t)(dv >> 32);
+      constexpr int kTile16 = Smem<D>::kTile / 16, kQTile16 = Smem<D>::kQTile / 16;
+      auto scores = [&](int t, int st, bool last) {  // S_t = Q_t K^T
+  #pragma unroll
+        for (int s = 0; s < D / 64; ++s)
+          mma4_ss(128 * t, q_lo + t * kQTile16 + s * 1024, k_lo + st * kTile16 + s * 512, q_hi,
+                  k_hi, id_s, s, one);
+        mma_commit(&bars.s_full[t], one);
+        if (last) mma_commit(&bars.q_empty[t], one);
       };
-      ok = tiles_there(0);
-      for (int k = 0; ok && k < nk; ++k) {
-        const bool last = k + 1 == nk, before_last = k + 2 == nk;
-        const uint32_t st = (kc + k) % kStages, nt = (kc + k + 1) % kStages;
-        ok = all_wait(&bars.p_full[0], t0++ & 1);
-        if (!ok) break;
-        sm100::tc_fence_after();
-        values(0, st, k == 0);
-        if (last) mma_commit(&bars.o_full[0], one);
-        else scores(0, nt, before_last);
-        if (!last && kStages > 2) {
-          ok = tiles_there(k + 1);
+      auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
+  #pragma unroll
+        for (int s = 0; s < 2; ++s)
+          mma4_ts(256 + D * t, 128 * t + 32 * s, v_lo + st * kTile16 + 64 * s, v_hi, id_o,
+                  !first || s > 0, one);
+      };
+      uint32_t n0 = 0, n1 = 0, t0 = 0, t1 = 0;  // segments and key tiles of the row tiles
+      uint32_t kc = 0;                          // key tiles before this one
+      bool ok = true;
+      for (;;) {
+        const Seg g = next_seg();
+        if (g.rows == 0) break;
+        if (rank != 0) continue;
+        // (a reduction's result is known to be uniform)
+        const bool two = __reduce_max_sync(~0u, g.rows) > 256;
+        const int nk = __reduce_max_sync(~0u, g.b1 - g.b0);
+        {
+          const uint32_t st = kc % kStages;
+          ok = all_wait(&bars.k_full[st], (kc / kStages) & 1) &&
+               all_wait(&bars.q_full[0][n0 & 1], (n0 >> 1) & 1);
           if (!ok) break;
+          ++n0;
+          sm100::tc_fence_after();
+          scores(0, st, nk == 1);
+          if (two) {
+            ok = all_wait(&bars.q_full[1][n1 & 1], (n1 >> 1) & 1);
+            if (!ok) break;
+            ++n1;
+            sm100::tc_fence_after();
+            scores(1, st, nk == 1);
+          }
+          mma_commit(&bars.k_empty[st], one);
         }
-        if (two) {
-          ok = all_wait(&bars.p_full[1], t1++ & 1);
+        // A key tile's weights meet the values, and the next key tile's scores
+        // follow as soon as their place is free.  What the next step needs of
+        // values and keys is waited for while row tile 1's softmax is awaited (it
+        // is there as a rule): a wait takes a few hundred cycles even so.
+        auto tiles_there = [&](int k) -> bool {
+          const uint32_t at = kc + k;
+          return all_wait(&bars.v_full[at % kStages], (at / kStages) & 1) &&
+                 (k + 1 == nk ||
+                  all_wait(&bars.k_full[(at + 1) % kStages], ((at + 1) / kStages) & 1));
+        };
+        ok = tiles_there(0);
+        for (int k = 0; ok && k < nk; ++k) {
+          const bool last = k + 1 == nk, before_last = k + 2 == nk;
+          const uint32_t st = (kc + k) % kStages, nt = (kc + k + 1) % kStages;
+          ok = all_wait(&bars.p_full[0], t0++ & 1);
           if (!ok) break;
           sm100::tc_fence_after();
-          values(1, st, k == 0);
-          if (last) mma_commit(&bars.o_full[1], one);
-          else scores(1, nt, before_last);
+          values(0, st, k == 0);
+          if (last) mma_commit(&bars.o_full[0], one);
+          else scores(0, nt, before_last);
+          if (!last) {
+            ok = tiles_there(k + 1);
+            if (!ok) break;
+          }
+          if (two) {
+            ok = all_wait(&bars.p_full[1], t1++ & 1);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            values(1, st, k == 0);
+            if (last) mma_commit(&bars.o_full[1], one);
+            else scores(1, nt, before_last);
+          }
+          mma_commit(&bars.v_empty[st], one);
+          if (!last) mma_commit(&bars.k_empty[nt], one);
         }
-        mma_commit(&bars.v_empty[st], one);
-        if (!last) mma_commit(&bars.k_empty[nt], one);
+        kc += nk;
+        if (!ok) break;
       }
-      kc += nk;
-      if (!ok) break;
-    }
-    // the last commits (of k_empty, v_empty) must land before the CTA leaves
-    if (rank == 0) mma_commit(&bars.drain, one);
-    sm100::mbar_wait(&bars.drain, 0);
+      // the last commits (of k_empty, v_empty) must land before the CTA leaves
+      if (rank == 0) mma_commit(&bars.drain, one);
+      sm100::mbar_wait(&bars.drain, 0);
     }
   }
   __syncwarp();

@@ -422,8 +422,9 @@ kda_status kda_debug_record_capacity(int64_t items);
  * kda_chunk_fwd takes); block_table [R, max_pages] holds the page number of
  * each request's tokens p * page .. p * page + page - 1 in column p.
  * Columns past a request's last page are never read.  Limits: R <= 16384,
- * max_pages * page <= 2^30, T <= 2^26.  What a page holds past
- * its request's length never reaches a result, whatever its bytes.
+ * max_pages * page <= 2^30, T <= 2^26, and the plan's slots are int32:
+ * num_pages * page < 2^31.  What a page holds past its request's length never
+ * reaches a result, whatever its bytes.
  */
 typedef enum { KDA_I8 = 0, KDA_E4M3 = 1 } kda_code;
 
@@ -484,10 +485,9 @@ kda_status kda_page_release(const int32_t* release, int R, int page, int32_t* kv
  * tensor, with a0 the scale held (0 if the run starts its page) and a1 =
  * max(a0, max |x| over the run): codes already in the page become
  * rn(c * a0 / a1), the new ones rn(x * top / a1) (top 127 or 448; to
- * nearest, ties to even), and the scale a1.  Both quotients are fp32
- * divisions whose rounded code equals exact arithmetic's for every bf16
- * input.  A run with an infinity or NaN makes its page and head's scale NaN:
- * attention over them is NaN until the page is reused.
+ * nearest, ties to even), and the scale a1.  Both are exact arithmetic's
+ * codes for every bf16 input.  A run with an infinity or NaN makes its page
+ * and head's scale NaN: attention over them is NaN until the page is reused.
  * Runs outside the pool or the rows are KDA_ERR_BAD_PAGES and skipped.
  * k, v 16-byte aligned, strides multiples of 8 elements and >= Hkv * d;
  * codes 16-byte aligned.
@@ -508,11 +508,14 @@ kda_status kda_cache_append(const uint16_t* k, const uint16_t* v, int64_t k_stri
  * A row that sees nothing (kv_lens[r] < n) gives out 0 and lse -infinity.
  *   q     bf16 [T, Hq, d], token stride q_stride elements (a multiple of 8)
  *   out   bf16 [T, Hq, d] contiguous;  lse  fp32 [T, Hq], or NULL
+ * Weights enter the products rounded to f16, relative to a row's reference (a
+ * score not far below its largest) and the largest value scale that it sees:
+ * beside their 11 bits, what is below 2^-25 of both together is lost.
  * Rows past cu_seqlens[R] are not written.  Hq a multiple of Hkv, at most
  * 64 query heads for each; R <= 16384.  max_new: the most new tokens any
  * request has, as far as the host knows (T is always right); a larger
  * request is KDA_ERR_BAD_SEQLENS.  A request whose new tokens make at most
- * 64 query rows for a key / value head runs on a kernel for few rows (bound
+ * 4096 / d query rows for a key / value head runs on a kernel for few rows (bound
  * by the cache's bytes), others on the tensor cores in tiles; both split a
  * long cache over the chip and join the parts.
  * Malformed cu_seqlens or lengths past the table are KDA_ERR_BAD_SEQLENS, a

@@ -77,6 +77,11 @@ def test_null_pointers(call, name):
     (_release, dict(R=0), INV), (_release, dict(page=8), UNS), (_release, dict(max_pages=0), INV),
     (_append, dict(T=-1), INV), (_append, dict(Hkv=0), INV), (_append, dict(num_pages=0), INV),
     (_append, dict(d=96), UNS), (_append, dict(page=256), UNS), (_append, dict(code=2), UNS),
+    (_append, dict(Hkv=4097, k_stride=4097 * 128, v_stride=4097 * 128), UNS),
+    (_append, dict(T=(1 << 26) + 1), UNS),
+    (_plan, dict(T=(1 << 26) + 1), UNS), (_plan, dict(max_pages=1 << 27), UNS),
+    (_attn, dict(T=(1 << 26) + 1), UNS), (_attn, dict(max_pages=1 << 27), UNS),
+    (_attn, dict(Hkv=4097, Hq=4097, q_stride=4097 * 128), UNS),
     (_append, dict(k_stride=504), INV), (_append, dict(v_stride=516), MIS),
     (_append, dict(k=A + 2), MIS), (_append, dict(v_codes=5 * A + 8), MIS),
     (_append, dict(runs=3 * A + 4), MIS), (_append, dict(k_scale=6 * A + 2), MIS),

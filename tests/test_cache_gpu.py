@@ -317,6 +317,11 @@ SHAPES = [
     ([2, 2], [300, 1000], 64, 1, 8),
     ([5, 1, 3], [77, 1500, 12], 32, 2, 7),
     ([16, 1], [0, 0], 16, 3, 1),
+    # groups of rows: up to 32 / 64 and past them, many parts and few
+    ([5, 9, 20], [700, 33, 260], 32, 2, 3),
+    ([7, 11, 2], [400, 90, 6000], 16, 1, 9),
+    ([16, 8, 4, 1], [5000, 100, 64, 2000], 64, 2, 4),
+    ([3] * 40, [50 * i for i in range(40)], 16, 4, 11),
     # prompts and pieces of prompts, odd lengths
     ([17], [0], 16, 1, 1),
     ([128], [0], 64, 1, 2),
@@ -415,6 +420,29 @@ def test_marked_page_of_later_tokens_stays_unseen(n, G, dtype):
     out, lse = call(b)
     assert torch.equal(out[:first], clean[:first]) and torch.equal(lse[:first], clean_lse[:first])
     assert out[first:].isnan().all() and lse[first:].isnan().all()
+
+
+@pytest.mark.parametrize("big", [2.0 ** 60, float("inf")])
+@pytest.mark.parametrize("n,G,d", [(4, 2, 128), (8, 1, 64), (4, 4, 64), (9, 7, 128), (90, 2, 64),
+                                   (150, 5, 128), (600, 1, 64)])
+@pytest.mark.parametrize("dtype", [I8, F8])
+def test_scales_of_later_pages_stay_unseen(n, G, d, dtype, big):
+    # the pages that hold the later half of the new tokens have enormous scales:
+    # what does not see them stays within the bounds that hold without them
+    page, ctx = 16, 48 - n // 2 % 16
+    b = batch([n], [ctx], page, 1, G, d, dtype, seed=59)
+    o, l, to, tl = plain.attend(b["q"], b["cu"], b["kv"], b["table"], b["kc"], b["vc"], b["ks"],
+                                b["vs"], d ** -0.5)
+    col = (ctx + n // 2) // page
+    first = col * page - ctx                         # the first new token in such a page
+    assert 0 < first < n
+    for pg in b["table"][0][col:]:
+        b["vs"][pg] = big
+        b["ks"][pg] = big
+    out, lse = call(b)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert ((out - o).abs() <= to)[:first].all()
+    assert ((lse - l).abs() <= tl)[:first].all()
 
 
 @pytest.mark.parametrize("new", [[1] * 7, [30, 1, 70]])
