@@ -233,7 +233,8 @@ struct AppendArgs {
 
 // Threads: kAppendPasses 16-byte pieces each where the page has so many.  More
 // pieces a thread are more bytes in flight an SM until registers run out: the
-// prompts' append took 51.6 / 43.6 / 85 us with 4 / 8 / 16.
+// prompts' append took 51.6 / 43.6 / 85 us with 4 / 8 / 16.  1024 threads an SM
+// (64 registers each) took 42.9 us, 1280 51.9.
 constexpr int kAppendPasses = 8;
 __host__ __device__ constexpr int append_threads(int page, int d) {
   const int n = page * d / 8 / kAppendPasses;
@@ -299,10 +300,11 @@ __device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float pre, floa
 // registers, their largest magnitude is found by an unsigned maximum of the bit
 // patterns without the sign (which orders finite < infinity < NaN), and the
 // codes are written from the registers.  A stream of 3 bytes a value: 17 prompts
-// with 37 000 tokens of 8 heads (230 MB) take 43.6 us, 5.27 TB/s; one token of
+// with 37 000 tokens of 8 heads (230 MB) take 42.9 us, 5.36 TB/s; one token of
 // each of 64 requests 4.0 us, which is latency.
 template <int CODE, int D, int PAGE>
-__global__ void __launch_bounds__(append_threads(PAGE, D)) kda_cache_append_kernel(AppendArgs p) {
+__global__ void __launch_bounds__(append_threads(PAGE, D))
+    kda_cache_append_kernel(AppendArgs p) {
   constexpr int NT = append_threads(PAGE, D);
   constexpr int TPR = D / 8;     // threads per token, 8 values each
   constexpr int RPP = NT / TPR;  // tokens per pass
@@ -320,9 +322,12 @@ __global__ void __launch_bounds__(append_threads(PAGE, D)) kda_cache_append_kern
     if (tid == 0) report(p.status, KDA_ERR_BAD_PAGES);
     return;
   }
-  const uint16_t* x = p.x[kv] + (int64_t)row * p.stride[kv] + h * D + (tid % TPR) * 8;
-  uint8_t* codes = p.codes[kv] + ((int64_t)page * p.H + h) * (PAGE * D) + (tid % TPR) * 8;
-  float* scale = p.scale[kv] + (int64_t)page * p.H + h;
+  // (an index into the arguments would copy them to local memory)
+  const int64_t stride = kv ? p.stride[1] : p.stride[0];
+  const uint16_t* x = (kv ? p.x[1] : p.x[0]) + (int64_t)row * stride + h * D + (tid % TPR) * 8;
+  uint8_t* codes =
+      (kv ? p.codes[1] : p.codes[0]) + ((int64_t)page * p.H + h) * (PAGE * D) + (tid % TPR) * 8;
+  float* scale = (kv ? p.scale[1] : p.scale[0]) + (int64_t)page * p.H + h;
   const int t0 = tid / TPR;
 
   uint4 v[PASSES];
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(append_threads(PAGE, D)) kda_cache_append_kern
   for (int i = 0; i < PASSES; ++i) {
     v[i] = make_uint4(0, 0, 0, 0);
     const int t = t0 + i * RPP;
-    if (t < count) v[i] = *reinterpret_cast<const uint4*>(x + t * p.stride[kv]);
+    if (t < count) v[i] = *reinterpret_cast<const uint4*>(x + t * stride);
   }
   const uint32_t had = off > 0 ? __float_as_uint(*scale) & 0x7fffffffu : 0;
 #pragma unroll
@@ -384,7 +389,7 @@ void launch_append(const AppendArgs& p, int page, unsigned grid, cudaStream_t s)
     case 16: kda_cache_append_kernel<CODE, D, 16><<<grid, append_threads(16, D), 0, s>>>(p); break;
     case 32: kda_cache_append_kernel<CODE, D, 32><<<grid, append_threads(32, D), 0, s>>>(p); break;
     case 64: kda_cache_append_kernel<CODE, D, 64><<<grid, append_threads(64, D), 0, s>>>(p); break;
-    default: kda_cache_append_kernel<CODE, D, 128><<<grid, append_threads(128, D), 0, s>>>(p); break;
+    default: kda_cache_append_kernel<CODE, D, 128><<<grid, append_threads(128, D), 0, s>>>(p);
   }
 }
 

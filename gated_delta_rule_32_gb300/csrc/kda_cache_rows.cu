@@ -570,15 +570,17 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
 // three parts a segment: 32 rows (8 or 128 took 110 and 125 us where 32 take
 // 104, a prompt's piece among decode steps).  The few-row kernel leaves as many
 // as there are CTAs for its segments: 16 rows where four or fewer are to be
-// expected (drafts of 32 requests: 38.6 us, 41.7 with 4 rows), else 4 (two long
-// contexts: 86.6 us, 97.7 with 16 rows).  Where the rows are fewer than its 8
-// warps, several warps share a row's parts.
+// expected (drafts of 32 requests: 38.6 us, 41.7 with fewer), else 8 (two long
+// contexts: 82.7 us, 80.8 with 4 rows, 97.7 with 16; one short request 11.1 us,
+// 11.6 with 4 rows).  Where the rows are at most half as many as its warps,
+// several warps share a row's parts; with 8 warps the long contexts took 86.4 us.
+constexpr int kJoinWarps = 16;
 template <int D>
-__global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, Parts rows_kernel,
-                                                            Parts tile_kernel,
-                                                            int few_blocks, int few_group) {
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    kda_attn_join_kernel(AttnArgs p, Parts rows_kernel, Parts tile_kernel, int few_blocks,
+                         int few_group) {
   constexpr int E = D / 32;
-  __shared__ float s_o[8][D], s_l[8];
+  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool few = (int)blockIdx.x < few_blocks;
   const Parts q = few ? rows_kernel : tile_kernel;
@@ -591,9 +593,10 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(AttnArgs p, Parts ro
   const int64_t share = quotient(*q.total + q.ctas - 1, q.ctas);
   const int ca = (int)quotient(ph.seg0, share), cb = (int)quotient(ph.seg1 - 1, share);
   if (ca != c0) return;
-  const int wpr = n > 4 ? 1 : n > 2 ? 2 : n > 1 ? 4 : 8;  // warps a row
+  int wpr = 1;  // warps a row
+  while (2 * n * wpr <= kJoinWarps) wpr *= 2;
   const int sub = warp % wpr;
-  for (int i = warp / wpr; i < n; i += 8 / wpr) {
+  for (int i = warp / wpr; i < n; i += kJoinWarps / wpr) {
     const int row = row0 + i;
     // the first CTA holds it as its last segment, the others as their first
     auto part = [&](int c) -> int64_t {
@@ -679,11 +682,11 @@ kda_status kda_launch_attn_join(const AttnArgs& p, const Parts& tile, int d, cud
   const int tile_rows = most < kTileRows ? (int)most : kTileRows;
   const int64_t groups = ((most < p.few_max ? most : p.few_max) + kFewRows - 1) / kFewRows;
   const int64_t segments = groups * p.R * p.Hkv;
-  const int few_group = 4 * segments >= p.parts.ctas ? kFewRows : 4;
+  const int few_group = 4 * segments >= p.parts.ctas ? kFewRows : 8;
   const int few_blocks = (p.parts.ctas - 1) * ((few_rows + few_group - 1) / few_group);
   const int tile_blocks = tile.ctas > 1 ? (tile.ctas - 1) * ((tile_rows + 31) / 32) : 0;
   if (few_blocks + tile_blocks == 0) return KDA_OK;
   return launch_following(d == 64 ? kda_attn_join_kernel<64> : kda_attn_join_kernel<128>,
-                          few_blocks + tile_blocks, 256, 0, s, p, p.parts, tile, few_blocks,
-                          few_group);
+                          few_blocks + tile_blocks, 32 * kJoinWarps, 0, s, p, p.parts, tile,
+                          few_blocks, few_group);
 }
