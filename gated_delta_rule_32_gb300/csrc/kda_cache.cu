@@ -233,8 +233,7 @@ struct AppendArgs {
 
 // Threads: kAppendPasses 16-byte pieces each where the page has so many.  More
 // pieces a thread are more bytes in flight an SM until registers run out: the
-// prompts' append took 51.6 / 43.6 / 85 us with 4 / 8 / 16.  1024 threads an SM
-// (64 registers each) took 42.9 us, 1280 51.9.
+// prompts' append took 48.0 / 41.0 / 44.5 us with 4 / 8 / 16.
 constexpr int kAppendPasses = 8;
 __host__ __device__ constexpr int append_threads(int page, int d) {
   const int n = page * d / 8 / kAppendPasses;
@@ -300,8 +299,8 @@ __device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float pre, floa
 // registers, their largest magnitude is found by an unsigned maximum of the bit
 // patterns without the sign (which orders finite < infinity < NaN), and the
 // codes are written from the registers.  A stream of 3 bytes a value: 17 prompts
-// with 37 000 tokens of 8 heads (230 MB) take 42.9 us, 5.36 TB/s; one token of
-// each of 64 requests 4.0 us, which is latency.
+// with 37 000 tokens of 8 heads (230 MB) take 41.0 us, 5.6 TB/s; one token of
+// each of 64 requests 3.5 us, which is latency.
 template <int CODE, int D, int PAGE>
 __global__ void __launch_bounds__(append_threads(PAGE, D))
     kda_cache_append_kernel(AppendArgs p) {

@@ -19,9 +19,9 @@ constexpr int kPartRows[2] = {kFewRows, kTileRows};
 
 Layout layout(int max_new, int G, int d) {
   Layout w{};
-  const int sms = kda_device_sms();
+  const int device_sms = kda_device_sms(), sms = device_sms < kMaxSms ? device_sms : kMaxSms;
   const int64_t rows = (int64_t)max_new * G;
-  w.ctas[0] = sms * 3;  // as many as the kernel's registers let an SM hold
+  w.ctas[0] = sms * kRowsPerSm;
   w.ctas[1] = rows > few_max(d) ? sms / 2 : 0;  // (pairs of CTAs)
   size_t at = 0;
   for (int i = 0; i < 2; ++i) {

@@ -47,6 +47,9 @@ struct AttnArgs {
 // 128 (48 requests, 1700 tokens, 4 heads) 32 rows 84 : 105, 64 rows 144 : 107.
 constexpr int kFewRows = 16;
 __host__ __device__ constexpr int few_max(int d) { return 4096 / d; }
+// CTAs of the few-row kernel an SM: as many as its registers allow.  SMs that the
+// kernels use at most (what the join has room for).
+constexpr int kRowsPerSm = 3, kMaxSms = 256;
 // Query rows of a segment on the tile kernel.
 constexpr int kTileRows = 512;
 

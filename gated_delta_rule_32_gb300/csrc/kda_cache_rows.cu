@@ -12,8 +12,8 @@
 // 64 requests' decode step on up to 8192 cached tokens (8 heads, d = 128, 654 MB
 // of codes): 140 us with the join, 4.7 TB/s; a kernel that only reads as many
 // bytes takes 108-118 us, and the SMs' times for equal shares differ by half.
-// Two contexts of up to 262144 tokens (4 heads): 86 us.  One request of 700
-// tokens: 11 us, of which the schedule, the chain of one CTA and the join take
+// Two contexts of up to 262144 tokens (4 heads): 79 us.  One request of 700
+// tokens: 12 us, of which the schedule, the chain of one CTA and the join take
 // about equal parts.  Three CTAs an SM, as many as the registers allow; shares
 // half as long (six an SM) took 141 us, four CTAs an SM with NB = 1 142 us.
 //
@@ -113,7 +113,7 @@ struct Cfg {
 };
 
 template <int CODE, int D, int NT>
-__global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnArgs p) {
+__global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kernel(AttnArgs p) {
   using C = Cfg<D, NT>;
   constexpr int KS = D / 16;         // k-steps of K Q^T = m-tiles of V^T P^T
   constexpr int KC = D / 64;         // 16-byte chunks of a key row per lane
@@ -563,91 +563,132 @@ __global__ void __launch_bounds__(kThreads, 3) kda_cache_attn_rows_kernel(AttnAr
   }
 }
 
-// Joins the parts of the segments that cross CTA boundaries, in CTA order:
-// out = sum_c w_c O_c / sum_c w_c l_c with w_c = 2^(m_c - max m).  A block looks
-// at the boundary between CTAs c and c + 1 of a kernel and works if it is the
-// first inside its segment, on up to `group` rows.  The tile kernel leaves two or
-// three parts a segment: 32 rows (8 or 128 took 110 and 125 us where 32 take
-// 104, a prompt's piece among decode steps).  The few-row kernel leaves as many
-// as there are CTAs for its segments: 16 rows where four or fewer are to be
-// expected (drafts of 32 requests: 38.6 us, 41.7 with fewer), else 8 (two long
-// contexts: 82.7 us, 80.8 with 4 rows, 97.7 with 16; one short request 11.1 us,
-// 11.6 with 4 rows).  Where the rows are at most half as many as its warps,
-// several warps share a row's parts; with 8 warps the long contexts took 86.4 us.
+// Joins the parts of the segments that cross a worker's share, in the workers'
+// order: out = sum_c w_c O_c / sum_c w_c l_c with w_c = 2^(m_c - max m).  Every
+// block lists the segments for itself, by the boundaries between workers c and
+// c + 1 that are the first inside theirs (one load a thread), and the blocks
+// share out pieces of `group` rows, the fewest with which a block has one piece,
+// 32 at most: a long cache leaves few rows with up to a part for each worker, a
+// batch of prompts many rows with two or three.  Where the rows are at most half
+// as many as a block's warps, several warps share a row's parts.  Bound by the
+// parts' trip through L2 and by latency: with pieces of a fixed size, a block
+// for each of every boundary's, one request with 100 000 tokens took 48 us (26
+// so), a prompt's 128 tokens on 4000 41 (29), one with 700 tokens 11 (12).
 constexpr int kJoinWarps = 16;
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-    kda_attn_join_kernel(AttnArgs p, Parts rows_kernel, Parts tile_kernel, int few_blocks,
-                         int few_group) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(32 * kJoinWarps, 2)
+    kda_attn_join_kernel(AttnArgs p, Parts rows_kernel, Parts tile_kernel) {
+  constexpr int E = D / 32, NT = 32 * kJoinWarps;
   __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
+  // first and last worker, first token, rows, first row and head of the segments
+  __shared__ int4 s_few[kRowsPerSm * kMaxSms], s_tile[kMaxSms / 2];
+  __shared__ int s_count[kJoinWarps], s_rows[kJoinWarps], s_most[kJoinWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool few = (int)blockIdx.x < few_blocks;
-  const Parts q = few ? rows_kernel : tile_kernel;
-  const int of = few ? blockIdx.x : (int)blockIdx.x - few_blocks, group = few ? few_group : 32;
-  const int c0 = of % (q.ctas - 1), row0 = group * (of / (q.ctas - 1));
   wait_for_kernel_before();
-  const PartHead ph = q.head[c0 + 1];
-  const int n = min(ph.rows - row0, group);
-  if (n <= 0) return;
-  const int64_t share = quotient(*q.total + q.ctas - 1, q.ctas);
-  const int ca = (int)quotient(ph.seg0, share), cb = (int)quotient(ph.seg1 - 1, share);
-  if (ca != c0) return;
-  int wpr = 1;  // warps a row
-  while (2 * n * wpr <= kJoinWarps) wpr *= 2;
-  const int sub = warp % wpr;
-  for (int i = warp / wpr; i < n; i += kJoinWarps / wpr) {
-    const int row = row0 + i;
-    // the first CTA holds it as its last segment, the others as their first
-    auto part = [&](int c) -> int64_t {
-      return (2 * (int64_t)c + (c == ca ? 1 : 0)) * q.rows + row;
-    };
-    float mx = -INFINITY, acc[E] = {}, sum = 0.0f;
-    for (int c = ca + lane; c <= cb; c += 32) mx = fmaxf(mx, q.ml[part(c) * 2]);
+  int count[2], most[2] = {1, 1}, rows_all = 0;  // (most: rows of one segment)
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-    const float mm = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll 8
-    for (int c = ca + sub; c <= cb; c += wpr) {
-      const int64_t at = part(c);
-      const float2 ml = *reinterpret_cast<const float2*>(q.ml + at * 2);
-      const float f = ex2(ml.x - mm);
-      sum += f * ml.y;
-      float v[E];
-      if constexpr (E == 4)
-        *reinterpret_cast<float4*>(v) = reinterpret_cast<const float4*>(q.o + at * D)[lane];
-      else
-        *reinterpret_cast<float2*>(v) = reinterpret_cast<const float2*>(q.o + at * D)[lane];
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += f * v[e];
-    }
-    if (wpr > 1) {  // (then each warp has one row at most)
-#pragma unroll
-      for (int e = 0; e < E; ++e) s_o[warp][E * lane + e] = acc[e];
-      if (lane == 0) s_l[warp] = sum;
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpr), "r"(32 * wpr) : "memory");
-      if (sub) break;
-      for (int w = 1; w < wpr; ++w) {
-        sum += s_l[warp + w];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += s_o[warp + w][E * lane + e];
+  for (int k = 0; k < 2; ++k) {
+    const Parts& q = k ? tile_kernel : rows_kernel;
+    count[k] = 0;
+    if (q.ctas < 2) continue;
+    const int64_t total = *q.total;
+    for (int base = 0; base < q.ctas - 1; base += NT) {
+      const int c = base + tid;
+      PartHead h{0, 0, 0, 0, 0, 0};
+      if (c < q.ctas - 1) h = q.head[c + 1];
+      const int64_t share = quotient(total + q.ctas - 1, q.ctas);
+      const int rows = h.rows > 0 && quotient(h.seg0, share) == c ? h.rows : 0;
+      const uint32_t those = __ballot_sync(~0u, rows > 0);
+      const int sum = __reduce_add_sync(~0u, rows), top = __reduce_max_sync(~0u, rows);
+      if (lane == 0) {
+        s_count[warp] = __popc(those);
+        s_rows[warp] = sum;
+        s_most[warp] = top;
       }
-    }
-    const int of_seg = ph.row0 + row;
-    const int64_t at = (int64_t)(ph.tok0 + of_seg / p.G) * p.Hq + ph.h * p.G + of_seg % p.G;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint32_t y[E / 2];
+      __syncthreads();
+      int at = count[k] + __popc(those & ((1u << lane) - 1));
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const __nv_bfloat162 z = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-      y[e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+      for (int w = 0; w < kJoinWarps; ++w) {
+        if (w < warp) at += s_count[w];
+        count[k] += s_count[w];
+        rows_all += s_rows[w];
+        most[k] = max(most[k], s_most[w]);
+      }
+      if (rows > 0)
+        (k ? s_tile : s_few)[at] = make_int4(c | (int)quotient(h.seg1 - 1, share) << 16, h.tok0,
+                                             rows | h.row0 << 16, h.h);
+      __syncthreads();
     }
-    if constexpr (E == 4)
-      reinterpret_cast<uint2*>(p.out + at * D)[lane] = make_uint2(y[0], y[1]);
-    else
-      reinterpret_cast<uint32_t*>(p.out + at * D)[lane] = y[0];
-    if (p.lse && lane == 0)
-      p.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+  }
+  int group = 1;
+  while (group < 32 && rows_all > group * (int)gridDim.x) group *= 2;
+  const int few_groups = (most[0] + group - 1) / group, tile_groups = (most[1] + group - 1) / group;
+  const int few_items = count[0] * few_groups, items = few_items + count[1] * tile_groups;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const bool few = item < few_items;
+    const Parts& q = few ? rows_kernel : tile_kernel;
+    const int of = few ? item : item - few_items, groups = few ? few_groups : tile_groups;
+    const int4 seg = (few ? s_few : s_tile)[of / groups];
+    const int ca = seg.x & 0xffff, cb = seg.x >> 16, row0 = group * (of % groups);
+    const int n = min((seg.z & 0xffff) - row0, group);
+    if (n <= 0) continue;
+    int wpr = 1;  // warps a row
+    while (2 * n * wpr <= kJoinWarps) wpr *= 2;
+    const int sub = warp % wpr;
+    for (int i = warp / wpr; i < n; i += kJoinWarps / wpr) {
+      const int row = row0 + i;
+      // the first CTA holds it as its last segment, the others as their first
+      auto part = [&](int c) -> int64_t {
+        return (2 * (int64_t)c + (c == ca ? 1 : 0)) * q.rows + row;
+      };
+      float mx = -INFINITY, acc[E] = {}, sum = 0.0f;
+      for (int c = ca + lane; c <= cb; c += 32) mx = fmaxf(mx, q.ml[part(c) * 2]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+      const float mm = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll 8
+      for (int c = ca + sub; c <= cb; c += wpr) {
+        const int64_t at = part(c);
+        const float2 ml = *reinterpret_cast<const float2*>(q.ml + at * 2);
+        const float f = ex2(ml.x - mm);
+        sum += f * ml.y;
+        float v[E];
+        if constexpr (E == 4)
+          *reinterpret_cast<float4*>(v) = reinterpret_cast<const float4*>(q.o + at * D)[lane];
+        else
+          *reinterpret_cast<float2*>(v) = reinterpret_cast<const float2*>(q.o + at * D)[lane];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += f * v[e];
+      }
+      if (wpr > 1) {  // (then each warp has one row at most)
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_o[warp][E * lane + e] = acc[e];
+        if (lane == 0) s_l[warp] = sum;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpr), "r"(32 * wpr) : "memory");
+        if (sub) break;
+        for (int w = 1; w < wpr; ++w) {
+          sum += s_l[warp + w];
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += s_o[warp + w][E * lane + e];
+        }
+      }
+      const int of_seg = (seg.z >> 16) + row;
+      const int64_t at = (int64_t)(seg.y + of_seg / p.G) * p.Hq + seg.w * p.G + of_seg % p.G;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint32_t y[E / 2];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const __nv_bfloat162 z = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+        y[e / 2] = *reinterpret_cast<const uint32_t*>(&z);
+      }
+      if constexpr (E == 4)
+        reinterpret_cast<uint2*>(p.out + at * D)[lane] = make_uint2(y[0], y[1]);
+      else
+        reinterpret_cast<uint32_t*>(p.out + at * D)[lane] = y[0];
+      if (p.lse && lane == 0)
+        p.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
@@ -677,16 +718,9 @@ kda_status kda_launch_attn_rows(const AttnArgs& p, int d, int code, cudaStream_t
 }
 
 kda_status kda_launch_attn_join(const AttnArgs& p, const Parts& tile, int d, cudaStream_t s) {
-  const int64_t most = (int64_t)p.max_new * p.G;
-  const int few_rows = most < kFewRows ? (int)most : kFewRows;
-  const int tile_rows = most < kTileRows ? (int)most : kTileRows;
-  const int64_t groups = ((most < p.few_max ? most : p.few_max) + kFewRows - 1) / kFewRows;
-  const int64_t segments = groups * p.R * p.Hkv;
-  const int few_group = 4 * segments >= p.parts.ctas ? kFewRows : 8;
-  const int few_blocks = (p.parts.ctas - 1) * ((few_rows + few_group - 1) / few_group);
-  const int tile_blocks = tile.ctas > 1 ? (tile.ctas - 1) * ((tile_rows + 31) / 32) : 0;
-  if (few_blocks + tile_blocks == 0) return KDA_OK;
-  return launch_following(d == 64 ? kda_attn_join_kernel<64> : kda_attn_join_kernel<128>,
-                          few_blocks + tile_blocks, 32 * kJoinWarps, 0, s, p, p.parts, tile,
-                          few_blocks, few_group);
+  // two blocks an SM, or one for each row of the batch where these are fewer
+  const int64_t rows = (int64_t)p.T * p.Hq, most = 2 * (p.parts.ctas / kRowsPerSm);
+  const int blocks = (int)(rows < most ? rows : most);
+  return launch_following(d == 64 ? kda_attn_join_kernel<64> : kda_attn_join_kernel<128>, blocks,
+                          32 * kJoinWarps, 0, s, p, p.parts, tile);
 }

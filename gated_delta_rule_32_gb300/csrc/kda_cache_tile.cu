@@ -31,7 +31,7 @@
 // least as large (vref), which leaves O at the end.
 //
 // Bound by the products where rows are many: 4 D flops for each row and token,
-// at 2048 tokens on 32768 cached (32 heads on 4, d = 128) 842 us, 1347 TFLOP/s;
+// at 2048 tokens on 32768 cached (32 heads on 4, d = 128) 837 us, 1355 TFLOP/s;
 // the tensor cores work 2 x 1024 of the 2.6-2.9k cycles that a key tile of both
 // row tiles takes, and the rest is the chain of one row tile, which the other's
 // products cover in part only: products 1024 -> softmax 1480-1900 (exponentials
@@ -39,7 +39,7 @@
 // one CTA a tile 1026 us; S in two halves, so that a row tile's products and
 // softmax overlap, 914-1040 us (products of 64 tokens take 48 cycles, not 32:
 // shared memory); a second warp issuing products 950-987 us.  Prompts without a
-// cache, 9 of up to 4096 tokens (32 heads on 8): 466 us, 916 TFLOP/s; half of
+// cache, 9 of up to 4096 tokens (32 heads on 8): 461 us, 925 TFLOP/s; half of
 // a tile on the diagonal is masked, and a segment's own cost (queries in, O out)
 // weighs more where its keys are few.
 #include <type_traits>
