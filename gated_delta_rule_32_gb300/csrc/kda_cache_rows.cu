@@ -10,7 +10,7 @@
 // parts, which kda_attn_join_kernel joins.
 //
 // 64 requests' decode step on up to 8192 cached tokens (8 heads, d = 128, 654 MB
-// of codes): 140 us with the join, 4.7 TB/s; a kernel that only reads as many
+// of codes): 143 us with the join, 4.6 TB/s; a kernel that only reads as many
 // bytes takes 108-118 us, and the SMs' times for equal shares differ by half.
 // Two contexts of up to 262144 tokens (4 heads): 79 us.  One request of 700
 // tokens: 12 us, of which the schedule, the chain of one CTA and the join take
