@@ -43,8 +43,8 @@ struct AttnArgs {
 // few-row kernel, in groups of kFewRows.  Every group converts all codes once
 // more, so its time grows with rows times d, the tile kernel's hardly up to its
 // 512-row segments.  Few-row against tile kernel: d = 64 (32 requests, 2400
-// cached tokens on average, 2 heads) 64 rows 41 : 55 us, 128 rows 68 : 56; d =
-// 128 (48 requests, 1700 tokens, 4 heads) 32 rows 84 : 105, 64 rows 144 : 107.
+// cached tokens on average, 2 heads) 64 rows 36 : 47 us, 128 rows 61 : 49; d =
+// 128 (48 requests, 1700 tokens, 4 heads) 32 rows 83 : 96, 48 rows 125 : 104.
 constexpr int kFewRows = 16;
 __host__ __device__ constexpr int few_max(int d) { return 4096 / d; }
 // CTAs of the few-row kernel an SM: as many as its registers allow.  SMs that the

@@ -101,10 +101,10 @@ __device__ __forceinline__ void copy_wait() {
 
 // NT: 8-row tiles of query rows.  NB: 16-token blocks that a warp takes at a
 // time: two where the registers allow it, so that one's products overlap the
-// other's conversion.
+// other's conversion (drafts of 32 requests, d = 64: 36.5 us, 38.1 with one).
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kBlocks = NT == 1 ? 2 : 1;
+  static constexpr int kBlocks = NT == 1 || D == 64 ? 2 : 1;
   static constexpr int kUnit = 16 * kBlocks * kWarps;      // tokens
   static constexpr int kBlockBytes = 32 * D;               // keys and values of a block
   static constexpr int kStage = kBlocks * kBlockBytes;
