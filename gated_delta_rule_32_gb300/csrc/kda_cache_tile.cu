@@ -16,10 +16,12 @@
 //   8-11       keys:   codes -> f16 operand tiles in shared memory
 //   12-15      values: the same; between segments 8-15 convert the queries
 //   16         owns tensor memory; of the first CTA: issues all products (in
-//              step, one thread carrying them out)
+//              step, one thread carrying them out); of the second: tells the
+//              first that its keys and queries are there
 //   17         walks the schedule and looks up the pages' scales, some key
 //              tiles ahead of the softmax
-//   18, 19     bring the next segment's queries into L2
+//   18, 19     bring the next segment's queries into L2; of the second CTA 19
+//              tells the first that its values are there
 // Tensor memory (512 columns): S of both tiles (the weights P replace S in
 // place, in f16), O of both tiles.
 //
@@ -79,14 +81,16 @@ struct Smem {
   static constexpr int kBytes = kStage + 8 * kStageWarp + 1024;
 };
 
-// "leader": only the first CTA's is used, both arrive there.  The others are
-// each CTA's own; those that products complete are completed in both.
+// "leader": only the first CTA's is used, both arrive there.  "operands": each
+// CTA's own, of its converting warps, and the first's has one arrival more, by
+// which the second CTA says that its half is there too.  The others are each
+// CTA's own; those that products complete are completed in both.
 struct Bars {
-  uint64_t q_full[2][2];              // leader; row tile, and parity of its segments
+  uint64_t q_full[2][2];              // operands; row tile, and parity of its segments
   uint64_t qs_full[2][2], q_empty[2];
   uint64_t s_full[2], o_full[2];
   uint64_t p_full[2];                 // leader
-  uint64_t k_full[kStages], v_full[kStages];  // leader
+  uint64_t k_full[kStages], v_full[kStages];  // operands
   uint64_t k_empty[kStages], v_empty[kStages];
   uint64_t seg_full[2], seg_empty[2];
   uint64_t sc_full[4], sc_empty[4];
@@ -112,17 +116,35 @@ constexpr int kRing = 4;
 
 // Bounded wait that also gives up when another warp of the CTA has.  The hint
 // lets the hardware suspend the warp for up to 1 ms at a time: a warp that
-// polls takes issue slots from the one that issues the products.
+// polls takes issue slots from the one that issues the products.  What is waited
+// for: of threads of this CTA (kOwn); of the pair or its products, after which
+// shared memory is written or handed to products (kPair); or tensor memory alone,
+// which the fences of tcgen05 order on both sides, so that the barrier has only to
+// order the execution (kTensor).
+enum Of { kOwn, kPair, kTensor };
+template <Of OF = kOwn>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   auto poll = [&]() -> bool {
     uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(1000000)
-        : "memory");
+    const uint32_t at = sm100::smem_u32(bar), hint = 1000000;
+    if (OF == kOwn)
+      asm volatile(
+          "{\n .reg .pred p;\n"
+          " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+          " selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(ok) : "r"(at), "r"(parity), "r"(hint) : "memory");
+    else if (OF == kPair)
+      asm volatile(
+          "{\n .reg .pred p;\n"
+          " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+          " selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(ok) : "r"(at), "r"(parity), "r"(hint) : "memory");
+    else
+      asm volatile(
+          "{\n .reg .pred p;\n"
+          " mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+          " selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(ok) : "r"(at), "r"(parity), "r"(hint) : "memory");
     return ok != 0;
   };
   if (poll()) return true;
@@ -137,14 +159,22 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
-// Arrives at the first CTA's copy of a barrier.  What it announces is this CTA's
-// own shared and tensor memory, which only products read, after the fences to
-// their proxy that come before: it needs no release of the generic writes to
-// the cluster (which took 1000 cycles a time).
-__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+// Arrives at the first CTA's copy of a barrier: with what this thread has seen
+// and written before, or (tensor memory, after tcgen05's fence) without.  A
+// release to the cluster waits for the thread's own accesses under way, 1000
+// cycles in a warp that fetches codes, so warps that have none do it for all:
+// 2048 tokens on 32768 cached took 1049 us with a release by each converting
+// warp (before later steps), 907 with both kinds of operands told by one warp, 826 by two.
+__device__ __forceinline__ void arrive_leader_release(uint64_t* bar) {
   asm volatile(
       "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
-      " mbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(sm100::smem_u32(bar))
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(sm100::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void arrive_leader_tensor(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(sm100::smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -445,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     s_abort = 0;
     for (int i = 0; i < 2; ++i) {
       for (int x = 0; x < 2; ++x) {
-        sm100::mbar_init(&bars.q_full[i][x], 16);   // (a warp's arrival is one)
+        sm100::mbar_init(&bars.q_full[i][x], 8 + (rank == 0));  // (a warp's arrival is one)
         sm100::mbar_init(&bars.qs_full[i][x], 8);
       }
       sm100::mbar_init(&bars.q_empty[i], 1);
@@ -456,8 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sm100::mbar_init(&bars.seg_empty[i], kReaders);
     }
     for (int i = 0; i < kStages; ++i) {
-      sm100::mbar_init(&bars.k_full[i], 8);
-      sm100::mbar_init(&bars.v_full[i], 8);
+      sm100::mbar_init(&bars.k_full[i], 4 + (rank == 0));
+      sm100::mbar_init(&bars.v_full[i], 4 + (rank == 0));
       sm100::mbar_init(&bars.k_empty[i], 1);
       sm100::mbar_init(&bars.v_empty[i], 1);
     }
@@ -482,6 +512,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // wait gave up)
   auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(~0u, wait(bar, parity, abort));
+  };
+  auto pair_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(~0u, wait<kPair>(bar, parity, abort));
+  };
+  auto tensor_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(~0u, wait<kTensor>(bar, parity, abort));
   };
   auto next_seg = [&]() -> Seg {
     const uint32_t slot = nseg & 1;
@@ -536,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = all_wait(&bars.sc_full[tiles % kRing], (tiles / kRing) & 1);
         if (!ok) break;
         const float vmax = sc.vmax;
-        ok = all_wait(&bars.s_full[wg], it & 1);
+        ok = tensor_wait(&bars.s_full[wg], it & 1);
         if (!ok) break;
         sm100::tc_fence_after();
         // Weights with the reference m of the tiles before, in the first tile
@@ -680,11 +716,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sm100::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          arrive_leader(&bars.p_full[wg]);
+          arrive_leader_tensor(&bars.p_full[wg]);
           sm100::mbar_arrive(&bars.sc_empty[tiles % kRing]);
         }
       }
-      if (!ok || !all_wait(&bars.o_full[wg], seg & 1)) break;
+      if (!ok || !tensor_wait(&bars.o_full[wg], seg & 1)) break;
       ++seg;
       sm100::tc_fence_after();
       const float ov = pow2_inverse(vrel) * (1.0f / code_top(CODE));
@@ -772,7 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint4 y[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) y[c] = load16_if<0>(src + 32 * c, of < g.rows);
-        if (g8 == warp - 8 && i > 0 && !all_wait(&bars.q_empty[t], (i - 1) & 1)) return false;
+        if (g8 == warp - 8 && i > 0 && !pair_wait(&bars.q_empty[t], (i - 1) & 1)) return false;
         uint32_t most = 0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -802,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         sm100::mbar_arrive(&bars.qs_full[t][i & 1]);
-        arrive_leader(&bars.q_full[t][i & 1]);
+        sm100::mbar_arrive(&bars.q_full[t][i & 1]);
       }
       return true;
     };
@@ -868,7 +904,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         auto place = [&]() -> bool {  // x -> the next stage
           const int st = cnt % kStages;
-          if (cnt >= kStages && !all_wait(&empty[st], (cnt / kStages - 1) & 1)) return false;
+          if (cnt >= kStages && !pair_wait(&empty[st], (cnt / kStages - 1) & 1)) return false;
           unsigned char* dst = tiles + st * Smem<D>::kTile;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -885,7 +921,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         auto placed = [&]() {
           sm100::fence_async_smem();
           __syncwarp();
-          if (lane == 0) arrive_leader(&full[cnt % kStages]);
+          if (lane == 0) sm100::mbar_arrive(&full[cnt % kStages]);
           ++cnt;
         };
         fetch(0, page_of(0, 0), V ? page_of(0, 1) : -1);
@@ -918,6 +954,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       convert(std::true_type{});
   } else {
     regs_down<kRegsIssue>();
+    // (second CTA) operands that are there: said to the first
+    auto tell = [&](uint64_t* bar, uint32_t parity) -> bool {
+      if (!all_wait(bar, parity)) return false;
+      if (lane == 0) arrive_leader_release(bar);
+      return true;
+    };
+    // the last commits (of k_empty, v_empty) must land before a CTA leaves
+    auto drained = [&]() {
+      volatile int alone = 0;  // (whatever gave up: the products end)
+      wait<kPair>(&bars.drain, 0, &alone);
+    };
     if (warp == 17) {
       // ------------------------------------------------ schedule and scales
       const float sm = fabsf(p.scale) * 1.4426950408889634f / code_top(CODE);
@@ -978,11 +1025,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         w.next();
       }
     } else if (warp >= 18) {
-      // ---------------------------------------------- queries ahead into L2
-      for (;;) {
+      // -------------- queries ahead into L2; values, told to the first CTA
+      uint32_t vc = 0;
+      for (bool ok = true; ok;) {
         const Seg g = next_seg();
         if (g.rows == 0) break;
-        for (int e = threadIdx.x - 18 * 32; e < 256 * (D / 64); e += 64) {
+        if (rank != 0 && warp == 19) {
+          for (int k = g.b0; ok && k < g.b1; ++k, ++vc)
+            ok = tell(&bars.v_full[vc % kStages], (vc / kStages) & 1);
+          continue;
+        }
+        const int step = rank ? 32 : 64;
+        for (int e = threadIdx.x - 18 * 32; e < 256 * (D / 64); e += step) {
           const int at = e / (D / 64), row = 256 * (at >> 7) + 128 * rank + (at & 127);
           if (row >= g.rows) continue;
           const uint16_t* src = p.q + (int64_t)(g.c0 + g.tok0 + row / p.G) * p.q_stride +
@@ -990,9 +1044,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
         }
       }
+    } else if (rank != 0) {
+      // -------------------------------- keys and queries, told to the first CTA
+      uint32_t n0 = 0, n1 = 0, kc = 0;
+      for (bool ok = true; ok;) {
+        const Seg g = next_seg();
+        if (g.rows == 0) break;
+        ok = tell(&bars.k_full[kc % kStages], (kc / kStages) & 1) &&
+             tell(&bars.q_full[0][n0 & 1], (n0 >> 1) & 1);
+        ++n0;
+        if (ok && g.rows > 256) {
+          ok = tell(&bars.q_full[1][n1 & 1], (n1 >> 1) & 1);
+          ++n1;
+        }
+        ++kc;
+        for (int k = g.b0 + 1; ok && k < g.b1; ++k, ++kc)
+          ok = tell(&bars.k_full[kc % kStages], (kc / kStages) & 1);
+      }
+      drained();
     } else {
       // ----------------------------------------------------------- products
-      // (of the second CTA this warp only lets the segments pass)
       const uint32_t id_s = idesc_f16(256, kTok, 0), id_o = idesc_f16(256, D, 1);
       const uint32_t one = elect_one();
       // (a descriptor's address field counts 16-byte units)
@@ -1024,20 +1095,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (;;) {
         const Seg g = next_seg();
         if (g.rows == 0) break;
-        if (rank != 0) continue;
         // (a reduction's result is known to be uniform)
         const bool two = __reduce_max_sync(~0u, g.rows) > 256;
         const int nk = __reduce_max_sync(~0u, g.b1 - g.b0);
         {
           const uint32_t st = kc % kStages;
-          ok = all_wait(&bars.k_full[st], (kc / kStages) & 1) &&
-               all_wait(&bars.q_full[0][n0 & 1], (n0 >> 1) & 1);
+          ok = pair_wait(&bars.k_full[st], (kc / kStages) & 1) &&
+               pair_wait(&bars.q_full[0][n0 & 1], (n0 >> 1) & 1);
           if (!ok) break;
           ++n0;
           sm100::tc_fence_after();
           scores(0, st, nk == 1);
           if (two) {
-            ok = all_wait(&bars.q_full[1][n1 & 1], (n1 >> 1) & 1);
+            ok = pair_wait(&bars.q_full[1][n1 & 1], (n1 >> 1) & 1);
             if (!ok) break;
             ++n1;
             sm100::tc_fence_after();
@@ -1051,15 +1121,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // is there as a rule): a wait takes a few hundred cycles even so.
         auto tiles_there = [&](int k) -> bool {
           const uint32_t at = kc + k;
-          return all_wait(&bars.v_full[at % kStages], (at / kStages) & 1) &&
+          return pair_wait(&bars.v_full[at % kStages], (at / kStages) & 1) &&
                  (k + 1 == nk ||
-                  all_wait(&bars.k_full[(at + 1) % kStages], ((at + 1) / kStages) & 1));
+                  pair_wait(&bars.k_full[(at + 1) % kStages], ((at + 1) / kStages) & 1));
         };
         ok = tiles_there(0);
         for (int k = 0; ok && k < nk; ++k) {
           const bool last = k + 1 == nk, before_last = k + 2 == nk;
           const uint32_t st = (kc + k) % kStages, nt = (kc + k + 1) % kStages;
-          ok = all_wait(&bars.p_full[0], t0++ & 1);
+          ok = tensor_wait(&bars.p_full[0], t0++ & 1);
           if (!ok) break;
           sm100::tc_fence_after();
           values(0, st, k == 0);
@@ -1070,7 +1140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
           }
           if (two) {
-            ok = all_wait(&bars.p_full[1], t1++ & 1);
+            ok = tensor_wait(&bars.p_full[1], t1++ & 1);
             if (!ok) break;
             sm100::tc_fence_after();
             values(1, st, k == 0);
@@ -1083,9 +1153,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         kc += nk;
         if (!ok) break;
       }
-      // the last commits (of k_empty, v_empty) must land before the CTA leaves
-      if (rank == 0) mma_commit(&bars.drain, one);
-      sm100::mbar_wait(&bars.drain, 0);
+      mma_commit(&bars.drain, one);
+      drained();
     }
   }
   __syncwarp();
