@@ -28,11 +28,13 @@
 // lanes fetched what they use themselves, L2 sent every byte twice -- with the
 // chunks permuted so that neither side meets bank conflicts.
 //
-// An int8 code enters a product as the f16 subnormal u 2^-24, u = c + 128 its
-// byte with the top bit flipped: two logic operations for four codes and no
-// arithmetic.  Q K^T is then 2^-24 (Q C^T + 128 sum_d Q), V^T P^T the same with
-// the sum of the weights, which one more product with ones gives; both are
-// taken out in fp32 (a bias of the codes' own size costs no accuracy).
+// Codes enter the products as the f16 values that they are (codes_to_half).  int8
+// codes as f16 subnormals of c + 128, with the bias taken out of the sums at the
+// end, would save two instructions for four codes, but the truncations of the
+// accumulators then go with 128 times the sum of the weights and not with the
+// output: over 32768 tokens a CTA the error was 2.3% of the output, over 131072
+// 18%.  Nor did it save time: 64 decode steps 144.5 us so, 142.6 without, with
+// 36 rows a request 181 and 161.
 #include <type_traits>
 
 #include "kda_cache_attn.cuh"
@@ -60,23 +62,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-
-// Codes as factors of the products.  int8: two pairs (0, 2), (1, 3) of a word;
-// e4m3: pairs (0, 1), (2, 3).
-template <int CODE>
-__device__ __forceinline__ void factors(uint32_t w, uint32_t& a, uint32_t& b) {
-  if (CODE == KDA_I8) {
-    a = (w ^ 0x00800080u) & 0x00ff00ffu;
-    b = ((w >> 8) ^ 0x00800080u) & 0x00ff00ffu;
-  } else {
-    codes_to_half<CODE>(w, a, b);
-  }
-}
-// (of int8) what a factor must be multiplied by, and the bias of a code
-template <int CODE>
-__device__ __forceinline__ constexpr float unit_of() { return CODE == KDA_I8 ? 0x1p24f : 1.0f; }
-template <int CODE>
-__device__ __forceinline__ constexpr float bias_of() { return CODE == KDA_I8 ? 128.0f : 0.0f; }
 
 // Byte offsets of 16-byte chunk c of token t in a block's keys and values.  A
 // quarter of a warp reads the chunks of two tokens of keys, and two chunks of
@@ -163,7 +148,6 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
     // queries, in the k order of the keys' chunks; each row scaled to f16
     uint32_t qf[NT][KS][2];
     float qs[NT][2];   // factors of this lane's two columns
-    float qb[NT][2];   // and their bias: bias_of times the sum of the query row
     int lim[NT][2];    // tokens that they see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -188,54 +172,33 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
       most = max(most, __shfl_xor_sync(~0u, most, 2));
       const int ex = row_exponent(most);
       const float down = exp2i(-ex);
-      float sum = 0.0f;
 #pragma unroll
       for (int c = 0; c < 2 * KC; ++c) {
         const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-        // channels 8 (c & 1) .. + 7 of the lane's chunk c / 2: two k-steps, in
-        // the order of factors()
+        // channels 8 (c & 1) .. + 7 of the lane's chunk c / 2: two k-steps
         const int s0 = 4 * (c >> 1) + 2 * (c & 1);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float y[4] = {__uint_as_float(w[2 * e] << 16) * down,
-                              __uint_as_float(w[2 * e] & 0xffff0000u) * down,
-                              __uint_as_float(w[2 * e + 1] << 16) * down,
-                              __uint_as_float(w[2 * e + 1] & 0xffff0000u) * down};
-          constexpr int B = CODE == KDA_I8 ? 2 : 1, A = CODE == KDA_I8 ? 1 : 2;
-          qf[nt][s0 + e][0] = pack_half(y[0], y[B]);
-          qf[nt][s0 + e][1] = pack_half(y[A], y[3]);
-          if (CODE == KDA_I8) {  // of what the products will see
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float2 z = __half22float2(*reinterpret_cast<__half2*>(&qf[nt][s0 + e][i]));
-              sum += z.x + z.y;
-            }
-          }
-        }
+        for (int e = 0; e < 4; ++e)
+          qf[nt][s0 + (e >> 1)][e & 1] = pack_half(__uint_as_float(w[e] << 16) * down,
+                                                   __uint_as_float(w[e] & 0xffff0000u) * down);
       }
-      const float up = exp2i(ex) * unit_of<CODE>();
-      sum += __shfl_xor_sync(~0u, sum, 1);
-      sum += __shfl_xor_sync(~0u, sum, 2);
-      sum *= -bias_of<CODE>() / unit_of<CODE>();
+      const float up = exp2i(ex);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int col = 8 * nt + 2 * j + c;
         qs[nt][c] = __shfl_sync(~0u, up, (2 * j + c) * 4);
-        qb[nt][c] = __shfl_sync(~0u, sum, (2 * j + c) * 4);
         lim[nt][c] = col < rows ? kv - rq.n + (row0 + col) / G + 1 : 0;
       }
     }
     const int all_see = kv - rq.n + row0 / G + 1;  // tokens that every row sees
     const float sm = p.scale * 1.4426950408889634f / code_top(CODE);
 
-    // (int8: o[.][KS] is the sum of the weights as the products see them)
-    constexpr int KO = CODE == KDA_I8 ? KS + 1 : KS;
-    float o[NT][KO][4], m[NT][2], l[NT][2];
+    float o[NT][KS][4], m[NT][2], l[NT][2];
     float vinv[NT][2];  // 1 / vref, a power of two not below the value scales seen
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int s = 0; s < KO; ++s)
+      for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.0f;
 #pragma unroll
@@ -341,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[b][nt][e] = qb[nt][e & 1];
+            for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.0f;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             const unsigned char* sk = st + b * C::kBlockBytes;
@@ -351,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
               uint32_t a0, a1, a2, a3;
-              factors<CODE>(wa[s], a0, a2);
-              factors<CODE>(wb[s], a1, a3);
+              codes_to_half<CODE>(wa[s], a0, a2);
+              codes_to_half<CODE>(wb[s], a1, a3);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma16816(x[b][nt], a0, a1, a2, a3, qf[nt][4 * c + s][0], qf[nt][4 * c + s][1]);
@@ -408,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
                 }
               }
 #pragma unroll
-              for (int s = 0; s < KO; ++s)
+              for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][s][e] *= f[e & 1];
             }
@@ -477,21 +440,14 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
           }
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
-            // channels 2 s and 2 s + 1 of two tokens, in the order of factors()
-            const uint32_t sel = CODE == KDA_I8 ? ((s & 1) ? 0x7632 : 0x5410)
-                                                : ((s & 1) ? 0x7362 : 0x5140);
+            // channels 2 s and 2 s + 1 of two tokens
+            const uint32_t sel = (s & 1) ? 0x7362 : 0x5140;
             uint32_t a0, a1, a2, a3;
-            factors<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
-            factors<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
+            codes_to_half<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
+            codes_to_half<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma16816(o[nt][s], a0, a1, a2, a3, pb[b][nt][0], pb[b][nt][1]);
-          }
-          if (CODE == KDA_I8) {
-            const uint32_t ones = 0x3c003c00u;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(o[nt][KO - 1], ones, ones, ones, ones, pb[b][nt][0], pb[b][nt][1]);
           }
         }
       };
@@ -510,8 +466,6 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float ov = pow2_inverse(vinv[nt][c]) * (1.0f / code_top(CODE));
-        const float ob =
-            CODE == KDA_I8 ? o[nt][KO - 1][c] * (bias_of<CODE>() / unit_of<CODE>()) : 0.0f;
         float y = l[nt][c];
         y += __shfl_xor_sync(~0u, y, 4);
         y += __shfl_xor_sync(~0u, y, 8);
@@ -524,8 +478,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
 #pragma unroll
         for (int s = 0; s < KS; ++s)
           *reinterpret_cast<float2*>(so + row * D + i8 * VB + 2 * s) =
-              make_float2((o[nt][s][c] - ob) * unit_of<CODE>() * ov,
-                          (o[nt][s][c + 2] - ob) * unit_of<CODE>() * ov);
+              make_float2(o[nt][s][c] * ov, o[nt][s][c + 2] * ov);
       }
     }
     __syncthreads();
