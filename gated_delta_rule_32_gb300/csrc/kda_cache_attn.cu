@@ -10,12 +10,14 @@ size_t r256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Workspace: for the few-row kernel, then (where a request may have more
 // rows) for the tile kernel, the batch's units, the CTAs' entered segments
-// and their parts, two for each CTA.
+// and their parts.
 struct Layout {
   int ctas[2];
   size_t total[2], head[2], ml[2], o[2], bytes;
 };
 constexpr int kPartRows[2] = {kFewRows, kTileRows};
+// (the tile kernel's third: a piece of a long run of key tiles)
+constexpr int kPartSlots[2] = {2, 3};
 
 Layout layout(int max_new, int G, int d) {
   Layout w{};
@@ -25,7 +27,7 @@ Layout layout(int max_new, int G, int d) {
   w.ctas[1] = rows > few_max(d) ? sms / 2 : 0;  // (pairs of CTAs)
   size_t at = 0;
   for (int i = 0; i < 2; ++i) {
-    const size_t parts = (size_t)2 * w.ctas[i] * kPartRows[i];
+    const size_t parts = (size_t)kPartSlots[i] * w.ctas[i] * kPartRows[i];
     w.total[i] = at;
     w.head[i] = at + 256;
     w.ml[i] = w.head[i] + r256(w.ctas[i] * sizeof(PartHead));

@@ -95,6 +95,10 @@ struct Cfg {
   static constexpr int kStage = kBlocks * kBlockBytes;
   static constexpr int kStages = (D == 128 ? 4 : 8) / kBlocks - (NT == 2 ? 1 : 0);
   static constexpr int kWarpBytes = kStage * kStages;      // 12 or 16 KiB
+  // Units after which a worker's sums go to its part in memory and start anew:
+  // each product's addition loses 2^-24 of the accumulator on the average, always
+  // towards zero; the 32768 tokens that a warp then has lose 2^-13.
+  static constexpr int kFold = kWarps * 32768 / kUnit;
 };
 
 template <int CODE, int D, int NT>
@@ -106,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
   constexpr int ROWS = 8 * NT, NB = C::kBlocks, S = C::kStages;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ float2 s_sum[2][ROWS];  // maximum and sum of the pieces before, one after the other
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i8 = lane >> 2, j = lane & 3;
   const int lg = p.page_log2, P = 1 << lg, G = p.G;
@@ -138,12 +143,12 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
     }
     const int hg = (int)quotient(u - base, nb), h = hg / groups;
     const int64_t seg0 = base + hg * nb;              // the (request, head, group)'s units
-    const int b0 = (int)(u - seg0);
-    const int b1 = (int)(min(sh.u1, seg0 + nb) - seg0);
-    const bool whole = b0 == 0 && b1 == nb;
+    // of them this worker's, in pieces of kFold
+    const int mine0 = (int)(max(sh.u0, seg0) - seg0), mine1 = (int)(min(sh.u1, seg0 + nb) - seg0);
+    const int b0 = (int)(u - seg0), b1 = min(mine1, b0 + C::kFold);
     const int row0 = kFewRows * (hg % groups);
     const int rows = min(kFewRows, rq.n * G - row0), kv = rq.kv;
-    if (tid == 0 && b0 > 0) p.parts.head[blockIdx.x] = {seg0, seg0 + nb, rq.c0, rows, h, row0};
+    if (tid == 0 && mine0 > 0) p.parts.head[blockIdx.x] = {seg0, seg0 + nb, rq.c0, rows, h, row0};
 
     // queries, in the k order of the keys' chunks; each row scaled to f16
     uint32_t qf[NT][KS][2];
@@ -482,21 +487,30 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
       }
     }
     __syncthreads();
-    const int64_t part = 2 * (int64_t)blockIdx.x + (b0 > 0 ? 0 : 1);
+    const bool last = b1 == mine1, whole = mine0 == 0 && mine1 == nb;
+    const int64_t part = 2 * (int64_t)blockIdx.x + (mine0 > 0 ? 0 : 1);
+    const int piece = (b0 - mine0) / C::kFold & 1;
     for (int e = tid; e < rows * D; e += kThreads) {
       const int row = e / D, ch = e % D;
+      float* po = p.parts.o + (part * kFewRows + row) * D + ch;
       float mx = s_m[0][row];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][row]);
+      if (b0 > mine0) mx = fmaxf(mx, s_sum[piece][row].x);
       const float mm = mx == -INFINITY ? 0.0f : mx;
       float sum = 0.0f, acc = 0.0f;
+      if (b0 > mine0) {
+        const float f = ex2(s_sum[piece][row].x - mm);
+        sum = f * s_sum[piece][row].y;
+        acc = f * *po;
+      }
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(s_m[w][row] - mm);
         sum += f * s_l[w][row];
         acc += f * *reinterpret_cast<float*>(smem + w * C::kWarpBytes + e * 4);
       }
-      if (whole) {
+      if (last && whole) {
         const int64_t at =
             (int64_t)(rq.c0 + (row0 + row) / G) * p.Hq + h * G + (row0 + row) % G;
         reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + ch] =
@@ -504,8 +518,9 @@ __global__ void __launch_bounds__(kThreads, kRowsPerSm) kda_cache_attn_rows_kern
         if (p.lse && ch == 0)
           p.lse[at] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
       } else {
-        p.parts.o[(part * kFewRows + row) * D + ch] = acc;
+        *po = acc;
         if (ch == 0) {
+          s_sum[piece ^ 1][row] = make_float2(mx, sum);
           p.parts.ml[(part * kFewRows + row) * 2] = mx;
           p.parts.ml[(part * kFewRows + row) * 2 + 1] = sum;
         }

@@ -62,6 +62,14 @@ constexpr int kThreads = 640;
 constexpr int kRegsSoftmax = 152, kRegsConvert = 64, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue == 5 * 96, "registers at launch");
 constexpr int kTok = 128;    // tokens per key tile
+// A worker takes a longer run of key tiles in pieces, O and the sums of weights
+// starting anew in each and put together in fp32: a product's addition to O loses
+// 2^-24 of it on the average, always towards zero, so that a million tokens with
+// values of one sign came out 0.7% too small.  The 65536 tokens of a piece lose 2^-12.
+// Only where the table has room for more tokens than that is the form with pieces
+// launched: 2048 tokens on 32768 cached take 867 us with it, 828 without (d = 128,
+// e4m3; int8 845 and 851, prompts 479 and 477): the code's size and layout.
+constexpr int kPiece = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Key and value tiles in shared memory: what 227 KB hold beside the queries at
@@ -101,7 +109,7 @@ struct Bars {
 struct Seg {
   int r, h, c0, n, kv;     // request and head
   int tok0, rows;          // first token of the row tile in the request, query rows
-  int b0, b1, nu;          // key tiles [b0, b1) of nu
+  int b0, b1, w0, w1, nu;  // key tiles [b0, b1), a piece of the worker's [w0, w1), of nu
 };
 constexpr int kReaders = 19;  // warps that read it
 
@@ -449,7 +457,7 @@ struct Walk {
   __device__ int tokens() const { return min(t.tt, q.n - tile * t.tt); }
 };
 
-template <int CODE, int D>
+template <int CODE, int D, bool PIECES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     kda_cache_attn_tile_kernel(AttnArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -539,6 +547,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int wg = warp >> 2, row = 256 * wg + 128 * rank + 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + 128 * wg, tO = tmem + lanes + 256 + D * wg;
+    // A row of a later piece is added to the sum of the pieces before, or ends it.
+    auto put_together = [&](const Seg& g, int64_t sum, int64_t piece, int64_t out_row, float m,
+                            float l) {
+      float2* ml = reinterpret_cast<float2*>(p.parts.ml) + sum;
+      const float ma = l == 0.0f ? -INFINITY : m, mb = ml->x, top = fmaxf(ma, mb);
+      const float mn = top == -INFINITY ? 0.0f : top;
+      float fa = ex2(ma - mn), fb = ex2(mb - mn);
+      l = l * fa + ml->y * fb;
+      const bool end = g.w0 == 0 && g.b1 == g.nu;
+      if (end) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        fa *= inv;
+        fb *= inv;
+        if (p.lse) p.lse[out_row] = l == 0.0f ? -INFINITY : (mn + log2f(l)) * 0.6931471805599453f;
+      } else {
+        *ml = make_float2(top, l);
+      }
+      float4* so = reinterpret_cast<float4*>(p.parts.o + sum * D);
+      const float4* po = reinterpret_cast<const float4*>(p.parts.o + piece * D);
+#pragma unroll 2
+      for (int c = 0; c < D / 4; ++c) {
+        const float4 a = po[c], b = so[c];
+        const float4 x = make_float4(a.x * fa + b.x * fb, a.y * fa + b.y * fb, a.z * fa + b.z * fb,
+                                     a.w * fa + b.w * fb);
+        if (end)
+          reinterpret_cast<uint2*>(p.out + out_row * D)[c] =
+              make_uint2(sm100::pack_bf16x2(x.x, x.y), sm100::pack_bf16x2(x.z, x.w));
+        else
+          so[c] = x;
+      }
+    };
     uint32_t seg = 0, it = 0;  // segments and key tiles that this row tile has had
     uint32_t tiles = 0;        // key tiles of every segment
     for (;;) {
@@ -723,10 +762,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok || !tensor_wait(&bars.o_full[wg], seg & 1)) break;
       ++seg;
       sm100::tc_fence_after();
-      const float ov = pow2_inverse(vrel) * (1.0f / code_top(CODE));
-      const bool whole = g.b0 == 0 && g.b1 == g.nu;
-      const int64_t slot = 2 * (int64_t)pair + (g.b0 > 0 ? 0 : 1);
+      // (a piece after the first goes to the pair's third slot, and from there to the sum)
+      const bool later = PIECES && g.b0 > g.w0, whole = g.b0 == 0 && g.b1 == g.nu;
+      const int64_t sum_slot = 2 * (int64_t)pair + ((PIECES ? g.w0 : g.b0) > 0 ? 0 : 1);
+      const int64_t slot = later ? 2 * (int64_t)p.parts.ctas + pair : sum_slot;
       const int64_t at = (int64_t)(g.c0 + tok) * p.Hq + g.h * p.G + row % p.G;
+      const float ov = pow2_inverse(vrel) * (1.0f / code_top(CODE));
       const float f = whole ? (l == 0.0f ? 0.0f : ov / l) : ov;
       // O leaves through 64-byte row pieces in shared memory, so that a store
       // writes 8 rows' whole sectors and not 32 rows' halves.
@@ -779,7 +820,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       sm100::tc_fence_before();
-      if (mine) {
+      if (mine && later) {
+        put_together(g, sum_slot * kTileRows + row, slot * kTileRows + row, at, m, l);
+      } else if (mine) {
         if (!whole) {
           p.parts.ml[(slot * kTileRows + row) * 2] = l == 0.0f ? -INFINITY : m;
           p.parts.ml[(slot * kTileRows + row) * 2 + 1] = l;
@@ -980,14 +1023,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       uint32_t tiles = 0;
       bool ok = true;
+      int b0 = w.b0;  // the piece [b0, b1) of the worker's key tiles
       for (uint32_t i = 0; ok; ++i) {
         ok = i < 2 || all_wait(&bars.seg_empty[i & 1], ((i >> 1) - 1) & 1);
         if (!ok) break;
+        if (!PIECES) b0 = w.b0;
+        int b1 = w.b1;
+        if (PIECES) {  // (equal ones)
+          const int pieces = (w.b1 - b0 + kPiece - 1) / kPiece;
+          if (pieces > 1) b1 = b0 + (w.b1 - b0 + pieces - 1) / pieces;
+        }
         if (lane == 0) {
           Seg g{};
           if (w.live())
-            g = {w.r, w.h, w.q.c0, w.q.n, w.q.kv, w.tile * w.t.tt, w.tokens() * p.G, w.b0, w.b1,
-                 w.nu};
+            g = {w.r, w.h, w.q.c0, w.q.n, w.q.kv, w.tile * w.t.tt, w.tokens() * p.G, b0, b1, w.b0,
+                 w.b1, w.nu};
           s_seg[i & 1] = g;
           sm100::mbar_arrive(&bars.seg_full[i & 1]);
         }
@@ -995,13 +1045,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // lane i < 8 looks up tokens 16 i .. 16 i + 15, a page a tile ahead
         const int32_t* table = p.table + (int64_t)w.r * p.max_pages;
         auto has = [&](int k) {
-          return k < w.b1 && (int64_t)k * kTok + 16 * (lane & 7) < w.q.kv;
+          return k < b1 && (int64_t)k * kTok + 16 * (lane & 7) < w.q.kv;
         };
         auto page_of = [&](int k) -> int {
           return load_page_if(table + (((int64_t)k * kTok + 16 * (lane & 7)) >> lg), has(k));
         };
-        int pg = page_of(w.b0);
-        for (int k = w.b0; k < w.b1; ++k, ++tiles) {
+        int pg = page_of(b0);
+        for (int k = b0; k < b1; ++k, ++tiles) {
           const bool in = (uint32_t)pg < (uint32_t)p.num_pages;
           if (!in && has(k)) report(p.status, KDA_ERR_BAD_PAGES);
           const float ks = load_scale_if(p.k_scale + (int64_t)pg * p.Hkv + w.h, in);
@@ -1022,7 +1072,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) sm100::mbar_arrive(&bars.sc_full[e]);
         }
-        w.next();
+        b0 = b1;
+        if (!PIECES || b1 == w.b1) {
+          w.next();
+          b0 = w.b0;
+        }
       }
     } else if (warp >= 18) {
       // -------------- queries ahead into L2; values, told to the first CTA
@@ -1166,18 +1220,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(s_tmem) : "memory");
 }
 
-template <int CODE, int D>
+template <int CODE, int D, bool PIECES>
 kda_status launch_tile(const AttnArgs& p, cudaStream_t s) {
-  auto kernel = kda_cache_attn_tile_kernel<CODE, D>;
+  auto kernel = kda_cache_attn_tile_kernel<CODE, D, PIECES>;
   const kda_status rc = kda_smem_attr((const void*)kernel, Smem<D>::kBytes);
   if (rc != KDA_OK) return rc;
   return launch_following(kernel, 2 * p.parts.ctas, kThreads, Smem<D>::kBytes, s, p);
+}
+
+template <int CODE, int D>
+kda_status launch_form(const AttnArgs& p, cudaStream_t s) {
+  if ((int64_t)p.max_pages << p.page_log2 > (int64_t)kPiece * kTok)
+    return launch_tile<CODE, D, true>(p, s);
+  return launch_tile<CODE, D, false>(p, s);
 }
 
 }  // namespace
 
 kda_status kda_launch_attn_tile(const AttnArgs& p, int d, int code, cudaStream_t s) {
   if (code == KDA_I8)
-    return d == 64 ? launch_tile<KDA_I8, 64>(p, s) : launch_tile<KDA_I8, 128>(p, s);
-  return d == 64 ? launch_tile<KDA_E4M3, 64>(p, s) : launch_tile<KDA_E4M3, 128>(p, s);
+    return d == 64 ? launch_form<KDA_I8, 64>(p, s) : launch_form<KDA_I8, 128>(p, s);
+  return d == 64 ? launch_form<KDA_E4M3, 64>(p, s) : launch_form<KDA_E4M3, 128>(p, s);
 }
