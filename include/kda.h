@@ -470,8 +470,9 @@ int kda_page_runs(int R, int T, int page);
  * their pages back: pushed onto the free stack request by request, page by
  * page; their table columns become -1 and their kv_lens 0.  kv_lens,
  * block_table, free_pages and free_count are updated in place.  Lengths that
- * do not fit the table are KDA_ERR_BAD_SEQLENS, a stack that would hold more
- * than num_pages KDA_ERR_BAD_PAGES; then nothing changes.  R <= 16384.
+ * do not fit the table are KDA_ERR_BAD_SEQLENS, a page number outside the pool
+ * or a stack that would hold more than num_pages KDA_ERR_BAD_PAGES; then nothing
+ * changes.  R <= 16384.
  */
 kda_status kda_page_release(const int32_t* release, int R, int page, int32_t* kv_lens,
                             int32_t* block_table, int max_pages, int32_t* free_pages,
