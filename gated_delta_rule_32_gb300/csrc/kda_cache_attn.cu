@@ -38,6 +38,16 @@ Layout layout(int max_new, int G, int d) {
   return w;
 }
 
+// Reports malformed requests of a call that computes nothing.
+constexpr int kCheckThreads = 256;
+__global__ void __launch_bounds__(kCheckThreads) kda_attn_check_kernel(AttnArgs p) {
+  for (int r = blockIdx.x * kCheckThreads + threadIdx.x; r < p.R; r += gridDim.x * kCheckThreads) {
+    bool bad;
+    load_req(p, r, bad);
+    if (bad) report(p.status, KDA_ERR_BAD_SEQLENS);
+  }
+}
+
 }  // namespace
 
 extern "C" size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv,
@@ -87,12 +97,16 @@ extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)
     return KDA_ERR_CUDA;
-  if (T == 0 || max_new == 0) return KDA_OK;
   int lg = 4;
   while ((1 << lg) < page) ++lg;
   AttnArgs p{q, q_stride, cu_seqlens, kv_lens, block_table, (const uint8_t*)k_codes,
              (const uint8_t*)v_codes, k_scale, v_scale, out, lse, dev_status, R, T, max_new,
              max_pages, Hq, Hkv, Hq / Hkv, num_pages, lg, few_max(d), scale, {}};
+  if (T == 0 || max_new == 0) {  // (what is new then is more than the caller has rows for)
+    if (!dev_status) return KDA_OK;
+    kda_attn_check_kernel<<<(R + kCheckThreads - 1) / kCheckThreads, kCheckThreads, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  }
   const Layout w = layout(max_new, p.G, d);
   if (w.ctas[0] < 1) return KDA_ERR_CUDA;
   const bool own = workspace == nullptr;

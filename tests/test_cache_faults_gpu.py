@@ -47,3 +47,31 @@ def test_release_of_a_request_without_pages_reads_no_table():
     st = status()
     pkg.page_release(ints([1, 0]), lens, tab, free, left, 16, dev_status=st)
     assert st.item() == 0 and left.item() == 4 and tab.tolist() == [[-7, -7], [9, -7]]
+
+
+def attend(cu, kv, T, max_new):
+    H, page, d = 2, 16, 64
+    c = torch.zeros(4, H, page, d, dtype=torch.int8, device="cuda")
+    s = torch.ones(4, H, device="cuda")
+    q = torch.ones(T, 2 * H, d, device="cuda").to(torch.bfloat16)
+    st = status()
+    table = ints([[i % 4, 1] for i in range(len(kv))])
+    pkg.cache_attend(q, ints(cu), ints(kv), table, c, c.clone(), s, s.clone(), max_new=max_new,
+                     dev_status=st)
+    return st.item()
+
+
+@pytest.mark.parametrize("cu,kv,T,max_new,code", [
+    ([0, 1, 1], [5, 3], 1, 0, kda.KDA_ERR_BAD_SEQLENS),    # a request with more than max_new tokens
+    ([0, 3, 5], [5, 3], 5, 0, kda.KDA_ERR_BAD_SEQLENS),
+    ([0, 0, 0], [5, 33], 4, 0, kda.KDA_ERR_BAD_SEQLENS),   # past the table
+    ([0, 0, 0], [-1, 3], 4, 0, kda.KDA_ERR_BAD_SEQLENS),
+    ([0, 0, -1], [5, 3], 4, 0, kda.KDA_ERR_BAD_SEQLENS),
+    ([0, 0, 0], [5, 32], 4, 0, 0),                         # rows of no request: nothing to do
+    ([0, 0, 1], [5, 3], 0, 1, kda.KDA_ERR_BAD_SEQLENS),    # more tokens than rows
+    ([0, 0, 0], [5, 40], 0, 0, kda.KDA_ERR_BAD_SEQLENS),
+    ([0, 0, 0], [5, 3], 0, 0, 0),
+    ([0] * 3001, [7] * 2999 + [-2], 0, 0, kda.KDA_ERR_BAD_SEQLENS),
+])
+def test_steps_without_tokens_are_checked_too(cu, kv, T, max_new, code):
+    assert attend(cu, kv, T, max_new) == code
