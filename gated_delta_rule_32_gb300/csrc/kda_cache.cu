@@ -524,7 +524,8 @@ extern "C" kda_status kda_cache_append(const uint16_t* k, const uint16_t* v, int
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   kda_status rc = clear_status(dev_status, s);
   if (rc != KDA_OK) return rc;
-  if (T == 0 || grid == 0) return KDA_OK;
+  // (without rows every run is outside them)
+  if (grid == 0 || (T == 0 && !dev_status)) return KDA_OK;
   AppendArgs p{{k, v}, {k_stride, v_stride}, {(uint8_t*)k_codes, (uint8_t*)v_codes},
                {k_scale, v_scale}, runs, dev_status, T, num_pages, Hkv};
   const unsigned g = (unsigned)grid;

@@ -75,3 +75,16 @@ def attend(cu, kv, T, max_new):
 ])
 def test_steps_without_tokens_are_checked_too(cu, kv, T, max_new, code):
     assert attend(cu, kv, T, max_new) == code
+
+
+@pytest.mark.parametrize("run,code", [([0, 1, 0, 0], kda.KDA_ERR_BAD_PAGES), ([0, 0, 0, 0], 0),
+                                      ([0, -1, 0, 0], kda.KDA_ERR_BAD_PAGES)])
+def test_runs_of_an_append_without_rows_are_checked_too(run, code):
+    c = torch.full((2, 1, 16, 64), 3, dtype=torch.int8, device="cuda")
+    s = torch.ones(2, 1, device="cuda")
+    x = torch.empty(0, 1, 64, dtype=torch.bfloat16, device="cuda")
+    st = status()
+    v, vs = c.clone(), s.clone()
+    pkg.cache_append(x, x, ints([run, [0, 0, 0, 0]]), c, v, s, vs, dev_status=st)
+    assert st.item() == code
+    assert (c == 3).all() and (v == 3).all() and (s == 1).all() and (vs == 1).all()
