@@ -435,7 +435,10 @@ extern "C" kda_status kda_page_plan(const int32_t* new_lens, const int32_t* ctx_
   if ((int64_t)num_pages * page > INT32_MAX || (int64_t)max_pages * page > (1 << 30) ||
       T > (1 << 26))
     return KDA_ERR_UNSUPPORTED;  // slots and lengths are int32
-  if (((uintptr_t)runs & 15) != 0) return KDA_ERR_MISALIGNED;
+  if (!aligned(16, runs) || !aligned(4, new_lens, ctx_lens, block_table, free_pages, free_count,
+                                     cu_seqlens, kv_lens, slots, positions, free_count_out,
+                                     dev_status))
+    return KDA_ERR_MISALIGNED;
   const int max_runs = kda_page_runs(R, T, page);
   const size_t n4 = sizeof(int32_t);
   const void* outs[] = {cu_seqlens, kv_lens, slots, positions, runs, free_count_out};
@@ -475,6 +478,8 @@ extern "C" kda_status kda_page_release(const int32_t* release, int R, int page, 
       max_pages < 1 || num_pages < 1)
     return KDA_ERR_INVALID_ARG;
   if (R > kMaxRequests || !page_ok(page)) return KDA_ERR_UNSUPPORTED;
+  if (!aligned(4, release, kv_lens, block_table, free_pages, free_count, dev_status))
+    return KDA_ERR_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int smem = R * (int)sizeof(int32_t);
   if (smem > 40 * 1024) {
@@ -502,10 +507,8 @@ extern "C" kda_status kda_cache_append(const uint16_t* k, const uint16_t* v, int
     return KDA_ERR_UNSUPPORTED;
   const int64_t width = (int64_t)Hkv * d;
   if (k_stride < width || v_stride < width) return KDA_ERR_INVALID_ARG;
-  if (k_stride % 8 || v_stride % 8 ||
-      (((uintptr_t)k | (uintptr_t)v | (uintptr_t)k_codes | (uintptr_t)v_codes |
-        (uintptr_t)runs) & 15) != 0 ||
-      (((uintptr_t)k_scale | (uintptr_t)v_scale) & 3) != 0)
+  if (k_stride % 8 || v_stride % 8 || !aligned(16, k, v, k_codes, v_codes, runs) ||
+      !aligned(4, k_scale, v_scale, dev_status))
     return KDA_ERR_MISALIGNED;
   const size_t pool = (size_t)num_pages * width * page, sc = (size_t)num_pages * Hkv * 4;
   const void* outs[] = {k_codes, v_codes, k_scale, v_scale};

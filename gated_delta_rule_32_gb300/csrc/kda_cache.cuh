@@ -21,6 +21,12 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && na && nb && x < y + nb && y < x + na;
 }
 
+// Whether all addresses are multiples of n (a power of two).
+template <class... Ptr>
+inline bool aligned(size_t n, Ptr... ptr) {
+  return (((uintptr_t)ptr | ...) & (n - 1)) == 0;
+}
+
 __device__ __forceinline__ void report(int32_t* dev_status, kda_status s) {
   if (dev_status) atomicExch(dev_status, (int32_t)s);
 }

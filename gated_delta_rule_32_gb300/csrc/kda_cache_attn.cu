@@ -77,8 +77,8 @@ extern "C" kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride,
   if ((int64_t)max_pages * page > (1 << 30) || T > (1 << 26)) return KDA_ERR_UNSUPPORTED;
   const int64_t width = (int64_t)Hq * d;
   if (q_stride < width) return KDA_ERR_INVALID_ARG;
-  if (q_stride % 8 || (((uintptr_t)q | (uintptr_t)out | (uintptr_t)k_codes |
-                        (uintptr_t)v_codes) & 15) != 0)
+  if (q_stride % 8 || !aligned(16, q, out, k_codes, v_codes) ||
+      !aligned(4, cu_seqlens, kv_lens, block_table, k_scale, v_scale, lse, dev_status))
     return KDA_ERR_MISALIGNED;
   const size_t pool = (size_t)num_pages * Hkv * page * d, sc = (size_t)num_pages * Hkv * 4;
   const size_t out_n = (size_t)T * width * 2, lse_n = (size_t)T * Hq * 4;

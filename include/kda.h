@@ -424,7 +424,8 @@ kda_status kda_debug_record_capacity(int64_t items);
  * Columns past a request's last page are never read.  Limits: R <= 16384,
  * max_pages * page <= 2^30, T <= 2^26, and the plan's slots are int32:
  * num_pages * page < 2^31.  What a page holds past its request's length never
- * reaches a result, whatever its bytes.
+ * reaches a result, whatever its bytes.  All pointers are aligned to their
+ * elements, those named below to 16 or 256 bytes (KDA_ERR_MISALIGNED).
  */
 typedef enum { KDA_I8 = 0, KDA_E4M3 = 1 } kda_code;
 
