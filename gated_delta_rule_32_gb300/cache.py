@@ -64,7 +64,12 @@ def _call(dev, dev_status, name, *args):
     `dev` and its current stream.  (A decode step's calls are short: no
     context manager where the device is current, no Stream object.)"""
     fn = getattr(kda._lib or kda.load(), name)
-    status = None if dev_status is None else dev_status.data_ptr()
+    status = None
+    if dev_status is not None:
+        if dev_status.dtype is not torch.int32 or dev_status.get_device() != dev or \
+                dev_status.numel() < 1:
+            raise ValueError("dev_status must be an int32 tensor of one element on cuda:%d" % dev)
+        status = dev_status.data_ptr()
     stream = torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch._C._cuda_getDevice():
         rc = fn(*args, status, stream)

@@ -88,3 +88,24 @@ def test_runs_of_an_append_without_rows_are_checked_too(run, code):
     pkg.cache_append(x, x, ints([run, [0, 0, 0, 0]]), c, v, s, vs, dev_status=st)
     assert st.item() == code
     assert (c == 3).all() and (v == 3).all() and (s == 1).all() and (vs == 1).all()
+
+
+@pytest.mark.parametrize("bad", ["cpu", "int64", "empty", "float"])
+def test_a_status_that_is_no_int32_on_the_device_is_refused(bad):
+    # a kernel would write to the host's address, or past the element
+    st = {"cpu": torch.zeros(1, dtype=torch.int32),
+          "int64": torch.zeros(1, dtype=torch.int64, device="cuda"),
+          "empty": torch.zeros(0, dtype=torch.int32, device="cuda"),
+          "float": torch.zeros(1, device="cuda")}[bad]
+    one, lens = ints([1]), ints([0])
+    tab, free, left = ints([[-1, -1]]), ints([0, 1]), ints([2])
+    c = torch.zeros(2, 1, 16, 64, dtype=torch.int8, device="cuda")
+    s = torch.zeros(2, 1, device="cuda")
+    x = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for f, a in ((pkg.page_plan, (one, lens, tab, free, left, 1, 16)),
+                 (pkg.page_release, (one, lens, tab, free, left, 16)),
+                 (pkg.cache_append, (x, x, ints([[0, 1, 0, 0]]), c, c.clone(), s, s.clone())),
+                 (pkg.cache_attend, (x, ints([0, 1]), one, ints([[0, 1]]), c, c.clone(), s, s.clone()))):
+        with pytest.raises(ValueError, match="dev_status"):
+            f(*a, dev_status=st)
+    assert left.item() == 2 and (tab == -1).all() and (c == 0).all() and (s == 0).all()
