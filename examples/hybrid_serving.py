@@ -105,7 +105,7 @@ class Hybrid:
         pkg.page_release(done, self.lens, self.table, self.free, self.left, self.page)
         for s in self.state:
             if s is not None:
-                s *= (done == 0)[:, None, None, None]
+                s.masked_fill_((done != 0)[:, None, None, None], 0.0)
 
 
 def main(argv=None):
