@@ -60,12 +60,28 @@ class Hybrid:
         self.lens = torch.zeros(requests, **ints)
         self.free = torch.arange(pages - 1, -1, -1, **ints)
         self.left = torch.full((1,), pages, **ints)
+        # what the device finds: of the plan, the release, and each layer's two calls
+        self.status = torch.zeros(2 + 2 * len(layers), **ints)
+
+    def check(self):
+        """Raises what the device has found since the last look (waits for it)."""
+        found = self.status.tolist()
+        if any(found):
+            self.status.zero_()
+            at = next(i for i, code in enumerate(found) if code)
+            what = ["kda_page_plan", "kda_page_release"] + ["kda_cache_append", "kda_cache_attn"] * \
+                len(self.layers)
+            raise kda.KdaError(what[at], found[at])
 
     def step(self, x, new_lens, max_new):
         """x [T, width]: the packed new tokens, new_lens[r] of request r, at
-        most max_new each.  Returns the last layer's output [T, width]."""
+        most max_new each.  Returns the last layer's output [T, width].  A step
+        that does not fit raises before anything has changed; what the layers'
+        calls find (more than max_new tokens, say) the next step or check() raises."""
         T = x.shape[0]
-        plan = pkg.page_plan(new_lens, self.lens, self.table, self.free, self.left, T, self.page)
+        plan = pkg.page_plan(new_lens, self.lens, self.table, self.free, self.left, T, self.page,
+                             dev_status=self.status[0:1])
+        self.check()
         for i, kind in enumerate(self.layers):
             y = x * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6).to(x.dtype)
             y = y @ self.w[i][0]
@@ -76,9 +92,10 @@ class Hybrid:
                     [n * self.dim for n in (self.q_heads, self.kv_heads, self.kv_heads)], dim=1))
                 kc, vc, ks, vs = self.cache[i]
                 # q, k, v stay views of the projection's output: token strides differ
-                pkg.cache_append(k, v, plan.runs, kc, vc, ks, vs)
+                at = 2 + 2 * i
+                pkg.cache_append(k, v, plan.runs, kc, vc, ks, vs, dev_status=self.status[at:at + 1])
                 y, _ = pkg.cache_attend(q, plan.cu_seqlens, plan.kv_lens, self.table, kc, vc, ks, vs,
-                                        max_new=max_new)
+                                        max_new=max_new, dev_status=self.status[at + 1:at + 2])
             x = x + y.reshape(T, -1) @ self.w[i][1]
         self.lens, self.left = plan.kv_lens, plan.free_count
         return x
@@ -102,7 +119,9 @@ class Hybrid:
 
     def finish(self, done):
         """Requests with done[r] != 0 leave: their pages go back, their states to zero."""
-        pkg.page_release(done, self.lens, self.table, self.free, self.left, self.page)
+        pkg.page_release(done, self.lens, self.table, self.free, self.left, self.page,
+                         dev_status=self.status[1:2])
+        self.check()
         for s in self.state:
             if s is not None:
                 s.masked_fill_((done != 0)[:, None, None, None], 0.0)
@@ -127,13 +146,14 @@ def main(argv=None):
     t = time.perf_counter()
     for _ in range(a.steps):
         out = model.step(out, one, 1)
-    torch.cuda.synchronize()
+    model.check()
     ms = (time.perf_counter() - t) / max(1, a.steps) * 1e3
     print("lengths %s, pages left %d, %.2f ms a decode step" % (model.lens.tolist(), model.left, ms))
     # the second request leaves, another takes its row
     model.finish(torch.tensor([0, 1, 0, 0], **ints))
     print("pages left %d after one request left" % model.left)
     out = model.step(tokens(3 + 50), torch.tensor([1, 50, 1, 1], **ints), 50)
+    model.check()
     print("lengths %s, pages left %d, output finite: %s" % (
         model.lens.tolist(), model.left, bool(out.isfinite().all())))
     return model, out
