@@ -6,6 +6,8 @@ marshals arguments (kda.py).  There is no CPU fallback: without the built
 library or a GPU, calls raise.  cache.py holds the tensor-level calls of the
 paged 8-bit cache that a hybrid model's attention layers keep.
 """
+import importlib.util
+
 from .kda import (forward, load, status_string, kda_chunk_fwd, kda_chunk_fwd_f32,  # noqa: F401
                   kda_chunk_fwd_ex, kda_chunk_fwd_host, kda_workspace_bytes,
                   kda_host_staging_bytes, kda_debug_intra, kda_build_info, kda_resolve_algo, KdaError,
@@ -28,5 +30,6 @@ __all__ = ["forward", "load", "status_string", "kda_chunk_fwd", "kda_chunk_fwd_f
            "kda_chunk_fwd_ex", "kda_chunk_fwd_host", "kda_workspace_bytes",
            "kda_host_staging_bytes", "kda_debug_intra", "kda_build_info", "KdaError",
            "kda_page_plan", "kda_page_runs", "kda_page_release", "kda_cache_append",
-           "kda_cache_attn", "kda_cache_attn_workspace_bytes", "PagePlan", "page_plan",
-           "page_release", "cache_append", "cache_attend"]
+           "kda_cache_attn", "kda_cache_attn_workspace_bytes"]
+if importlib.util.find_spec("torch"):  # (a star import fetches every name listed)
+    __all__ += _CACHE
