@@ -7,7 +7,7 @@ A step of a serving loop::
     plan = page_plan(new_lens, ctx_lens, block_table, free_pages, free_count, T, page)
     cache_append(k, v, plan.runs, k_codes, v_codes, k_scale, v_scale)
     out, lse = cache_attend(q, plan.cu_seqlens, plan.kv_lens, block_table,
-                            k_codes, v_codes, k_scale, v_scale)
+                            k_codes, v_codes, k_scale, v_scale, max_new=max_new)
     ctx_lens, free_count = plan.kv_lens, plan.free_count
 
 plan.cu_seqlens is also what the packed gated delta rule forward takes.  The
@@ -16,7 +16,10 @@ checked, outputs allocated and the library called, on the current stream of
 the tensors' device, or on `stream`, which then also owns the outputs' memory
 (record_stream() them where another stream uses them).  Errors that the host can see raise
 ValueError or KdaError before anything is queued; those that only the device
-can see go to `dev_status` (an int32 CUDA tensor of one element) if given.
+can see go to `dev_status` (an int32 CUDA tensor of one element, set by every
+call it is given to: one for each call whose status is wanted).  Without it
+they go unnoticed: after a plan that did not fit, or for a request with more
+than max_new tokens, rows of the attention's output are never written.
 """
 from __future__ import annotations
 
@@ -112,7 +115,8 @@ def page_plan(new_lens, ctx_lens, block_table, free_pages, free_count, T, page, 
     """Bookkeeping of a step in which request r brings new_lens[r] tokens (at
     most T in all) to its ctx_lens[r] cached ones: a PagePlan.  New page
     numbers come from the top of the stack free_pages[: free_count] and are
-    entered into block_table [R, max_pages] in place."""
+    entered into block_table [R, max_pages] in place.  free_pages has room for
+    every page of the pool: its length is the pool's size."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return page_plan(new_lens, ctx_lens, block_table, free_pages, free_count, T, page,
@@ -184,9 +188,11 @@ def _workspace_bytes(dev, R, T, max_new, Hq, Hkv, d):
 def cache_attend(q, cu_seqlens, kv_lens, block_table, k_codes, v_codes, k_scale, v_scale,
                  scale=None, max_new=None, dev_status=None, stream=None):
     """Causal attention of a step's queries (bf16 [T, Hq, d], any token
-    stride) over the cache: (out bf16 [T, Hq, d], lse fp32 [T, Hq]).  `scale`
-    defaults to d ** -0.5; max_new is the most new tokens any request has
-    (default: T)."""
+    stride) over the cache: (out bf16 [T, Hq, d], lse fp32 [T, Hq]); rows past
+    cu_seqlens[R] are left as they were allocated.  `scale`
+    defaults to d ** -0.5; max_new is the most new tokens any request has.  Its
+    default, T, is always right but runs kernels for that many rows: a decode step
+    of 64 requests takes 155 us so, 139 with max_new=1, 2 long ones 83 and 78."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return cache_attend(q, cu_seqlens, kv_lens, block_table, k_codes, v_codes, k_scale,

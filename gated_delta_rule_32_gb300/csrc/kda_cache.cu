@@ -245,7 +245,7 @@ struct AppendArgs {
 
 // Threads: kAppendPasses 16-byte pieces each where the page has so many.  More
 // pieces a thread are more bytes in flight an SM until registers run out: the
-// prompts' append took 48.0 / 41.0 / 44.5 us with 4 / 8 / 16.
+// prompts' append took 48.0 / 41.0 / 44.5 us with 4 / 8 / 16 (e4m3; int8 41.3 with 8).
 constexpr int kAppendPasses = 8;
 __host__ __device__ constexpr int append_threads(int page, int d) {
   const int n = page * d / 8 / kAppendPasses;

@@ -42,9 +42,13 @@ struct AttnArgs {
 // A request with at most few_max(d) query rows per key / value head runs on the
 // few-row kernel, in groups of kFewRows.  Every group converts all codes once
 // more, so its time grows with rows times d, the tile kernel's hardly up to its
-// 512-row segments.  Few-row against tile kernel: d = 64 (32 requests, 2400
-// cached tokens on average, 2 heads) 64 rows 36 : 47 us, 128 rows 61 : 49; d =
-// 128 (48 requests, 1700 tokens, 4 heads) 32 rows 83 : 96, 48 rows 125 : 104.
+// 512-row segments.  Few-row against tile kernel, us (e4m3): d = 64, 2 heads: 32
+// requests with up to 4096 cached tokens, 64 rows 38 : 47, 96 rows 49 : 48, 128 rows
+// 61 : 49; 4 requests with up to 65536, 64 rows 46 : 67, 128 rows 71 : 68.  d = 128: 48
+// requests with up to 3000, 4 heads, 32 rows 73 : 98, 48 rows 97 : 96; 4 requests with up
+// to 65536, 2 heads, 32 rows 52 : 79, 48 rows 64 : 79, 64 rows 74 : 80; single tokens of
+// 64 requests with up to 8192, 48 rows 113 : 133.  (So the rule is right for short
+// contexts, and 16 to 32 rows low for long ones.)
 constexpr int kFewRows = 16;
 __host__ __device__ constexpr int few_max(int d) { return 4096 / d; }
 // CTAs of the few-row kernel an SM: as many as its registers allow.  SMs that the

@@ -10,12 +10,13 @@
 // parts, which kda_attn_join_kernel joins.
 //
 // 64 requests' decode step on up to 8192 cached tokens (8 heads, d = 128, 654 MB
-// of codes): 143 us with the join, 4.6 TB/s; a kernel that only reads as many
+// of codes): 140 us with the join, 4.7 TB/s; a kernel that only reads as many
 // bytes takes 108-118 us, and the SMs' times for equal shares differ by half.
-// Two contexts of up to 262144 tokens (4 heads): 79 us.  One request of 700
+// Two contexts of up to 262144 tokens (4 heads): 78 us.  One request of 700
 // tokens: 12 us, of which the schedule, the chain of one CTA and the join take
-// about equal parts.  Three CTAs an SM, as many as the registers allow; shares
-// half as long (six an SM) took 141 us, four CTAs an SM with NB = 1 142 us.
+// about equal parts.  Three CTAs an SM, as many as the registers allow (168 a
+// thread; with 16 rows at d = 128 20 bytes spill).  Against 143 us then, shares
+// half as long (six an SM) took 141, four CTAs an SM with NB = 1 142.
 //
 // Warp w of a CTA takes every fourth run of NB 16-token blocks.  Products run on
 // mma.m16n8k16 with the tokens (then the channels) on the 16-row side, which
@@ -673,7 +674,8 @@ kda_status launch_rows(const AttnArgs& p, cudaStream_t s) {
 template <int CODE, int D>
 kda_status launch_nt(const AttnArgs& p, cudaStream_t s) {
   // one 8-row tile where no request can have more rows than that: two, the
-  // second empty, took 160 us where one takes 142 (64 decode steps of 4 rows)
+  // second empty, take 148 us where one takes 139 (64 decode steps of 4 rows, int8;
+  // e4m3 142 and 137)
   if ((int64_t)p.max_new * p.G <= 8) return launch_rows<CODE, D, 1>(p, s);
   return launch_rows<CODE, D, 2>(p, s);
 }

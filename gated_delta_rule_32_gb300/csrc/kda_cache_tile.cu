@@ -33,7 +33,7 @@
 // least as large (vref), which leaves O at the end.
 //
 // Bound by the products where rows are many: 4 D flops for each row and token,
-// at 2048 tokens on 32768 cached (32 heads on 4, d = 128) 837 us, 1355 TFLOP/s;
+// at 2048 tokens on 32768 cached (32 heads on 4, d = 128, e4m3) 827 us, 1371 TFLOP/s;
 // the tensor cores work 2 x 1024 of the 2.6-2.9k cycles that a key tile of both
 // row tiles takes, and the rest is the chain of one row tile, which the other's
 // products cover in part only: products 1024 -> softmax 1480-1900 (exponentials
@@ -41,9 +41,9 @@
 // one CTA a tile 1026 us; S in two halves, so that a row tile's products and
 // softmax overlap, 914-1040 us (products of 64 tokens take 48 cycles, not 32:
 // shared memory); a second warp issuing products 950-987 us.  Prompts without a
-// cache, 9 of up to 4096 tokens (32 heads on 8): 461 us, 925 TFLOP/s; half of
-// a tile on the diagonal is masked, and a segment's own cost (queries in, O out)
-// weighs more where its keys are few.
+// cache, 9 of up to 4096 tokens (32 heads on 8): int8 475 us, 898 TFLOP/s, e4m3 458;
+// half of a tile on the diagonal is masked, and a segment's own cost (queries in, O
+// out) weighs more where its keys are few.
 #include <type_traits>
 
 #include "kda_cache_attn.cuh"
@@ -57,7 +57,8 @@ using namespace kda_cache;
 // anew (setmaxnreg): 2 x 152 + 2 x 64 + 48 = 5 x 96.  Prompts of up to 4096
 // tokens and 2048 tokens on 32768 cached took 466 and 842 us so, 502 and 878
 // with 136 / 72 / 64, 481 and 880 with 144 / 72 / 48, 479 and 894 with
-// 160 / 56 / 48, where the converters spill in their loop.
+// 160 / 56 / 48, where the converters spill in their loop.  (At d = 128 84 to 88
+// bytes a thread are spilled all the same, at d = 64 none without pieces.)
 constexpr int kThreads = 640;
 constexpr int kRegsSoftmax = 152, kRegsConvert = 64, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue == 5 * 96, "registers at launch");

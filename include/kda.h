@@ -516,13 +516,17 @@ kda_status kda_cache_append(const uint16_t* k, const uint16_t* v, int64_t k_stri
  * Rows past cu_seqlens[R] are not written.  Hq a multiple of Hkv, at most
  * 64 query heads for each; R <= 16384.  max_new: the most new tokens any
  * request has, as far as the host knows (T is always right); a larger
- * request is KDA_ERR_BAD_SEQLENS.  A request whose new tokens make at most
+ * request is KDA_ERR_BAD_SEQLENS.  What is launched goes by it: a decode step
+ * given T runs wider kernels than its rows need (64 requests with up to 8192
+ * cached tokens: 155 us, 139 with 1).  A request whose new tokens make at most
  * 4096 / d query rows for a key / value head runs on a kernel for few rows (bound
  * by the cache's bytes), others on the tensor cores in tiles; both split a
  * long cache over the chip and join the parts.
  * Malformed cu_seqlens or lengths past the table are KDA_ERR_BAD_SEQLENS, a
  * page number outside the pool KDA_ERR_BAD_PAGES; the request's outputs are
- * then unspecified.
+ * then unspecified, or not written.  The same call gives the same bits each
+ * time; a request's last bits depend on what else is in the batch, which moves
+ * the borders of the parts that are summed apart.
  *   workspace  device scratch of kda_cache_attn_workspace_bytes() bytes,
  *              256-byte aligned, contents arbitrary; or NULL: taken from the
  *              stream-ordered allocator.
