@@ -16,13 +16,14 @@ struct PartHead {
 
 // What a kernel leaves for the join, in the workspace.  A worker leaves at most
 // two parts: of the segment that its share begins in (slot 2 c) and of the one
-// that it ends in (slot 2 c + 1).
+// that it ends in (slot 2 c + 1).  A long run of tokens is put together in the same
+// slot, piece by piece; the tile kernel's pieces come through a third one (2 ctas + c).
 struct Parts {
   int ctas, rows;    // workers of the kernel (CTAs, or pairs); a part's rows
   int64_t* total;    // units of the whole batch
   PartHead* head;    // [ctas]
-  float* ml;         // [2 ctas][rows][2] maximum (log2) and sum of a part's rows
-  float* o;          // [2 ctas][rows][D] a part's sum of weighted values
+  float* ml;         // [slot][rows][2] maximum (log2) and sum of a part's rows
+  float* o;          // [slot][rows][D] a part's sum of weighted values
 };
 
 struct AttnArgs {

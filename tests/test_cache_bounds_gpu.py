@@ -94,7 +94,8 @@ def test_most_requests_bring_nothing(dtype, G):
 @pytest.mark.parametrize("dtype", [I8, F8])
 @pytest.mark.parametrize("span", [60.0, 700.0, -60.0, -700.0])
 @pytest.mark.parametrize("new,ctx,d", [([1], [3000], 64), ([1, 2], [30000, 500], 128), ([60], [2500], 64),
-                                       ([100, 1], [20000, 700], 128), ([3], [120000], 64)])
+                                       ([100, 1], [20000, 700], 128), ([3], [120000], 64),
+                                       ([60], [150000], 64)])
 def test_scores_and_value_scales_that_rise_or_fall_along_the_context(new, ctx, d, span, dtype):
     # scores change by `span` from the first page to the last, value scales by a
     # factor of 2^20 the same way: references and scales are passed all the time
