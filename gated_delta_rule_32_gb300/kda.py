@@ -80,6 +80,11 @@ _SIGS = {
     "kda_cache_attn": (_i, [_vp, _l] + [_vp] * 3 + [_i] + [_vp] * 6 + [_i] * 9 +
                        [ctypes.c_float, _vp, ctypes.c_size_t, _vp, _vp]),
     "kda_cache_attn_workspace_bytes": (ctypes.c_size_t, [_i] * 6),
+    "kda_linear_fwd": (_i, [_vp, _l] * 4 + [_vp] * 3 + [_i] * 6 + [_vp, _i, ctypes.c_float, _vp,
+                                                             ctypes.c_size_t, _vp, _vp]),
+    "kda_linear_workspace_bytes": (ctypes.c_size_t, [_i] * 7),
+    "kda_linear_decode": (_i, [_vp, _l] * 4 + [_vp] * 2 + [_i] * 7 + [ctypes.c_float, _vp]),
+    "kda_rotary": (_i, [_vp, _l] * 4 + [_vp] * 2 + [_i] * 5 + [ctypes.c_float] + [_i] * 3 + [_vp]),
 }
 
 
@@ -367,3 +372,32 @@ def kda_cache_attn(q, q_stride, cu_seqlens, kv_lens, block_table, max_pages, k_c
 
 def kda_cache_attn_workspace_bytes(R, T, max_new, Hq, Hkv, d) -> int:
     return load().kda_cache_attn_workspace_bytes(R, T, max_new, Hq, Hkv, d)
+
+
+def kda_linear_fwd(q, q_stride, k, k_stride, v, v_stride, log_decay, decay_stride, init_state, out,
+                   final_state, B, T, H, Hk, dk, dv, cu_seqlens=None, dtype=KDA_BF16, scale=1.0,
+                   workspace=None, workspace_bytes=0, dev_status=None, stream=None) -> int:
+    return load().kda_linear_fwd(_p(q), q_stride, _p(k), k_stride, _p(v), v_stride, _p(log_decay),
+                                 decay_stride, _p(init_state), _p(out), _p(final_state), B, T, H,
+                                 Hk, dk, dv, _p(cu_seqlens), dtype, float(scale), _p(workspace),
+                                 workspace_bytes, _p(dev_status), _stream(stream))
+
+
+def kda_linear_workspace_bytes(B, T, H, dk, dv, dtype=KDA_BF16, packed=0) -> int:
+    return load().kda_linear_workspace_bytes(B, T, H, dk, dv, dtype, int(packed))
+
+
+def kda_linear_decode(q, q_stride, k, k_stride, v, v_stride, log_decay, decay_stride, state, out, N,
+                      T, H, Hk, dk, dv, dtype=KDA_BF16, scale=1.0, stream=None) -> int:
+    return load().kda_linear_decode(_p(q), q_stride, _p(k), k_stride, _p(v), v_stride,
+                                    _p(log_decay), decay_stride, _p(state), _p(out), N, T, H, Hk,
+                                    dk, dv, dtype, float(scale), _stream(stream))
+
+
+def kda_rotary(q, q_stride, q_out, q_out_stride, k, k_stride, k_out, k_out_stride, positions,
+               frequencies, T, Hq, Hk, d, part, amplitude=1.0, interleaved=0, inverse=0,
+               dtype=KDA_BF16, stream=None) -> int:
+    return load().kda_rotary(_p(q), q_stride, _p(q_out), q_out_stride, _p(k), k_stride, _p(k_out),
+                             k_out_stride, _p(positions), _p(frequencies), T, Hq, Hk, d, part,
+                             float(amplitude), int(interleaved), int(inverse), dtype,
+                             _stream(stream))

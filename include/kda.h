@@ -543,6 +543,93 @@ kda_status kda_cache_attn(const uint16_t* q, int64_t q_stride, const int32_t* cu
 /* Scratch bytes of kda_cache_attn for these sizes on the current device. */
 size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv, int d);
 
+/*
+ * Linear attention with a decay for each head: the plain member of the
+ * recurrent family above, without the erase and with one decay factor a token
+ * and head.  (No counterpart on the pages.)  For every sequence and head:
+ *
+ *   a_t = min(log_decay_t, 0)
+ *   S_t = exp(a_t) S_{t-1} + k_t v_t^T          (S: dk x dv)
+ *   o_t = scale * S_t^T q_t
+ *
+ * A log-decay of -infinity forgets everything before its token; one above 0
+ * counts as 0, a NaN makes what follows it NaN.
+ *
+ *   q, k       [rows, Hk, dk]   rows q_stride, k_stride elements apart
+ *   v          [rows, H, dv]    v_stride; out [rows, H, dv] contiguous
+ *   log_decay  fp32 [rows, H], decay_stride elements apart, or with a
+ *              decay_stride of 0 one value for each head, [H]
+ *   states     fp32 [N, H, dk, dv], contiguous
+ *
+ * H is a multiple of Hk: head h reads the queries and keys of head
+ * h / (H / Hk).  Heads and channels of a row are contiguous; strides are
+ * multiples of 16 bytes, at most 2^30 elements.  q, k, v, out and the states
+ * are 16-byte aligned.  dk, dv in {16, 32, 64, 128}; dtype (of q, k, v and
+ * out) KDA_BF16 or KDA_F32; H <= 65536, N * H <= 2^28, at most 2^30 rows.
+ * Sums and states are fp32.
+ */
+
+/*
+ * kda_linear_fwd -- whole prompts.  Dense: B sequences of T rows each; packed:
+ * B carries the number of sequences N, T the rows there are, and cu_seqlens
+ * (device int32, N + 1 entries, cu_seqlens[0] = 0, non-decreasing, the last at
+ * most T) their borders; rows behind the last sequence are not written.
+ * init_state NULL starts from zero; final_state may be NULL or init_state;
+ * otherwise no output overlaps an input.  Malformed cu_seqlens are
+ * KDA_ERR_BAD_SEQLENS in dev_status (as in kda_chunk_fwd_ex), the outputs then
+ * unspecified.
+ *   workspace  device scratch of kda_linear_workspace_bytes() bytes, 256-byte
+ *              aligned, contents arbitrary; or NULL: taken from the
+ *              stream-ordered allocator.
+ */
+kda_status kda_linear_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const float* log_decay,
+                          int64_t decay_stride, const float* init_state, void* out,
+                          float* final_state, int B, int T, int H, int Hk, int dk, int dv,
+                          const int32_t* cu_seqlens, kda_dtype dtype, float scale,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                          kda_stream_t stream);
+
+/* Scratch bytes of kda_linear_fwd for these sizes on the current device. */
+size_t kda_linear_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype dtype,
+                                  int packed);
+
+/*
+ * kda_linear_decode -- T tokens of each of N sequences (row n * T + t), token
+ * by token: a decode step (T = 1) or a few drafted tokens.  `state` is updated
+ * in place; it moves through memory once whatever T is.
+ */
+kda_status kda_linear_decode(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const float* log_decay,
+                             int64_t decay_stride, float* state, void* out, int N, int T, int H,
+                             int Hk, int dk, int dv, kda_dtype dtype, float scale,
+                             kda_stream_t stream);
+
+/*
+ * kda_rotary -- rotary positions of a step's queries and keys (for linear
+ * attention, or before kda_cache_append and kda_cache_attn; kda_page_plan's
+ * positions are what it takes).  Pair i < part / 2 of each head, channels
+ * (i, i + part / 2), or (2 i, 2 i + 1) where `interleaved`, is turned by
+ * t = positions[row] * frequencies[i], or -t where `inverse`:
+ *   (x, y) -> amplitude * (x cos t - y sin t, x sin t + y cos t)
+ * (inverse is the gradient of the same call: the transposed map.)  Channels
+ * part .. d - 1 are copied.  Rows with a negative position are not written.
+ *   q [T, Hq, d], k [T, Hk, d] and their outputs: rows `*_stride` elements
+ *     apart (multiples of 16 bytes, at most 2^30), heads and channels
+ *     contiguous, 16-byte aligned.  An output is its input (the same pointer
+ *     and stride: in place) or overlaps nothing.  Hq or Hk may be 0.
+ *   positions    device int32 [T]
+ *   frequencies  device double [part / 2], radians a token (8-byte aligned)
+ * d and part are multiples of 16, d at most 512; T <= 2^30; dtype KDA_BF16 or
+ * KDA_F32.  Angles are taken modulo a turn in 64-bit integers: positions far
+ * out lose nothing.  The products are fp32, rounded once.
+ */
+kda_status kda_rotary(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                      const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride,
+                      const int32_t* positions, const double* frequencies, int T, int Hq, int Hk,
+                      int d, int part, float amplitude, int interleaved, int inverse,
+                      kda_dtype dtype, kda_stream_t stream);
+
 /* The path family kda_chunk_fwd_ex would take for these arguments:
  * KDA_ALGO_SIMT, KDA_ALGO_TC (AUTO on the tensor cores: fused, segmented or
  * two-kernel form by the sizes) or KDA_ALGO_SPLIT when asked for; -1 if the
