@@ -53,7 +53,9 @@ kda_status check(const LinearArgs& p, kda_dtype dtype, int64_t rows) {
 
 extern "C" size_t kda_linear_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype dtype,
                                              int packed) {
-  return 0;
+  if (B < 1 || T < 1 || H < 1 || !kda_linear_tile_ok(dk, dv, dtype)) return 0;
+  if (H > 65536 || (int64_t)B * H > (1 << 28)) return 0;
+  return kda_linear_tile_workspace(B, T, H, dk, dv, packed != 0);
 }
 
 extern "C" kda_status kda_linear_fwd(const void* q, int64_t q_stride, const void* k,
@@ -68,15 +70,21 @@ extern "C" kda_status kda_linear_fwd(const void* q, int64_t q_stride, const void
                      out, final_state, cu_seqlens, dev_status, B, T, H, Hk, dk, dv, scale};
   const kda_status rc = check(p, dtype, cu_seqlens ? T : (int64_t)B * T);
   if (rc != KDA_OK) return rc;
+  const size_t need = kda_linear_workspace_bytes(B, T, H, dk, dv, dtype, cu_seqlens != nullptr);
   if (workspace) {
     if (!aligned(256, workspace)) return KDA_ERR_MISALIGNED;
-    if (workspace_bytes < kda_linear_workspace_bytes(B, T, H, dk, dv, dtype, cu_seqlens != nullptr))
-      return KDA_ERR_WORKSPACE;
+    if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)
     return KDA_ERR_CUDA;
-  return kda_launch_linear_rec(p, dtype, s);
+  // (without rows the tensor maps have nothing to describe: states only)
+  if (T == 0 || !kda_linear_tile_ok(dk, dv, dtype)) return kda_launch_linear_rec(p, dtype, s);
+  const bool own = need > 0 && workspace == nullptr;
+  if (own && cudaMallocAsync(&workspace, need, s) != cudaSuccess) return KDA_ERR_CUDA;
+  kda_status r = kda_launch_linear_tile(p, workspace, s);
+  if (own && cudaFreeAsync(workspace, s) != cudaSuccess && r == KDA_OK) r = KDA_ERR_CUDA;
+  return r;
 }
 
 extern "C" kda_status kda_linear_decode(const void* q, int64_t q_stride, const void* k,

@@ -52,3 +52,10 @@ __device__ __forceinline__ float clamp_decay(float a) { return a > 0.0f ? 0.0f :
 
 kda_status kda_launch_linear_rec(const kda_linear::LinearArgs& p, kda_dtype dtype,
                                  cudaStream_t stream);
+
+// The tensor-core kernels (kda_linear_tile.cu): what they serve, the scratch
+// that they need for these sizes, and the launch (with rows to work on).
+bool kda_linear_tile_ok(int dk, int dv, kda_dtype dtype);
+size_t kda_linear_tile_workspace(int N, int T, int H, int dk, int dv, bool packed);
+kda_status kda_launch_linear_tile(const kda_linear::LinearArgs& p, void* workspace,
+                                  cudaStream_t stream);

@@ -1,0 +1,808 @@
+// kda_linear_tile.cu -- linear attention with a decay for each head, whole
+// prompts on the tensor cores (bf16, dk and dv 64 or 128).
+//
+// In chunks of 128 tokens, with G_i the sum of the log-decays of a chunk's
+// tokens 0 .. i, E its last and S the state before it:
+//
+//   O  = diag(e^G) (Q S) + P V,      P_ij = e^(G_i - G_j) (q_i . k_j), j <= i
+//   S' = e^E S + K^T V',             V'_j = e^(E - G_j) v_j
+//
+// A CTA takes items (a sequence or a segment of one, a head, 64 value columns)
+// and walks their chunks, its state S in registers (fp32); Q K^T, P V, Q S and
+// K^T V' are tcgen05 products into tensor memory.  Warps have roles: one feeds
+// Q, K and V by TMA (two chunks ahead), one issues products, one takes the
+// decays' sums, and three groups of four turn scores into P, carry the state,
+// and make V' and write rows out.  The products of a chunk run in the order
+// scores of the next chunk, P V, K^T V', Q S: each waits for what was made
+// while the ones before it ran.
+//
+// Rounding: P and the state as an operand enter as bf16; rows of Q keep their
+// bits, e^G being applied to the product.  The state itself is summed from V'
+// in two bf16 parts (16 bits), so what is carried and returned is fp32 to
+// about 2^-17.  Sums of log-decays are taken in 64 bits and held in two fp32,
+// as their differences are what counts.  Where a tile lies below the diagonal
+// of 32-token blocks, e^(G_i - G_j) is e^(G_i - G_b) e^(G_b - G_j) with b the
+// last token of j's block: both factors are at most 1, so neither overflows
+// and the product only vanishes where the weight does.
+//
+// Few items (long rows of few heads) would leave SMs idle: sequences are then
+// cut into segments.  A first pass sums each segment's own state (no Q, no
+// output), a scan composes the states that segments start from, and the full
+// pass runs every segment at once.
+#include <cudaTypedefs.h>
+
+#include "kda_linear.cuh"
+#include "kda_tc_util.cuh"
+
+namespace {
+
+using namespace kda_linear;
+
+constexpr int C = 128;          // tokens of a chunk
+constexpr int NV = 64;          // value columns of a CTA
+constexpr int kThreads = 512;
+constexpr int kGates = 3;
+constexpr uint32_t TM_O1 = 256, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
+
+struct TileArgs {
+  LinearArgs a;
+  int seg;         // tokens of a segment, a multiple of C (longer than any sequence: none)
+  int segs;        // dense: segments of a sequence
+  int cols;        // (sequence, segment) columns; packed: the most there can be
+  int halves;      // dv / NV
+  float* states;   // [cols, H, dk, dv]: what segments end with (first pass), then start from
+  float2* gammas;  // [cols, H] a segment's decay factor, in two parts
+};
+
+struct alignas(16) Gate {
+  float2 g[C];     // sums of log2-decays, in two parts
+  float col[C];    // 2^(G_b - G_j), b the last token of j's 32
+  float row[C];    // scale * 2^G_i
+  float v[C];      // 2^(E - G_j)
+  float2 gamma;    // 2^E in two parts
+};
+
+struct Bars {
+  uint64_t qk_full[2], v_full[2], kv_empty[2], q_empty[2];
+  uint64_t s_raw[2], p_full[2], o_full, o_empty, vp_full, ds_full, ds_empty, st_full;
+  uint64_t gate_full[kGates], gate_empty[kGates], drain;
+};
+
+template <int DK>
+struct Smem {
+  static constexpr int kTile = C * DK * 2;                 // Q or K of a chunk
+  static constexpr int kBox = C * 128;                     // 64 channels of it
+  static constexpr int kQ = 0, kK = kQ + 2 * kTile, kV = kK + 2 * kTile;
+  static constexpr int kVP = kV + 2 * kBox;                // V' in two parts
+  static constexpr int kS = kVP + 2 * kBox;                // S as an operand
+  static constexpr int kGate = kS + DK * NV * 2;
+  static constexpr int kBars = kGate + kGates * (int)sizeof(Gate);
+  static constexpr int kBytes = kBars + (int)sizeof(Bars) + 16 + 1024;  // (and the alignment)
+};
+
+struct Item {
+  int64_t row;  // first token row
+  int len;      // tokens
+  int n, h, half, col;
+  bool first, last;  // segment of its sequence
+};
+
+// Item `id` of the grid's; false: there is none of that number (packed columns
+// are as many as there can be), or nothing to do in this pass.
+template <bool OUT>
+__device__ __forceinline__ bool locate(const TileArgs& p, int64_t id, Item& it) {
+  it.half = (int)(id % p.halves);
+  const int64_t x = id / p.halves;
+  it.h = (int)(x % p.a.H);
+  it.col = (int)(x / p.a.H);
+  int seg;
+  if (!p.a.cu) {
+    it.n = it.col / p.segs;
+    seg = it.col - it.n * p.segs;
+  } else {
+    // sequence n has the columns cu[n] / seg + n and up: as many as it has
+    // segments, and at most one more
+    int lo = 0, hi = p.a.N - 1;
+    if (p.seg > p.a.T) {
+      lo = it.col;
+    } else {
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.a.cu[mid] / p.seg + mid <= it.col) lo = mid;
+        else hi = mid - 1;
+      }
+    }
+    it.n = lo;
+    seg = it.col - (p.seg > p.a.T ? lo : p.a.cu[lo] / p.seg + lo);
+  }
+  int64_t row;
+  int len;
+  if (!span(p.a, it.n, row, len)) return false;
+  const int segs = len == 0 ? 1 : (len + p.seg - 1) / p.seg;
+  if (seg < 0 || seg >= segs) return false;
+  it.first = seg == 0;
+  it.last = seg == segs - 1;
+  if (!OUT && it.last) return false;
+  it.row = row + (int64_t)seg * p.seg;
+  it.len = it.last ? len - seg * p.seg : p.seg;
+  return true;
+}
+
+// The chunks of a CTA's items, one after the other.
+template <bool OUT>
+struct Walk {
+  const TileArgs& p;
+  int64_t id, ids;
+  Item it;
+  int t;       // first token of the chunk in its item
+  bool valid;
+  __device__ __forceinline__ explicit Walk(const TileArgs& args)
+      : p(args), id(blockIdx.x), ids((int64_t)args.cols * args.a.H * args.halves) {
+    settle();
+  }
+  __device__ __forceinline__ void settle() {
+    for (; id < ids; id += gridDim.x)
+      if (locate<OUT>(p, id, it) && it.len > 0) break;
+    valid = id < ids;
+    t = 0;
+  }
+  __device__ __forceinline__ void next() {
+    t += C;
+    if (t < it.len) return;
+    id += gridDim.x;
+    settle();
+  }
+  __device__ __forceinline__ int rows() const { return it.len - t < C ? it.len - t : C; }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Products are issued by a whole warp that runs in step, of which one thread
+// (`one`) carries them out: so their operands are known to be uniform, and a
+// product issues at the tensor cores' own rate.  Four k-steps; the descriptors'
+// low words (16-byte units) go up by AS and BS a step.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(r));
+  return r;
+}
+template <int AS, int BS>
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n"
+      " setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " add.u64 a, %1, %6;\n add.u64 b, %2, %7;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u64 a, a, %6;\n add.u64 b, b, %7;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u64 a, a, %6;\n add.u64 b, b, %7;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one), "n"(AS), "n"(BS)
+      : "memory");
+}
+// A in tensor memory, 8 columns a step
+template <int BS>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 a;\n"
+      " setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " add.u32 a, %1, 8;\n add.u64 b, %2, %6;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.u32 a, a, 8;\n add.u64 b, b, %6;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.u32 a, a, 8;\n add.u64 b, b, %6;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one), "n"(BS)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
+          sm100::smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+
+template <int DK, bool OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    kda_linear_tile_kernel(const __grid_constant__ CUtensorMap map_q,
+                           const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v, const TileArgs p) {
+  using M = Smem<DK>;
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + ((1024u - (sm100::smem_u32(raw) & 1023u)) & 1023u);
+  Gate* gates = reinterpret_cast<Gate*>(smem + M::kGate);
+  Bars& bars = *reinterpret_cast<Bars*>(smem + M::kBars);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::kBars + sizeof(Bars));
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (warp == 1) {
+    sm100::tmem_alloc(s_tmem, kTmemCols);
+    sm100::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&bars.qk_full[i], OUT ? 2 : 1);
+      sm100::mbar_init(&bars.v_full[i], 1);
+      sm100::mbar_init(&bars.kv_empty[i], 1);
+      sm100::mbar_init(&bars.q_empty[i], 1);
+      sm100::mbar_init(&bars.s_raw[i], 1);
+      sm100::mbar_init(&bars.p_full[i], 4);
+    }
+    sm100::mbar_init(&bars.o_full, 1);
+    sm100::mbar_init(&bars.o_empty, 4);
+    sm100::mbar_init(&bars.vp_full, 4);
+    sm100::mbar_init(&bars.ds_full, 1);
+    sm100::mbar_init(&bars.ds_empty, 4);
+    sm100::mbar_init(&bars.st_full, 4);
+    for (int i = 0; i < kGates; ++i) {
+      sm100::mbar_init(&bars.gate_full[i], 1);
+      sm100::mbar_init(&bars.gate_empty[i], OUT ? 12 : 8);
+    }
+    sm100::mbar_init(&bars.drain, 1);
+    sm100::fence_mbar_init();
+    *s_abort = 0;
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  // A wait that gives up (seconds after any legitimate one) ends its role; the
+  // others' then run out too.
+  auto wait = [&](uint64_t* bar, uint32_t n) -> bool {  // the barrier's phase n
+    if (sm100::mbar_wait(bar, n & 1)) return true;
+    *s_abort = 1;
+    return false;
+  };
+  // a warp's arrival, after all of its threads' work before it
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(bar);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------ Q, K and V come
+    uint32_t g = 0;
+    for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
+      const uint32_t s = g & 1, use = g >> 1;
+      const int row = (int)(w.it.row + w.t), hk = w.it.h / (p.a.H / p.a.HK);
+      if (use > 0 && !wait(&bars.kv_empty[s], use - 1)) break;
+      if (lane == 0) {
+        unsigned char* k = smem + M::kK + s * M::kTile;
+        sm100::mbar_arrive_expect_tx(&bars.qk_full[s], M::kTile);
+#pragma unroll
+        for (int b = 0; b < DK / 64; ++b)
+          sm100::tma_load_3d(k + b * M::kBox, &map_k, &bars.qk_full[s], 64 * b, hk, row);
+        sm100::mbar_arrive_expect_tx(&bars.v_full[s], M::kBox);
+        sm100::tma_load_3d(smem + M::kV + s * M::kBox, &map_v, &bars.v_full[s], NV * w.it.half,
+                           w.it.h, row);
+      }
+      __syncwarp();
+      if (OUT) {
+        // (a give-up leaves the chunk's barrier without its second arrival: nobody passes it)
+        if (use > 0 && !wait(&bars.q_empty[s], use - 1)) {
+          ++g;
+          break;
+        }
+        if (lane == 0) {
+          unsigned char* q = smem + M::kQ + s * M::kTile;
+          sm100::mbar_arrive_expect_tx(&bars.qk_full[s], M::kTile);
+#pragma unroll
+          for (int b = 0; b < DK / 64; ++b)
+            sm100::tma_load_3d(q + b * M::kBox, &map_q, &bars.qk_full[s], 64 * b, hk, row);
+        }
+        __syncwarp();
+      }
+    }
+    // copies in flight end before the CTA does
+    for (uint32_t i = g < 2 ? 0 : g - 2; i < g; ++i) {
+      sm100::mbar_wait(&bars.qk_full[i & 1], (i >> 1) & 1, 200000000ull);
+      sm100::mbar_wait(&bars.v_full[i & 1], (i >> 1) & 1, 200000000ull);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- products
+    const uint32_t one = elect_one();
+    constexpr uint32_t id_s = sm100::idesc_bf16(C, C, 0, 0), id_q = sm100::idesc_bf16(C, NV, 0, 1);
+    constexpr uint32_t id_p = sm100::idesc_bf16(C, NV, 0, 1);
+    constexpr uint32_t id_d = sm100::idesc_bf16(DK, 2 * NV, 1, 1);
+    const uint32_t at = sm100::smem_u32(smem);
+    // (addresses in a descriptor count 16 bytes)
+    const uint64_t dq = sm100::smem_desc_sw128(at + M::kQ, 16, 1024);
+    const uint64_t dk = sm100::smem_desc_sw128(at + M::kK, 16, 1024);
+    const uint64_t dkt = sm100::smem_desc_sw128(at + M::kK, M::kBox, 1024);  // as K^T
+    const uint64_t dv = sm100::smem_desc_sw128(at + M::kV, M::kBox, 1024);
+    const uint64_t dvp = sm100::smem_desc_sw128(at + M::kVP, M::kBox, 1024);
+    const uint64_t dst = sm100::smem_desc(at + M::kS, 1024, 128);
+    constexpr int kTile16 = M::kTile / 16, kBox16 = M::kBox / 16;
+    auto scores = [&](uint32_t s) {
+#pragma unroll
+      for (int b = 0; b < DK / 64; ++b)
+        mma4_ss<2, 2>(tmem + C * s, dq + s * kTile16 + b * kBox16, dk + s * kTile16 + b * kBox16,
+                      id_s, b, one);
+      commit(&bars.s_raw[s], one);
+    };
+    uint32_t g = 0;
+    Walk<OUT> w(p);
+    bool ok = true;
+    if (OUT && w.valid) {
+      ok = wait(&bars.qk_full[0], 0);
+      sm100::tc_fence_after();
+      if (ok) scores(0);
+    }
+    for (; ok && w.valid; ++g) {
+      const uint32_t s = g & 1;
+      w.next();
+      if (OUT && w.valid) {
+        // the next chunk's scores take the place of the last one's P
+        ok = wait(&bars.qk_full[s ^ 1], (g + 1) >> 1) && (g == 0 || wait(&bars.o_full, g - 1));
+        if (!ok) break;
+        sm100::tc_fence_after();
+        scores(s ^ 1);
+      }
+      if (OUT) {
+        ok = wait(&bars.v_full[s], g >> 1) && wait(&bars.p_full[s], g >> 1) &&
+             (g == 0 || wait(&bars.o_empty, g - 1));
+        if (!ok) break;
+        sm100::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          mma4_ts<128>(tmem + TM_O2, tmem + C * s + 32 * k, dv + s * kBox16 + 512 * k, id_p, k,
+                       one);
+      } else {
+        ok = wait(&bars.qk_full[s], g >> 1);
+        if (!ok) break;
+      }
+      ok = wait(&bars.vp_full, g) && (g == 0 || wait(&bars.ds_empty, g - 1));
+      if (!ok) break;
+      sm100::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        mma4_ss<128, 128>(tmem + TM_DS, dkt + s * kTile16 + 512 * k, dvp + 512 * k, id_d, k, one);
+      commit(&bars.ds_full, one);
+      commit(&bars.kv_empty[s], one);
+      if (OUT) {
+        ok = wait(&bars.st_full, g);
+        if (!ok) break;
+        sm100::tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < DK / 64; ++b)
+          mma4_ss<2, 128>(tmem + TM_O1, dq + s * kTile16 + b * kBox16, dst + 512 * b, id_q, b, one);
+        commit(&bars.o_full, one);
+        commit(&bars.q_empty[s], one);
+      }
+    }
+    commit(&bars.drain, one);
+    sm100::mbar_wait(&bars.drain, 0, 200000000ull);
+  } else if (warp == 2) {
+    // ------------------------------------------------ sums of the log-decays
+    uint32_t g = 0;
+    double all = 0.0;  // of a segment
+    for (Walk<OUT> w(p); w.valid; ++g) {
+      const uint32_t slot = g % kGates, use = g / kGates;
+      const int L = w.rows();
+      const float* a = p.a.decay + (w.it.row + w.t) * p.a.decay_stride + w.it.h;
+      double x[4], sum = 0.0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 4 * lane + e;
+        const double y = t < L ? (double)clamp_decay(a[t * p.a.decay_stride]) * 1.4426950408889634074 : 0.0;
+        // 2^-160 vanishes in 32 bits: what decays more than that decays so much
+        sum += y < -160.0 ? -160.0 : y;
+        x[e] = sum;
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const double y = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += y;
+      }
+      const double before = __shfl_up_sync(0xffffffffu, sum, 1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = lane ? before + x[e] : x[e];
+      const double end = __shfl_sync(0xffffffffu, sum, 31);
+      const double block = __shfl_sync(0xffffffffu, sum, lane | 7);
+      const double gamma = exp2(end);
+      if (use > 0 && !wait(&bars.gate_empty[slot], use - 1)) break;
+      Gate& gt = gates[slot];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 4 * lane + e;
+        const float hi = (float)x[e];
+        gt.g[t] = make_float2(hi, (float)(x[e] - (double)hi));
+        gt.col[t] = exp2f((float)(block - x[e]));
+        gt.row[t] = p.a.scale * exp2f(hi);
+        gt.v[t] = exp2f((float)(end - x[e]));
+      }
+      if (lane == 0) {
+        const float hi = (float)gamma;
+        gt.gamma = make_float2(hi, (float)(gamma - (double)hi));
+      }
+      if (L < C) {
+        // rows past the end, which belong to others: zeros, whatever they hold
+        const uint32_t s = g & 1;
+        if (!wait(&bars.qk_full[s], g >> 1) || !wait(&bars.v_full[s], g >> 1)) break;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int e = L * 8 + lane; e < C * 8; e += 32) {
+#pragma unroll
+          for (int b = 0; b < DK / 64; ++b)
+            reinterpret_cast<uint4*>(smem + M::kK + s * M::kTile + b * M::kBox)[e] = zero;
+          reinterpret_cast<uint4*>(smem + M::kV + s * M::kBox)[e] = zero;
+        }
+        sm100::fence_async_smem();
+      }
+      arrive(&bars.gate_full[slot]);
+      all += end;
+      const Item it = w.it;
+      const int64_t id = w.id;
+      w.next();
+      if (!w.valid || w.id != id) {
+        if (!OUT && it.half == 0 && lane == 0) {
+          const double f = exp2(all);
+          const float hi = (float)f;
+          p.gammas[(int64_t)it.col * p.a.H + it.h] = make_float2(hi, (float)(f - (double)hi));
+        }
+        all = 0.0;
+      }
+    }
+  } else if (warp == 3) {
+    // ------------------------------------- malformed offsets of any sequence
+    if (OUT && p.a.cu && blockIdx.x == 0)
+      for (int n = lane; n < p.a.N; n += 32) {
+        int64_t row;
+        int len;
+        span(p.a, n, row, len);
+      }
+  } else if (warp < 8) {
+    // ------------------------------------------------------- scores become P
+    const int q = warp & 3, i = 32 * q + lane;
+    const uint32_t tm = sm100::taddr(tmem, 32 * q, 0);
+    uint32_t g = 0;
+    if (OUT)
+      for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
+        const uint32_t slot = g % kGates, base = tm + C * (g & 1);
+        if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.s_raw[g & 1], g >> 1)) break;
+        sm100::tc_fence_after();
+        const Gate& gt = gates[slot];
+        const float2 mine = gt.g[i];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t out[16];
+          if (b > q) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) out[e] = 0;
+          } else {
+            float v[32];
+            sm100::tmem_ld16(base + 32 * b, *reinterpret_cast<float(*)[16]>(v));
+            sm100::tmem_ld16(base + 32 * b + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+            sm100::tmem_wait_ld();
+            if (b < q) {
+              const float2 e = gt.g[32 * b + 31];
+              const float f = ex2((mine.x - e.x) + (mine.y - e.y));
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 c = *reinterpret_cast<const float4*>(&gt.col[32 * b + j]);
+                v[j] *= c.x * f;
+                v[j + 1] *= c.y * f;
+                v[j + 2] *= c.z * f;
+                v[j + 3] *= c.w * f;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float2 o = gt.g[32 * b + j];
+                const float f = ex2((mine.x - o.x) + (mine.y - o.y));
+                v[j] = j <= lane ? v[j] * f : 0.0f;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) out[e] = sm100::pack_bf16x2(v[2 * e], v[2 * e + 1]);
+          }
+          sm100::tmem_st16(base + 16 * b, out);
+        }
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        arrive(&bars.p_full[g & 1]);
+        arrive(&bars.gate_empty[slot]);
+      }
+  } else if (warp < 12) {
+    // -------------------------------------------------------------- the state
+    const int q = warp & 3;
+    // (a product of 64 rows has them in the first half of each warp's lanes)
+    const int i = DK == 128 ? 32 * q + lane : 16 * q + lane;
+    const bool mine = DK == 128 || lane < 16;
+    const uint32_t tm = sm100::taddr(tmem, 32 * q, TM_DS);
+    float S[NV];
+    uint32_t g = 0;
+    bool ok = true;
+    const int64_t ids = (int64_t)p.cols * p.a.H * p.halves;
+    for (int64_t id = blockIdx.x; ok && id < ids; id += gridDim.x) {
+      Item it;
+      if (!locate<OUT>(p, id, it)) continue;
+      const int64_t size = (int64_t)DK * p.a.dv;
+      const int64_t in_head = (int64_t)i * p.a.dv + NV * it.half;
+      const float* from = it.first ? (p.a.init ? p.a.init + ((int64_t)it.n * p.a.H + it.h) * size
+                                               : nullptr)
+                          : OUT    ? p.states + ((int64_t)(it.col - 1) * p.a.H + it.h) * size
+                                   : nullptr;
+      float* to = !OUT      ? p.states + ((int64_t)it.col * p.a.H + it.h) * size
+                  : it.last ? (p.a.final_state
+                                   ? p.a.final_state + ((int64_t)it.n * p.a.H + it.h) * size
+                                   : nullptr)
+                            : nullptr;
+#pragma unroll
+      for (int j = 0; j < NV; j += 4) {
+        const float4 x = from && mine ? *reinterpret_cast<const float4*>(from + in_head + j)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[j] = x.x;
+        S[j + 1] = x.y;
+        S[j + 2] = x.z;
+        S[j + 3] = x.w;
+      }
+      for (int t = 0; t < it.len; t += C, ++g) {
+        if (OUT) {
+          ok = g == 0 || wait(&bars.o_full, g - 1);  // (the last Q S has read the operand)
+          if (!ok) break;
+          if (mine) {
+#pragma unroll
+            for (int j = 0; j < NV; j += 8)
+              kda_tc::st8_bf16(smem + M::kS + kda_tc::mn_off(j, i, 1024), S + j);
+          }
+          sm100::fence_async_smem();
+          arrive(&bars.st_full);
+        }
+        const uint32_t slot = g % kGates;
+        ok = wait(&bars.gate_full[slot], g / kGates) && wait(&bars.ds_full, g);
+        if (!ok) break;
+        sm100::tc_fence_after();
+        const float2 f = gates[slot].gamma;
+#pragma unroll
+        for (int j = 0; j < NV; j += 16) {
+          float x[16], y[16];
+          sm100::tmem_ld16(tm + j, x);
+          sm100::tmem_ld16(tm + NV + j, y);
+          sm100::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            S[j + e] = fmaf(f.x, S[j + e], fmaf(f.y, S[j + e], x[e] + y[e]));
+        }
+        sm100::tc_fence_before();
+        arrive(&bars.ds_empty);
+        arrive(&bars.gate_empty[slot]);
+      }
+      if (to && mine && ok) {
+#pragma unroll
+        for (int j = 0; j < NV; j += 4)
+          *reinterpret_cast<float4*>(to + in_head + j) =
+              make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      }
+    }
+  } else {
+    // ------------------------------------------------- V', and rows go out
+    const int q = warp & 3, i = 32 * q + lane;
+    const uint32_t tm = sm100::taddr(tmem, 32 * q, 0);
+    // V' of chunk g, `rows` of it tokens
+    auto weigh = [&](uint32_t g, int rows) -> bool {
+      const uint32_t slot = g % kGates, s = g & 1;
+      if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.v_full[s], g >> 1) ||
+          (g > 0 && !wait(&bars.ds_full, g - 1)))
+        return false;
+      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox);
+      uint4* hi = reinterpret_cast<uint4*>(smem + M::kVP);
+      uint4* lo = hi + M::kBox / 16;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int e = 128 * k + tid - 384, row = e >> 3;
+        const float f = gates[slot].v[row];
+        const uint4 w = v[e];
+        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float y0 = __uint_as_float(r[x] << 16) * f;
+          const float y1 = __uint_as_float(r[x] & 0xffff0000u) * f;
+          a[x] = sm100::pack_bf16x2(y0, y1);
+          b[x] = sm100::pack_bf16x2(y0 - __uint_as_float(a[x] << 16),
+                                    y1 - __uint_as_float(a[x] & 0xffff0000u));
+        }
+        if (row >= rows) a[0] = a[1] = a[2] = a[3] = b[0] = b[1] = b[2] = b[3] = 0;
+        hi[e] = make_uint4(a[0], a[1], a[2], a[3]);
+        lo[e] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+      sm100::fence_async_smem();
+      arrive(&bars.vp_full);
+      if (!OUT) arrive(&bars.gate_empty[slot]);
+      return true;
+    };
+    uint32_t g = 0;
+    Walk<OUT> w(p), ahead(p);
+    bool ok = !ahead.valid || weigh(0, ahead.rows());
+    for (; ok && w.valid; w.next(), ++g) {
+      if (ahead.valid) ahead.next();
+      if (ahead.valid && !weigh(g + 1, ahead.rows())) break;
+      if (!OUT) continue;
+      if (!wait(&bars.o_full, g)) break;
+      sm100::tc_fence_after();
+      const uint32_t slot = g % kGates;
+      const float f = gates[slot].row[i], scale = p.a.scale;
+      uint32_t out[NV / 2];
+#pragma unroll
+      for (int j = 0; j < NV; j += 16) {
+        float x[16], y[16];
+        sm100::tmem_ld16(tm + TM_O1 + j, x);
+        sm100::tmem_ld16(tm + TM_O2 + j, y);
+        sm100::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          out[(j + e) / 2] = sm100::pack_bf16x2(fmaf(f, x[e], scale * y[e]),
+                                                fmaf(f, x[e + 1], scale * y[e + 1]));
+      }
+      sm100::tc_fence_before();
+      arrive(&bars.o_empty);
+      arrive(&bars.gate_empty[slot]);
+      if (i < w.rows()) {
+        uint4* dst = reinterpret_cast<uint4*>(
+            static_cast<__nv_bfloat16*>(p.a.out) +
+            ((w.it.row + w.t + i) * p.a.H + w.it.h) * p.a.dv + NV * w.it.half);
+#pragma unroll
+        for (int j = 0; j < NV / 8; ++j)
+          dst[j] = make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *s_abort) report(p.a.status, KDA_ERR_TIMEOUT);
+  if (warp == 1) sm100::tmem_dealloc(tmem, kTmemCols);
+}
+
+// The states that segments start from: column by column of a sequence,
+// S(s) <- gamma(s) S(s - 1) + S(s).
+constexpr int kScanThreads = 256;
+__global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const TileArgs p) {
+  const int size = p.a.dk * p.a.dv, blocks = size / (4 * kScanThreads);
+  const int unit = blockIdx.x / blocks, n = unit / p.a.H, h = unit - n * p.a.H;
+  const int e = 4 * ((blockIdx.x - unit * blocks) * kScanThreads + threadIdx.x);
+  int64_t row;
+  int len;
+  if (!span(p.a, n, row, len)) return;
+  const int segs = (len + p.seg - 1) / p.seg;
+  const int col = p.a.cu ? (int)(row / p.seg) + n : n * p.segs;
+  if (segs < 3) return;
+  auto at = [&](int s) {
+    return reinterpret_cast<float4*>(p.states + ((int64_t)(col + s) * p.a.H + h) * size + e);
+  };
+  float4 x = *at(0);
+#pragma unroll 4
+  for (int s = 1; s < segs - 1; ++s) {
+    const float2 f = p.gammas[(int64_t)(col + s) * p.a.H + h];
+    const float4 y = *at(s);
+    x.x = fmaf(f.x, x.x, fmaf(f.y, x.x, y.x));
+    x.y = fmaf(f.x, x.y, fmaf(f.y, x.y, y.y));
+    x.z = fmaf(f.x, x.z, fmaf(f.y, x.z, y.z));
+    x.w = fmaf(f.x, x.w, fmaf(f.y, x.w, y.w));
+    *at(s) = x;
+  }
+}
+
+// 3-D map over rows `stride` elements apart of `heads` heads of d channels:
+// boxes of 64 channels x 1 head x 128 rows, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int64_t stride) {
+  auto enc = kda_tc::get_encode();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, 1, C};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How the token axis is cut.  Times in chunks of one CTA: a chunk of the first
+// pass costs about half of one of the full pass, and a second and third launch
+// some six.  Packed lengths are not known here: the longest is taken for twice
+// the mean.
+struct Cut {
+  int seg, segs, cols;
+};
+Cut cut(int N, int64_t T, int H, int dv, bool packed) {
+  const int sms = kda_device_sms() > 0 ? kda_device_sms() : 148;
+  const int64_t units = (int64_t)H * (dv / NV);
+  const int64_t longest = packed ? (T < 2 * T / N ? T : 2 * T / N) : T;
+  const int64_t chunks = (longest + C - 1) / C;
+  auto waves = [&](int64_t items, int64_t each) {  // items of `each` chunks on all SMs
+    return (items + sms - 1) / sms * each;
+  };
+  const int64_t all = packed ? (T + C - 1) / C + N / 2 : chunks * N;  // chunks of a head's columns
+  double best = packed ? (double)(all * units / sms > chunks ? all * units / sms : chunks)
+                       : (double)waves((int64_t)N * units, chunks);
+  int64_t pick = 0;
+  for (int64_t segs = 2; segs <= 64 && segs * 2 <= chunks; ++segs) {
+    const int64_t each = (chunks + segs - 1) / segs;
+    const int64_t items = packed ? ((all + each - 1) / each) * units : N * segs * units;
+    const double t = 1.5 * waves(items, each) + 6.0;
+    if (t < 0.9 * best) {
+      best = t;
+      pick = each;
+    }
+  }
+  Cut c;
+  c.seg = pick ? (int)(pick * C) : 1 << 30;
+  if (!packed)
+    c.segs = pick ? (int)((T + c.seg - 1) / c.seg) : 1;
+  else
+    c.segs = 1;
+  c.cols = packed ? (pick ? (int)(T / c.seg) + N : N) : N * c.segs;
+  return c;
+}
+
+size_t r256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <int DK, bool OUT>
+kda_status launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                  const TileArgs& p, cudaStream_t s) {
+  auto kernel = kda_linear_tile_kernel<DK, OUT>;
+  const kda_status rc = kda_smem_attr((const void*)kernel, Smem<DK>::kBytes);
+  if (rc != KDA_OK) return rc;
+  const int64_t items = (int64_t)p.cols * p.a.H * p.halves;
+  const int sms = kda_device_sms();
+  const unsigned grid = (unsigned)(items < sms ? items : sms);
+  kernel<<<grid, kThreads, Smem<DK>::kBytes, s>>>(q, k, v, p);
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <int DK>
+kda_status run(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+               const TileArgs& p, cudaStream_t s) {
+  if (p.states) {
+    kda_status rc = launch<DK, false>(q, k, v, p, s);
+    if (rc != KDA_OK) return rc;
+    const unsigned grid = (unsigned)(p.a.N * p.a.H * (p.a.dk * p.a.dv / (4 * kScanThreads)));
+    kda_linear_scan_kernel<<<grid, kScanThreads, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+  }
+  return launch<DK, true>(q, k, v, p, s);
+}
+
+}  // namespace
+
+bool kda_linear_tile_ok(int dk, int dv, kda_dtype dtype) {
+  return dtype == KDA_BF16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128);
+}
+
+size_t kda_linear_tile_workspace(int N, int T, int H, int dk, int dv, bool packed) {
+  const Cut c = cut(N, T, H, dv, packed);
+  if (c.seg > T) return 0;
+  return r256((size_t)c.cols * H * dk * dv * 4) + r256((size_t)c.cols * H * 8);
+}
+
+kda_status kda_launch_linear_tile(const LinearArgs& a, void* workspace, cudaStream_t s) {
+  const bool packed = a.cu != nullptr;
+  const Cut c = cut(a.N, a.T, a.H, a.dv, packed);
+  TileArgs p{a, c.seg, c.segs, c.cols, a.dv / NV, nullptr, nullptr};
+  if (c.seg <= a.T) {
+    p.states = static_cast<float*>(workspace);
+    p.gammas = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) +
+                                         r256((size_t)c.cols * a.H * a.dk * a.dv * 4));
+  }
+  const int64_t rows = packed ? a.T : (int64_t)a.N * a.T;
+  CUtensorMap q, k, v;
+  if (!make_map(&q, a.q, rows, a.HK, a.dk, a.q_stride) ||
+      !make_map(&k, a.k, rows, a.HK, a.dk, a.k_stride) ||
+      !make_map(&v, a.v, rows, a.H, a.dv, a.v_stride))
+    return KDA_ERR_CUDA;
+  return a.dk == 64 ? run<64>(q, k, v, p, s) : run<128>(q, k, v, p, s);
+}
