@@ -13,8 +13,9 @@
 // Q, K and V by TMA (two chunks ahead), one issues products, one takes the
 // decays' sums, and three groups of four turn scores into P, carry the state,
 // and make V' and write rows out.  The products of a chunk run in the order
-// scores of the next chunk, P V, K^T V', Q S: each waits for what was made
-// while the ones before it ran.
+// K^T V', Q S, P V and the next chunk's scores: what each waits for is made while
+// the three before it run, and K, Q and V are let go of early enough for the
+// copies of two chunks on.
 //
 // Rounding: P and the state as an operand enter as bf16; rows of Q keep their
 // bits, e^G being applied to the product.  The state itself is summed from V'
@@ -41,7 +42,7 @@ using namespace kda_linear;
 constexpr int C = 128;          // tokens of a chunk
 constexpr int NV = 64;          // value columns of a CTA
 constexpr int kThreads = 512;
-constexpr int kGates = 3;
+constexpr int kGates = 4;
 constexpr uint32_t TM_O1 = 256, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
 
 struct TileArgs {
@@ -55,16 +56,17 @@ struct TileArgs {
 };
 
 struct alignas(16) Gate {
-  float2 g[C];     // sums of log2-decays, in two parts
-  float col[C];    // 2^(G_b - G_j), b the last token of j's 32
+  float rel[C];    // G_j - G_b, b the last token of j's 32 (sums of log2-decays)
+  float col[C];    // 2^(G_b - G_j)
   float row[C];    // scale * 2^G_i
   float v[C];      // 2^(E - G_j)
+  float2 end[4];   // G of the last token of each 32, in two parts
   float2 gamma;    // 2^E in two parts
 };
 
 struct Bars {
-  uint64_t qk_full[2], v_full[2], kv_empty[2], q_empty[2];
-  uint64_t s_raw[2], p_full[2], o_full, o_empty, vp_full, ds_full, ds_empty, st_full;
+  uint64_t qk_full[2], v_full[2], k_empty[2], q_empty[2], v_empty[2];
+  uint64_t s_raw[2], p_full[2], o_full, o_empty, vp_full, ds_full, ds_empty, st_full, st_empty;
   uint64_t gate_full[kGates], gate_empty[kGates], drain;
 };
 
@@ -90,11 +92,11 @@ struct Item {
 // Item `id` of the grid's; false: there is none of that number (packed columns
 // are as many as there can be), or nothing to do in this pass.
 template <bool OUT>
-__device__ __forceinline__ bool locate(const TileArgs& p, int64_t id, Item& it) {
-  it.half = (int)(id % p.halves);
-  const int64_t x = id / p.halves;
-  it.h = (int)(x % p.a.H);
-  it.col = (int)(x / p.a.H);
+__device__ __noinline__ bool locate(const TileArgs& p, int id, Item& it) {
+  const int x = id / p.halves;
+  it.half = id - x * p.halves;
+  it.col = x / p.a.H;
+  it.h = x - it.col * p.a.H;
   int seg;
   if (!p.a.cu) {
     it.n = it.col / p.segs;
@@ -132,17 +134,23 @@ __device__ __forceinline__ bool locate(const TileArgs& p, int64_t id, Item& it) 
 template <bool OUT>
 struct Walk {
   const TileArgs& p;
-  int64_t id, ids;
+  int id, ids;
   Item it;
   int t;       // first token of the chunk in its item
   bool valid;
   __device__ __forceinline__ explicit Walk(const TileArgs& args)
-      : p(args), id(blockIdx.x), ids((int64_t)args.cols * args.a.H * args.halves) {
+      : p(args), id(blockIdx.x), ids(args.cols * args.a.H * args.halves) {
     settle();
+  }
+  __device__ __forceinline__ bool find() {
+    Item x;  // (the call's copy is in memory, this one's in registers)
+    const bool there = locate<OUT>(p, id, x);
+    it = x;
+    return there;
   }
   __device__ __forceinline__ void settle() {
     for (; id < ids; id += gridDim.x)
-      if (locate<OUT>(p, id, it) && it.len > 0) break;
+      if (find() && it.len > 0) break;
     valid = id < ids;
     t = 0;
   }
@@ -155,6 +163,12 @@ struct Walk {
   __device__ __forceinline__ int rows() const { return it.len - t < C ? it.len - t : C; }
 };
 
+__device__ __forceinline__ void tmem_st8(uint32_t ta, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -213,11 +227,70 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
       : "memory");
 }
 
+// Bounded wait (2 s), which also gives up when another role of the CTA has.  The
+// hint lets the hardware suspend the warp for up to 1 ms at a time: one that
+// polls takes issue slots and shared memory's from those that work.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
+                                             volatile int* abort) {
+  auto poll = [&]() -> bool {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(1000000)
+        : "memory");
+    return ok != 0;
+  };
+  uint64_t t0 = 0;
+  while (!poll()) {
+    const uint64_t t = sm100::globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (*abort || t - t0 > 2000000000ull) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// Two fp32 at a time.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(f32x2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(f32x2 x) {
+  float a, b;
+  unpair(x, a, b);
+  return sm100::pack_bf16x2(a, b);
+}
+
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_linear_tile_kernel(const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k,
-                           const __grid_constant__ CUtensorMap map_v, const TileArgs p) {
+                           const __grid_constant__ CUtensorMap map_v,
+                           const __grid_constant__ TileArgs p) {
   using M = Smem<DK>;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024u - (sm100::smem_u32(raw) & 1023u)) & 1023u);
@@ -235,8 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&bars.qk_full[i], OUT ? 2 : 1);
       sm100::mbar_init(&bars.v_full[i], 1);
-      sm100::mbar_init(&bars.kv_empty[i], 1);
+      sm100::mbar_init(&bars.k_empty[i], 1);
       sm100::mbar_init(&bars.q_empty[i], 1);
+      sm100::mbar_init(&bars.v_empty[i], 1);
       sm100::mbar_init(&bars.s_raw[i], 1);
       sm100::mbar_init(&bars.p_full[i], 4);
     }
@@ -246,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::mbar_init(&bars.ds_full, 1);
     sm100::mbar_init(&bars.ds_empty, 4);
     sm100::mbar_init(&bars.st_full, 4);
+    sm100::mbar_init(&bars.st_empty, 1);
     for (int i = 0; i < kGates; ++i) {
       sm100::mbar_init(&bars.gate_full[i], 1);
       sm100::mbar_init(&bars.gate_empty[i], OUT ? 12 : 8);
@@ -259,12 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm100::tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  // A wait that gives up (seconds after any legitimate one) ends its role; the
-  // others' then run out too.
   auto wait = [&](uint64_t* bar, uint32_t n) -> bool {  // the barrier's phase n
-    if (sm100::mbar_wait(bar, n & 1)) return true;
-    *s_abort = 1;
-    return false;
+    return bounded_wait(bar, n & 1, s_abort);
   };
   // a warp's arrival, after all of its threads' work before it
   auto arrive = [&](uint64_t* bar) {
@@ -278,20 +349,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
       const uint32_t s = g & 1, use = g >> 1;
       const int row = (int)(w.it.row + w.t), hk = w.it.h / (p.a.H / p.a.HK);
-      if (use > 0 && !wait(&bars.kv_empty[s], use - 1)) break;
+      // (in the order in which the products let go of them)
+      if (use > 0 && !wait(&bars.k_empty[s], use - 1)) break;
       if (lane == 0) {
         unsigned char* k = smem + M::kK + s * M::kTile;
         sm100::mbar_arrive_expect_tx(&bars.qk_full[s], M::kTile);
 #pragma unroll
         for (int b = 0; b < DK / 64; ++b)
           sm100::tma_load_3d(k + b * M::kBox, &map_k, &bars.qk_full[s], 64 * b, hk, row);
-        sm100::mbar_arrive_expect_tx(&bars.v_full[s], M::kBox);
-        sm100::tma_load_3d(smem + M::kV + s * M::kBox, &map_v, &bars.v_full[s], NV * w.it.half,
-                           w.it.h, row);
       }
       __syncwarp();
+      // (a give-up leaves the chunk's barriers short of an arrival: nobody passes them)
       if (OUT) {
-        // (a give-up leaves the chunk's barrier without its second arrival: nobody passes it)
         if (use > 0 && !wait(&bars.q_empty[s], use - 1)) {
           ++g;
           break;
@@ -305,6 +374,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      if (use > 0 && !wait(&bars.v_empty[s], use - 1)) {
+        ++g;
+        break;
+      }
+      if (lane == 0) {
+        sm100::mbar_arrive_expect_tx(&bars.v_full[s], M::kBox);
+        sm100::tma_load_3d(smem + M::kV + s * M::kBox, &map_v, &bars.v_full[s], NV * w.it.half,
+                           w.it.h, row);
+      }
+      __syncwarp();
     }
     // copies in flight end before the CTA does
     for (uint32_t i = g < 2 ? 0 : g - 2; i < g; ++i) {
@@ -343,63 +422,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (; ok && w.valid; ++g) {
       const uint32_t s = g & 1;
-      w.next();
-      if (OUT && w.valid) {
-        // the next chunk's scores take the place of the last one's P
-        ok = wait(&bars.qk_full[s ^ 1], (g + 1) >> 1) && (g == 0 || wait(&bars.o_full, g - 1));
-        if (!ok) break;
-        sm100::tc_fence_after();
-        scores(s ^ 1);
-      }
-      if (OUT) {
-        ok = wait(&bars.v_full[s], g >> 1) && wait(&bars.p_full[s], g >> 1) &&
-             (g == 0 || wait(&bars.o_empty, g - 1));
-        if (!ok) break;
-        sm100::tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          mma4_ts<128>(tmem + TM_O2, tmem + C * s + 32 * k, dv + s * kBox16 + 512 * k, id_p, k,
-                       one);
-      } else {
-        ok = wait(&bars.qk_full[s], g >> 1);
-        if (!ok) break;
-      }
-      ok = wait(&bars.vp_full, g) && (g == 0 || wait(&bars.ds_empty, g - 1));
+      ok = (OUT || wait(&bars.qk_full[s], g >> 1)) && wait(&bars.vp_full, g) &&
+           (g == 0 || wait(&bars.ds_empty, g - 1));
       if (!ok) break;
       sm100::tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         mma4_ss<128, 128>(tmem + TM_DS, dkt + s * kTile16 + 512 * k, dvp + 512 * k, id_d, k, one);
       commit(&bars.ds_full, one);
-      commit(&bars.kv_empty[s], one);
-      if (OUT) {
-        ok = wait(&bars.st_full, g);
+      commit(&bars.k_empty[s], one);
+      if (!OUT) commit(&bars.v_empty[s], one);  // (V' was made from it)
+      w.next();
+      if (!OUT) continue;
+      ok = wait(&bars.st_full, g) && (g == 0 || wait(&bars.o_empty, g - 1));
+      if (!ok) break;
+      sm100::tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < DK / 64; ++b)
+        mma4_ss<2, 128>(tmem + TM_O1, dq + s * kTile16 + b * kBox16, dst + 512 * b, id_q, b, one);
+      commit(&bars.st_empty, one);
+      commit(&bars.q_empty[s], one);
+      // (P of the chunk before has been read: waited for here, since a barrier's phase has to
+      // be seen before its next one can end)
+      ok = wait(&bars.v_full[s], g >> 1) && wait(&bars.p_full[s], g >> 1) &&
+           (g == 0 || wait(&bars.o_full, g - 1));
+      if (!ok) break;
+      sm100::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        mma4_ts<128>(tmem + TM_O2, tmem + C * s + 32 * k, dv + s * kBox16 + 512 * k, id_p, k, one);
+      commit(&bars.o_full, one);
+      commit(&bars.v_empty[s], one);
+      if (w.valid) {
+        // the next chunk's scores take the place of the last one's P
+        ok = wait(&bars.qk_full[s ^ 1], (g + 1) >> 1);
         if (!ok) break;
         sm100::tc_fence_after();
-#pragma unroll
-        for (int b = 0; b < DK / 64; ++b)
-          mma4_ss<2, 128>(tmem + TM_O1, dq + s * kTile16 + b * kBox16, dst + 512 * b, id_q, b, one);
-        commit(&bars.o_full, one);
-        commit(&bars.q_empty[s], one);
+        scores(s ^ 1);
       }
     }
     commit(&bars.drain, one);
     sm100::mbar_wait(&bars.drain, 0, 200000000ull);
-  } else if (warp == 2) {
-    // ------------------------------------------------ sums of the log-decays
+  } else if (warp < 4) {
+    // --------------------- sums of the log-decays: two warps, chunks in turn
+    const uint32_t turn = warp - 2;
+    if (OUT && turn && p.a.cu && blockIdx.x == 0)  // malformed offsets of any sequence
+      for (int n = lane; n < p.a.N; n += 32) {
+        int64_t row;
+        int len;
+        span(p.a, n, row, len);
+      }
     uint32_t g = 0;
-    double all = 0.0;  // of a segment
-    for (Walk<OUT> w(p); w.valid; ++g) {
+    for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
+      if ((g & 1) != turn) continue;
       const uint32_t slot = g % kGates, use = g / kGates;
       const int L = w.rows();
       const float* a = p.a.decay + (w.it.row + w.t) * p.a.decay_stride + w.it.h;
-      double x[4], sum = 0.0;
+      float y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = 4 * lane + e;
-        const double y = t < L ? (double)clamp_decay(a[t * p.a.decay_stride]) * 1.4426950408889634074 : 0.0;
+        y[e] = t < L ? a[t * p.a.decay_stride] : 0.0f;
+      }
+      double x[4], sum = 0.0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
         // 2^-160 vanishes in 32 bits: what decays more than that decays so much
-        sum += y < -160.0 ? -160.0 : y;
+        const float c = clamp_decay(y[e]);
+        sum += (double)(c < -110.9f ? -110.9f : c) * 1.4426950408889634074;
         x[e] = sum;
       }
 #pragma unroll
@@ -407,24 +497,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const double y = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += y;
       }
-      const double before = __shfl_up_sync(0xffffffffu, sum, 1);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = lane ? before + x[e] : x[e];
+      const double before = sum - x[3];
       const double end = __shfl_sync(0xffffffffu, sum, 31);
       const double block = __shfl_sync(0xffffffffu, sum, lane | 7);
-      const double gamma = exp2(end);
       if (use > 0 && !wait(&bars.gate_empty[slot], use - 1)) break;
       Gate& gt = gates[slot];
+      float rel[4], col[4], row[4], v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = 4 * lane + e;
-        const float hi = (float)x[e];
-        gt.g[t] = make_float2(hi, (float)(x[e] - (double)hi));
-        gt.col[t] = exp2f((float)(block - x[e]));
-        gt.row[t] = p.a.scale * exp2f(hi);
-        gt.v[t] = exp2f((float)(end - x[e]));
+        const double G = before + x[e];
+        rel[e] = (float)(G - block);
+        col[e] = ex2(-rel[e]);
+        row[e] = p.a.scale * ex2((float)G);
+        v[e] = ex2((float)(end - G));
+      }
+      reinterpret_cast<float4*>(gt.rel)[lane] = make_float4(rel[0], rel[1], rel[2], rel[3]);
+      reinterpret_cast<float4*>(gt.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
+      reinterpret_cast<float4*>(gt.row)[lane] = make_float4(row[0], row[1], row[2], row[3]);
+      reinterpret_cast<float4*>(gt.v)[lane] = make_float4(v[0], v[1], v[2], v[3]);
+      if ((lane & 7) == 7) {
+        const float hi = (float)block;
+        gt.end[lane >> 3] = make_float2(hi, (float)(block - (double)hi));
       }
       if (lane == 0) {
+        const double gamma = exp2(end);
         const float hi = (float)gamma;
         gt.gamma = make_float2(hi, (float)(gamma - (double)hi));
       }
@@ -433,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s = g & 1;
         if (!wait(&bars.qk_full[s], g >> 1) || !wait(&bars.v_full[s], g >> 1)) break;
         const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
         for (int e = L * 8 + lane; e < C * 8; e += 32) {
 #pragma unroll
           for (int b = 0; b < DK / 64; ++b)
@@ -442,27 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm100::fence_async_smem();
       }
       arrive(&bars.gate_full[slot]);
-      all += end;
-      const Item it = w.it;
-      const int64_t id = w.id;
-      w.next();
-      if (!w.valid || w.id != id) {
-        if (!OUT && it.half == 0 && lane == 0) {
-          const double f = exp2(all);
-          const float hi = (float)f;
-          p.gammas[(int64_t)it.col * p.a.H + it.h] = make_float2(hi, (float)(f - (double)hi));
-        }
-        all = 0.0;
-      }
     }
-  } else if (warp == 3) {
-    // ------------------------------------- malformed offsets of any sequence
-    if (OUT && p.a.cu && blockIdx.x == 0)
-      for (int n = lane; n < p.a.N; n += 32) {
-        int64_t row;
-        int len;
-        span(p.a, n, row, len);
-      }
   } else if (warp < 8) {
     // ------------------------------------------------------- scores become P
     const int q = warp & 3, i = 32 * q + lane;
@@ -474,41 +551,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.s_raw[g & 1], g >> 1)) break;
         sm100::tc_fence_after();
         const Gate& gt = gates[slot];
-        const float2 mine = gt.g[i];
+        const float mine = gt.rel[i];
+        // blocks of 32 columns below the diagonal's, 16 at a time
+#pragma unroll 1
+        for (int b = 0; b < 2 * q; ++b) {
+          float x[16];
+          uint32_t out[8];
+          sm100::tmem_ld16(base + 16 * b, x);
+          const float2 e = gt.end[q], o = gt.end[b >> 1];
+          const float f = ex2(mine + ((e.x - o.x) + (e.y - o.y)));
+          const f32x2 ff = pair(f, f);
+          const float4* c = reinterpret_cast<const float4*>(gt.col + 16 * b);
+          f32x2 w[8];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t out[16];
-          if (b > q) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) out[e] = 0;
-          } else {
-            float v[32];
-            sm100::tmem_ld16(base + 32 * b, *reinterpret_cast<float(*)[16]>(v));
-            sm100::tmem_ld16(base + 32 * b + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-            sm100::tmem_wait_ld();
-            if (b < q) {
-              const float2 e = gt.g[32 * b + 31];
-              const float f = ex2((mine.x - e.x) + (mine.y - e.y));
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 c = *reinterpret_cast<const float4*>(&gt.col[32 * b + j]);
-                v[j] *= c.x * f;
-                v[j + 1] *= c.y * f;
-                v[j + 2] *= c.z * f;
-                v[j + 3] *= c.w * f;
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float2 o = gt.g[32 * b + j];
-                const float f = ex2((mine.x - o.x) + (mine.y - o.y));
-                v[j] = j <= lane ? v[j] * f : 0.0f;
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) out[e] = sm100::pack_bf16x2(v[2 * e], v[2 * e + 1]);
+          for (int j = 0; j < 4; ++j) {
+            const float4 y = c[j];
+            w[2 * j] = mul2(ff, pair(y.x, y.y));
+            w[2 * j + 1] = mul2(ff, pair(y.z, y.w));
           }
-          sm100::tmem_st16(base + 16 * b, out);
+          sm100::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) out[j] = bf16x2(mul2(w[j], pair(x[2 * j], x[2 * j + 1])));
+          tmem_st8(base + 8 * b, out);
+        }
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {  // the diagonal's
+          float x[16];
+          uint32_t out[8];
+          sm100::tmem_ld16(base + 32 * q + 16 * b, x);
+          const float4* c = reinterpret_cast<const float4*>(gt.rel + 32 * q + 16 * b);
+          float w[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 y = c[j];
+            w[4 * j] = ex2(mine - y.x);
+            w[4 * j + 1] = ex2(mine - y.y);
+            w[4 * j + 2] = ex2(mine - y.z);
+            w[4 * j + 3] = ex2(mine - y.w);
+          }
+          sm100::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = 16 * b + j <= lane ? x[j] * w[j] : 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) out[j] = sm100::pack_bf16x2(x[2 * j], x[2 * j + 1]);
+          tmem_st8(base + 16 * q + 8 * b, out);
+        }
+#pragma unroll 1
+        for (int b = 2 * q + 2; b < 8; ++b) {
+          const uint32_t zero[8] = {};
+          tmem_st8(base + 8 * b, zero);
         }
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
@@ -522,11 +613,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = DK == 128 ? 32 * q + lane : 16 * q + lane;
     const bool mine = DK == 128 || lane < 16;
     const uint32_t tm = sm100::taddr(tmem, 32 * q, TM_DS);
-    float S[NV];
+    f32x2 S[NV / 2];
     uint32_t g = 0;
     bool ok = true;
-    const int64_t ids = (int64_t)p.cols * p.a.H * p.halves;
-    for (int64_t id = blockIdx.x; ok && id < ids; id += gridDim.x) {
+    const int ids = p.cols * p.a.H * p.halves;
+    for (int id = blockIdx.x; ok && id < ids; id += gridDim.x) {
       Item it;
       if (!locate<OUT>(p, id, it)) continue;
       const int64_t size = (int64_t)DK * p.a.dv;
@@ -544,19 +635,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < NV; j += 4) {
         const float4 x = from && mine ? *reinterpret_cast<const float4*>(from + in_head + j)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[j] = x.x;
-        S[j + 1] = x.y;
-        S[j + 2] = x.z;
-        S[j + 3] = x.w;
+        S[j / 2] = pair(x.x, x.y);
+        S[j / 2 + 1] = pair(x.z, x.w);
       }
+      double all = 1.0;  // the segment's decay
       for (int t = 0; t < it.len; t += C, ++g) {
         if (OUT) {
-          ok = g == 0 || wait(&bars.o_full, g - 1);  // (the last Q S has read the operand)
+          ok = g == 0 || wait(&bars.st_empty, g - 1);  // (the last Q S has read the operand)
           if (!ok) break;
           if (mine) {
 #pragma unroll
             for (int j = 0; j < NV; j += 8)
-              kda_tc::st8_bf16(smem + M::kS + kda_tc::mn_off(j, i, 1024), S + j);
+              kda_tc::st16(smem + M::kS + kda_tc::mn_off(j, i, 1024), bf16x2(S[j / 2]),
+                           bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
           }
           sm100::fence_async_smem();
           arrive(&bars.st_full);
@@ -566,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         sm100::tc_fence_after();
         const float2 f = gates[slot].gamma;
+        const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
 #pragma unroll
         for (int j = 0; j < NV; j += 16) {
           float x[16], y[16];
@@ -573,18 +665,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm100::tmem_ld16(tm + NV + j, y);
           sm100::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            S[j + e] = fmaf(f.x, S[j + e], fmaf(f.y, S[j + e], x[e] + y[e]));
+          for (int e = 0; e < 16; e += 2) {
+            f32x2& z = S[(j + e) / 2];
+            z = fma2(hi, z, fma2(lo, z, add2(pair(x[e], x[e + 1]), pair(y[e], y[e + 1]))));
+          }
         }
+        if (!OUT) all *= (double)f.x + (double)f.y;
         sm100::tc_fence_before();
         arrive(&bars.ds_empty);
         arrive(&bars.gate_empty[slot]);
       }
       if (to && mine && ok) {
 #pragma unroll
-        for (int j = 0; j < NV; j += 4)
-          *reinterpret_cast<float4*>(to + in_head + j) =
-              make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        for (int j = 0; j < NV; j += 4) {
+          float4 x;
+          unpair(S[j / 2], x.x, x.y);
+          unpair(S[j / 2 + 1], x.z, x.w);
+          *reinterpret_cast<float4*>(to + in_head + j) = x;
+        }
+      }
+      if (!OUT && ok && it.half == 0 && tid == 256) {
+        const float hi = (float)all;
+        p.gammas[(int64_t)it.col * p.a.H + it.h] = make_float2(hi, (float)(all - (double)hi));
       }
     }
   } else {
@@ -600,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox);
       uint4* hi = reinterpret_cast<uint4*>(smem + M::kVP);
       uint4* lo = hi + M::kBox / 16;
-#pragma unroll
+#pragma unroll 2
       for (int k = 0; k < 8; ++k) {
         const int e = 128 * k + tid - 384, row = e >> 3;
         const float f = gates[slot].v[row];
@@ -635,29 +737,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_after();
       const uint32_t slot = g % kGates;
       const float f = gates[slot].row[i], scale = p.a.scale;
-      uint32_t out[NV / 2];
-#pragma unroll
+      const f32x2 ff = pair(f, f), ss = pair(scale, scale);
+      const bool mine = i < w.rows();
+      uint4* dst = reinterpret_cast<uint4*>(
+          static_cast<__nv_bfloat16*>(p.a.out) +
+          ((w.it.row + w.t + i) * p.a.H + w.it.h) * p.a.dv + NV * w.it.half);
+#pragma unroll 1
       for (int j = 0; j < NV; j += 16) {
         float x[16], y[16];
         sm100::tmem_ld16(tm + TM_O1 + j, x);
         sm100::tmem_ld16(tm + TM_O2 + j, y);
         sm100::tmem_wait_ld();
+        uint32_t out[8];
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
-          out[(j + e) / 2] = sm100::pack_bf16x2(fmaf(f, x[e], scale * y[e]),
-                                                fmaf(f, x[e + 1], scale * y[e + 1]));
+          out[e / 2] = bf16x2(fma2(ff, pair(x[e], x[e + 1]), mul2(ss, pair(y[e], y[e + 1]))));
+        if (mine) {
+          dst[j / 8] = make_uint4(out[0], out[1], out[2], out[3]);
+          dst[j / 8 + 1] = make_uint4(out[4], out[5], out[6], out[7]);
+        }
       }
       sm100::tc_fence_before();
       arrive(&bars.o_empty);
       arrive(&bars.gate_empty[slot]);
-      if (i < w.rows()) {
-        uint4* dst = reinterpret_cast<uint4*>(
-            static_cast<__nv_bfloat16*>(p.a.out) +
-            ((w.it.row + w.t + i) * p.a.H + w.it.h) * p.a.dv + NV * w.it.half);
-#pragma unroll
-        for (int j = 0; j < NV / 8; ++j)
-          dst[j] = make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
-      }
     }
   }
   __syncwarp();
@@ -757,7 +859,7 @@ kda_status launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap&
   auto kernel = kda_linear_tile_kernel<DK, OUT>;
   const kda_status rc = kda_smem_attr((const void*)kernel, Smem<DK>::kBytes);
   if (rc != KDA_OK) return rc;
-  const int64_t items = (int64_t)p.cols * p.a.H * p.halves;
+  const int64_t items = (int64_t)p.cols * p.a.H * p.halves;  // (below 2^30: N * H is)
   const int sms = kda_device_sms();
   const unsigned grid = (unsigned)(items < sms ? items : sms);
   kernel<<<grid, kThreads, Smem<DK>::kBytes, s>>>(q, k, v, p);
