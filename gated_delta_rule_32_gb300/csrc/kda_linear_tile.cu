@@ -13,9 +13,9 @@
 // Q, K and V by TMA (two chunks ahead), one issues products, one takes the
 // decays' sums, and three groups of four turn scores into P, carry the state,
 // and make V' and write rows out.  The products of a chunk run in the order
-// K^T V', Q S, P V and the next chunk's scores: what each waits for is made while
-// the three before it run, and K, Q and V are let go of early enough for the
-// copies of two chunks on.
+// K^T V', Q S, the next chunk's scores, P V: what each waits for is made while the
+// others run, and K, Q and V are let go of early enough for the copies of two
+// chunks on.
 //
 // Rounding: P and the state as an operand enter as bf16; rows of Q keep their
 // bits, e^G being applied to the product.  The state itself is summed from V'
@@ -64,9 +64,17 @@ struct alignas(16) Gate {
   float2 gamma;    // 2^E in two parts
 };
 
+// [2]: by a chunk's stage.  A phase has to be seen by all that wait for it before
+// the next one of the same barrier can end: each of these is followed, before its
+// next phase, by something that they all have a part in.
 struct Bars {
-  uint64_t qk_full[2], v_full[2], k_empty[2], q_empty[2], v_empty[2];
-  uint64_t s_raw[2], p_full[2], o_full, o_empty, vp_full, ds_full, ds_empty, st_full, st_empty;
+  uint64_t qk_full[2], v_full[2];    // copies have landed
+  uint64_t ds_done[2];               // K^T V' is there: V' and K are free
+  uint64_t qs_done[2];               // Q S is there: Q and S's operand are free
+  uint64_t s_done[2];                // the scores are there
+  uint64_t o_done[2];                // O is there: V and P are free
+  uint64_t ready_d, ready_q;         // V' is made, K^T V' read; S's operand made, O read
+  uint64_t p_full[2];
   uint64_t gate_full[kGates], gate_empty[kGates], drain;
 };
 
@@ -85,7 +93,7 @@ struct Smem {
 struct Item {
   int64_t row;  // first token row
   int len;      // tokens
-  int n, h, half, col;
+  int n, h, hk, half, col;
   bool first, last;  // segment of its sequence
 };
 
@@ -97,6 +105,7 @@ __device__ __noinline__ bool locate(const TileArgs& p, int id, Item& it) {
   it.half = id - x * p.halves;
   it.col = x / p.a.H;
   it.h = x - it.col * p.a.H;
+  it.hk = it.h / (p.a.H / p.a.HK);
   int seg;
   if (!p.a.cu) {
     it.n = it.col / p.segs;
@@ -186,36 +195,42 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 template <int AS, int BS>
-__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate, uint32_t one) {
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t a_hi,
+                                        uint32_t b_hi, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n"
-      " setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-      " add.u64 a, %1, %6;\n add.u64 b, %2, %7;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.u64 a, a, %6;\n add.u64 b, b, %7;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.u64 a, a, %6;\n add.u64 b, b, %7;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one), "n"(AS), "n"(BS)
+      "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n .reg .b32 x, y;\n"
+      " setp.ne.b32 q, %7, 0;\n setp.ne.b32 p, %6, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n"
+      " add.u32 x, %1, %8;\n add.u32 y, %2, %9;\n mov.b64 a, {x, %3};\n mov.b64 b, {y, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
+      " add.u32 x, %1, 2 * %8;\n add.u32 y, %2, 2 * %9;\n mov.b64 a, {x, %3};\n"
+      " mov.b64 b, {y, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
+      " add.u32 x, %1, 3 * %8;\n add.u32 y, %2, 3 * %9;\n mov.b64 a, {x, %3};\n"
+      " mov.b64 b, {y, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(one), "n"(AS),
+      "n"(BS)
       : "memory");
 }
 // A in tensor memory, 8 columns a step
 template <int BS>
-__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate, uint32_t one) {
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 a;\n"
-      " setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-      " add.u32 a, %1, 8;\n add.u64 b, %2, %6;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-      " add.u32 a, a, 8;\n add.u64 b, b, %6;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-      " add.u32 a, a, 8;\n add.u64 b, b, %6;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one), "n"(BS)
+      "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 x, y;\n"
+      " setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
+      " add.u32 x, %1, 8;\n add.u32 y, %2, %7;\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      " add.u32 x, %1, 16;\n add.u32 y, %2, 2 * %7;\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+      " add.u32 x, %1, 24;\n add.u32 y, %2, 3 * %7;\n mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(one), "n"(BS)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
@@ -228,30 +243,31 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
 }
 
 // Bounded wait (2 s), which also gives up when another role of the CTA has.  The
-// hint lets the hardware suspend the warp for up to 1 ms at a time: one that
-// polls takes issue slots and shared memory's from those that work.
-__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
-                                             volatile int* abort) {
-  auto poll = [&]() -> bool {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(1000000)
-        : "memory");
-    return ok != 0;
-  };
-  uint64_t t0 = 0;
-  while (!poll()) {
-    const uint64_t t = sm100::globaltimer_ns();
-    if (t0 == 0) t0 = t;
-    if (*abort || t - t0 > 2000000000ull) {
+// hint lets the hardware suspend the warp for up to 1 ms: one that polls takes
+// issue slots and shared memory's from those that work.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000000)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = sm100::globaltimer_ns();
+  while (!poll(bar, parity))
+    if (*abort || sm100::globaltimer_ns() - t0 > 2000000000ull) {
       *abort = 1;
       return false;
     }
-  }
   return true;
+}
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
+                                             volatile int* abort) {
+  const uint32_t at = sm100::smem_u32(bar);
+  return poll(at, parity) || wait_on(at, parity, abort);
 }
 
 // Two fp32 at a time.
@@ -308,19 +324,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&bars.qk_full[i], OUT ? 2 : 1);
       sm100::mbar_init(&bars.v_full[i], 1);
-      sm100::mbar_init(&bars.k_empty[i], 1);
-      sm100::mbar_init(&bars.q_empty[i], 1);
-      sm100::mbar_init(&bars.v_empty[i], 1);
-      sm100::mbar_init(&bars.s_raw[i], 1);
+      sm100::mbar_init(&bars.ds_done[i], 1);
+      sm100::mbar_init(&bars.qs_done[i], 1);
+      sm100::mbar_init(&bars.s_done[i], 1);
+      sm100::mbar_init(&bars.o_done[i], 1);
       sm100::mbar_init(&bars.p_full[i], 4);
     }
-    sm100::mbar_init(&bars.o_full, 1);
-    sm100::mbar_init(&bars.o_empty, 4);
-    sm100::mbar_init(&bars.vp_full, 4);
-    sm100::mbar_init(&bars.ds_full, 1);
-    sm100::mbar_init(&bars.ds_empty, 4);
-    sm100::mbar_init(&bars.st_full, 4);
-    sm100::mbar_init(&bars.st_empty, 1);
+    sm100::mbar_init(&bars.ready_d, 8);
+    sm100::mbar_init(&bars.ready_q, 8);
     for (int i = 0; i < kGates; ++i) {
       sm100::mbar_init(&bars.gate_full[i], 1);
       sm100::mbar_init(&bars.gate_empty[i], OUT ? 12 : 8);
@@ -332,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  // (the whole of tensor memory is this CTA's: its columns count from 0)
+  const uint32_t tmem = 0;
 
   auto wait = [&](uint64_t* bar, uint32_t n) -> bool {  // the barrier's phase n
     return bounded_wait(bar, n & 1, s_abort);
@@ -348,9 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0;
     for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
       const uint32_t s = g & 1, use = g >> 1;
-      const int row = (int)(w.it.row + w.t), hk = w.it.h / (p.a.H / p.a.HK);
+      const int row = (int)(w.it.row + w.t), hk = w.it.hk;
       // (in the order in which the products let go of them)
-      if (use > 0 && !wait(&bars.k_empty[s], use - 1)) break;
+      if (use > 0 && !wait(&bars.ds_done[s], use - 1)) break;
       if (lane == 0) {
         unsigned char* k = smem + M::kK + s * M::kTile;
         sm100::mbar_arrive_expect_tx(&bars.qk_full[s], M::kTile);
@@ -361,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       // (a give-up leaves the chunk's barriers short of an arrival: nobody passes them)
       if (OUT) {
-        if (use > 0 && !wait(&bars.q_empty[s], use - 1)) {
+        if (use > 0 && !wait(&bars.qs_done[s], use - 1)) {
           ++g;
           break;
         }
@@ -374,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      if (use > 0 && !wait(&bars.v_empty[s], use - 1)) {
+      if (use > 0 && !wait(OUT ? &bars.o_done[s] : &bars.ds_done[s], use - 1)) {
         ++g;
         break;
       }
@@ -394,73 +406,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------- products
     const uint32_t one = elect_one();
     constexpr uint32_t id_s = sm100::idesc_bf16(C, C, 0, 0), id_q = sm100::idesc_bf16(C, NV, 0, 1);
-    constexpr uint32_t id_p = sm100::idesc_bf16(C, NV, 0, 1);
     constexpr uint32_t id_d = sm100::idesc_bf16(DK, 2 * NV, 1, 1);
-    const uint32_t at = sm100::smem_u32(smem);
-    // (addresses in a descriptor count 16 bytes)
-    const uint64_t dq = sm100::smem_desc_sw128(at + M::kQ, 16, 1024);
-    const uint64_t dk = sm100::smem_desc_sw128(at + M::kK, 16, 1024);
-    const uint64_t dkt = sm100::smem_desc_sw128(at + M::kK, M::kBox, 1024);  // as K^T
-    const uint64_t dv = sm100::smem_desc_sw128(at + M::kV, M::kBox, 1024);
-    const uint64_t dvp = sm100::smem_desc_sw128(at + M::kVP, M::kBox, 1024);
-    const uint64_t dst = sm100::smem_desc(at + M::kS, 1024, 128);
-    constexpr int kTile16 = M::kTile / 16, kBox16 = M::kBox / 16;
+    // (addresses in a descriptor count 16 bytes; a box of 64 channels is one span along M or N)
+    constexpr uint32_t kTile16 = M::kTile / 16, kBox16 = M::kBox / 16;
+    const uint32_t at = (uint32_t)sm100::smem_desc(sm100::smem_u32(smem), M::kBox, 1024);
+    const uint32_t hi = (uint32_t)(sm100::smem_desc_sw128(0, M::kBox, 1024) >> 32);
+    const uint32_t dq = at + M::kQ / 16, dk = at + M::kK / 16, dv = at + M::kV / 16;
+    const uint32_t dvp = at + M::kVP / 16;
+    const uint64_t st = sm100::smem_desc(sm100::smem_u32(smem) + M::kS, 1024, 128);
+    const uint32_t dst = (uint32_t)st, st_hi = (uint32_t)(st >> 32);
+    // every thread takes the same way (and the compiler knows)
+    auto all = [&](bool x) -> bool { return __all_sync(~0u, x); };
     auto scores = [&](uint32_t s) {
 #pragma unroll
       for (int b = 0; b < DK / 64; ++b)
-        mma4_ss<2, 2>(tmem + C * s, dq + s * kTile16 + b * kBox16, dk + s * kTile16 + b * kBox16,
+        mma4_ss<2, 2>(C * s, dq + s * kTile16 + b * kBox16, dk + s * kTile16 + b * kBox16, hi, hi,
                       id_s, b, one);
-      commit(&bars.s_raw[s], one);
+      commit(&bars.s_done[s], one);
     };
     uint32_t g = 0;
     Walk<OUT> w(p);
-    bool ok = true;
-    if (OUT && w.valid) {
-      ok = wait(&bars.qk_full[0], 0);
+    bool more = all(w.valid);
+    if (OUT && more) {
+      more = all(wait(&bars.qk_full[0], 0));
       sm100::tc_fence_after();
-      if (ok) scores(0);
+      if (more) scores(0);
     }
-    for (; ok && w.valid; ++g) {
+    // chunk g; false: the last one, or a wait gave up
+    auto chunk = [&]() -> bool {
       const uint32_t s = g & 1;
-      ok = (OUT || wait(&bars.qk_full[s], g >> 1)) && wait(&bars.vp_full, g) &&
-           (g == 0 || wait(&bars.ds_empty, g - 1));
-      if (!ok) break;
+      if (!all((OUT || wait(&bars.qk_full[s], g >> 1)) && wait(&bars.ready_d, g))) return false;
       sm100::tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        mma4_ss<128, 128>(tmem + TM_DS, dkt + s * kTile16 + 512 * k, dvp + 512 * k, id_d, k, one);
-      commit(&bars.ds_full, one);
-      commit(&bars.k_empty[s], one);
-      if (!OUT) commit(&bars.v_empty[s], one);  // (V' was made from it)
+      for (uint32_t k = 0; k < 2; ++k)
+        mma4_ss<128, 128>(TM_DS, dk + s * kTile16 + 512 * k, dvp + 512 * k, hi, hi, id_d, k, one);
+      commit(&bars.ds_done[s], one);
       w.next();
-      if (!OUT) continue;
-      ok = wait(&bars.st_full, g) && (g == 0 || wait(&bars.o_empty, g - 1));
-      if (!ok) break;
-      sm100::tc_fence_after();
-#pragma unroll
-      for (int b = 0; b < DK / 64; ++b)
-        mma4_ss<2, 128>(tmem + TM_O1, dq + s * kTile16 + b * kBox16, dst + 512 * b, id_q, b, one);
-      commit(&bars.st_empty, one);
-      commit(&bars.q_empty[s], one);
-      // (P of the chunk before has been read: waited for here, since a barrier's phase has to
-      // be seen before its next one can end)
-      ok = wait(&bars.v_full[s], g >> 1) && wait(&bars.p_full[s], g >> 1) &&
-           (g == 0 || wait(&bars.o_full, g - 1));
-      if (!ok) break;
-      sm100::tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        mma4_ts<128>(tmem + TM_O2, tmem + C * s + 32 * k, dv + s * kBox16 + 512 * k, id_p, k, one);
-      commit(&bars.o_full, one);
-      commit(&bars.v_empty[s], one);
-      if (w.valid) {
-        // the next chunk's scores take the place of the last one's P
-        ok = wait(&bars.qk_full[s ^ 1], (g + 1) >> 1);
-        if (!ok) break;
+      const bool next = all(w.valid);
+      if (OUT) {
+        if (!all(wait(&bars.ready_q, g))) return false;
         sm100::tc_fence_after();
-        scores(s ^ 1);
+#pragma unroll
+        for (uint32_t b = 0; b < DK / 64; ++b)
+          mma4_ss<2, 128>(TM_O1, dq + s * kTile16 + b * kBox16, dst + 512 * b, hi, st_hi, id_q, b,
+                          one);
+        commit(&bars.qs_done[s], one);
+        if (next) {
+          // the next chunk's scores take the place of the last one's P (which O's readers saw used)
+          if (!all(wait(&bars.qk_full[s ^ 1], (g + 1) >> 1))) return false;
+          sm100::tc_fence_after();
+          scores(s ^ 1);
+        }
+        if (!all(wait(&bars.p_full[s], g >> 1))) return false;
+        sm100::tc_fence_after();
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k)
+          mma4_ts<128>(TM_O2, C * s + 32 * k, dv + s * kBox16 + 512 * k, hi, id_q, k, one);
+        commit(&bars.o_done[s], one);
       }
-    }
+      ++g;
+      return next;
+    };
+    while (more) more = chunk();
     commit(&bars.drain, one);
     sm100::mbar_wait(&bars.drain, 0, 200000000ull);
   } else if (warp < 4) {
@@ -548,17 +555,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (OUT)
       for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
         const uint32_t slot = g % kGates, base = tm + C * (g & 1);
-        if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.s_raw[g & 1], g >> 1)) break;
+        if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.s_done[g & 1], g >> 1)) break;
         sm100::tc_fence_after();
         const Gate& gt = gates[slot];
         const float mine = gt.rel[i];
-        // blocks of 32 columns below the diagonal's, 16 at a time
+        const float2 e = gt.end[q];
+        // 16 columns at a time: those below the diagonal's 32, the diagonal's, the rest
 #pragma unroll 1
         for (int b = 0; b < 2 * q; ++b) {
           float x[16];
           uint32_t out[8];
           sm100::tmem_ld16(base + 16 * b, x);
-          const float2 e = gt.end[q], o = gt.end[b >> 1];
+          const float2 o = gt.end[b >> 1];
           const float f = ex2(mine + ((e.x - o.x) + (e.y - o.y)));
           const f32x2 ff = pair(f, f);
           const float4* c = reinterpret_cast<const float4*>(gt.col + 16 * b);
@@ -575,12 +583,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st8(base + 8 * b, out);
         }
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) {  // the diagonal's
-          float x[16];
+        for (int b = 0; b < 32; b += 16) {
+          float x[16], w[16];
           uint32_t out[8];
-          sm100::tmem_ld16(base + 32 * q + 16 * b, x);
-          const float4* c = reinterpret_cast<const float4*>(gt.rel + 32 * q + 16 * b);
-          float w[16];
+          sm100::tmem_ld16(base + 32 * q + b, x);
+          const float4* c = reinterpret_cast<const float4*>(gt.rel + 32 * q + b);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4 y = c[j];
@@ -590,16 +597,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[4 * j + 3] = ex2(mine - y.w);
           }
           sm100::tmem_wait_ld();
+          const int last = lane - b;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = 16 * b + j <= lane ? x[j] * w[j] : 0.0f;
+          for (int j = 0; j < 16; ++j) x[j] = j <= last ? x[j] * w[j] : 0.0f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) out[j] = sm100::pack_bf16x2(x[2 * j], x[2 * j + 1]);
-          tmem_st8(base + 16 * q + 8 * b, out);
+          tmem_st8(base + 16 * q + (b >> 1), out);
         }
 #pragma unroll 1
-        for (int b = 2 * q + 2; b < 8; ++b) {
-          const uint32_t zero[8] = {};
-          tmem_st8(base + 8 * b, zero);
+        for (int b = q + 1; b < 4; ++b) {
+          const uint32_t zero[16] = {};
+          sm100::tmem_st16(base + 16 * b, zero);
         }
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
@@ -616,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     f32x2 S[NV / 2];
     uint32_t g = 0;
     bool ok = true;
+    arrive(&bars.ready_d);  // (nothing to read before the first chunk)
     const int ids = p.cols * p.a.H * p.halves;
     for (int id = blockIdx.x; ok && id < ids; id += gridDim.x) {
       Item it;
@@ -641,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       double all = 1.0;  // the segment's decay
       for (int t = 0; t < it.len; t += C, ++g) {
         if (OUT) {
-          ok = g == 0 || wait(&bars.st_empty, g - 1);  // (the last Q S has read the operand)
+          // (the last Q S has read the operand)
+          ok = g == 0 || wait(&bars.qs_done[(g - 1) & 1], (g - 1) >> 1);
           if (!ok) break;
           if (mine) {
 #pragma unroll
@@ -650,10 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                            bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
           }
           sm100::fence_async_smem();
-          arrive(&bars.st_full);
+          arrive(&bars.ready_q);
         }
         const uint32_t slot = g % kGates;
-        ok = wait(&bars.gate_full[slot], g / kGates) && wait(&bars.ds_full, g);
+        ok = wait(&bars.gate_full[slot], g / kGates) && wait(&bars.ds_done[g & 1], g >> 1);
         if (!ok) break;
         sm100::tc_fence_after();
         const float2 f = gates[slot].gamma;
@@ -672,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!OUT) all *= (double)f.x + (double)f.y;
         sm100::tc_fence_before();
-        arrive(&bars.ds_empty);
+        arrive(&bars.ready_d);  // (of the next chunk)
         arrive(&bars.gate_empty[slot]);
       }
       if (to && mine && ok) {
@@ -693,51 +703,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- V', and rows go out
     const int q = warp & 3, i = 32 * q + lane;
     const uint32_t tm = sm100::taddr(tmem, 32 * q, 0);
-    // V' of chunk g, `rows` of it tokens
-    auto weigh = [&](uint32_t g, int rows) -> bool {
+    // V' of chunk g (whose rows of V past the end are zeros by now)
+    auto weigh = [&](uint32_t g) -> bool {
       const uint32_t slot = g % kGates, s = g & 1;
       if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.v_full[s], g >> 1) ||
-          (g > 0 && !wait(&bars.ds_full, g - 1)))
+          (g > 0 && !wait(&bars.ds_done[(g - 1) & 1], (g - 1) >> 1)))
         return false;
-      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox);
-      uint4* hi = reinterpret_cast<uint4*>(smem + M::kVP);
-      uint4* lo = hi + M::kBox / 16;
-#pragma unroll 2
+      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox) + tid - 384;
+      uint4* to = reinterpret_cast<uint4*>(smem + M::kVP) + tid - 384;
+      const float* f = gates[slot].v + ((tid - 384) >> 3);
+      const f32x2 minus = pair(-1.0f, -1.0f);
+#pragma unroll 1
       for (int k = 0; k < 8; ++k) {
-        const int e = 128 * k + tid - 384, row = e >> 3;
-        const float f = gates[slot].v[row];
-        const uint4 w = v[e];
+        const uint4 w = v[128 * k];
+        const f32x2 ff = pair(f[16 * k], f[16 * k]);
         const uint32_t r[4] = {w.x, w.y, w.z, w.w};
         uint32_t a[4], b[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const float y0 = __uint_as_float(r[x] << 16) * f;
-          const float y1 = __uint_as_float(r[x] & 0xffff0000u) * f;
-          a[x] = sm100::pack_bf16x2(y0, y1);
-          b[x] = sm100::pack_bf16x2(y0 - __uint_as_float(a[x] << 16),
-                                    y1 - __uint_as_float(a[x] & 0xffff0000u));
+          const f32x2 y = mul2(ff, pair(__uint_as_float(r[x] << 16),
+                                        __uint_as_float(r[x] & 0xffff0000u)));
+          a[x] = bf16x2(y);
+          b[x] = bf16x2(fma2(minus, pair(__uint_as_float(a[x] << 16),
+                                         __uint_as_float(a[x] & 0xffff0000u)), y));
         }
-        if (row >= rows) a[0] = a[1] = a[2] = a[3] = b[0] = b[1] = b[2] = b[3] = 0;
-        hi[e] = make_uint4(a[0], a[1], a[2], a[3]);
-        lo[e] = make_uint4(b[0], b[1], b[2], b[3]);
+        to[128 * k] = make_uint4(a[0], a[1], a[2], a[3]);
+        to[128 * k + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
       }
       sm100::fence_async_smem();
-      arrive(&bars.vp_full);
+      arrive(&bars.ready_d);
       if (!OUT) arrive(&bars.gate_empty[slot]);
       return true;
     };
     uint32_t g = 0;
     Walk<OUT> w(p), ahead(p);
-    bool ok = !ahead.valid || weigh(0, ahead.rows());
+    bool ok = !ahead.valid || weigh(0);
+    if (OUT) arrive(&bars.ready_q);  // (nothing to read before the first chunk)
     for (; ok && w.valid; w.next(), ++g) {
       if (ahead.valid) ahead.next();
-      if (ahead.valid && !weigh(g + 1, ahead.rows())) break;
+      if (ahead.valid && !weigh(g + 1)) break;
       if (!OUT) continue;
-      if (!wait(&bars.o_full, g)) break;
+      if (!wait(&bars.o_done[g & 1], g >> 1)) break;
       sm100::tc_fence_after();
       const uint32_t slot = g % kGates;
-      const float f = gates[slot].row[i], scale = p.a.scale;
-      const f32x2 ff = pair(f, f), ss = pair(scale, scale);
+      const float f = gates[slot].row[i];
+      const f32x2 ff = pair(f, f), ss = pair(p.a.scale, p.a.scale);
       const bool mine = i < w.rows();
       uint4* dst = reinterpret_cast<uint4*>(
           static_cast<__nv_bfloat16*>(p.a.out) +
@@ -758,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       sm100::tc_fence_before();
-      arrive(&bars.o_empty);
+      arrive(&bars.ready_q);  // (of the next chunk)
       arrive(&bars.gate_empty[slot]);
     }
   }
@@ -766,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm100::tc_fence_before();
   __syncthreads();
   if (tid == 0 && *s_abort) report(p.a.status, KDA_ERR_TIMEOUT);
-  if (warp == 1) sm100::tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) sm100::tmem_dealloc(*s_tmem, kTmemCols);
 }
 
 // The states that segments start from: column by column of a sequence,
