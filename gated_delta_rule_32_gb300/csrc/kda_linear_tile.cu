@@ -10,9 +10,11 @@
 // A CTA takes items (a sequence or a segment of one, a head, 64 value columns)
 // and walks their chunks, its state S in registers (fp32); Q K^T, P V, Q S and
 // K^T V' are tcgen05 products into tensor memory.  Warps have roles: one feeds
-// Q, K and V by TMA (two chunks ahead), one issues products, one takes the
-// decays' sums, and three groups of four turn scores into P, carry the state,
-// and make V' and write rows out.  The products of a chunk run in the order
+// Q, K and V by TMA (two chunks ahead), one issues products, two take the
+// decays' sums, and four groups of four turn scores into P, carry the state,
+// write rows out and make V'.  Their loops are kept short: what the warps of a
+// scheduler run must fit its instruction cache (unrolled twice as far, the same
+// kernel took twice the time).  The products of a chunk run in the order
 // K^T V', Q S, the next chunk's scores, P V: what each waits for is made while the
 // others run, and K, Q and V are let go of early enough for the copies of two
 // chunks on.
@@ -20,8 +22,8 @@
 // Rounding: P and the state as an operand enter as bf16; rows of Q keep their
 // bits, e^G being applied to the product.  The state itself is summed from V'
 // in two bf16 parts (16 bits), so what is carried and returned is fp32 to
-// about 2^-17.  Sums of log-decays are taken in 64 bits and held in two fp32,
-// as their differences are what counts.  Where a tile lies below the diagonal
+// about 2^-17.  Sums of log-decays are exact, in fixed point, as their
+// differences are what counts.  Where a tile lies below the diagonal
 // of 32-token blocks, e^(G_i - G_j) is e^(G_i - G_b) e^(G_b - G_j) with b the
 // last token of j's block: both factors are at most 1, so neither overflows
 // and the product only vanishes where the weight does.
@@ -41,7 +43,7 @@ using namespace kda_linear;
 
 constexpr int C = 128;          // tokens of a chunk
 constexpr int NV = 64;          // value columns of a CTA
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kGates = 4;
 constexpr uint32_t TM_O1 = 256, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
 
@@ -60,7 +62,7 @@ struct alignas(16) Gate {
   float col[C];    // 2^(G_b - G_j)
   float row[C];    // scale * 2^G_i
   float v[C];      // 2^(E - G_j)
-  float2 end[4];   // G of the last token of each 32, in two parts
+  int2 end[4];     // G of the last token of each 32, in units of 2^-16 and 2^-40
   float2 gamma;    // 2^E in two parts
 };
 
@@ -172,6 +174,16 @@ struct Walk {
   __device__ __forceinline__ int rows() const { return it.len - t < C ? it.len - t : C; }
 };
 
+// A fixed-point number of units of 2^-16 and 2^-40.
+__device__ __forceinline__ float fixed(int hi, int lo) {
+  return fmaf((float)lo, 1.0f / 1099511627776.0f, (float)hi * (1.0f / 65536.0f));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t ta, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "r"(ta));
+}
 __device__ __forceinline__ void tmem_st8(uint32_t ta, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
@@ -334,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::mbar_init(&bars.ready_q, 8);
     for (int i = 0; i < kGates; ++i) {
       sm100::mbar_init(&bars.gate_full[i], 1);
-      sm100::mbar_init(&bars.gate_empty[i], OUT ? 12 : 8);
+      sm100::mbar_init(&bars.gate_empty[i], OUT ? 16 : 8);
     }
     sm100::mbar_init(&bars.drain, 1);
     sm100::fence_mbar_init();
@@ -479,57 +491,78 @@ __global__ void __launch_bounds__(kThreads, 1)
         int len;
         span(p.a, n, row, len);
       }
-    uint32_t g = 0;
-    for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
-      if ((g & 1) != turn) continue;
-      const uint32_t slot = g % kGates, use = g / kGates;
-      const int L = w.rows();
+    // the log-decays of a chunk, four tokens a lane
+    auto fetch = [&](const Walk<OUT>& w, float (&y)[4]) {
       const float* a = p.a.decay + (w.it.row + w.t) * p.a.decay_stride + w.it.h;
-      float y[4];
+      const int L = w.rows();
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = 4 * lane + e;
         y[e] = t < L ? a[t * p.a.decay_stride] : 0.0f;
       }
-      double x[4], sum = 0.0;
+    };
+    Walk<OUT> w(p);
+    if (turn && w.valid) w.next();
+    float y[4];
+    if (w.valid) fetch(w, y);
+    for (uint32_t g = turn; w.valid; g += 2) {
+      const uint32_t slot = g % kGates, use = g / kGates;
+      const int L = w.rows();
+      // fixed point, exact in its sums: 2^-16 and 2^-40 a unit
+      int hi[4], lo[4], sum_hi = 0, sum_lo = 0;
+      uint32_t nan = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         // 2^-160 vanishes in 32 bits: what decays more than that decays so much
-        const float c = clamp_decay(y[e]);
-        sum += (double)(c < -110.9f ? -110.9f : c) * 1.4426950408889634074;
-        x[e] = sum;
+        const float c = clamp_decay(y[e]) * 1.4426950408889634f, x = c < -160.0f ? -160.0f : c;
+        nan |= (x != x) << e;
+        const int i = __float2int_rn(x * 65536.0f);
+        hi[e] = sum_hi += i;
+        lo[e] = sum_lo += __float2int_rn(fmaf((float)i, -1.0f / 65536.0f, x) * 1099511627776.0f);
       }
+      // (the next ones on their way meanwhile)
+      w.next();
+      if (w.valid) w.next();
+      if (w.valid) fetch(w, y);
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
-        const double y = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += y;
+        const int a = __shfl_up_sync(~0u, sum_hi, d), b = __shfl_up_sync(~0u, sum_lo, d);
+        if (lane >= d) sum_hi += a, sum_lo += b;
       }
-      const double before = sum - x[3];
-      const double end = __shfl_sync(0xffffffffu, sum, 31);
-      const double block = __shfl_sync(0xffffffffu, sum, lane | 7);
+      const int end_hi = __shfl_sync(~0u, sum_hi, 31), end_lo = __shfl_sync(~0u, sum_lo, 31);
+      const int blk_hi = __shfl_sync(~0u, sum_hi, lane | 7), blk_lo = __shfl_sync(~0u, sum_lo, lane | 7);
+      const int pre_hi = sum_hi - hi[3], pre_lo = sum_lo - lo[3];
+      // a NaN makes what follows it NaN
+      const uint32_t bad = __ballot_sync(~0u, nan != 0);
       if (use > 0 && !wait(&bars.gate_empty[slot], use - 1)) break;
       Gate& gt = gates[slot];
       float rel[4], col[4], row[4], v[4];
+      const float none = __int_as_float(0x7fffffff);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const double G = before + x[e];
-        rel[e] = (float)(G - block);
+        const int h = pre_hi + hi[e], l = pre_lo + lo[e];
+        rel[e] = fixed(h - blk_hi, l - blk_lo);
         col[e] = ex2(-rel[e]);
-        row[e] = p.a.scale * ex2((float)G);
-        v[e] = ex2((float)(end - G));
+        row[e] = p.a.scale * ex2(fixed(h, l));
+        v[e] = ex2(fixed(end_hi - h, end_lo - l));
+        if (bad) {
+          // (rare) no sum for tokens from the first NaN on, and no weight to the chunk's end
+          if ((bad & ((1u << lane) - 1)) || (nan & ((2u << e) - 1))) rel[e] = row[e] = none;
+          v[e] = none;
+        }
       }
       reinterpret_cast<float4*>(gt.rel)[lane] = make_float4(rel[0], rel[1], rel[2], rel[3]);
       reinterpret_cast<float4*>(gt.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
       reinterpret_cast<float4*>(gt.row)[lane] = make_float4(row[0], row[1], row[2], row[3]);
       reinterpret_cast<float4*>(gt.v)[lane] = make_float4(v[0], v[1], v[2], v[3]);
-      if ((lane & 7) == 7) {
-        const float hi = (float)block;
-        gt.end[lane >> 3] = make_float2(hi, (float)(block - (double)hi));
-      }
+      if ((lane & 7) == 7) gt.end[lane >> 3] = make_int2(blk_hi, blk_lo);
       if (lane == 0) {
-        const double gamma = exp2(end);
-        const float hi = (float)gamma;
-        gt.gamma = make_float2(hi, (float)(gamma - (double)hi));
+        // close to 1, as 1 + (2^E - 1) and what that lost (see the kernel for single tokens)
+        const float x = fixed(end_hi, end_lo) * 0.6931471805599453f;
+        const float m = expm1f(x), f = 1.0f + m;
+        gt.gamma = bad ? make_float2(none, none)
+                   : x > -0.5f ? make_float2(f, m - (f - 1.0f))
+                               : make_float2(expf(x), 0.0f);
       }
       if (L < C) {
         // rows past the end, which belong to others: zeros, whatever they hold
@@ -559,15 +592,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm100::tc_fence_after();
         const Gate& gt = gates[slot];
         const float mine = gt.rel[i];
-        const float2 e = gt.end[q];
+        const int2 e = gt.end[q];
         // 16 columns at a time: those below the diagonal's 32, the diagonal's, the rest
 #pragma unroll 1
         for (int b = 0; b < 2 * q; ++b) {
           float x[16];
           uint32_t out[8];
           sm100::tmem_ld16(base + 16 * b, x);
-          const float2 o = gt.end[b >> 1];
-          const float f = ex2(mine + ((e.x - o.x) + (e.y - o.y)));
+          const int2 o = gt.end[b >> 1];
+          const float f = ex2(mine + fixed(e.x - o.x, e.y - o.y));
           const f32x2 ff = pair(f, f);
           const float4* c = reinterpret_cast<const float4*>(gt.col + 16 * b);
           f32x2 w[8];
@@ -669,13 +702,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 f = gates[slot].gamma;
         const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
 #pragma unroll
-        for (int j = 0; j < NV; j += 16) {
-          float x[16], y[16];
-          sm100::tmem_ld16(tm + j, x);
-          sm100::tmem_ld16(tm + NV + j, y);
+        for (int j = 0; j < NV; j += 8) {
+          float x[8], y[8];
+          tmem_ld8(tm + j, x);
+          tmem_ld8(tm + NV + j, y);
           sm100::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
+          for (int e = 0; e < 8; e += 2) {
             f32x2& z = S[(j + e) / 2];
             z = fma2(hi, z, fma2(lo, z, add2(pair(x[e], x[e + 1]), pair(y[e], y[e + 1]))));
           }
@@ -699,76 +732,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.gammas[(int64_t)it.col * p.a.H + it.h] = make_float2(hi, (float)(all - (double)hi));
       }
     }
-  } else {
-    // ------------------------------------------------- V', and rows go out
+  } else if (warp < 16) {
+    // ----------------------------------------------------------- rows go out
     const int q = warp & 3, i = 32 * q + lane;
     const uint32_t tm = sm100::taddr(tmem, 32 * q, 0);
-    // V' of chunk g (whose rows of V past the end are zeros by now)
-    auto weigh = [&](uint32_t g) -> bool {
-      const uint32_t slot = g % kGates, s = g & 1;
-      if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.v_full[s], g >> 1) ||
-          (g > 0 && !wait(&bars.ds_done[(g - 1) & 1], (g - 1) >> 1)))
-        return false;
-      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox) + tid - 384;
-      uint4* to = reinterpret_cast<uint4*>(smem + M::kVP) + tid - 384;
-      const float* f = gates[slot].v + ((tid - 384) >> 3);
-      const f32x2 minus = pair(-1.0f, -1.0f);
+    uint32_t g = 0;
+    if (OUT) {
+      arrive(&bars.ready_q);  // (nothing to read before the first chunk)
+      for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
+        const uint32_t slot = g % kGates;
+        if (!wait(&bars.gate_full[slot], g / kGates)) break;
+        const float f = gates[slot].row[i];
+        const f32x2 ff = pair(f, f), ss = pair(p.a.scale, p.a.scale);
+        arrive(&bars.gate_empty[slot]);
+        const bool mine = i < w.rows();
+        uint4* dst = reinterpret_cast<uint4*>(
+            static_cast<__nv_bfloat16*>(p.a.out) +
+            ((w.it.row + w.t + i) * p.a.H + w.it.h) * p.a.dv + NV * w.it.half);
+        if (!wait(&bars.o_done[g & 1], g >> 1)) break;
+        sm100::tc_fence_after();
 #pragma unroll 1
+        for (int j = 0; j < NV; j += 32) {
+          float x[32], y[32];
+          sm100::tmem_ld16(tm + TM_O1 + j, *reinterpret_cast<float(*)[16]>(x));
+          sm100::tmem_ld16(tm + TM_O2 + j, *reinterpret_cast<float(*)[16]>(y));
+          sm100::tmem_ld16(tm + TM_O1 + j + 16, *reinterpret_cast<float(*)[16]>(x + 16));
+          sm100::tmem_ld16(tm + TM_O2 + j + 16, *reinterpret_cast<float(*)[16]>(y + 16));
+          sm100::tmem_wait_ld();
+          if (j == NV - 32) {
+            sm100::tc_fence_before();
+            arrive(&bars.ready_q);  // (of the next chunk)
+          }
+          uint32_t out[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            out[e / 2] = bf16x2(fma2(ff, pair(x[e], x[e + 1]), mul2(ss, pair(y[e], y[e + 1]))));
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[j / 8 + e] = make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------------- V'
+    uint32_t g = 0;
+    for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
+      const uint32_t slot = g % kGates, s = g & 1;
+      // (rows of V past the end are zeros by then)
+      if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.v_full[s], g >> 1) ||
+          (g > 0 && !wait(&bars.ds_done[s ^ 1], (g - 1) >> 1)))
+        break;
+      const int e = tid - 512;
+      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox) + e;
+      uint4* to = reinterpret_cast<uint4*>(smem + M::kVP) + e;
+      const float* f = gates[slot].v + (e >> 3);
+      const f32x2 minus = pair(-1.0f, -1.0f);
+#pragma unroll 2
       for (int k = 0; k < 8; ++k) {
-        const uint4 w = v[128 * k];
+        const uint4 x = v[128 * k];
         const f32x2 ff = pair(f[16 * k], f[16 * k]);
-        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t r[4] = {x.x, x.y, x.z, x.w};
         uint32_t a[4], b[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const f32x2 y = mul2(ff, pair(__uint_as_float(r[x] << 16),
-                                        __uint_as_float(r[x] & 0xffff0000u)));
-          a[x] = bf16x2(y);
-          b[x] = bf16x2(fma2(minus, pair(__uint_as_float(a[x] << 16),
-                                         __uint_as_float(a[x] & 0xffff0000u)), y));
+        for (int c = 0; c < 4; ++c) {
+          const f32x2 y = mul2(ff, pair(__uint_as_float(r[c] << 16),
+                                        __uint_as_float(r[c] & 0xffff0000u)));
+          a[c] = bf16x2(y);
+          b[c] = bf16x2(fma2(minus, pair(__uint_as_float(a[c] << 16),
+                                         __uint_as_float(a[c] & 0xffff0000u)), y));
         }
         to[128 * k] = make_uint4(a[0], a[1], a[2], a[3]);
         to[128 * k + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
       }
       sm100::fence_async_smem();
       arrive(&bars.ready_d);
-      if (!OUT) arrive(&bars.gate_empty[slot]);
-      return true;
-    };
-    uint32_t g = 0;
-    Walk<OUT> w(p), ahead(p);
-    bool ok = !ahead.valid || weigh(0);
-    if (OUT) arrive(&bars.ready_q);  // (nothing to read before the first chunk)
-    for (; ok && w.valid; w.next(), ++g) {
-      if (ahead.valid) ahead.next();
-      if (ahead.valid && !weigh(g + 1)) break;
-      if (!OUT) continue;
-      if (!wait(&bars.o_done[g & 1], g >> 1)) break;
-      sm100::tc_fence_after();
-      const uint32_t slot = g % kGates;
-      const float f = gates[slot].row[i];
-      const f32x2 ff = pair(f, f), ss = pair(p.a.scale, p.a.scale);
-      const bool mine = i < w.rows();
-      uint4* dst = reinterpret_cast<uint4*>(
-          static_cast<__nv_bfloat16*>(p.a.out) +
-          ((w.it.row + w.t + i) * p.a.H + w.it.h) * p.a.dv + NV * w.it.half);
-#pragma unroll 1
-      for (int j = 0; j < NV; j += 16) {
-        float x[16], y[16];
-        sm100::tmem_ld16(tm + TM_O1 + j, x);
-        sm100::tmem_ld16(tm + TM_O2 + j, y);
-        sm100::tmem_wait_ld();
-        uint32_t out[8];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          out[e / 2] = bf16x2(fma2(ff, pair(x[e], x[e + 1]), mul2(ss, pair(y[e], y[e + 1]))));
-        if (mine) {
-          dst[j / 8] = make_uint4(out[0], out[1], out[2], out[3]);
-          dst[j / 8 + 1] = make_uint4(out[4], out[5], out[6], out[7]);
-        }
-      }
-      sm100::tc_fence_before();
-      arrive(&bars.ready_q);  // (of the next chunk)
       arrive(&bars.gate_empty[slot]);
     }
   }
