@@ -11,8 +11,8 @@
 // and walks their chunks, its state S in registers (fp32); Q K^T, P V, Q S and
 // K^T V' are tcgen05 products into tensor memory.  Warps have roles: one feeds
 // Q, K and V by TMA (two chunks ahead), one issues products, two take the
-// decays' sums, and four groups of four turn scores into P, carry the state,
-// write rows out and make V'.  Their loops are kept short: what the warps of a
+// decays' sums; a group of four turns scores into P, two groups carry half of the
+// state each and write half of the rows out, one makes V'.  Their loops are kept short: what the warps of a
 // scheduler run must fit its instruction cache (unrolled twice as far, the same
 // kernel took twice the time).  The products of a chunk run in the order
 // K^T V', Q S, the next chunk's scores, P V: what each waits for is made while the
@@ -178,12 +178,6 @@ struct Walk {
 __device__ __forceinline__ float fixed(int hi, int lo) {
   return fmaf((float)lo, 1.0f / 1099511627776.0f, (float)hi * (1.0f / 65536.0f));
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t ta, float (&v)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
-                 "=f"(v[6]), "=f"(v[7])
-               : "r"(ta));
-}
 __device__ __forceinline__ void tmem_st8(uint32_t ta, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
@@ -342,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::mbar_init(&bars.o_done[i], 1);
       sm100::mbar_init(&bars.p_full[i], 4);
     }
-    sm100::mbar_init(&bars.ready_d, 8);
+    sm100::mbar_init(&bars.ready_d, 12);
     sm100::mbar_init(&bars.ready_q, 8);
     for (int i = 0; i < kGates; ++i) {
       sm100::mbar_init(&bars.gate_full[i], 1);
-      sm100::mbar_init(&bars.gate_empty[i], OUT ? 16 : 8);
+      sm100::mbar_init(&bars.gate_empty[i], OUT ? 16 : 12);
     }
     sm100::mbar_init(&bars.drain, 1);
     sm100::fence_mbar_init();
@@ -566,7 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (L < C) {
         // rows past the end, which belong to others: zeros, whatever they hold
-        const uint32_t s = g & 1;
+        // (A wait tells a phase only from the one before, and this warp may be ahead of the copies
+        // of two chunks before in the same place: their chunk has to be over.)
+        const uint32_t s = g & 1, before = (g - 2) % kGates;
+        if (g >= 2 && !wait(&bars.gate_empty[before], (g - 2) / kGates)) break;
         if (!wait(&bars.qk_full[s], g >> 1) || !wait(&bars.v_full[s], g >> 1)) break;
         const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
@@ -647,133 +644,140 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(&bars.p_full[g & 1]);
         arrive(&bars.gate_empty[slot]);
       }
-  } else if (warp < 12) {
-    // -------------------------------------------------------------- the state
-    const int q = warp & 3;
+  } else if (warp < 16) {
+    // ------------- the state, and rows out: 32 value columns a group of four
+    const int q = warp & 3, c0 = 32 * ((warp - 8) >> 2), row = 32 * q + lane;
     // (a product of 64 rows has them in the first half of each warp's lanes)
-    const int i = DK == 128 ? 32 * q + lane : 16 * q + lane;
+    const int i = DK == 128 ? row : 16 * q + lane;
     const bool mine = DK == 128 || lane < 16;
-    const uint32_t tm = sm100::taddr(tmem, 32 * q, TM_DS);
-    f32x2 S[NV / 2];
-    uint32_t g = 0;
-    bool ok = true;
-    arrive(&bars.ready_d);  // (nothing to read before the first chunk)
-    const int ids = p.cols * p.a.H * p.halves;
-    for (int id = blockIdx.x; ok && id < ids; id += gridDim.x) {
-      Item it;
-      if (!locate<OUT>(p, id, it)) continue;
-      const int64_t size = (int64_t)DK * p.a.dv;
-      const int64_t in_head = (int64_t)i * p.a.dv + NV * it.half;
-      const float* from = it.first ? (p.a.init ? p.a.init + ((int64_t)it.n * p.a.H + it.h) * size
-                                               : nullptr)
-                          : OUT    ? p.states + ((int64_t)(it.col - 1) * p.a.H + it.h) * size
-                                   : nullptr;
-      float* to = !OUT      ? p.states + ((int64_t)it.col * p.a.H + it.h) * size
-                  : it.last ? (p.a.final_state
-                                   ? p.a.final_state + ((int64_t)it.n * p.a.H + it.h) * size
-                                   : nullptr)
-                            : nullptr;
+    const uint32_t tm = sm100::taddr(tmem, 32 * q, c0);
+    const f32x2 scale = pair(p.a.scale, p.a.scale);
+    f32x2 S[16];
+    float* to = nullptr;  // where the item's state goes
+    double all = 1.0;     // a segment's decay
+    Item it{};
+    int id = blockIdx.x, t = 0;
+    auto leave = [&]() {
+      if (to && mine)
 #pragma unroll
-      for (int j = 0; j < NV; j += 4) {
-        const float4 x = from && mine ? *reinterpret_cast<const float4*>(from + in_head + j)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[j / 2] = pair(x.x, x.y);
-        S[j / 2 + 1] = pair(x.z, x.w);
-      }
-      double all = 1.0;  // the segment's decay
-      for (int t = 0; t < it.len; t += C, ++g) {
-        if (OUT) {
-          // (the last Q S has read the operand)
-          ok = g == 0 || wait(&bars.qs_done[(g - 1) & 1], (g - 1) >> 1);
-          if (!ok) break;
-          if (mine) {
-#pragma unroll
-            for (int j = 0; j < NV; j += 8)
-              kda_tc::st16(smem + M::kS + kda_tc::mn_off(j, i, 1024), bf16x2(S[j / 2]),
-                           bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
-          }
-          sm100::fence_async_smem();
-          arrive(&bars.ready_q);
-        }
-        const uint32_t slot = g % kGates;
-        ok = wait(&bars.gate_full[slot], g / kGates) && wait(&bars.ds_done[g & 1], g >> 1);
-        if (!ok) break;
-        sm100::tc_fence_after();
-        const float2 f = gates[slot].gamma;
-        const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
-#pragma unroll
-        for (int j = 0; j < NV; j += 8) {
-          float x[8], y[8];
-          tmem_ld8(tm + j, x);
-          tmem_ld8(tm + NV + j, y);
-          sm100::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            f32x2& z = S[(j + e) / 2];
-            z = fma2(hi, z, fma2(lo, z, add2(pair(x[e], x[e + 1]), pair(y[e], y[e + 1]))));
-          }
-        }
-        if (!OUT) all *= (double)f.x + (double)f.y;
-        sm100::tc_fence_before();
-        arrive(&bars.ready_d);  // (of the next chunk)
-        arrive(&bars.gate_empty[slot]);
-      }
-      if (to && mine && ok) {
-#pragma unroll
-        for (int j = 0; j < NV; j += 4) {
+        for (int j = 0; j < 32; j += 4) {
           float4 x;
           unpair(S[j / 2], x.x, x.y);
           unpair(S[j / 2 + 1], x.z, x.w);
-          *reinterpret_cast<float4*>(to + in_head + j) = x;
+          *reinterpret_cast<float4*>(to + j) = x;
         }
-      }
-      if (!OUT && ok && it.half == 0 && tid == 256) {
+      if (!OUT && it.half == 0 && tid == 256) {
         const float hi = (float)all;
         p.gammas[(int64_t)it.col * p.a.H + it.h] = make_float2(hi, (float)(all - (double)hi));
       }
+    };
+    // the next item with tokens, from id on: its entry state (an empty sequence's state passes)
+    auto enter = [&]() -> bool {
+      const int ids = p.cols * p.a.H * p.halves;
+      for (; id < ids; id += gridDim.x) {
+        Item x;
+        if (!locate<OUT>(p, id, x)) continue;
+        it = x;
+        const int64_t size = (int64_t)DK * p.a.dv, unit = (int64_t)it.n * p.a.H + it.h;
+        const int64_t in = (int64_t)i * p.a.dv + NV * it.half + c0;
+        const int64_t col = (int64_t)it.col * p.a.H + it.h;
+        const float* from = it.first ? (p.a.init ? p.a.init + unit * size : nullptr)
+                            : OUT    ? p.states + (col - p.a.H) * size
+                                     : nullptr;
+        to = !OUT      ? p.states + col * size
+             : it.last ? (p.a.final_state ? p.a.final_state + unit * size : nullptr)
+                       : nullptr;
+        if (to) to += in;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 x = from && mine ? *reinterpret_cast<const float4*>(from + in + j)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+          S[j / 2] = pair(x.x, x.y);
+          S[j / 2 + 1] = pair(x.z, x.w);
+        }
+        t = 0;
+        all = 1.0;
+        if (it.len > 0) return true;
+        leave();
+      }
+      return false;
+    };
+    auto operand = [&]() {
+      if (mine)
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+          kda_tc::st16(smem + M::kS + kda_tc::mn_off(c0 + j, i, 1024), bf16x2(S[j / 2]),
+                       bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
+      sm100::fence_async_smem();
+    };
+    bool more = enter();
+    arrive(&bars.ready_d);  // (nothing to read before the first chunk)
+    if (OUT && more) {
+      operand();
+      arrive(&bars.ready_q);
     }
-  } else if (warp < 16) {
-    // ----------------------------------------------------------- rows go out
-    const int q = warp & 3, i = 32 * q + lane;
-    const uint32_t tm = sm100::taddr(tmem, 32 * q, 0);
-    uint32_t g = 0;
-    if (OUT) {
-      arrive(&bars.ready_q);  // (nothing to read before the first chunk)
-      for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
-        const uint32_t slot = g % kGates;
-        if (!wait(&bars.gate_full[slot], g / kGates)) break;
-        const float f = gates[slot].row[i];
-        const f32x2 ff = pair(f, f), ss = pair(p.a.scale, p.a.scale);
-        arrive(&bars.gate_empty[slot]);
-        const bool mine = i < w.rows();
-        uint4* dst = reinterpret_cast<uint4*>(
-            static_cast<__nv_bfloat16*>(p.a.out) +
-            ((w.it.row + w.t + i) * p.a.H + w.it.h) * p.a.dv + NV * w.it.half);
-        if (!wait(&bars.o_done[g & 1], g >> 1)) break;
+    for (uint32_t g = 0; more; ++g) {
+      const uint32_t slot = g % kGates, s = g & 1;
+      if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.ds_done[s], g >> 1)) break;
+      sm100::tc_fence_after();
+      const float2 f = gates[slot].gamma;
+      const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
+#pragma unroll
+      for (int j = 0; j < 32; j += 16) {
+        float x[16], y[16];
+        sm100::tmem_ld16(tm + TM_DS + j, x);
+        sm100::tmem_ld16(tm + TM_DS + NV + j, y);
+        sm100::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          f32x2& z = S[(j + e) / 2];
+          z = fma2(hi, z, fma2(lo, z, add2(pair(x[e], x[e + 1]), pair(y[e], y[e + 1]))));
+        }
+      }
+      if (!OUT) all *= (double)f.x + (double)f.y;
+      sm100::tc_fence_before();
+      arrive(&bars.ready_d);  // (of the next chunk)
+      // this chunk's rows go out below; the state goes on first
+      const bool live = row < it.len - t;
+      uint4* dst = reinterpret_cast<uint4*>(
+          static_cast<__nv_bfloat16*>(p.a.out) +
+          ((it.row + t + row) * p.a.H + it.h) * p.a.dv + NV * it.half + c0);
+      t += C;
+      if (t >= it.len) {
+        leave();
+        id += gridDim.x;
+        more = enter();
+      }
+      if (OUT) {
+        if (more) {
+          if (!wait(&bars.qs_done[s], g >> 1)) break;
+          operand();
+        }
+        const float w = gates[slot].row[row];
+        const f32x2 ww = pair(w, w);
+        if (!wait(&bars.o_done[s], g >> 1)) break;
         sm100::tc_fence_after();
 #pragma unroll 1
-        for (int j = 0; j < NV; j += 32) {
-          float x[32], y[32];
-          sm100::tmem_ld16(tm + TM_O1 + j, *reinterpret_cast<float(*)[16]>(x));
-          sm100::tmem_ld16(tm + TM_O2 + j, *reinterpret_cast<float(*)[16]>(y));
-          sm100::tmem_ld16(tm + TM_O1 + j + 16, *reinterpret_cast<float(*)[16]>(x + 16));
-          sm100::tmem_ld16(tm + TM_O2 + j + 16, *reinterpret_cast<float(*)[16]>(y + 16));
+        for (int j = 0; j < 32; j += 16) {
+          float x[16], y[16];
+          sm100::tmem_ld16(tm + TM_O1 + j, x);
+          sm100::tmem_ld16(tm + TM_O2 + j, y);
           sm100::tmem_wait_ld();
-          if (j == NV - 32) {
+          if (j > 0 && more) {
             sm100::tc_fence_before();
             arrive(&bars.ready_q);  // (of the next chunk)
           }
-          uint32_t out[16];
+          uint32_t out[8];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            out[e / 2] = bf16x2(fma2(ff, pair(x[e], x[e + 1]), mul2(ss, pair(y[e], y[e + 1]))));
-          if (mine) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[j / 8 + e] = make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
+          for (int e = 0; e < 16; e += 2)
+            out[e / 2] = bf16x2(fma2(ww, pair(x[e], x[e + 1]), mul2(scale, pair(y[e], y[e + 1]))));
+          if (live) {
+            dst[j / 8] = make_uint4(out[0], out[1], out[2], out[3]);
+            dst[j / 8 + 1] = make_uint4(out[4], out[5], out[6], out[7]);
           }
         }
       }
+      arrive(&bars.gate_empty[slot]);
     }
   } else {
     // ---------------------------------------------------------------------- V'

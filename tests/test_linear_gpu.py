@@ -152,6 +152,19 @@ def test_a_sequence_of_nan_stays_alone():
     assert torch.equal(state[::2], ws[::2]) and not state[1].isfinite().any()
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
+def test_short_and_ragged_ones_in_turn(dk, dv):
+    # hundreds of sequences that end inside a chunk, many on each SM, whatever the warps' pace
+    lens = [1 + (i * 7919) % 401 for i in range(400)]
+    x = made(1, sum(lens), 3, 1, dk, dv, N=len(lens), seed=3)
+    out, state = check(x, lens)
+    cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    for _ in range(30):
+        torch.cuda.synchronize()
+        again = pkg.linear_attend(**x, cu_seqlens=cu, scale=0.3)
+        assert torch.equal(again[0], out) and torch.equal(again[1], state)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_decays_at_the_ends(dtype):
     # nothing forgotten, everything forgotten at single tokens, factors that vanish in 32 bits, values above 0
