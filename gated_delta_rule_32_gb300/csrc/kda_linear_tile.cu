@@ -9,15 +9,14 @@
 //
 // A CTA takes items (a sequence or a segment of one, a head, 64 value columns)
 // and walks their chunks, its state S in registers (fp32); Q K^T, P V, Q S and
-// K^T V' are tcgen05 products into tensor memory.  Warps have roles: one feeds
-// Q, K and V by TMA (two chunks ahead), one issues products, two take the
-// decays' sums; a group of four turns scores into P, two groups carry half of the
-// state each and write half of the rows out, one makes V'.  Their loops are kept short: what the warps of a
-// scheduler run must fit its instruction cache (unrolled twice as far, the same
-// kernel took twice the time).  The products of a chunk run in the order
-// K^T V', Q S, the next chunk's scores, P V: what each waits for is made while the
-// others run, and K, Q and V are let go of early enough for the copies of two
-// chunks on.
+// K^T V' are tcgen05 products into tensor memory.  One warp feeds Q, K and V by
+// TMA (two chunks ahead), one issues products, two take the decays' sums, and
+// sixteen do the same work side by side, each a quarter of the rows and a fourth
+// of the columns: V', S and its operand, P, O.  The products of a chunk run in
+// the order K^T V', Q S, the next chunk's scores, P V; while each runs, the
+// sixteen work on what the one before it left.  (With groups of warps for P, S,
+// V' and O the same work took 1.5 to 2 times as long: four kinds of loops on
+// each scheduler do not fit its instruction caches.)
 //
 // Rounding: P and the state as an operand enter as bf16; rows of Q keep their
 // bits, e^G being applied to the product.  The state itself is summed from V'
@@ -45,7 +44,9 @@ constexpr int C = 128;          // tokens of a chunk
 constexpr int NV = 64;          // value columns of a CTA
 constexpr int kThreads = 640;
 constexpr int kGates = 4;
-constexpr uint32_t TM_O1 = 256, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
+// tensor memory: scores, P by stage, Q S, P V, K^T V' of V's two parts
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_O1 = 256, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
+constexpr int kWorkers = kThreads / 32 - 4;
 
 struct TileArgs {
   LinearArgs a;
@@ -59,24 +60,20 @@ struct TileArgs {
 
 struct alignas(16) Gate {
   float rel[C];    // G_j - G_b, b the last token of j's 32 (sums of log2-decays)
-  float col[C];    // 2^(G_b - G_j)
   float row[C];    // scale * 2^G_i
   float v[C];      // 2^(E - G_j)
   int2 end[4];     // G of the last token of each 32, in units of 2^-16 and 2^-40
   float2 gamma;    // 2^E in two parts
 };
 
-// [2]: by a chunk's stage.  A phase has to be seen by all that wait for it before
-// the next one of the same barrier can end: each of these is followed, before its
-// next phase, by something that they all have a part in.
 struct Bars {
   uint64_t qk_full[2], v_full[2];    // copies have landed
   uint64_t ds_done[2];               // K^T V' is there: V' and K are free
   uint64_t qs_done[2];               // Q S is there: Q and S's operand are free
-  uint64_t s_done[2];                // the scores are there
   uint64_t o_done[2];                // O is there: V and P are free
+  uint64_t s_done;                   // the scores are there
   uint64_t ready_d, ready_q;         // V' is made, K^T V' read; S's operand made, O read
-  uint64_t p_full[2];
+  uint64_t p_full;                   // P is made, the scores read
   uint64_t gate_full[kGates], gate_empty[kGates], drain;
 };
 
@@ -332,15 +329,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::mbar_init(&bars.v_full[i], 1);
       sm100::mbar_init(&bars.ds_done[i], 1);
       sm100::mbar_init(&bars.qs_done[i], 1);
-      sm100::mbar_init(&bars.s_done[i], 1);
       sm100::mbar_init(&bars.o_done[i], 1);
-      sm100::mbar_init(&bars.p_full[i], 4);
     }
-    sm100::mbar_init(&bars.ready_d, 12);
-    sm100::mbar_init(&bars.ready_q, 8);
+    sm100::mbar_init(&bars.s_done, 1);
+    sm100::mbar_init(&bars.ready_d, kWorkers);
+    sm100::mbar_init(&bars.ready_q, kWorkers);
+    sm100::mbar_init(&bars.p_full, kWorkers);
     for (int i = 0; i < kGates; ++i) {
       sm100::mbar_init(&bars.gate_full[i], 1);
-      sm100::mbar_init(&bars.gate_empty[i], OUT ? 16 : 12);
+      sm100::mbar_init(&bars.gate_empty[i], kWorkers);
     }
     sm100::mbar_init(&bars.drain, 1);
     sm100::fence_mbar_init();
@@ -426,9 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto scores = [&](uint32_t s) {
 #pragma unroll
       for (int b = 0; b < DK / 64; ++b)
-        mma4_ss<2, 2>(C * s, dq + s * kTile16 + b * kBox16, dk + s * kTile16 + b * kBox16, hi, hi,
+        mma4_ss<2, 2>(TM_S, dq + s * kTile16 + b * kBox16, dk + s * kTile16 + b * kBox16, hi, hi,
                       id_s, b, one);
-      commit(&bars.s_done[s], one);
+      commit(&bars.s_done, one);
     };
     uint32_t g = 0;
     Walk<OUT> w(p);
@@ -457,17 +454,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma4_ss<2, 128>(TM_O1, dq + s * kTile16 + b * kBox16, dst + 512 * b, hi, st_hi, id_q, b,
                           one);
         commit(&bars.qs_done[s], one);
-        if (next) {
-          // the next chunk's scores take the place of the last one's P (which O's readers saw used)
-          if (!all(wait(&bars.qk_full[s ^ 1], (g + 1) >> 1))) return false;
-          sm100::tc_fence_after();
-          scores(s ^ 1);
-        }
-        if (!all(wait(&bars.p_full[s], g >> 1))) return false;
+        if (!all(wait(&bars.p_full, g) && (!next || wait(&bars.qk_full[s ^ 1], (g + 1) >> 1))))
+          return false;
         sm100::tc_fence_after();
+        if (next) scores(s ^ 1);
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k)
-          mma4_ts<128>(TM_O2, C * s + 32 * k, dv + s * kBox16 + 512 * k, hi, id_q, k, one);
+          mma4_ts<128>(TM_O2, TM_P + 64 * s + 32 * k, dv + s * kBox16 + 512 * k, hi, id_q, k, one);
         commit(&bars.o_done[s], one);
       }
       ++g;
@@ -530,13 +523,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bad = __ballot_sync(~0u, nan != 0);
       if (use > 0 && !wait(&bars.gate_empty[slot], use - 1)) break;
       Gate& gt = gates[slot];
-      float rel[4], col[4], row[4], v[4];
+      float rel[4], row[4], v[4];
       const float none = __int_as_float(0x7fffffff);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int h = pre_hi + hi[e], l = pre_lo + lo[e];
         rel[e] = fixed(h - blk_hi, l - blk_lo);
-        col[e] = ex2(-rel[e]);
         row[e] = p.a.scale * ex2(fixed(h, l));
         v[e] = ex2(fixed(end_hi - h, end_lo - l));
         if (bad) {
@@ -546,7 +538,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       reinterpret_cast<float4*>(gt.rel)[lane] = make_float4(rel[0], rel[1], rel[2], rel[3]);
-      reinterpret_cast<float4*>(gt.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
       reinterpret_cast<float4*>(gt.row)[lane] = make_float4(row[0], row[1], row[2], row[3]);
       reinterpret_cast<float4*>(gt.v)[lane] = make_float4(v[0], v[1], v[2], v[3]);
       if ((lane & 7) == 7) gt.end[lane >> 3] = make_int2(blk_hi, blk_lo);
@@ -577,82 +568,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       arrive(&bars.gate_full[slot]);
     }
-  } else if (warp < 8) {
-    // ------------------------------------------------------- scores become P
-    const int q = warp & 3, i = 32 * q + lane;
-    const uint32_t tm = sm100::taddr(tmem, 32 * q, 0);
-    uint32_t g = 0;
-    if (OUT)
-      for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
-        const uint32_t slot = g % kGates, base = tm + C * (g & 1);
-        if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.s_done[g & 1], g >> 1)) break;
-        sm100::tc_fence_after();
-        const Gate& gt = gates[slot];
-        const float mine = gt.rel[i];
-        const int2 e = gt.end[q];
-        // 16 columns at a time: those below the diagonal's 32, the diagonal's, the rest
-#pragma unroll 1
-        for (int b = 0; b < 2 * q; ++b) {
-          float x[16];
-          uint32_t out[8];
-          sm100::tmem_ld16(base + 16 * b, x);
-          const int2 o = gt.end[b >> 1];
-          const float f = ex2(mine + fixed(e.x - o.x, e.y - o.y));
-          const f32x2 ff = pair(f, f);
-          const float4* c = reinterpret_cast<const float4*>(gt.col + 16 * b);
-          f32x2 w[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 y = c[j];
-            w[2 * j] = mul2(ff, pair(y.x, y.y));
-            w[2 * j + 1] = mul2(ff, pair(y.z, y.w));
-          }
-          sm100::tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) out[j] = bf16x2(mul2(w[j], pair(x[2 * j], x[2 * j + 1])));
-          tmem_st8(base + 8 * b, out);
-        }
-#pragma unroll 1
-        for (int b = 0; b < 32; b += 16) {
-          float x[16], w[16];
-          uint32_t out[8];
-          sm100::tmem_ld16(base + 32 * q + b, x);
-          const float4* c = reinterpret_cast<const float4*>(gt.rel + 32 * q + b);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 y = c[j];
-            w[4 * j] = ex2(mine - y.x);
-            w[4 * j + 1] = ex2(mine - y.y);
-            w[4 * j + 2] = ex2(mine - y.z);
-            w[4 * j + 3] = ex2(mine - y.w);
-          }
-          sm100::tmem_wait_ld();
-          const int last = lane - b;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = j <= last ? x[j] * w[j] : 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) out[j] = sm100::pack_bf16x2(x[2 * j], x[2 * j + 1]);
-          tmem_st8(base + 16 * q + (b >> 1), out);
-        }
-#pragma unroll 1
-        for (int b = q + 1; b < 4; ++b) {
-          const uint32_t zero[16] = {};
-          sm100::tmem_st16(base + 16 * b, zero);
-        }
-        sm100::tmem_wait_st();
-        sm100::tc_fence_before();
-        arrive(&bars.p_full[g & 1]);
-        arrive(&bars.gate_empty[slot]);
-      }
-  } else if (warp < 16) {
-    // ------------- the state, and rows out: 32 value columns a group of four
-    const int q = warp & 3, c0 = 32 * ((warp - 8) >> 2), row = 32 * q + lane;
+  } else {
+    // ------ sixteen warps that all do a quarter's fourth of V', S, P and O in turn
+    const int q = warp & 3, part = (warp >> 2) - 1, row = 32 * q + lane, e0 = tid - 128;
+    const int c0 = 16 * part;  // value columns c0 .. c0 + 15 of S and O
     // (a product of 64 rows has them in the first half of each warp's lanes)
     const int i = DK == 128 ? row : 16 * q + lane;
     const bool mine = DK == 128 || lane < 16;
-    const uint32_t tm = sm100::taddr(tmem, 32 * q, c0);
-    const f32x2 scale = pair(p.a.scale, p.a.scale);
-    f32x2 S[16];
+    const uint32_t tm = sm100::taddr(tmem, 32 * q, 0);
+    f32x2 S[8];
     float* to = nullptr;  // where the item's state goes
     double all = 1.0;     // a segment's decay
     Item it{};
@@ -660,13 +584,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto leave = [&]() {
       if (to && mine)
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 4) {
           float4 x;
           unpair(S[j / 2], x.x, x.y);
           unpair(S[j / 2 + 1], x.z, x.w);
           *reinterpret_cast<float4*>(to + j) = x;
         }
-      if (!OUT && it.half == 0 && tid == 256) {
+      if (!OUT && it.half == 0 && e0 == 0) {
         const float hi = (float)all;
         p.gammas[(int64_t)it.col * p.a.H + it.h] = make_float2(hi, (float)(all - (double)hi));
       }
@@ -689,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : nullptr;
         if (to) to += in;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 4) {
           const float4 x = from && mine ? *reinterpret_cast<const float4*>(from + in + j)
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
           S[j / 2] = pair(x.x, x.y);
@@ -702,117 +626,139 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return false;
     };
-    auto operand = [&]() {
-      if (mine)
-#pragma unroll
-        for (int j = 0; j < 32; j += 8)
-          kda_tc::st16(smem + M::kS + kda_tc::mn_off(c0 + j, i, 1024), bf16x2(S[j / 2]),
-                       bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
-      sm100::fence_async_smem();
-    };
-    bool more = enter();
-    arrive(&bars.ready_d);  // (nothing to read before the first chunk)
-    if (OUT && more) {
-      operand();
-      arrive(&bars.ready_q);
-    }
-    for (uint32_t g = 0; more; ++g) {
-      const uint32_t slot = g % kGates, s = g & 1;
-      if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.ds_done[s], g >> 1)) break;
-      sm100::tc_fence_after();
-      const float2 f = gates[slot].gamma;
-      const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
-#pragma unroll
-      for (int j = 0; j < 32; j += 16) {
-        float x[16], y[16];
-        sm100::tmem_ld16(tm + TM_DS + j, x);
-        sm100::tmem_ld16(tm + TM_DS + NV + j, y);
-        sm100::tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          f32x2& z = S[(j + e) / 2];
-          z = fma2(hi, z, fma2(lo, z, add2(pair(x[e], x[e + 1]), pair(y[e], y[e + 1]))));
-        }
-      }
-      if (!OUT) all *= (double)f.x + (double)f.y;
-      sm100::tc_fence_before();
-      arrive(&bars.ready_d);  // (of the next chunk)
-      // this chunk's rows go out below; the state goes on first
+    // A chunk g is begun and ended by the same code, one chunk apart: chunk g's K^T V' and O
+    // (`old`), chunk g + 1's V', operand of S and P (`more`).
+    bool more = enter(), old = false;
+    for (uint32_t g = ~0u; more || old; ++g) {
+      const uint32_t s = g & 1, slot = g % kGates, next = (g + 1) % kGates;
+      const int64_t at = it.row + t + row;  // this chunk's rows go out last
       const bool live = row < it.len - t;
-      uint4* dst = reinterpret_cast<uint4*>(
-          static_cast<__nv_bfloat16*>(p.a.out) +
-          ((it.row + t + row) * p.a.H + it.h) * p.a.dv + NV * it.half + c0);
-      t += C;
-      if (t >= it.len) {
-        leave();
-        id += gridDim.x;
-        more = enter();
-      }
-      if (OUT) {
-        if (more) {
-          if (!wait(&bars.qs_done[s], g >> 1)) break;
-          operand();
-        }
-        const float w = gates[slot].row[row];
-        const f32x2 ww = pair(w, w);
-        if (!wait(&bars.o_done[s], g >> 1)) break;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) +
+                                            (at * p.a.H + it.h) * p.a.dv + NV * it.half + c0);
+      if (old) {
+        if (!wait(&bars.ds_done[s], g >> 1)) break;
         sm100::tc_fence_after();
-#pragma unroll 1
-        for (int j = 0; j < 32; j += 16) {
-          float x[16], y[16];
-          sm100::tmem_ld16(tm + TM_O1 + j, x);
-          sm100::tmem_ld16(tm + TM_O2 + j, y);
-          sm100::tmem_wait_ld();
-          if (j > 0 && more) {
-            sm100::tc_fence_before();
-            arrive(&bars.ready_q);  // (of the next chunk)
+        float x[16], y[16];
+        sm100::tmem_ld16(tm + TM_DS + c0, x);
+        sm100::tmem_ld16(tm + TM_DS + NV + c0, y);
+        const float2 f = gates[slot].gamma;
+        const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
+        sm100::tmem_wait_ld();
+        sm100::tc_fence_before();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          S[e] = fma2(hi, S[e], fma2(lo, S[e], add2(pair(x[2 * e], x[2 * e + 1]),
+                                                    pair(y[2 * e], y[2 * e + 1]))));
+        if (!OUT) all *= (double)f.x + (double)f.y;
+        t += C;
+        if (t >= it.len) {
+          leave();
+          id += gridDim.x;
+          more = enter();
+        }
+      }
+      if (more) {
+        // V', two pieces of 16 bytes a thread (rows of V past the end are zeros by then)
+        if (!wait(&bars.gate_full[next], (g + 1) / kGates) ||
+            !wait(&bars.v_full[s ^ 1], (g + 1) >> 1))
+          break;
+        const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + (s ^ 1) * M::kBox) + e0;
+        uint4* to = reinterpret_cast<uint4*>(smem + M::kVP) + e0;
+        const f32x2 minus = pair(-1.0f, -1.0f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint4 x = v[512 * k];
+          const float f = gates[next].v[(e0 >> 3) + 64 * k];
+          const f32x2 ff = pair(f, f);
+          const uint32_t r[4] = {x.x, x.y, x.z, x.w};
+          uint32_t a[4], b[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const f32x2 y = mul2(ff, pair(__uint_as_float(r[c] << 16),
+                                          __uint_as_float(r[c] & 0xffff0000u)));
+            a[c] = bf16x2(y);
+            b[c] = bf16x2(fma2(minus, pair(__uint_as_float(a[c] << 16),
+                                           __uint_as_float(a[c] & 0xffff0000u)), y));
           }
+          to[512 * k] = make_uint4(a[0], a[1], a[2], a[3]);
+          to[512 * k + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+        sm100::fence_async_smem();
+        arrive(&bars.ready_d);
+        if (OUT) {
+          // the state as an operand
+          if (old && !wait(&bars.qs_done[s], g >> 1)) break;
+          if (mine)
+#pragma unroll
+            for (int j = 0; j < 16; j += 8)
+              kda_tc::st16(smem + M::kS + kda_tc::mn_off(c0 + j, i, 1024), bf16x2(S[j / 2]),
+                           bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
+          sm100::fence_async_smem();
+          if (!old) arrive(&bars.ready_q);  // (no O to read yet)
+          // P, 16 columns at a time: columns 16 b of the row's 32 (2 q + 1) are on the diagonal
+          if (!wait(&bars.s_done, g + 1)) break;
+          sm100::tc_fence_after();
+          const Gate& gt = gates[next];
+#pragma unroll 1
+          for (int b = part; b < 8; b += 4) {
+            uint32_t out[8] = {};
+            if (b < 2 * q + 2) {
+              float x[16];
+              sm100::tmem_ld16(tm + TM_S + 16 * b, x);
+              const int2 e = gt.end[q], o = gt.end[b >> 1];
+              const float from = gt.rel[row] + fixed(e.x - o.x, e.y - o.y);
+              const float4* c = reinterpret_cast<const float4*>(gt.rel + 16 * b);
+              const int last = row - 16 * b;
+              float w[16];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float4 y = c[j];
+                w[4 * j] = ex2(from - y.x);
+                w[4 * j + 1] = ex2(from - y.y);
+                w[4 * j + 2] = ex2(from - y.z);
+                w[4 * j + 3] = ex2(from - y.w);
+              }
+              sm100::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = j <= last ? x[j] * w[j] : 0.0f;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) out[j] = sm100::pack_bf16x2(x[2 * j], x[2 * j + 1]);
+            }
+            tmem_st8(tm + TM_P + 64 * (s ^ 1) + 8 * b, out);
+          }
+          sm100::tmem_wait_st();
+          sm100::tc_fence_before();
+          arrive(&bars.p_full);
+        }
+      }
+      if (old) {
+        if (OUT) {
+          const float f = gates[slot].row[row];
+          const f32x2 ff = pair(f, f), scale = pair(p.a.scale, p.a.scale);
+          if (!wait(&bars.o_done[s], g >> 1)) break;
+          sm100::tc_fence_after();
+          float x[16], y[16];
+          sm100::tmem_ld16(tm + TM_O1 + c0, x);
+          sm100::tmem_ld16(tm + TM_O2 + c0, y);
+          sm100::tmem_wait_ld();
+          sm100::tc_fence_before();
+          // (before the stores: an arrival right behind them would wait for them)
+          if (more) arrive(&bars.ready_q);
+          arrive(&bars.gate_empty[slot]);
           uint32_t out[8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            out[e / 2] = bf16x2(fma2(ww, pair(x[e], x[e + 1]), mul2(scale, pair(y[e], y[e + 1]))));
+          for (int e = 0; e < 8; ++e)
+            out[e] = bf16x2(fma2(ff, pair(x[2 * e], x[2 * e + 1]),
+                                 mul2(scale, pair(y[2 * e], y[2 * e + 1]))));
           if (live) {
-            dst[j / 8] = make_uint4(out[0], out[1], out[2], out[3]);
-            dst[j / 8 + 1] = make_uint4(out[4], out[5], out[6], out[7]);
+            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
           }
+        } else {
+          arrive(&bars.gate_empty[slot]);
         }
       }
-      arrive(&bars.gate_empty[slot]);
-    }
-  } else {
-    // ---------------------------------------------------------------------- V'
-    uint32_t g = 0;
-    for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
-      const uint32_t slot = g % kGates, s = g & 1;
-      // (rows of V past the end are zeros by then)
-      if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.v_full[s], g >> 1) ||
-          (g > 0 && !wait(&bars.ds_done[s ^ 1], (g - 1) >> 1)))
-        break;
-      const int e = tid - 512;
-      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox) + e;
-      uint4* to = reinterpret_cast<uint4*>(smem + M::kVP) + e;
-      const float* f = gates[slot].v + (e >> 3);
-      const f32x2 minus = pair(-1.0f, -1.0f);
-#pragma unroll 2
-      for (int k = 0; k < 8; ++k) {
-        const uint4 x = v[128 * k];
-        const f32x2 ff = pair(f[16 * k], f[16 * k]);
-        const uint32_t r[4] = {x.x, x.y, x.z, x.w};
-        uint32_t a[4], b[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const f32x2 y = mul2(ff, pair(__uint_as_float(r[c] << 16),
-                                        __uint_as_float(r[c] & 0xffff0000u)));
-          a[c] = bf16x2(y);
-          b[c] = bf16x2(fma2(minus, pair(__uint_as_float(a[c] << 16),
-                                         __uint_as_float(a[c] & 0xffff0000u)), y));
-        }
-        to[128 * k] = make_uint4(a[0], a[1], a[2], a[3]);
-        to[128 * k + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
-      }
-      sm100::fence_async_smem();
-      arrive(&bars.ready_d);
-      arrive(&bars.gate_empty[slot]);
+      old = more;
     }
   }
   __syncwarp();

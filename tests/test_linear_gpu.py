@@ -155,8 +155,8 @@ def test_a_sequence_of_nan_stays_alone():
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
 def test_short_and_ragged_ones_in_turn(dk, dv):
     # hundreds of sequences that end inside a chunk, many on each SM, whatever the warps' pace
-    lens = [1 + (i * 7919) % 401 for i in range(400)]
-    x = made(1, sum(lens), 3, 1, dk, dv, N=len(lens), seed=3)
+    lens = [1 + (i * 7919) % 301 for i in range(100)]
+    x = made(1, sum(lens), 8, 2, dk, dv, N=len(lens), seed=3)
     out, state = check(x, lens)
     cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
     for _ in range(30):
