@@ -59,7 +59,8 @@ struct TileArgs {
 };
 
 struct alignas(16) Gate {
-  float rel[C];    // G_j - G_b, b the last token of j's 32 (sums of log2-decays)
+  float back[C];   // G_b - G_j, b the last token of j's 32 (sums of log2-decays)
+  float col[C];    // 2^(G_b - G_j)
   float row[C];    // scale * 2^G_i
   float v[C];      // 2^(E - G_j)
   int2 end[4];     // G of the last token of each 32, in units of 2^-16 and 2^-40
@@ -523,21 +524,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bad = __ballot_sync(~0u, nan != 0);
       if (use > 0 && !wait(&bars.gate_empty[slot], use - 1)) break;
       Gate& gt = gates[slot];
-      float rel[4], row[4], v[4];
+      float back[4], col[4], row[4], v[4];
       const float none = __int_as_float(0x7fffffff);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int h = pre_hi + hi[e], l = pre_lo + lo[e];
-        rel[e] = fixed(h - blk_hi, l - blk_lo);
+        back[e] = fixed(blk_hi - h, blk_lo - l);
+        col[e] = ex2(back[e]);
         row[e] = p.a.scale * ex2(fixed(h, l));
         v[e] = ex2(fixed(end_hi - h, end_lo - l));
         if (bad) {
           // (rare) no sum for tokens from the first NaN on, and no weight to the chunk's end
-          if ((bad & ((1u << lane) - 1)) || (nan & ((2u << e) - 1))) rel[e] = row[e] = none;
+          if ((bad & ((1u << lane) - 1)) || (nan & ((2u << e) - 1))) back[e] = row[e] = none;
           v[e] = none;
         }
       }
-      reinterpret_cast<float4*>(gt.rel)[lane] = make_float4(rel[0], rel[1], rel[2], rel[3]);
+      reinterpret_cast<float4*>(gt.back)[lane] = make_float4(back[0], back[1], back[2], back[3]);
+      reinterpret_cast<float4*>(gt.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
       reinterpret_cast<float4*>(gt.row)[lane] = make_float4(row[0], row[1], row[2], row[3]);
       reinterpret_cast<float4*>(gt.v)[lane] = make_float4(v[0], v[1], v[2], v[3]);
       if ((lane & 7) == 7) gt.end[lane >> 3] = make_int2(blk_hi, blk_lo);
@@ -570,8 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------ sixteen warps that all do a quarter's fourth of V', S, P and O in turn
-    const int q = warp & 3, part = (warp >> 2) - 1, row = 32 * q + lane, e0 = tid - 128;
+    const int q = warp & 3, part = (warp >> 2) - 1, row = 32 * q + lane;
     const int c0 = 16 * part;  // value columns c0 .. c0 + 15 of S and O
+    const int k0 = q == 0 ? 0 : 2 * q + 1, k1 = q == 3 ? 8 : 2 * q + 3;  // pieces of V'
     // (a product of 64 rows has them in the first half of each warp's lanes)
     const int i = DK == 128 ? row : 16 * q + lane;
     const bool mine = DK == 128 || lane < 16;
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unpair(S[j / 2 + 1], x.z, x.w);
           *reinterpret_cast<float4*>(to + j) = x;
         }
-      if (!OUT && it.half == 0 && e0 == 0) {
+      if (!OUT && it.half == 0 && tid == 128) {
         const float hi = (float)all;
         p.gammas[(int64_t)it.col * p.a.H + it.h] = make_float2(hi, (float)(all - (double)hi));
       }
@@ -658,17 +662,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (more) {
-        // V', two pieces of 16 bytes a thread (rows of V past the end are zeros by then)
+        // V', 16 bytes a thread at a time (rows of V past the end are zeros by then).  Warps of a
+        // quarter share a scheduler, and later quarters have more of P to make: they take 3, 2, 2
+        // and 1 of its eight pieces.
         if (!wait(&bars.gate_full[next], (g + 1) / kGates) ||
             !wait(&bars.v_full[s ^ 1], (g + 1) >> 1))
           break;
-        const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + (s ^ 1) * M::kBox) + e0;
-        uint4* to = reinterpret_cast<uint4*>(smem + M::kVP) + e0;
+        const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + (s ^ 1) * M::kBox);
+        uint4* to = reinterpret_cast<uint4*>(smem + M::kVP);
         const f32x2 minus = pair(-1.0f, -1.0f);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint4 x = v[512 * k];
-          const float f = gates[next].v[(e0 >> 3) + 64 * k];
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k) {
+          const int e = 128 * k + 32 * part + lane;
+          const uint4 x = v[e];
+          const float f = gates[next].v[e >> 3];
           const f32x2 ff = pair(f, f);
           const uint32_t r[4] = {x.x, x.y, x.z, x.w};
           uint32_t a[4], b[4];
@@ -680,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             b[c] = bf16x2(fma2(minus, pair(__uint_as_float(a[c] << 16),
                                            __uint_as_float(a[c] & 0xffff0000u)), y));
           }
-          to[512 * k] = make_uint4(a[0], a[1], a[2], a[3]);
-          to[512 * k + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
+          to[e] = make_uint4(a[0], a[1], a[2], a[3]);
+          to[e + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
         }
         sm100::fence_async_smem();
         arrive(&bars.ready_d);
@@ -695,34 +702,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                            bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
           sm100::fence_async_smem();
           if (!old) arrive(&bars.ready_q);  // (no O to read yet)
-          // P, 16 columns at a time: columns 16 b of the row's 32 (2 q + 1) are on the diagonal
+          // P, 16 columns at a time
           if (!wait(&bars.s_done, g + 1)) break;
           sm100::tc_fence_after();
           const Gate& gt = gates[next];
+          const float own = gt.back[row];
+          const int2 e = gt.end[q];
 #pragma unroll 1
           for (int b = part; b < 8; b += 4) {
             uint32_t out[8] = {};
             if (b < 2 * q + 2) {
               float x[16];
+              f32x2 w[8];
               sm100::tmem_ld16(tm + TM_S + 16 * b, x);
-              const int2 e = gt.end[q], o = gt.end[b >> 1];
-              const float from = gt.rel[row] + fixed(e.x - o.x, e.y - o.y);
-              const float4* c = reinterpret_cast<const float4*>(gt.rel + 16 * b);
-              const int last = row - 16 * b;
-              float w[16];
+              const bool below = b < 2 * q;  // (of the diagonal's 32 columns)
+              const int2 o = gt.end[b >> 1];
+              float f = fixed(e.x - o.x, e.y - o.y) - own;
+              if (below) f = ex2(f);
+              const f32x2 ff = pair(f, f);
+              const float4* c = reinterpret_cast<const float4*>((below ? gt.col : gt.back) + 16 * b);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const float4 y = c[j];
-                w[4 * j] = ex2(from - y.x);
-                w[4 * j + 1] = ex2(from - y.y);
-                w[4 * j + 2] = ex2(from - y.z);
-                w[4 * j + 3] = ex2(from - y.w);
+                w[2 * j] = pair(y.x, y.y);
+                w[2 * j + 1] = pair(y.z, y.w);
+              }
+              if (below) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = mul2(ff, w[j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  float u, v;
+                  unpair(add2(ff, w[j]), u, v);
+                  w[j] = pair(ex2(u), ex2(v));
+                }
               }
               sm100::tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = j <= last ? x[j] * w[j] : 0.0f;
+              for (int j = 0; j < 8; ++j) w[j] = mul2(w[j], pair(x[2 * j], x[2 * j + 1]));
+              if (!below) {
+                // (tokens to come are cleared, not multiplied by 0: they may be anything)
+                const int last = row - 16 * b;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) out[j] = sm100::pack_bf16x2(x[2 * j], x[2 * j + 1]);
+                for (int j = 0; j < 8; ++j) {
+                  float u, v;
+                  unpair(w[j], u, v);
+                  w[j] = pair(2 * j <= last ? u : 0.0f, 2 * j + 1 <= last ? v : 0.0f);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) out[j] = bf16x2(w[j]);
             }
             tmem_st8(tm + TM_P + 64 * (s ^ 1) + 8 * b, out);
           }
