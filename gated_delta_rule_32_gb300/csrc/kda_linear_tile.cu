@@ -580,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = DK == 128 ? row : 16 * q + lane;
     const bool mine = DK == 128 || lane < 16;
     const uint32_t tm = sm100::taddr(tmem, 32 * q, 0);
+    const bool whole = (reinterpret_cast<uint64_t>(p.a.out) & 31) == 0;
     f32x2 S[8];
     float* to = nullptr;  // where the item's state goes
     double all = 1.0;     // a segment's decay
@@ -781,8 +782,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             out[e] = bf16x2(fma2(ff, pair(x[2 * e], x[2 * e + 1]),
                                  mul2(scale, pair(y[2 * e], y[2 * e + 1]))));
           if (live) {
-            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+            // (32 rows' sectors are what a warp stores: once each, where out is aligned to them)
+            if (whole) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+                           "r"(out[0]), "r"(out[1]), "r"(out[2]), "r"(out[3]), "r"(out[4]),
+                           "r"(out[5]), "r"(out[6]), "r"(out[7])
+                           : "memory");
+            } else {
+              dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+              dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+            }
           }
         } else {
           arrive(&bars.gate_empty[slot]);
