@@ -44,6 +44,7 @@ constexpr int C = 128;          // tokens of a chunk
 constexpr int NV = 64;          // value columns of a CTA
 constexpr int kThreads = 640;
 constexpr int kGates = 4;
+constexpr int kOrdered = 1024;  // most sequences of a packed batch that are put in order
 // tensor memory: scores, P by stage, Q S, P V, K^T V' of V's two parts
 constexpr uint32_t TM_S = 0, TM_P = 128, TM_O1 = 256, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
 constexpr int kWorkers = kThreads / 32 - 4;
@@ -73,7 +74,8 @@ struct Bars {
   uint64_t qs_done[2];               // Q S is there: Q and S's operand are free
   uint64_t o_done[2];                // O is there: V and P are free
   uint64_t s_done;                   // the scores are there
-  uint64_t ready_d, ready_q;         // V' is made, K^T V' read; S's operand made, O read
+  uint64_t ready_d[2];               // V' is made, its product's place read
+  uint64_t ready_q;                  // S's operand is made, O read
   uint64_t p_full;                   // P is made, the scores read
   uint64_t gate_full[kGates], gate_empty[kGates], drain;
 };
@@ -87,8 +89,16 @@ struct Smem {
   static constexpr int kS = kVP + 2 * kBox;                // S as an operand
   static constexpr int kGate = kS + DK * NV * 2;
   static constexpr int kBars = kGate + kGates * (int)sizeof(Gate);
-  static constexpr int kBytes = kBars + (int)sizeof(Bars) + 16 + 1024;  // (and the alignment)
+  static constexpr int kOrder = kBars + (int)sizeof(Bars) + 16;
+  static constexpr int kBytes = kOrder + 2 * kOrdered + 1024;  // (and the alignment)
 };
+
+// Items go to the CTAs there and back: round by round, every other one from the
+// last CTA to the first, so that with the longest first all get about as much.
+__device__ __forceinline__ int following(int id) {
+  const int G = gridDim.x, round = id / G;
+  return (2 * round + 2) * G - 1 - id;
+}
 
 struct Item {
   int64_t row;  // first token row
@@ -100,7 +110,7 @@ struct Item {
 // Item `id` of the grid's; false: there is none of that number (packed columns
 // are as many as there can be), or nothing to do in this pass.
 template <bool OUT>
-__device__ __noinline__ bool locate(const TileArgs& p, int id, Item& it) {
+__device__ __noinline__ bool locate(const TileArgs& p, const uint16_t* order, int id, Item& it) {
   const int x = id / p.halves;
   it.half = id - x * p.halves;
   it.col = x / p.a.H;
@@ -115,7 +125,7 @@ __device__ __noinline__ bool locate(const TileArgs& p, int id, Item& it) {
     // segments, and at most one more
     int lo = 0, hi = p.a.N - 1;
     if (p.seg > p.a.T) {
-      lo = it.col;
+      lo = p.a.N <= kOrdered ? order[it.col] : it.col;
     } else {
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -124,7 +134,7 @@ __device__ __noinline__ bool locate(const TileArgs& p, int id, Item& it) {
       }
     }
     it.n = lo;
-    seg = it.col - (p.seg > p.a.T ? lo : p.a.cu[lo] / p.seg + lo);
+    seg = p.seg > p.a.T ? 0 : it.col - (p.a.cu[lo] / p.seg + lo);
   }
   int64_t row;
   int len;
@@ -143,22 +153,24 @@ __device__ __noinline__ bool locate(const TileArgs& p, int id, Item& it) {
 template <bool OUT>
 struct Walk {
   const TileArgs& p;
+  const uint16_t* order;
   int id, ids;
   Item it;
   int t;       // first token of the chunk in its item
   bool valid;
-  __device__ __forceinline__ explicit Walk(const TileArgs& args)
-      : p(args), id(blockIdx.x), ids(args.cols * args.a.H * args.halves) {
-    settle();
+  __device__ __forceinline__ Walk(const TileArgs& args, const uint16_t* ord, bool begin = true)
+      : p(args), order(ord), id(blockIdx.x), ids(args.cols * args.a.H * args.halves), t(0),
+        valid(false) {
+    if (begin) settle();
   }
   __device__ __forceinline__ bool find() {
     Item x;  // (the call's copy is in memory, this one's in registers)
-    const bool there = locate<OUT>(p, id, x);
+    const bool there = locate<OUT>(p, order, id, x);
     it = x;
     return there;
   }
   __device__ __forceinline__ void settle() {
-    for (; id < ids; id += gridDim.x)
+    for (; id < ids; id = following(id))
       if (find() && it.len > 0) break;
     valid = id < ids;
     t = 0;
@@ -166,7 +178,7 @@ struct Walk {
   __device__ __forceinline__ void next() {
     t += C;
     if (t < it.len) return;
-    id += gridDim.x;
+    id = following(id);
     settle();
   }
   __device__ __forceinline__ int rows() const { return it.len - t < C ? it.len - t : C; }
@@ -329,11 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::mbar_init(&bars.qk_full[i], OUT ? 2 : 1);
       sm100::mbar_init(&bars.v_full[i], 1);
       sm100::mbar_init(&bars.ds_done[i], 1);
+      sm100::mbar_init(&bars.ready_d[i], kWorkers);
       sm100::mbar_init(&bars.qs_done[i], 1);
       sm100::mbar_init(&bars.o_done[i], 1);
     }
     sm100::mbar_init(&bars.s_done, 1);
-    sm100::mbar_init(&bars.ready_d, kWorkers);
     sm100::mbar_init(&bars.ready_q, kWorkers);
     sm100::mbar_init(&bars.p_full, kWorkers);
     for (int i = 0; i < kGates; ++i) {
@@ -344,6 +356,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::fence_mbar_init();
     *s_abort = 0;
   }
+  // whole sequences of a packed batch: the longest first, equal ones in order.  (Lengths of malformed
+  // offsets are some numbers too: every sequence gets a place of its own.)
+  uint16_t* order = reinterpret_cast<uint16_t*>(smem + M::kOrder);
+  if (p.a.cu && p.seg > p.a.T && p.a.N <= kOrdered)
+    for (int n = tid; n < p.a.N; n += kThreads) {
+      const int len = p.a.cu[n + 1] - p.a.cu[n];
+      int rank = 0;
+      for (int m = 0; m < p.a.N; ++m) {
+        const int other = p.a.cu[m + 1] - p.a.cu[m];
+        rank += other > len || (other == len && m < n);
+      }
+      order[rank] = (uint16_t)n;
+    }
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
@@ -362,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------ Q, K and V come
     uint32_t g = 0;
-    for (Walk<OUT> w(p); w.valid; w.next(), ++g) {
+    for (Walk<OUT> w(p, order); w.valid; w.next(), ++g) {
       const uint32_t s = g & 1, use = g >> 1;
       const int row = (int)(w.it.row + w.t), hk = w.it.hk;
       // (in the order in which the products let go of them)
@@ -416,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at = (uint32_t)sm100::smem_desc(sm100::smem_u32(smem), M::kBox, 1024);
     const uint32_t hi = (uint32_t)(sm100::smem_desc_sw128(0, M::kBox, 1024) >> 32);
     const uint32_t dq = at + M::kQ / 16, dk = at + M::kK / 16, dv = at + M::kV / 16;
-    const uint32_t dvp = at + M::kVP / 16;
+    // (the first pass has V' and its product by stage, in places that only the full one uses)
+    const uint32_t dvp = at + M::kVP / 16, dvp1 = OUT ? dvp : at + M::kQ / 16;
     const uint64_t st = sm100::smem_desc(sm100::smem_u32(smem) + M::kS, 1024, 128);
     const uint32_t dst = (uint32_t)st, st_hi = (uint32_t)(st >> 32);
     // every thread takes the same way (and the compiler knows)
@@ -429,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit(&bars.s_done, one);
     };
     uint32_t g = 0;
-    Walk<OUT> w(p);
+    Walk<OUT> w(p, order);
     bool more = all(w.valid);
     if (OUT && more) {
       more = all(wait(&bars.qk_full[0], 0));
@@ -439,11 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunk g; false: the last one, or a wait gave up
     auto chunk = [&]() -> bool {
       const uint32_t s = g & 1;
-      if (!all((OUT || wait(&bars.qk_full[s], g >> 1)) && wait(&bars.ready_d, g))) return false;
+      if (!all((OUT || wait(&bars.qk_full[s], g >> 1)) && wait(&bars.ready_d[s], g >> 1))) return false;
       sm100::tc_fence_after();
 #pragma unroll
       for (uint32_t k = 0; k < 2; ++k)
-        mma4_ss<128, 128>(TM_DS, dk + s * kTile16 + 512 * k, dvp + 512 * k, hi, hi, id_d, k, one);
+        mma4_ss<128, 128>(!OUT && s ? TM_S : TM_DS, dk + s * kTile16 + 512 * k,
+                          (s ? dvp1 : dvp) + 512 * k, hi, hi, id_d, k, one);
       commit(&bars.ds_done[s], one);
       w.next();
       const bool next = all(w.valid);
@@ -489,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         y[e] = t < L ? a[t * p.a.decay_stride] : 0.0f;
       }
     };
-    Walk<OUT> w(p);
+    Walk<OUT> w(p, order);
     if (turn && w.valid) w.next();
     float y[4];
     if (w.valid) fetch(w, y);
@@ -603,9 +630,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the next item with tokens, from id on: its entry state (an empty sequence's state passes)
     auto enter = [&]() -> bool {
       const int ids = p.cols * p.a.H * p.halves;
-      for (; id < ids; id += gridDim.x) {
+      for (; id < ids; id = following(id)) {
         Item x;
-        if (!locate<OUT>(p, id, x)) continue;
+        if (!locate<OUT>(p, order, id, x)) continue;
         it = x;
         const int64_t size = (int64_t)DK * p.a.dv, unit = (int64_t)it.n * p.a.H + it.h;
         const int64_t in = (int64_t)i * p.a.dv + NV * it.half + c0;
@@ -631,21 +658,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return false;
     };
-    // A chunk g is begun and ended by the same code, one chunk apart: chunk g's K^T V' and O
-    // (`old`), chunk g + 1's V', operand of S and P (`more`).
+    // V' of chunk g, 16 bytes a thread at a time (rows of V past the end are zeros by then).
+    // Warps of a quarter share a scheduler, and later quarters have more of P to make: they take
+    // 3, 2, 2 and 1 of its eight pieces.
+    auto weigh = [&](uint32_t g) -> bool {
+      const uint32_t s = g & 1, slot = g % kGates;
+      if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.v_full[s], g >> 1)) return false;
+      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox);
+      uint4* to = reinterpret_cast<uint4*>(smem + (!OUT && s ? M::kQ : M::kVP));
+      const f32x2 minus = pair(-1.0f, -1.0f);
+#pragma unroll 1
+      for (int k = k0; k < k1; ++k) {
+        const int e = 128 * k + 32 * part + lane;
+        const uint4 x = v[e];
+        const float f = gates[slot].v[e >> 3];
+        const f32x2 ff = pair(f, f);
+        const uint32_t r[4] = {x.x, x.y, x.z, x.w};
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x2 y = mul2(ff, pair(__uint_as_float(r[c] << 16),
+                                        __uint_as_float(r[c] & 0xffff0000u)));
+          a[c] = bf16x2(y);
+          b[c] = bf16x2(fma2(minus, pair(__uint_as_float(a[c] << 16),
+                                         __uint_as_float(a[c] & 0xffff0000u)), y));
+        }
+        to[e] = make_uint4(a[0], a[1], a[2], a[3]);
+        to[e + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+      sm100::fence_async_smem();
+      arrive(&bars.ready_d[s]);
+      return true;
+    };
+    // The full pass begins and ends a chunk by the same code, one chunk apart: chunk g's K^T V' and
+    // O (`old`), chunk g + 1's V', operand of S and P (`more`).  The first pass, whose V' and
+    // product have two places each, makes V' of chunk g + 1 before it waits for chunk g's product.
     bool more = enter(), old = false;
+    Walk<OUT> ahead(p, order, !OUT);
     for (uint32_t g = ~0u; more || old; ++g) {
       const uint32_t s = g & 1, slot = g % kGates, next = (g + 1) % kGates;
       const int64_t at = it.row + t + row;  // this chunk's rows go out last
       const bool live = row < it.len - t;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) +
                                             (at * p.a.H + it.h) * p.a.dv + NV * it.half + c0);
+      if (!OUT && ahead.valid) {
+        if (!weigh(g + 1)) break;
+        ahead.next();
+      }
       if (old) {
         if (!wait(&bars.ds_done[s], g >> 1)) break;
         sm100::tc_fence_after();
         float x[16], y[16];
-        sm100::tmem_ld16(tm + TM_DS + c0, x);
-        sm100::tmem_ld16(tm + TM_DS + NV + c0, y);
+        const uint32_t from = tm + (!OUT && s ? TM_S : TM_DS) + c0;
+        sm100::tmem_ld16(from, x);
+        sm100::tmem_ld16(from + NV, y);
         const float2 f = gates[slot].gamma;
         const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
         sm100::tmem_wait_ld();
@@ -658,41 +724,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         t += C;
         if (t >= it.len) {
           leave();
-          id += gridDim.x;
+          id = following(id);
           more = enter();
         }
       }
       if (more) {
-        // V', 16 bytes a thread at a time (rows of V past the end are zeros by then).  Warps of a
-        // quarter share a scheduler, and later quarters have more of P to make: they take 3, 2, 2
-        // and 1 of its eight pieces.
-        if (!wait(&bars.gate_full[next], (g + 1) / kGates) ||
-            !wait(&bars.v_full[s ^ 1], (g + 1) >> 1))
-          break;
-        const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + (s ^ 1) * M::kBox);
-        uint4* to = reinterpret_cast<uint4*>(smem + M::kVP);
-        const f32x2 minus = pair(-1.0f, -1.0f);
-#pragma unroll 1
-        for (int k = k0; k < k1; ++k) {
-          const int e = 128 * k + 32 * part + lane;
-          const uint4 x = v[e];
-          const float f = gates[next].v[e >> 3];
-          const f32x2 ff = pair(f, f);
-          const uint32_t r[4] = {x.x, x.y, x.z, x.w};
-          uint32_t a[4], b[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const f32x2 y = mul2(ff, pair(__uint_as_float(r[c] << 16),
-                                          __uint_as_float(r[c] & 0xffff0000u)));
-            a[c] = bf16x2(y);
-            b[c] = bf16x2(fma2(minus, pair(__uint_as_float(a[c] << 16),
-                                           __uint_as_float(a[c] & 0xffff0000u)), y));
-          }
-          to[e] = make_uint4(a[0], a[1], a[2], a[3]);
-          to[e + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
-        }
-        sm100::fence_async_smem();
-        arrive(&bars.ready_d);
+        if (OUT && !weigh(g + 1)) break;
         if (OUT) {
           // the state as an operand
           if (old && !wait(&bars.qs_done[s], g >> 1)) break;
@@ -824,15 +861,24 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Til
     return reinterpret_cast<float4*>(p.states + ((int64_t)(col + s) * p.a.H + h) * size + e);
   };
   float4 x = *at(0);
-#pragma unroll 4
-  for (int s = 1; s < segs - 1; ++s) {
-    const float2 f = p.gammas[(int64_t)(col + s) * p.a.H + h];
-    const float4 y = *at(s);
-    x.x = fmaf(f.x, x.x, fmaf(f.y, x.x, y.x));
-    x.y = fmaf(f.x, x.y, fmaf(f.y, x.y, y.y));
-    x.z = fmaf(f.x, x.z, fmaf(f.y, x.z, y.z));
-    x.w = fmaf(f.x, x.w, fmaf(f.y, x.w, y.w));
-    *at(s) = x;
+  for (int s0 = 1; s0 < segs - 1; s0 += 8) {  // (their loads together)
+    float4 y[8];
+    float2 f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k < segs - 1) {
+        y[k] = *at(s0 + k);
+        f[k] = p.gammas[(int64_t)(col + s0 + k) * p.a.H + h];
+      }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k < segs - 1) {
+        x.x = fmaf(f[k].x, x.x, fmaf(f[k].y, x.x, y[k].x));
+        x.y = fmaf(f[k].x, x.y, fmaf(f[k].y, x.y, y[k].y));
+        x.z = fmaf(f[k].x, x.z, fmaf(f[k].y, x.z, y[k].z));
+        x.w = fmaf(f[k].x, x.w, fmaf(f[k].y, x.w, y[k].w));
+        *at(s0 + k) = x;
+      }
   }
 }
 
@@ -852,7 +898,7 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, 
 }
 
 // How the token axis is cut.  Times in chunks of one CTA: a chunk of the first
-// pass costs about half of one of the full pass, and a second and third launch
+// pass costs 0.4 of one of the full pass, and a second and third launch
 // some six.  Packed lengths are not known here: the longest is taken for twice
 // the mean.
 struct Cut {
@@ -873,7 +919,7 @@ Cut cut(int N, int64_t T, int H, int dv, bool packed) {
   for (int64_t segs = 2; segs <= 64 && segs * 2 <= chunks; ++segs) {
     const int64_t each = (chunks + segs - 1) / segs;
     const int64_t items = packed ? ((all + each - 1) / each) * units : N * segs * units;
-    const double t = 1.5 * waves(items, each) + 6.0;
+    const double t = 1.4 * waves(items, each) + 6.0;
     if (t < 0.9 * best) {
       best = t;
       pick = each;
