@@ -13,7 +13,7 @@
 // TMA (two chunks ahead), one issues products, two take the decays' sums, and
 // sixteen do the same work side by side, each a quarter of the rows and a fourth
 // of the columns: V', S and its operand, P, O.  The products of a chunk run in
-// the order K^T V', Q S, the next chunk's scores, P V; while each runs, the
+// the order K^T V', the next chunk's scores, Q S, P V; while each runs, the
 // sixteen work on what the one before it left.  (With groups of warps for P, S,
 // V' and O the same work took 1.5 to 2 times as long: four kinds of loops on
 // each scheduler do not fit its instruction caches.)
@@ -475,6 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.next();
       const bool next = all(w.valid);
       if (OUT) {
+        if (!all(wait(&bars.p_full, g) && (!next || wait(&bars.qk_full[s ^ 1], (g + 1) >> 1))))
+          return false;
+        sm100::tc_fence_after();
+        if (next) scores(s ^ 1);
         if (!all(wait(&bars.ready_q, g))) return false;
         sm100::tc_fence_after();
 #pragma unroll
@@ -482,10 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma4_ss<2, 128>(TM_O1, dq + s * kTile16 + b * kBox16, dst + 512 * b, hi, st_hi, id_q, b,
                           one);
         commit(&bars.qs_done[s], one);
-        if (!all(wait(&bars.p_full, g) && (!next || wait(&bars.qk_full[s ^ 1], (g + 1) >> 1))))
-          return false;
-        sm100::tc_fence_after();
-        if (next) scores(s ^ 1);
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k)
           mma4_ts<128>(TM_O2, TM_P + 64 * s + 32 * k, dv + s * kBox16 + 512 * k, hi, id_q, k, one);
@@ -731,15 +731,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more) {
         if (OUT && !weigh(g + 1)) break;
         if (OUT) {
-          // the state as an operand
-          if (old && !wait(&bars.qs_done[s], g >> 1)) break;
-          if (mine)
-#pragma unroll
-            for (int j = 0; j < 16; j += 8)
-              kda_tc::st16(smem + M::kS + kda_tc::mn_off(c0 + j, i, 1024), bf16x2(S[j / 2]),
-                           bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
-          sm100::fence_async_smem();
-          if (!old) arrive(&bars.ready_q);  // (no O to read yet)
           // P, 16 columns at a time
           if (!wait(&bars.s_done, g + 1)) break;
           sm100::tc_fence_after();
@@ -797,6 +788,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm100::tmem_wait_st();
           sm100::tc_fence_before();
           arrive(&bars.p_full);
+          // the state as an operand
+          if (old && !wait(&bars.qs_done[s], g >> 1)) break;
+          if (mine)
+#pragma unroll
+            for (int j = 0; j < 16; j += 8)
+              kda_tc::st16(smem + M::kS + kda_tc::mn_off(c0 + j, i, 1024), bf16x2(S[j / 2]),
+                           bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
+          sm100::fence_async_smem();
+          if (!old) arrive(&bars.ready_q);  // (no O to read yet)
         }
       }
       if (old) {
