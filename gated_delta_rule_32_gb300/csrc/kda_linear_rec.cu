@@ -57,23 +57,50 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
   const Tin* v = static_cast<const Tin*>(p.v) + row * p.v_stride + (int64_t)h * p.dv + c0;
   const float* a = p.decay + row * p.decay_stride + h;
   Tin* out = static_cast<Tin*>(p.out) + (row * p.H + h) * p.dv + c0;
+  // a block's inputs: fetched into registers while the block before is at work
+  constexpr int NK = (TB * DK + L::kThreads - 1) / L::kThreads;
+  constexpr int NV = (TB * DVB + L::kThreads - 1) / L::kThreads;
+  float fk[NK], fq[NK], fv[NV], fa = 0.0f;
+  auto fetch = [&](int t0) {
+    const int nt = len - t0 < TB ? len - t0 : TB;
+#pragma unroll
+    for (int x = 0; x < NK; ++x) {
+      const int e = tid + x * L::kThreads, t = e / DK, i = e - t * DK;
+      if (t < nt) {
+        fk[x] = kda::to_f32(k[(t0 + t) * p.k_stride + i]);
+        fq[x] = kda::to_f32(q[(t0 + t) * p.q_stride + i]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < NV; ++x) {
+      const int e = tid + x * L::kThreads, t = e / DVB, c = e - t * DVB;
+      if (t < nt) fv[x] = kda::to_f32(v[(t0 + t) * p.v_stride + c]);
+    }
+    if (tid < nt) fa = a[(t0 + tid) * p.decay_stride];
+  };
+  if (len > 0) fetch(0);
   for (int t0 = 0; t0 < len; t0 += TB) {
     const int nt = len - t0 < TB ? len - t0 : TB;
-    for (int e = tid; e < nt * DK; e += L::kThreads) {
-      const int t = e / DK, i = e - t * DK;
-      s_k[t][i] = kda::to_f32(k[(t0 + t) * p.k_stride + i]);
-      s_q[t][i] = kda::to_f32(q[(t0 + t) * p.q_stride + i]);
+#pragma unroll
+    for (int x = 0; x < NK; ++x) {
+      const int e = tid + x * L::kThreads, t = e / DK, i = e - t * DK;
+      if (t < nt) {
+        s_k[t][i] = fk[x];
+        s_q[t][i] = fq[x];
+      }
     }
-    for (int e = tid; e < nt * DVB; e += L::kThreads) {
-      const int t = e / DVB, c = e - t * DVB;
-      s_v[t][c] = kda::to_f32(v[(t0 + t) * p.v_stride + c]);
+#pragma unroll
+    for (int x = 0; x < NV; ++x) {
+      const int e = tid + x * L::kThreads, t = e / DVB, c = e - t * DVB;
+      if (t < nt) s_v[t][c] = fv[x];
     }
     if (tid < nt) {
-      const float x = clamp_decay(a[(t0 + tid) * p.decay_stride]);
+      const float x = clamp_decay(fa);
       const float m = expm1f(x), e = 1.0f + m;
       s_e[tid] = x > -0.5f ? e : expf(x);
       s_l[tid] = x > -0.5f ? m - (e - 1.0f) : 0.0f;
     }
+    if (t0 + TB < len) fetch(t0 + TB);
     __syncthreads();
     for (int t = 0; t < nt; ++t) {
       const float e = s_e[t], l = s_l[t];

@@ -120,23 +120,36 @@ __global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs p
     s[i] *= p.inverse ? -p.amplitude : p.amplitude;
   }
   const int a = INTER ? 16 * u : 8 * u, b = INTER ? a + 8 : p.part / 2 + 8 * u;
-  for (int h = h0; h < h1; ++h) {
-    const int64_t o = (int64_t)h * p.d;
-    Vec<T> va = load8(in + o + a), vb = load8(in + o + b);
-    float x[16];
-    va.get(x);
-    vb.get(x + 8);
+  // (the loads of several heads before their first store)
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+  for (int h = h0; h < h1; h += kBatch) {
+    Vec<T> va[kBatch], vb[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + 8;
-      const float xa = x[ia], xb = x[ib];
-      x[ia] = xa * c[i] - xb * s[i];
-      x[ib] = xa * s[i] + xb * c[i];
-    }
-    va.put(x);
-    vb.put(x + 8);
-    store8(out + o + a, va);
-    store8(out + o + b, vb);
+    for (int k = 0; k < kBatch; ++k)
+      if (h + k < h1) {
+        const int64_t o = (int64_t)(h + k) * p.d;
+        va[k] = load8(in + o + a);
+        vb[k] = load8(in + o + b);
+      }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (h + k < h1) {
+        const int64_t o = (int64_t)(h + k) * p.d;
+        float x[16];
+        va[k].get(x);
+        vb[k].get(x + 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + 8;
+          const float xa = x[ia], xb = x[ib];
+          x[ia] = xa * c[i] - xb * s[i];
+          x[ib] = xa * s[i] + xb * c[i];
+        }
+        va[k].put(x);
+        vb[k].put(x + 8);
+        store8(out + o + a, va[k]);
+        store8(out + o + b, vb[k]);
+      }
   }
 }
 

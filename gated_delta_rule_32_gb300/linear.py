@@ -31,26 +31,30 @@ from .kda import KDA_BF16, KDA_F32, KDA_OK, KdaError
 _DTYPES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 
 
+# (messages are put together only where they are raised: a decode step's calls are short)
+
 def _rows(x, name, dev, dtype):
     """Checks a [B, T, heads, d] tensor whose heads and channels are contiguous
     and whose rows follow each other at one distance: that distance."""
-    _need(x.dim() == 4 and x.dtype is dtype and x.get_device() == dev,
-          "%s must be [B, T, heads, d] of one type (bfloat16 or float32) on cuda:%d" % (name, dev))
+    if x.dim() != 4 or x.dtype is not dtype or x.get_device() != dev:
+        raise ValueError("%s must be [B, T, heads, d] of one type (bfloat16 or float32) on cuda:%d"
+                         % (name, dev))
     B, T, H, d = x.shape
     b, t, h, c = x.stride()
     if B * T == 0:
         return H * d
-    _need((c == 1 or d == 1) and (h == d or H == 1), "%s must have contiguous heads and channels" % name)
-    step = t if T > 1 else b if B > 1 else H * d
-    _need(B == 1 or T == 1 or b == T * t, "%s must have its rows at one distance" % name)
-    return step
+    if (c != 1 and d > 1) or (h != d and H > 1):
+        raise ValueError("%s must have contiguous heads and channels" % name)
+    if B > 1 and T > 1 and b != T * t:
+        raise ValueError("%s must have its rows at one distance" % name)
+    return t if T > 1 else b if B > 1 else H * d
 
 
 def _decay(a, B, T, H, dev):
-    _need(a.dtype is torch.float32 and a.get_device() == dev,
-          "log_decay must be a float32 tensor on cuda:%d" % dev)
+    if a.dtype is not torch.float32 or a.get_device() != dev:
+        raise ValueError("log_decay must be a float32 tensor on cuda:%d" % dev)
     if a.dim() == 1:
-        _need(a.shape[0] == H and (a.stride(0) == 1 or H == 1), "log_decay must be [H], contiguous")
+        _need(a.shape[0] == H and (H == 1 or a.stride(0) == 1), "log_decay must be [H], contiguous")
         return 0
     _need(a.shape == (B, T, H), "log_decay must be [B, T, H] or [H]")
     b, t, h = a.stride()
@@ -62,9 +66,10 @@ def _decay(a, B, T, H, dev):
 
 
 def _state(x, name, shape, dev):
-    _need(x.dtype is torch.float32 and x.shape == shape and x.is_contiguous() and
-          x.get_device() == dev, "%s must be a contiguous float32 tensor %s on cuda:%d"
-          % (name, list(shape), dev))
+    if x.dtype is not torch.float32 or x.shape != shape or not x.is_contiguous() or \
+            x.get_device() != dev:
+        raise ValueError("%s must be a contiguous float32 tensor %s on cuda:%d"
+                         % (name, list(shape), dev))
 
 
 def _shapes(q, k, v, log_decay):
@@ -74,8 +79,8 @@ def _shapes(q, k, v, log_decay):
     _need(code is not None, "q must be bfloat16 or float32")
     qs, ks, vs = _rows(q, "q", dev, dtype), _rows(k, "k", dev, dtype), _rows(v, "v", dev, dtype)
     B, T, Hk, dk = q.shape
-    H, dv = v.shape[2:]
-    _need(k.shape == q.shape and v.shape[0] == B and v.shape[1] == T and Hk > 0 and H % Hk == 0,
+    Bv, Tv, H, dv = v.shape
+    _need(k.shape == q.shape and Bv == B and Tv == T and Hk > 0 and H % Hk == 0,
           "q and k must be [B, T, Hk, dk], v [B, T, H, dv], H a multiple of Hk")
     return dev, code, qs, ks, vs, _decay(log_decay, B, T, H, dev), B, T, H, Hk, dk, dv
 
@@ -98,10 +103,11 @@ def linear_attend(q, k, v, log_decay, init_state=None, cu_seqlens=None, scale=1.
     dev, code, qs, ks, vs, ds, B, T, H, Hk, dk, dv = _shapes(q, k, v, log_decay)
     N = B
     if cu_seqlens is not None:
-        _need(cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and
-              cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev and
-              cu_seqlens.numel() > 1 and B == 1,
-              "cu_seqlens must be a contiguous int32 tensor [N + 1] on cuda:%d, with B = 1" % dev)
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or B != 1 or \
+                cu_seqlens.numel() < 2 or not cu_seqlens.is_contiguous() or \
+                cu_seqlens.get_device() != dev:
+            raise ValueError("cu_seqlens must be a contiguous int32 tensor [N + 1] on cuda:%d, "
+                             "with B = 1" % dev)
         N = cu_seqlens.numel() - 1
     if init_state is not None:
         _state(init_state, "init_state", (N, H, dk, dv), dev)

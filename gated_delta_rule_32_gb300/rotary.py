@@ -57,11 +57,13 @@ def rotary_frequencies(part, base=10000.0, scaling=None, factor=1.0, trained=409
 
 
 def _stride(x, name, dev, dtype, T, d):
-    _need(x.dim() == 3 and x.dtype is dtype and x.get_device() == dev and x.shape[0] == T and
-          x.shape[2] == d, "%s must be [T, heads, d] of one type on cuda:%d" % (name, dev))
+    if x.dim() != 3 or x.dtype is not dtype or x.get_device() != dev or x.shape[0] != T or \
+            x.shape[2] != d:
+        raise ValueError("%s must be [T, heads, d] of one type on cuda:%d" % (name, dev))
     t, h, c = x.stride()
     H = x.shape[1]
-    _need(T == 0 or (c == 1 and (h == d or H == 1)), "%s must have contiguous heads and channels" % name)
+    if T > 0 and (c != 1 or (h != d and H > 1)):
+        raise ValueError("%s must have contiguous heads and channels" % name)
     return t if T > 1 else H * d
 
 
@@ -83,12 +85,12 @@ def rotary_embed(q, k, positions, frequencies, interleaved=False, amplitude=1.0,
     _need(code is not None and q.dim() == 3, "q must be [T, heads, d], bfloat16 or float32")
     T, Hq, d = q.shape
     qs = _stride(q, "q", dev, q.dtype, T, d)
-    _need(positions.dtype is torch.int32 and positions.shape == (T,) and
-          positions.is_contiguous() and positions.get_device() == dev,
-          "positions must be a contiguous int32 tensor [T] on cuda:%d" % dev)
-    _need(frequencies.dtype is torch.float64 and frequencies.dim() == 1 and
-          frequencies.is_contiguous() and frequencies.get_device() == dev,
-          "frequencies must be a contiguous float64 tensor [part / 2] on cuda:%d" % dev)
+    if positions.dtype is not torch.int32 or positions.shape != (T,) or \
+            not positions.is_contiguous() or positions.get_device() != dev:
+        raise ValueError("positions must be a contiguous int32 tensor [T] on cuda:%d" % dev)
+    if frequencies.dtype is not torch.float64 or frequencies.dim() != 1 or \
+            not frequencies.is_contiguous() or frequencies.get_device() != dev:
+        raise ValueError("frequencies must be a contiguous float64 tensor [part / 2] on cuda:%d" % dev)
     Hk, ks, kp = 0, 0, None
     if k is not None:
         ks = _stride(k, "k", dev, q.dtype, T, d)
