@@ -104,6 +104,7 @@ struct Item {
   int64_t row;  // first token row
   int len;      // tokens
   int n, h, hk, half, col;
+  int tail;     // column of its sequence's last segment
   bool first, last;  // segment of its sequence
 };
 
@@ -143,6 +144,7 @@ __device__ __noinline__ bool locate(const TileArgs& p, const uint16_t* order, in
   if (seg < 0 || seg >= segs) return false;
   it.first = seg == 0;
   it.last = seg == segs - 1;
+  it.tail = it.col + segs - 1 - seg;
   if (!OUT && it.last) return false;
   it.row = row + (int64_t)seg * p.seg;
   it.len = it.last ? len - seg * p.seg : p.seg;
@@ -637,9 +639,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t size = (int64_t)DK * p.a.dv, unit = (int64_t)it.n * p.a.H + it.h;
         const int64_t in = (int64_t)i * p.a.dv + NV * it.half + c0;
         const int64_t col = (int64_t)it.col * p.a.H + it.h;
-        const float* from = it.first ? (p.a.init ? p.a.init + unit * size : nullptr)
-                            : OUT    ? p.states + (col - p.a.H) * size
-                                     : nullptr;
+        // (final_state may be init_state: where other segments follow, the first one of the full
+        // pass starts from the copy that the scan has left in the last one's place)
+        const float* from =
+            !it.first              ? (OUT ? p.states + (col - p.a.H) * size : nullptr)
+            : OUT && it.tail != it.col ? p.states + ((int64_t)it.tail * p.a.H + it.h) * size
+            : p.a.init             ? p.a.init + unit * size
+                                   : nullptr;
         to = !OUT      ? p.states + col * size
              : it.last ? (p.a.final_state ? p.a.final_state + unit * size : nullptr)
                        : nullptr;
@@ -845,7 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The states that segments start from: column by column of a sequence,
-// S(s) <- gamma(s) S(s - 1) + S(s).
+// S(s) <- gamma(s) S(s - 1) + S(s), and a copy of the initial state in the
+// last one's place.
 constexpr int kScanThreads = 256;
 __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const TileArgs p) {
   const int size = p.a.dk * p.a.dv, blocks = size / (4 * kScanThreads);
@@ -856,10 +863,12 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Til
   if (!span(p.a, n, row, len)) return;
   const int segs = (len + p.seg - 1) / p.seg;
   const int col = p.a.cu ? (int)(row / p.seg) + n : n * p.segs;
-  if (segs < 3) return;
+  if (segs < 2) return;
   auto at = [&](int s) {
     return reinterpret_cast<float4*>(p.states + ((int64_t)(col + s) * p.a.H + h) * size + e);
   };
+  *at(segs - 1) = p.a.init ? *reinterpret_cast<const float4*>(p.a.init + unit * (int64_t)size + e)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
   float4 x = *at(0);
   for (int s0 = 1; s0 < segs - 1; s0 += 8) {  // (their loads together)
     float4 y[8];

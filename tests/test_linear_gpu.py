@@ -231,6 +231,39 @@ def test_state_in_place_and_in_pieces():
     assert ((whole.double() - s).abs() <= 2.0 ** -16 * sm).all()
 
 
+@pytest.mark.parametrize("T,H,lens", [(6000, 2, None), (40000, 4, None), (5000, 3, [4000, 0, 1000])])
+def test_state_in_place_over_segments(T, H, lens):
+    # one buffer for the states before and after, long rows of few heads: segments read the one
+    # while others write the other
+    N = 1 if lens is None else len(lens)
+    x = made(1, T, H, H, 128, 128, N=N, seed=T)
+    cu = None if lens is None else torch.tensor([0, 4000, 4000, 5000], dtype=torch.int32, device="cuda")
+    want, after = pkg.linear_attend(**x, cu_seqlens=cu, scale=0.3)
+    for _ in range(10):
+        state = x["init_state"].clone()
+        out = torch.empty_like(want)
+        rc = kda.kda_linear_fwd(x["q"], H * 128, x["k"], H * 128, x["v"], H * 128, x["log_decay"], H, state,
+                                out, state, N, T, H, H, 128, 128, cu, scale=0.3,
+                                stream=torch.cuda.current_stream())
+        assert rc == 0
+        assert torch.equal(out, want) and torch.equal(state, after)
+
+
+def test_a_decay_that_is_nan():
+    # what follows it in its head and sequence is NaN, nothing else
+    lens = [300, 200]
+    x = made(1, 500, 3, 3, 128, 64, N=2, seed=5)
+    cu = torch.tensor([0, 300, 500], dtype=torch.int32, device="cuda")
+    want, ws = pkg.linear_attend(**x, cu_seqlens=cu)
+    x["log_decay"][0, 142, 1] = math.nan
+    out, state = pkg.linear_attend(**x, cu_seqlens=cu)
+    assert out[0, 142:300, 1].isnan().all() and state[0, 1].isnan().all()
+    for t in (out, want):
+        t[0, 142:300, 1] = 0
+    assert torch.equal(out, want)
+    assert torch.equal(state[1], ws[1]) and torch.equal(state[0, ::2], ws[0, ::2])
+
+
 @pytest.mark.parametrize("cu", [[0, 50, 30, 100], [5, 50, 100], [0, 50, 101], [0, -1, 100], [0, 200, 100],
                                 [0, 2 ** 31 - 1, 100], [0, 100, 100, 60]])
 @pytest.mark.parametrize("dtype", [BF, F32])
