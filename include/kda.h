@@ -566,7 +566,10 @@ size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv
  * multiples of 16 bytes, at most 2^30 elements.  q, k, v, out and the states
  * are 16-byte aligned.  dk, dv in {16, 32, 64, 128}; dtype (of q, k, v and
  * out) KDA_BF16 or KDA_F32; H <= 65536, N * H <= 2^28, at most 2^30 rows.
- * Sums and states are fp32.
+ * Sums and states are fp32.  What lies outside the rows of a sequence never
+ * reaches its results, whatever it is.  Inside one, prompts on the tensor cores
+ * multiply values by weights that are 0 for the tokens before them: a NaN or an
+ * infinity in v reaches all rows of its 128 tokens, not only those behind it.
  */
 
 /*
@@ -578,6 +581,13 @@ size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv
  * otherwise no output overlaps an input.  Malformed cu_seqlens are
  * KDA_ERR_BAD_SEQLENS in dev_status (as in kda_chunk_fwd_ex), the outputs then
  * unspecified.
+ * bf16 with dk and dv 64 or 128 runs on the tensor cores in chunks of 128
+ * tokens: weights within a chunk and the state that queries read are rounded
+ * to bf16, the state that is carried and returned is summed from 16 bits of each
+ * weighted value (2.5e-6 of its norm against 64 bits).  Other types and sizes run
+ * token by token in fp32.  Few heads with long rows are cut into segments of the
+ * token axis; where, and so the last bits, goes by B, T, H, dv and the device's
+ * SM count.  The same call gives the same bits each time.
  *   workspace  device scratch of kda_linear_workspace_bytes() bytes, 256-byte
  *              aligned, contents arbitrary; or NULL: taken from the
  *              stream-ordered allocator.
