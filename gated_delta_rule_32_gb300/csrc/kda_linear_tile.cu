@@ -13,7 +13,7 @@
 // TMA (two chunks ahead), one issues products, two take the decays' sums, and
 // sixteen do the same work side by side, each a quarter of the rows and a fourth
 // of the columns: V', S and its operand, P, O.  The products of a chunk run in
-// the order K^T V', the next chunk's scores, Q S, P V; while each runs, the
+// the order Q S, K^T V', P V, the next chunk's scores; while each runs, the
 // sixteen work on what the one before it left.  (With groups of warps for P, S,
 // V' and O the same work took 1.5 to 2 times as long: four kinds of loops on
 // each scheduler do not fit its instruction caches.)
@@ -45,8 +45,8 @@ constexpr int NV = 64;          // value columns of a CTA
 constexpr int kThreads = 640;
 constexpr int kGates = 4;
 constexpr int kOrdered = 1024;  // most sequences of a packed batch that are put in order
-// tensor memory: scores, P by stage, Q S, P V, K^T V' of V's two parts
-constexpr uint32_t TM_S = 0, TM_P = 128, TM_O1 = 256, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
+// tensor memory: scores, P, Q S by stage, P V, K^T V' of V's two parts
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_O1 = 192, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
 constexpr int kWorkers = kThreads / 32 - 4;
 
 struct TileArgs {
@@ -70,13 +70,11 @@ struct alignas(16) Gate {
 
 struct Bars {
   uint64_t qk_full[2], v_full[2];    // copies have landed
-  uint64_t ds_done[2];               // K^T V' is there: V' and K are free
-  uint64_t qs_done[2];               // Q S is there: Q and S's operand are free
-  uint64_t o_done[2];                // O is there: V and P are free
+  uint64_t ds_done[2];               // K^T V' and Q S are there: V', K, Q and S's operand are free
+  uint64_t o_done[2];                // P V is there: V and P are free
   uint64_t s_done;                   // the scores are there
-  uint64_t ready_d[2];               // V' is made, its product's place read
-  uint64_t ready_q;                  // S's operand is made, O read
-  uint64_t p_full;                   // P is made, the scores read
+  uint64_t ready[2];                 // V' and S's operand are made, K^T V' and Q S's places read
+  uint64_t p_full;                   // P is made, the scores and P V's place read
   uint64_t gate_full[kGates], gate_empty[kGates], drain;
 };
 
@@ -340,15 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&bars.qk_full[i], OUT ? 2 : 1);
+      sm100::mbar_init(&bars.qk_full[i], 1);
       sm100::mbar_init(&bars.v_full[i], 1);
       sm100::mbar_init(&bars.ds_done[i], 1);
-      sm100::mbar_init(&bars.ready_d[i], kWorkers);
-      sm100::mbar_init(&bars.qs_done[i], 1);
       sm100::mbar_init(&bars.o_done[i], 1);
+      sm100::mbar_init(&bars.ready[i], kWorkers);
     }
     sm100::mbar_init(&bars.s_done, 1);
-    sm100::mbar_init(&bars.ready_q, kWorkers);
     sm100::mbar_init(&bars.p_full, kWorkers);
     for (int i = 0; i < kGates; ++i) {
       sm100::mbar_init(&bars.gate_full[i], 1);
@@ -395,29 +391,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (in the order in which the products let go of them)
       if (use > 0 && !wait(&bars.ds_done[s], use - 1)) break;
       if (lane == 0) {
-        unsigned char* k = smem + M::kK + s * M::kTile;
-        sm100::mbar_arrive_expect_tx(&bars.qk_full[s], M::kTile);
+        sm100::mbar_arrive_expect_tx(&bars.qk_full[s], (OUT ? 2 : 1) * M::kTile);
 #pragma unroll
-        for (int b = 0; b < DK / 64; ++b)
-          sm100::tma_load_3d(k + b * M::kBox, &map_k, &bars.qk_full[s], 64 * b, hk, row);
+        for (int b = 0; b < DK / 64; ++b) {
+          const int at = s * M::kTile + b * M::kBox;
+          sm100::tma_load_3d(smem + M::kK + at, &map_k, &bars.qk_full[s], 64 * b, hk, row);
+          if (OUT) sm100::tma_load_3d(smem + M::kQ + at, &map_q, &bars.qk_full[s], 64 * b, hk, row);
+        }
       }
       __syncwarp();
-      // (a give-up leaves the chunk's barriers short of an arrival: nobody passes them)
-      if (OUT) {
-        if (use > 0 && !wait(&bars.qs_done[s], use - 1)) {
-          ++g;
-          break;
-        }
-        if (lane == 0) {
-          unsigned char* q = smem + M::kQ + s * M::kTile;
-          sm100::mbar_arrive_expect_tx(&bars.qk_full[s], M::kTile);
-#pragma unroll
-          for (int b = 0; b < DK / 64; ++b)
-            sm100::tma_load_3d(q + b * M::kBox, &map_q, &bars.qk_full[s], 64 * b, hk, row);
-        }
-        __syncwarp();
-      }
-      if (use > 0 && !wait(OUT ? &bars.o_done[s] : &bars.ds_done[s], use - 1)) {
+      // (a give-up leaves the chunk's V out: nobody gets beyond its barrier)
+      if (OUT && use > 0 && !wait(&bars.o_done[s], use - 1)) {
         ++g;
         break;
       }
@@ -467,8 +451,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunk g; false: the last one, or a wait gave up
     auto chunk = [&]() -> bool {
       const uint32_t s = g & 1;
-      if (!all((OUT || wait(&bars.qk_full[s], g >> 1)) && wait(&bars.ready_d[s], g >> 1))) return false;
+      if (!all((OUT || wait(&bars.qk_full[s], g >> 1)) && wait(&bars.ready[s], g >> 1))) return false;
       sm100::tc_fence_after();
+      if (OUT) {
+#pragma unroll
+        for (uint32_t b = 0; b < DK / 64; ++b)
+          mma4_ss<2, 128>(TM_O1 + NV * s, dq + s * kTile16 + b * kBox16, dst + 512 * b, hi, st_hi,
+                          id_q, b, one);
+      }
 #pragma unroll
       for (uint32_t k = 0; k < 2; ++k)
         mma4_ss<128, 128>(!OUT && s ? TM_S : TM_DS, dk + s * kTile16 + 512 * k,
@@ -477,21 +467,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.next();
       const bool next = all(w.valid);
       if (OUT) {
-        if (!all(wait(&bars.p_full, g) && (!next || wait(&bars.qk_full[s ^ 1], (g + 1) >> 1))))
-          return false;
+        if (!all(wait(&bars.p_full, g))) return false;
         sm100::tc_fence_after();
-        if (next) scores(s ^ 1);
-        if (!all(wait(&bars.ready_q, g))) return false;
-        sm100::tc_fence_after();
-#pragma unroll
-        for (uint32_t b = 0; b < DK / 64; ++b)
-          mma4_ss<2, 128>(TM_O1, dq + s * kTile16 + b * kBox16, dst + 512 * b, hi, st_hi, id_q, b,
-                          one);
-        commit(&bars.qs_done[s], one);
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k)
-          mma4_ts<128>(TM_O2, TM_P + 64 * s + 32 * k, dv + s * kBox16 + 512 * k, hi, id_q, k, one);
+          mma4_ts<128>(TM_O2, TM_P + 32 * k, dv + s * kBox16 + 512 * k, hi, id_q, k, one);
         commit(&bars.o_done[s], one);
+        if (next) {
+          if (!all(wait(&bars.qk_full[s ^ 1], (g + 1) >> 1))) return false;
+          sm100::tc_fence_after();
+          scores(s ^ 1);
+        }
       }
       ++g;
       return next;
@@ -581,13 +567,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                    : x > -0.5f ? make_float2(f, m - (f - 1.0f))
                                : make_float2(expf(x), 0.0f);
       }
+      // (this warp's chunks are those of one stage: it sees each of its copies land)
+      const uint32_t s = g & 1;
+      if (!wait(&bars.qk_full[s], g >> 1) || !wait(&bars.v_full[s], g >> 1)) break;
       if (L < C) {
         // rows past the end, which belong to others: zeros, whatever they hold
-        // (A wait tells a phase only from the one before, and this warp may be ahead of the copies
-        // of two chunks before in the same place: their chunk has to be over.)
-        const uint32_t s = g & 1, before = (g - 2) % kGates;
-        if (g >= 2 && !wait(&bars.gate_empty[before], (g - 2) / kGates)) break;
-        if (!wait(&bars.qk_full[s], g >> 1) || !wait(&bars.v_full[s], g >> 1)) break;
         const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
         for (int e = L * 8 + lane; e < C * 8; e += 32) {
@@ -604,7 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------ sixteen warps that all do a quarter's fourth of V', S, P and O in turn
     const int q = warp & 3, part = (warp >> 2) - 1, row = 32 * q + lane;
     const int c0 = 16 * part;  // value columns c0 .. c0 + 15 of S and O
-    const int k0 = q == 0 ? 0 : 2 * q + 1, k1 = q == 3 ? 8 : 2 * q + 3;  // pieces of V'
     // (a product of 64 rows has them in the first half of each warp's lanes)
     const int i = DK == 128 ? row : 16 * q + lane;
     const bool mine = DK == 128 || lane < 16;
@@ -665,17 +648,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       return false;
     };
     // V' of chunk g, 16 bytes a thread at a time (rows of V past the end are zeros by then).
-    // Warps of a quarter share a scheduler, and later quarters have more of P to make: they take
-    // 3, 2, 2 and 1 of its eight pieces.
     auto weigh = [&](uint32_t g) -> bool {
       const uint32_t s = g & 1, slot = g % kGates;
-      if (!wait(&bars.gate_full[slot], g / kGates) || !wait(&bars.v_full[s], g >> 1)) return false;
+      if (!wait(&bars.gate_full[slot], g / kGates)) return false;  // (and V is there)
       const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox);
       uint4* to = reinterpret_cast<uint4*>(smem + (!OUT && s ? M::kQ : M::kVP));
       const f32x2 minus = pair(-1.0f, -1.0f);
-#pragma unroll 1
-      for (int k = k0; k < k1; ++k) {
-        const int e = 128 * k + 32 * part + lane;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int e = 512 * k + tid - 128;
         const uint4 x = v[e];
         const float f = gates[slot].v[e >> 3];
         const f32x2 ff = pair(f, f);
@@ -692,9 +673,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         to[e] = make_uint4(a[0], a[1], a[2], a[3]);
         to[e + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
       }
-      sm100::fence_async_smem();
-      arrive(&bars.ready_d[s]);
       return true;
+    };
+    // the state as an operand; and V' and it are ready for chunk g
+    auto hand_over = [&](uint32_t g) {
+      if (OUT && mine)
+#pragma unroll
+        for (int j = 0; j < 16; j += 8)
+          kda_tc::st16(smem + M::kS + kda_tc::mn_off(c0 + j, i, 1024), bf16x2(S[j / 2]),
+                       bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
+      sm100::fence_async_smem();
+      arrive(&bars.ready[g & 1]);
     };
     // The full pass begins and ends a chunk by the same code, one chunk apart: chunk g's K^T V' and
     // O (`old`), chunk g + 1's V', operand of S and P (`more`).  The first pass, whose V' and
@@ -709,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             (at * p.a.H + it.h) * p.a.dv + NV * it.half + c0);
       if (!OUT && ahead.valid) {
         if (!weigh(g + 1)) break;
+        hand_over(g + 1);
         ahead.next();
       }
       if (old) {
@@ -734,110 +724,97 @@ __global__ void __launch_bounds__(kThreads, 1)
           more = enter();
         }
       }
-      if (more) {
-        if (OUT && !weigh(g + 1)) break;
-        if (OUT) {
-          // P, 16 columns at a time
-          if (!wait(&bars.s_done, g + 1)) break;
-          sm100::tc_fence_after();
-          const Gate& gt = gates[next];
-          const float own = gt.back[row];
-          const int2 e = gt.end[q];
-#pragma unroll 1
-          for (int b = part; b < 8; b += 4) {
-            uint32_t out[8] = {};
-            if (b < 2 * q + 2) {
-              float x[16];
-              f32x2 w[8];
-              sm100::tmem_ld16(tm + TM_S + 16 * b, x);
-              const bool below = b < 2 * q;  // (of the diagonal's 32 columns)
-              const int2 o = gt.end[b >> 1];
-              float f = fixed(e.x - o.x, e.y - o.y) - own;
-              if (below) f = ex2(f);
-              const f32x2 ff = pair(f, f);
-              const float4* c = reinterpret_cast<const float4*>((below ? gt.col : gt.back) + 16 * b);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float4 y = c[j];
-                w[2 * j] = pair(y.x, y.y);
-                w[2 * j + 1] = pair(y.z, y.w);
-              }
-              if (below) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = mul2(ff, w[j]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  float u, v;
-                  unpair(add2(ff, w[j]), u, v);
-                  w[j] = pair(ex2(u), ex2(v));
-                }
-              }
-              sm100::tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 8; ++j) w[j] = mul2(w[j], pair(x[2 * j], x[2 * j + 1]));
-              if (!below) {
-                // (tokens to come are cleared, not multiplied by 0: they may be anything)
-                const int last = row - 16 * b;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  float u, v;
-                  unpair(w[j], u, v);
-                  w[j] = pair(2 * j <= last ? u : 0.0f, 2 * j + 1 <= last ? v : 0.0f);
-                }
-              }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) out[j] = bf16x2(w[j]);
-            }
-            tmem_st8(tm + TM_P + 64 * (s ^ 1) + 8 * b, out);
-          }
-          sm100::tmem_wait_st();
-          sm100::tc_fence_before();
-          arrive(&bars.p_full);
-          // the state as an operand
-          if (old && !wait(&bars.qs_done[s], g >> 1)) break;
-          if (mine)
-#pragma unroll
-            for (int j = 0; j < 16; j += 8)
-              kda_tc::st16(smem + M::kS + kda_tc::mn_off(c0 + j, i, 1024), bf16x2(S[j / 2]),
-                           bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
-          sm100::fence_async_smem();
-          if (!old) arrive(&bars.ready_q);  // (no O to read yet)
-        }
+      if (OUT && more) {
+        if (!weigh(g + 1)) break;
+        hand_over(g + 1);
       }
-      if (old) {
-        if (OUT) {
-          const float f = gates[slot].row[row];
-          const f32x2 ff = pair(f, f), scale = pair(p.a.scale, p.a.scale);
-          if (!wait(&bars.o_done[s], g >> 1)) break;
-          sm100::tc_fence_after();
-          float x[16], y[16];
-          sm100::tmem_ld16(tm + TM_O1 + c0, x);
-          sm100::tmem_ld16(tm + TM_O2 + c0, y);
-          sm100::tmem_wait_ld();
-          sm100::tc_fence_before();
-          // (before the stores: an arrival right behind them would wait for them)
-          if (more) arrive(&bars.ready_q);
-          arrive(&bars.gate_empty[slot]);
-          uint32_t out[8];
+      uint32_t rows[8];  // O of chunk g, 16 columns
+      if (OUT && old) {
+        const float f = gates[slot].row[row];
+        const f32x2 ff = pair(f, f), scale = pair(p.a.scale, p.a.scale);
+        if (!wait(&bars.o_done[s], g >> 1)) break;
+        sm100::tc_fence_after();
+        float x[16], y[16];
+        sm100::tmem_ld16(tm + TM_O1 + NV * s + c0, x);
+        sm100::tmem_ld16(tm + TM_O2 + c0, y);
+        sm100::tmem_wait_ld();
+        sm100::tc_fence_before();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            out[e] = bf16x2(fma2(ff, pair(x[2 * e], x[2 * e + 1]),
-                                 mul2(scale, pair(y[2 * e], y[2 * e + 1]))));
-          if (live) {
-            // (32 rows' sectors are what a warp stores: once each, where out is aligned to them)
-            if (whole) {
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
-                           "r"(out[0]), "r"(out[1]), "r"(out[2]), "r"(out[3]), "r"(out[4]),
-                           "r"(out[5]), "r"(out[6]), "r"(out[7])
-                           : "memory");
-            } else {
-              dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-              dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+        for (int e = 0; e < 8; ++e)
+          rows[e] = bf16x2(fma2(ff, pair(x[2 * e], x[2 * e + 1]),
+                                mul2(scale, pair(y[2 * e], y[2 * e + 1]))));
+      }
+      if (old) arrive(&bars.gate_empty[slot]);
+      if (OUT && more) {
+        // P, 16 columns at a time
+        if (!wait(&bars.s_done, g + 1)) break;
+        sm100::tc_fence_after();
+        const Gate& gt = gates[next];
+        const float own = gt.back[row];
+        const int2 e = gt.end[q];
+#pragma unroll 1
+        for (int b = part; b < 8; b += 4) {
+          uint32_t out[8] = {};
+          if (b < 2 * q + 2) {
+            float x[16];
+            f32x2 w[8];
+            sm100::tmem_ld16(tm + TM_S + 16 * b, x);
+            const bool below = b < 2 * q;  // (of the diagonal's 32 columns)
+            const int2 o = gt.end[b >> 1];
+            float f = fixed(e.x - o.x, e.y - o.y) - own;
+            if (below) f = ex2(f);
+            const f32x2 ff = pair(f, f);
+            const float4* c = reinterpret_cast<const float4*>((below ? gt.col : gt.back) + 16 * b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 y = c[j];
+              w[2 * j] = pair(y.x, y.y);
+              w[2 * j + 1] = pair(y.z, y.w);
             }
+            if (below) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[j] = mul2(ff, w[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float u, v;
+                unpair(add2(ff, w[j]), u, v);
+                w[j] = pair(ex2(u), ex2(v));
+              }
+            }
+            sm100::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = mul2(w[j], pair(x[2 * j], x[2 * j + 1]));
+            if (!below) {
+              // (tokens to come are cleared, not multiplied by 0: they may be anything)
+              const int last = row - 16 * b;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float u, v;
+                unpair(w[j], u, v);
+                w[j] = pair(2 * j <= last ? u : 0.0f, 2 * j + 1 <= last ? v : 0.0f);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[j] = bf16x2(w[j]);
           }
+          tmem_st8(tm + TM_P + 8 * b, out);
+        }
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        arrive(&bars.p_full);
+      }
+      // (the stores come last: an arrival right behind them would wait for them, some 750 cycles.
+      // 32 rows' sectors are what a warp stores: once each, where out is aligned to them)
+      if (OUT && old && live) {
+        if (whole) {
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+                       "r"(rows[0]), "r"(rows[1]), "r"(rows[2]), "r"(rows[3]), "r"(rows[4]),
+                       "r"(rows[5]), "r"(rows[6]), "r"(rows[7])
+                       : "memory");
         } else {
-          arrive(&bars.gate_empty[slot]);
+          dst[0] = make_uint4(rows[0], rows[1], rows[2], rows[3]);
+          dst[1] = make_uint4(rows[4], rows[5], rows[6], rows[7]);
         }
       }
       old = more;
