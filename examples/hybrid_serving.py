@@ -1,5 +1,6 @@
 """Serving a hybrid model: gated delta rule layers with a state of fixed size
-beside attention layers with a paged 8-bit cache, on one GPU.
+beside attention layers with a paged 8-bit cache, on one GPU; also layers of
+linear attention with a decay for each head, and rotary positions.
 
 A batch of ragged prompts is taken in one packed step, then every request
 decodes token by token; finished requests give their pages back and new ones
@@ -7,7 +8,7 @@ take their place.  One page plan serves every layer of a step: its cu_seqlens
 is what the packed gated delta rule forward takes, its runs say where the
 attention layers append, its lengths and the block table where they read.
 
-    python examples/hybrid_serving.py [--code int8|e4m3] [--steps 16]
+    python examples/hybrid_serving.py [--code int8|e4m3] [--steps 16] [--layers kkka] [--rotary]
 
 Weights are random; the projections are plain matrix products.
 """
@@ -27,10 +28,11 @@ CODES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 
 
 class Hybrid:
-    """`layers`: a string of "k" (gated delta rule) and "a" (attention)."""
+    """`layers`: a string of "k" (gated delta rule), "l" (linear attention with a decay for
+    each head, rotary positions) and "a" (attention, with rotary positions if `rotary`)."""
 
     def __init__(self, layers="kkka", width=512, heads=4, q_heads=8, kv_heads=2, dim=64, page=32,
-                 requests=4, pages=256, pages_per_request=64, code="int8", seed=0):
+                 requests=4, pages=256, pages_per_request=64, code="int8", seed=0, rotary=False):
         self.layers, self.width, self.heads = layers, width, heads
         self.q_heads, self.kv_heads, self.dim, self.page = q_heads, kv_heads, dim, page
         gen = torch.Generator(device="cuda").manual_seed(seed)
@@ -39,11 +41,20 @@ class Hybrid:
             w = torch.randn(rows, cols, generator=gen, device="cuda") / math.sqrt(rows)
             return w.to(torch.bfloat16)
         ints = {"dtype": torch.int32, "device": "cuda"}
+        self.rotary = rotary
+        # radians a token of each pair, for linear attention's heads and for attention's
+        self.freq = [pkg.rotary_frequencies(d)[0] for d in (128, dim)]
+        # log-decays: halved after some 20 tokens (the first head) to some thousand
+        self.decay = -torch.exp2(-5.0 - 6.0 * torch.arange(heads, device="cuda") / heads)
         self.w, self.state, self.cache = [], [], []
         for kind in layers:
             if kind == "k":
                 # q, k, v, decay logits (128 channels a head), write strength
                 self.w.append((weight(width, heads * (4 * 128 + 1)), weight(heads * 128, width)))
+                self.state.append(torch.zeros(requests, heads, 128, 128, device="cuda"))
+                self.cache.append(None)
+            elif kind == "l":
+                self.w.append((weight(width, heads * 3 * 128), weight(heads * 128, width)))
                 self.state.append(torch.zeros(requests, heads, 128, 128, device="cuda"))
                 self.cache.append(None)
             else:
@@ -69,8 +80,9 @@ class Hybrid:
         if any(found):
             self.status.zero_()
             at = next(i for i, code in enumerate(found) if code)
-            what = ["kda_page_plan", "kda_page_release"] + ["kda_cache_append", "kda_cache_attn"] * \
-                len(self.layers)
+            what = ["kda_page_plan", "kda_page_release"]
+            for kind in self.layers:
+                what += ["kda_linear_fwd" if kind == "l" else "kda_cache_append", "kda_cache_attn"]
             raise kda.KdaError(what[at], found[at])
 
     def step(self, x, new_lens, max_new):
@@ -87,12 +99,16 @@ class Hybrid:
             y = y @ self.w[i][0]
             if kind == "k":
                 y = self.delta_rule(i, y, plan, max_new)
+            elif kind == "l":
+                y = self.linear(i, y, plan, max_new)
             else:
                 q, k, v = (t.reshape(T, -1, self.dim) for t in y.split(
                     [n * self.dim for n in (self.q_heads, self.kv_heads, self.kv_heads)], dim=1))
                 kc, vc, ks, vs = self.cache[i]
                 # q, k, v stay views of the projection's output: token strides differ
                 at = 2 + 2 * i
+                if self.rotary:
+                    pkg.rotary_embed(q, k, plan.positions, self.freq[1], inplace=True)
                 pkg.cache_append(k, v, plan.runs, kc, vc, ks, vs, dev_status=self.status[at:at + 1])
                 y, _ = pkg.cache_attend(q, plan.cu_seqlens, plan.kv_lens, self.table, kc, vc, ks, vs,
                                         max_new=max_new, dev_status=self.status[at + 1:at + 2])
@@ -117,6 +133,20 @@ class Hybrid:
             out, self.state[i] = pkg.forward(q, k, v, g, b, state, plan.cu_seqlens)
         return out
 
+    def linear(self, i, y, plan, max_new):
+        T, H = y.shape[0], self.heads
+        q, k, v = (t.reshape(T, H, 128) for t in y.split([H * 128] * 3, dim=1))
+        pkg.rotary_embed(q, k, plan.positions, self.freq[0], inplace=True)
+        state = self.state[i]
+        if max_new == 1 and T == state.shape[0]:  # one token of every request
+            return pkg.linear_decode(q[:, None], k[:, None], v[:, None], self.decay, state,
+                                     scale=128 ** -0.5)
+        at = 2 + 2 * i
+        out, self.state[i] = pkg.linear_attend(q[None], k[None], v[None], self.decay, state,
+                                               plan.cu_seqlens, scale=128 ** -0.5,
+                                               dev_status=self.status[at:at + 1])
+        return out
+
     def finish(self, done):
         """Requests with done[r] != 0 leave: their pages go back, their states to zero."""
         pkg.page_release(done, self.lens, self.table, self.free, self.left, self.page,
@@ -131,10 +161,12 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--code", choices=sorted(CODES), default="int8")
     ap.add_argument("--steps", type=int, default=16)
+    ap.add_argument("--layers", default="kkka", help="k, l and a, in order")
+    ap.add_argument("--rotary", action="store_true", help="rotary positions in attention layers")
     a = ap.parse_args(argv)
     torch.manual_seed(1)
     lens = [301, 17, 96, 640]
-    model = Hybrid(code=a.code, requests=len(lens))
+    model = Hybrid(a.layers, code=a.code, requests=len(lens), rotary=a.rotary)
 
     def tokens(n):
         return torch.randn(n, model.width, device="cuda").to(torch.bfloat16)

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
     }
     if (t0 + TB < len) fetch(t0 + TB);
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
+    auto token = [&](int t) {
       const float e = s_e[t], l = s_l[t];
       const float4 vv = *reinterpret_cast<const float4*>(&s_v[t][cl]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -126,6 +126,14 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
         o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
       }
       if (lane < L::CL) *reinterpret_cast<float4*>(&s_o[t][warp][cl]) = o;
+    };
+    // (a whole block's tokens are unrolled: only S goes from one to the next, the rest overlaps)
+    if (nt == TB) {
+#pragma unroll(L::R <= 4 ? 4 : 1)
+      for (int t = 0; t < TB; ++t) token(t);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t) token(t);
     }
     __syncthreads();
     for (int e = tid; e < nt * DVB; e += L::kThreads) {
