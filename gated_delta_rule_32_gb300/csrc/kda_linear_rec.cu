@@ -7,10 +7,16 @@
 // A CTA holds DVB value columns of one S in registers, so S moves through
 // memory once a call whatever the number of tokens: a thread has four adjacent
 // columns of DK / RG rows, and at each step of its loads the CTA reads
-// consecutive 16-byte pieces.  The inputs of TB tokens are staged in shared
-// memory while the state is on its way; then every thread runs its tokens
-// without a barrier, leaving each token's sum over its warp's rows in shared
-// memory, and one pass adds the warps' parts.
+// consecutive 16-byte pieces.  The inputs of TB tokens are fetched into registers
+// while the block before is at work (the first while the state is on its way) and
+// put into shared memory; then every thread runs its tokens without a barrier,
+// leaving each token's sum over its warp's rows in shared memory, and one pass
+// adds the warps' parts.
+//
+// A decode step is bound by the states' bytes: 64 sequences, 32 heads of 128 x
+// 128 take 43 us, 6.3 TB/s (inputs fetched after the states: 50 us).  Long runs
+// are bound by the chain of tokens, some 180 ns each: 2 rows of 333 tokens, 4
+// heads of 64 x 32, fp32, 59 us.
 //
 // A slow decay's factor is close to 1, and its rounding to 24 bits would be the
 // same at every token: 2^-25 times 10 000 tokens is more than the sums' own
@@ -21,8 +27,6 @@ namespace {
 
 using namespace kda_linear;
 
-constexpr int TB = 8;  // tokens staged at a time
-
 template <typename Tin, int DK, int DVB>
 struct Rec {
   static constexpr int kThreads = DK * DVB / 4 < 256 ? DK * DVB / 4 : 256;
@@ -30,12 +34,16 @@ struct Rec {
   static constexpr int RG = kThreads / CL;      // rows read at a time
   static constexpr int R = DK / RG;             // rows of a thread: RG apart
   static constexpr int kWarps = kThreads / 32;
+  // tokens at a time, as many as static shared memory has room for (8 instead of 16: 61 us
+  // where 16 take 59)
+  static constexpr int TB = DVB <= 32 ? 16 : 8;
 };
 
 template <typename Tin, int DK, int DVB>
 __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
     kda_linear_rec_kernel(const LinearArgs p) {
   using L = Rec<Tin, DK, DVB>;
+  constexpr int TB = L::TB;
   __shared__ float s_k[TB][DK], s_q[TB][DK], s_e[TB], s_l[TB];
   __shared__ __align__(16) float s_v[TB][DVB], s_o[TB][L::kWarps][DVB];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -102,7 +110,7 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
     }
     if (t0 + TB < len) fetch(t0 + TB);
     __syncthreads();
-    auto token = [&](int t) {
+    for (int t = 0; t < nt; ++t) {
       const float e = s_e[t], l = s_l[t];
       const float4 vv = *reinterpret_cast<const float4*>(&s_v[t][cl]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -126,14 +134,6 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
         o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
       }
       if (lane < L::CL) *reinterpret_cast<float4*>(&s_o[t][warp][cl]) = o;
-    };
-    // (a whole block's tokens are unrolled: only S goes from one to the next, the rest overlaps)
-    if (nt == TB) {
-#pragma unroll(L::R <= 4 ? 4 : 1)
-      for (int t = 0; t < TB; ++t) token(t);
-    } else {
-#pragma unroll 1
-      for (int t = 0; t < nt; ++t) token(t);
     }
     __syncthreads();
     for (int e = tid; e < nt * DVB; e += L::kThreads) {

@@ -31,6 +31,11 @@
 // cut into segments.  A first pass sums each segment's own state (no Q, no
 // output), a scan composes the states that segments start from, and the full
 // pass runs every segment at once.
+//
+// Measured: two rows of 32 768 tokens, 32 heads of 128 channels, 460 us, 4.7 TB/s
+// (0.70 of a copy's); 17 ragged prompts, 16 heads, 145 us; one row of 131 072
+// tokens, 16 heads, 673 us (260 of them the first pass).  A chunk takes some 3700
+// cycles, the products 1700 of them; without V', P and the stores it is 2500.
 #include <cudaTypedefs.h>
 
 #include "kda_linear.cuh"
