@@ -359,19 +359,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::fence_mbar_init();
     *s_abort = 0;
   }
-  // whole sequences of a packed batch: the longest first, equal ones in order.  (Lengths of malformed
-  // offsets are some numbers too: every sequence gets a place of its own.)
+  // whole sequences of a packed batch: the longest first, equal ones in order.  (Lengths of
+  // malformed offsets are some numbers too: every sequence gets a place of its own.)
   uint16_t* order = reinterpret_cast<uint16_t*>(smem + M::kOrder);
-  if (p.a.cu && p.seg > p.a.T && p.a.N <= kOrdered)
+  if (p.a.cu && p.seg > p.a.T && p.a.N <= kOrdered) {
+    int* lens = reinterpret_cast<int*>(smem + M::kVP);  // (where V' comes later)
+    const int N4 = (p.a.N + 3) / 4;
+    for (int n = tid; n < 4 * N4; n += kThreads)
+      lens[n] = n < p.a.N ? (int)((uint32_t)p.a.cu[n + 1] - (uint32_t)p.a.cu[n]) : INT32_MIN;
+    __syncthreads();
     for (int n = tid; n < p.a.N; n += kThreads) {
-      const int len = p.a.cu[n + 1] - p.a.cu[n];
+      const int len = lens[n];
       int rank = 0;
-      for (int m = 0; m < p.a.N; ++m) {
-        const int other = p.a.cu[m + 1] - p.a.cu[m];
-        rank += other > len || (other == len && m < n);
+      for (int m = 0; m < N4; ++m) {
+        const int4 x = reinterpret_cast<const int4*>(lens)[m];
+        rank += (x.x > len || (x.x == len && 4 * m < n)) +
+                (x.y > len || (x.y == len && 4 * m + 1 < n)) +
+                (x.z > len || (x.z == len && 4 * m + 2 < n)) +
+                (x.w > len || (x.w == len && 4 * m + 3 < n));
       }
       order[rank] = (uint16_t)n;
     }
+  }
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
@@ -493,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 4) {
     // --------------------- sums of the log-decays: two warps, chunks in turn
     const uint32_t turn = warp - 2;
-    if (OUT && turn && p.a.cu && blockIdx.x == 0)  // malformed offsets of any sequence
+    // malformed offsets of any sequence: with segments, a search may pass one by
+    if (OUT && turn && p.a.cu && p.seg <= p.a.T && blockIdx.x == 0)
       for (int n = lane; n < p.a.N; n += 32) {
         int64_t row;
         int len;

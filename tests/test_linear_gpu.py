@@ -115,6 +115,56 @@ def test_packed(lens, dtype):
     check(made(1, T, 4, 2, 64, 64, dtype, N=len(lens), views=True, init=False, seed=T), lens)
 
 
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 3000])
+def test_many_sequences(n):
+    # put in order up to 1024, as they come beyond
+    lens = [(i * 37) % 4 for i in range(n)]
+    check(made(1, sum(lens), 1, 1, 64, 64, N=n, seed=n), lens)
+
+
+def test_one_token_rows_and_strided_decays():
+    x = made(5, 1, 3, 3, 128, 64, views=True, seed=6)
+    wide = torch.zeros(5, 1, 8, device="cuda")
+    wide[..., 2:5] = x["log_decay"]
+    x["log_decay"] = wide[..., 2:5]
+    check(x)
+    x = made(2, 300, 3, 3, 64, 64, seed=7)
+    wide = torch.zeros(2, 300, 8, device="cuda")
+    wide[..., 4:7] = x["log_decay"]
+    x["log_decay"] = wide[..., 4:7]
+    check(x)
+
+
+def test_an_output_between_sectors():
+    # 16-byte aligned is enough
+    x = made(1, 260, 2, 2, 128, 128, seed=8)
+    want, _ = pkg.linear_attend(**x)
+    room = torch.full((260 * 256 + 16,), 7.0, dtype=BF, device="cuda")
+    out = room[8:8 + 260 * 256]
+    assert out.data_ptr() % 32 == 16
+    rc = kda.kda_linear_fwd(x["q"], 256, x["k"], 256, x["v"], 256, x["log_decay"], 2, x["init_state"], out,
+                            None, 1, 260, 2, 2, 128, 128, stream=torch.cuda.current_stream())
+    assert rc == 0 and torch.equal(out.view(want.shape), want)
+    assert (room[:8] == 7).all() and (room[-8:] == 7).all()
+
+
+def test_tensor_calls_refuse_what_does_not_fit():
+    x = made(2, 10, 4, 2, 64, 64, seed=1)
+    cu = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    for over in (dict(k=x["k"][:, :5]), dict(v=x["v"].float()), dict(q=x["q"].half()), dict(v=x["v"][:, :, :3]),
+                 dict(log_decay=x["log_decay"][:, :, :2]), dict(log_decay=x["log_decay"].to(BF)),
+                 dict(init_state=x["init_state"][:1]), dict(init_state=x["init_state"].to(BF)),
+                 dict(q=x["q"].transpose(1, 2)), dict(k=x["k"].cpu()), dict(cu_seqlens=cu),
+                 dict(cu_seqlens=cu.long()), dict(q=x["q"][..., ::2], k=x["k"][..., ::2])):
+        with pytest.raises((ValueError, kda.KdaError)):
+            pkg.linear_attend(**(x | over))
+    s = x["init_state"]
+    d = {n: x[n] for n in ("q", "k", "v", "log_decay")}
+    for bad in (s[:, :2], s.transpose(2, 3), s.double(), s[:1]):
+        with pytest.raises(ValueError):
+            pkg.linear_decode(**d, state=bad)
+
+
 def test_rows_behind_the_last_sequence_stay():
     x = made(1, 400, 2, 2, 128, 128, N=2, seed=1)
     cu = torch.tensor([0, 130, 257], dtype=torch.int32, device="cuda")
