@@ -10,7 +10,7 @@
 // A CTA takes items (a sequence or a segment of one, a head, 64 value columns)
 // and walks their chunks, its state S in registers (fp32); Q K^T, P V, Q S and
 // K^T V' are tcgen05 products into tensor memory.  One warp feeds Q, K and V by
-// TMA (two chunks ahead), one issues products, two take the decays' sums, and
+// TMA (two or three chunks ahead), one issues products, two take the decays' sums, and
 // sixteen do the same work side by side, each a quarter of the rows and a fourth
 // of the columns: V', S and its operand, P, O.  The products of a chunk run in
 // the order Q S, K^T V', P V, the next chunk's scores; while each runs, the
@@ -34,7 +34,7 @@
 //
 // Measured: two rows of 32 768 tokens, 32 heads of 128 channels, 460 us, 4.7 TB/s
 // (0.70 of a copy's); 17 ragged prompts, 16 heads, 145 us; one row of 131 072
-// tokens, 16 heads, 673 us (260 of them the first pass).  A chunk takes some 3700
+// tokens, 16 heads, 627 us (213 of them the first pass; with two stages 260).  A chunk takes some 3700
 // cycles, the products 1700 of them; without V', P and the stores it is 2500.
 #include <cudaTypedefs.h>
 
@@ -74,8 +74,8 @@ struct alignas(16) Gate {
 };
 
 struct Bars {
-  uint64_t qk_full[2], v_full[2];    // copies have landed
-  uint64_t ds_done[2];               // K^T V' and Q S are there: V', K, Q and S's operand are free
+  uint64_t qk_full[3], v_full[3];    // copies have landed
+  uint64_t ds_done[3];               // K^T V' and Q S are there: V', K, Q and S's operand are free
   uint64_t o_done[2];                // P V is there: V and P are free
   uint64_t s_done;                   // the scores are there
   uint64_t ready[2];                 // V' and S's operand are made, K^T V' and Q S's places read
@@ -83,14 +83,18 @@ struct Bars {
   uint64_t gate_full[kGates], gate_empty[kGates], drain;
 };
 
-template <int DK>
+// The full pass: Q, K and V in two stages, V' and S's operand.  The first pass: K
+// and V in three, V' in two places.
+template <int DK, bool OUT>
 struct Smem {
+  static constexpr int kStages = OUT ? 2 : 3;
   static constexpr int kTile = C * DK * 2;                 // Q or K of a chunk
   static constexpr int kBox = C * 128;                     // 64 channels of it
-  static constexpr int kQ = 0, kK = kQ + 2 * kTile, kV = kK + 2 * kTile;
-  static constexpr int kVP = kV + 2 * kBox;                // V' in two parts
-  static constexpr int kS = kVP + 2 * kBox;                // S as an operand
-  static constexpr int kGate = kS + DK * NV * 2;
+  static constexpr int kQ = 0, kK = OUT ? 2 * kTile : 0, kV = kK + kStages * kTile;
+  static constexpr int kVP = kV + kStages * kBox;          // V' in two parts
+  static constexpr int kVP1 = OUT ? kVP : kVP + 2 * kBox;  // the same of odd chunks
+  static constexpr int kS = kVP1 + 2 * kBox;               // S as an operand
+  static constexpr int kGate = kS + (OUT ? DK * NV * 2 : 0);
   static constexpr int kBars = kGate + kGates * (int)sizeof(Gate);
   static constexpr int kOrder = kBars + (int)sizeof(Bars) + 16;
   static constexpr int kBytes = kOrder + 2 * kOrdered + 1024;  // (and the alignment)
@@ -328,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap map_k,
                            const __grid_constant__ CUtensorMap map_v,
                            const __grid_constant__ TileArgs p) {
-  using M = Smem<DK>;
+  using M = Smem<DK, OUT>;
+  constexpr uint32_t NS = M::kStages;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024u - (sm100::smem_u32(raw) & 1023u)) & 1023u);
   Gate* gates = reinterpret_cast<Gate*>(smem + M::kGate);
@@ -342,10 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       sm100::mbar_init(&bars.qk_full[i], 1);
       sm100::mbar_init(&bars.v_full[i], 1);
       sm100::mbar_init(&bars.ds_done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&bars.o_done[i], 1);
       sm100::mbar_init(&bars.ready[i], kWorkers);
     }
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------ Q, K and V come
     uint32_t g = 0;
     for (Walk<OUT> w(p, order); w.valid; w.next(), ++g) {
-      const uint32_t s = g & 1, use = g >> 1;
+      const uint32_t s = g % NS, use = g / NS;
       const int row = (int)(w.it.row + w.t), hk = w.it.hk;
       // (in the order in which the products let go of them)
       if (use > 0 && !wait(&bars.ds_done[s], use - 1)) break;
@@ -427,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     // copies in flight end before the CTA does
-    for (uint32_t i = g < 2 ? 0 : g - 2; i < g; ++i) {
-      sm100::mbar_wait(&bars.qk_full[i & 1], (i >> 1) & 1, 200000000ull);
-      sm100::mbar_wait(&bars.v_full[i & 1], (i >> 1) & 1, 200000000ull);
+    for (uint32_t i = g < NS ? 0 : g - NS; i < g; ++i) {
+      sm100::mbar_wait(&bars.qk_full[i % NS], (i / NS) & 1, 200000000ull);
+      sm100::mbar_wait(&bars.v_full[i % NS], (i / NS) & 1, 200000000ull);
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- products
@@ -441,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at = (uint32_t)sm100::smem_desc(sm100::smem_u32(smem), M::kBox, 1024);
     const uint32_t hi = (uint32_t)(sm100::smem_desc_sw128(0, M::kBox, 1024) >> 32);
     const uint32_t dq = at + M::kQ / 16, dk = at + M::kK / 16, dv = at + M::kV / 16;
-    // (the first pass has V' and its product by stage, in places that only the full one uses)
-    const uint32_t dvp = at + M::kVP / 16, dvp1 = OUT ? dvp : at + M::kQ / 16;
+    // (the first pass has V' and its product twice, by odd and even chunks)
+    const uint32_t dvp = at + M::kVP / 16, dvp1 = at + M::kVP1 / 16;
     const uint64_t st = sm100::smem_desc(sm100::smem_u32(smem) + M::kS, 1024, 128);
     const uint32_t dst = (uint32_t)st, st_hi = (uint32_t)(st >> 32);
     // every thread takes the same way (and the compiler knows)
@@ -464,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // chunk g; false: the last one, or a wait gave up
     auto chunk = [&]() -> bool {
-      const uint32_t s = g & 1;
-      if (!all((OUT || wait(&bars.qk_full[s], g >> 1)) && wait(&bars.ready[s], g >> 1))) return false;
+      const uint32_t s = g % NS, odd = g & 1;
+      if (!all((OUT || wait(&bars.qk_full[s], g / NS)) && wait(&bars.ready[odd], g >> 1))) return false;
       sm100::tc_fence_after();
       if (OUT) {
 #pragma unroll
@@ -475,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (uint32_t k = 0; k < 2; ++k)
-        mma4_ss<128, 128>(!OUT && s ? TM_S : TM_DS, dk + s * kTile16 + 512 * k,
-                          (s ? dvp1 : dvp) + 512 * k, hi, hi, id_d, k, one);
+        mma4_ss<128, 128>(!OUT && odd ? TM_S : TM_DS, dk + s * kTile16 + 512 * k,
+                          (odd ? dvp1 : dvp) + 512 * k, hi, hi, id_d, k, one);
       commit(&bars.ds_done[s], one);
       w.next();
       const bool next = all(w.valid);
@@ -582,9 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                    : x > -0.5f ? make_float2(f, m - (f - 1.0f))
                                : make_float2(expf(x), 0.0f);
       }
-      // (this warp's chunks are those of one stage: it sees each of its copies land)
-      const uint32_t s = g & 1;
-      if (!wait(&bars.qk_full[s], g >> 1) || !wait(&bars.v_full[s], g >> 1)) break;
+      // In the full pass this warp's chunks are those of one stage, and it sees each of its copies
+      // land.  In the first it only looks at a chunk that ends inside: there it may be ahead of the
+      // copy before in the same place, whose chunk has to be over, as a wait tells a phase only
+      // from the one before.
+      const uint32_t s = g % NS;
+      if (OUT || L < C) {
+        if (!OUT && g >= NS && !wait(&bars.gate_empty[(g - NS) % kGates], (g - NS) / kGates)) break;
+        if (!wait(&bars.qk_full[s], g / NS) || !wait(&bars.v_full[s], g / NS)) break;
+      }
       if (L < C) {
         // rows past the end, which belong to others: zeros, whatever they hold
         const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -664,10 +677,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // V' of chunk g, 16 bytes a thread at a time (rows of V past the end are zeros by then).
     auto weigh = [&](uint32_t g) -> bool {
-      const uint32_t s = g & 1, slot = g % kGates;
-      if (!wait(&bars.gate_full[slot], g / kGates)) return false;  // (and V is there)
+      const uint32_t s = g % NS, slot = g % kGates;
+      if (!wait(&bars.gate_full[slot], g / kGates)) return false;  // (in the full pass V is there)
+      if (!OUT && !wait(&bars.v_full[s], g / NS)) return false;
       const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox);
-      uint4* to = reinterpret_cast<uint4*>(smem + (!OUT && s ? M::kQ : M::kVP));
+      uint4* to = reinterpret_cast<uint4*>(smem + (g & 1 ? M::kVP1 : M::kVP));
       const f32x2 minus = pair(-1.0f, -1.0f);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -717,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ahead.next();
       }
       if (old) {
-        if (!wait(&bars.ds_done[s], g >> 1)) break;
+        if (!wait(&bars.ds_done[g % NS], g / NS)) break;
         sm100::tc_fence_after();
         float x[16], y[16];
         const uint32_t from = tm + (!OUT && s ? TM_S : TM_DS) + c0;
@@ -942,12 +956,12 @@ template <int DK, bool OUT>
 kda_status launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                   const TileArgs& p, cudaStream_t s) {
   auto kernel = kda_linear_tile_kernel<DK, OUT>;
-  const kda_status rc = kda_smem_attr((const void*)kernel, Smem<DK>::kBytes);
+  const kda_status rc = kda_smem_attr((const void*)kernel, Smem<DK, OUT>::kBytes);
   if (rc != KDA_OK) return rc;
   const int64_t items = (int64_t)p.cols * p.a.H * p.halves;  // (below 2^30: N * H is)
   const int sms = kda_device_sms();
   const unsigned grid = (unsigned)(items < sms ? items : sms);
-  kernel<<<grid, kThreads, Smem<DK>::kBytes, s>>>(q, k, v, p);
+  kernel<<<grid, kThreads, Smem<DK, OUT>::kBytes, s>>>(q, k, v, p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
