@@ -38,12 +38,16 @@
 // cycles, the products 1700 of them; without V', P and the stores it is 2500.
 #include <cudaTypedefs.h>
 
+#include "kda_cache_attn.cuh"
 #include "kda_linear.cuh"
 #include "kda_tc_util.cuh"
 
 namespace {
 
 using namespace kda_linear;
+using kda_cache::kernel_may_follow;
+using kda_cache::launch_following;
+using kda_cache::wait_for_kernel_before;
 
 constexpr int C = 128;          // tokens of a chunk
 constexpr int NV = 64;          // value columns of a CTA
@@ -341,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::kBars + sizeof(Bars));
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!OUT) kernel_may_follow();
 
   if (warp == 1) {
     sm100::tmem_alloc(s_tmem, kTmemCols);
@@ -717,6 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The full pass begins and ends a chunk by the same code, one chunk apart: chunk g's K^T V' and
     // O (`old`), chunk g + 1's V', operand of S and P (`more`).  The first pass, whose V' and
     // product have two places each, makes V' of chunk g + 1 before it waits for chunk g's product.
+    // (the full pass of segments starts while the scan is at work: Q, K, V and the decays were
+    // there before the first pass, and the states are what it waits for here)
+    if (OUT && p.states) wait_for_kernel_before();
     bool more = enter(), old = false;
     Walk<OUT> ahead(p, order, !OUT);
     for (uint32_t g = ~0u; more || old; ++g) {
@@ -861,6 +869,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // last one's place.
 constexpr int kScanThreads = 256;
 __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const TileArgs p) {
+  kernel_may_follow();
+  wait_for_kernel_before();
   const int size = p.a.dk * p.a.dv, blocks = size / (4 * kScanThreads);
   const int unit = blockIdx.x / blocks, n = unit / p.a.H, h = unit - n * p.a.H;
   const int e = 4 * ((blockIdx.x - unit * blocks) * kScanThreads + threadIdx.x);
@@ -961,6 +971,8 @@ kda_status launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap&
   const int64_t items = (int64_t)p.cols * p.a.H * p.halves;  // (below 2^30: N * H is)
   const int sms = kda_device_sms();
   const unsigned grid = (unsigned)(items < sms ? items : sms);
+  if (OUT && p.states)
+    return launch_following(kernel, grid, kThreads, Smem<DK, OUT>::kBytes, s, q, k, v, p);
   kernel<<<grid, kThreads, Smem<DK, OUT>::kBytes, s>>>(q, k, v, p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -972,8 +984,8 @@ kda_status run(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
     kda_status rc = launch<DK, false>(q, k, v, p, s);
     if (rc != KDA_OK) return rc;
     const unsigned grid = (unsigned)(p.a.N * p.a.H * (p.a.dk * p.a.dv / (4 * kScanThreads)));
-    kda_linear_scan_kernel<<<grid, kScanThreads, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    rc = launch_following(kda_linear_scan_kernel, grid, kScanThreads, 0, s, p);
+    if (rc != KDA_OK) return rc;
   }
   return launch<DK, true>(q, k, v, p, s);
 }
