@@ -3,9 +3,13 @@
 // Pair i of a head's first `part` channels is turned by t = position * f_i
 // (or -t): (x, y) -> amplitude * (x cos t - y sin t, x sin t + y cos t).
 // The angle is taken in whole turns as a 64-bit fraction: f / 2 pi times 2^64
-// as an integer times the position, modulo 2^64, which is what is left of a
-// turn to 2^-33 of one at any 31-bit position, with no reduction of large
-// angles; sincospif takes it in half turns.
+// as an integer times the position, modulo 2^64, with no reduction of large
+// angles; sincospif takes it in half turns.  The quotient is formed in two parts
+// (one 64-bit floating point number of it would err by up to 2^-54 of itself, times
+// the position: 2^-18 of a turn at positions near 2^31 and 100 radians a token) and
+// errs by 2^-64 of a turn each: at most 2^-32 of one at any 31-bit position.  That is
+// a dozen 64-bit floating point operations, slow here, so a CTA does it once for each
+// frequency and its threads read the integers from shared memory.
 //
 // A thread turns eight pairs of one token in up to eight heads (fewer where the
 // batch is small): their sines and cosines are taken once and stay in registers,
@@ -87,8 +91,20 @@ __device__ __forceinline__ void store8(T* p, const Vec<T>& v) {
   }
 }
 
+// What a token turns at f radians, in units of 2^-64 of a turn.
+__device__ __forceinline__ uint64_t turn_of(double f) {
+  // 1 / 2 pi to some 107 bits
+  constexpr double c = 0.15915494309189535, c_lo = -9.839338337591243e-18;
+  const double hi = f * c, lo = fma(f, c_lo, fma(f, c, -hi));
+  return (uint64_t)__double2ll_rn((hi - rint(hi)) * 18446744073709551616.0) +
+         (uint64_t)__double2ll_rn((lo - rint(lo)) * 18446744073709551616.0);
+}
+
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs p) {
+  __shared__ __align__(16) uint64_t s_turn[256];  // (d is at most 512)
+  for (int i = threadIdx.x; i < p.part / 2; i += kThreads) s_turn[i] = turn_of(p.freq[i]);
+  __syncthreads();
   // a unit: 16 channels of a head (eight pairs, or two pieces to copy)
   const int units = p.d / 16;
   const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -114,9 +130,7 @@ __global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs p
   float c[8], s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    double f = p.freq[8 * u + i] * 0.15915494309189533577;  // turns a token
-    f -= floor(f);
-    const uint64_t turn = (uint64_t)(f * 18446744073709551616.0) * (uint64_t)(uint32_t)pos;
+    const uint64_t turn = s_turn[8 * u + i] * (uint64_t)(uint32_t)pos;
     sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s[i], &c[i]);
     c[i] *= p.amplitude;
     s[i] *= p.inverse ? -p.amplitude : p.amplitude;

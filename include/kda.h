@@ -631,8 +631,9 @@ kda_status kda_linear_decode(const void* q, int64_t q_stride, const void* k, int
  *   positions    device int32 [T]
  *   frequencies  device double [part / 2], radians a token (8-byte aligned)
  * d and part are multiples of 16, d at most 512; T <= 2^30; dtype KDA_BF16 or
- * KDA_F32.  Angles are taken modulo a turn in 64-bit integers: positions far
- * out lose nothing.  The products are fp32, rounded once.
+ * KDA_F32.  Angles are taken modulo a turn in 64-bit integers, to 2^-32 of a
+ * turn at any position: positions far out lose nothing that their sine and
+ * cosine in fp32 would keep.  The products are fp32, rounded once.
  */
 kda_status kda_rotary(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
                       const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride,
