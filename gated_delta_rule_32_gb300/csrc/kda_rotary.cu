@@ -103,7 +103,13 @@ __device__ __forceinline__ uint64_t turn_of(double f) {
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs p) {
   __shared__ __align__(16) uint64_t s_turn[256];  // (d is at most 512)
-  for (int i = threadIdx.x; i < p.part / 2; i += kThreads) s_turn[i] = turn_of(p.freq[i]);
+  __shared__ __align__(16) float s_amplitude[256];
+  for (int i = threadIdx.x; i < p.part / 2; i += kThreads) {
+    const double f = p.freq[i];
+    s_turn[i] = turn_of(f);
+    // (integers have no NaN: what a frequency that is no number turns gets one here)
+    s_amplitude[i] = isfinite(f) ? p.amplitude : __int_as_float(0x7fffffff);
+  }
   __syncthreads();
   // a unit: 16 channels of a head (eight pairs, or two pieces to copy)
   const int units = p.d / 16;
@@ -132,8 +138,9 @@ __global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs p
   for (int i = 0; i < 8; ++i) {
     const uint64_t turn = s_turn[8 * u + i] * (uint64_t)(uint32_t)pos;
     sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s[i], &c[i]);
-    c[i] *= p.amplitude;
-    s[i] *= p.inverse ? -p.amplitude : p.amplitude;
+    const float amplitude = s_amplitude[8 * u + i];
+    c[i] *= amplitude;
+    s[i] *= p.inverse ? -amplitude : amplitude;
   }
   const int a = INTER ? 16 * u : 8 * u, b = INTER ? a + 8 : p.part / 2 + 8 * u;
   // (the loads of several heads before their first store)

@@ -629,7 +629,8 @@ kda_status kda_linear_decode(const void* q, int64_t q_stride, const void* k, int
  *     contiguous, 16-byte aligned.  An output is its input (the same pointer
  *     and stride: in place) or overlaps nothing.  Hq or Hk may be 0.
  *   positions    device int32 [T]
- *   frequencies  device double [part / 2], radians a token (8-byte aligned)
+ *   frequencies  device double [part / 2], radians a token (8-byte aligned); a
+ *                NaN or an infinity makes its pair NaN
  * d and part are multiples of 16, d at most 512; T <= 2^30; dtype KDA_BF16 or
  * KDA_F32.  Angles are taken modulo a turn in 64-bit integers, to 2^-32 of a
  * turn at any position: positions far out lose nothing that their sine and

@@ -90,3 +90,18 @@ def test_angles_far_out(name, interleaved, dtype):
                 tol = half * want.abs() + (1 + half) * 2.0 ** -20.5 * size
                 assert (err <= tol).all(), (at, w, (err / tol).max())
         assert torch.equal(got[..., 16:], y[..., 16:])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_frequencies_that_are_no_numbers(dtype):
+    # as a position times an infinity or a NaN has no sine: the pair is NaN, at position 0 too,
+    # and nothing else is
+    x = torch.ones(3, 2, 48, dtype=dtype, device="cuda")
+    f = torch.full((16,), 0.5, dtype=torch.float64, device="cuda")
+    f[2], f[5], f[11] = math.inf, -math.inf, math.nan
+    p = torch.tensor([0, 1, 1 << 30], dtype=torch.int32, device="cuda")
+    for interleaved in (False, True):
+        y, _ = pkg.rotary_embed(x, None, p, f, interleaved=interleaved)
+        bad = {(2 * i + k) if interleaved else (i + 16 * k) for i in (2, 5, 11) for k in (0, 1)}
+        want = torch.tensor([c in bad for c in range(48)], device="cuda").expand(3, 2, 48)
+        assert torch.equal(y.isnan(), want) and bool(y[~want].isfinite().all())
