@@ -48,7 +48,8 @@ def rotary_frequencies(part, base=10000.0, scaling=None, factor=1.0, trained=409
         def at(n):
             return part * math.log(trained / (2 * math.pi * n)) / (2 * math.log(base))
         lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), part - 1)
-        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        # (hi <= 0: not even the fastest pair makes more than `slow` turns)
+        ramp = ((i - lo) / (hi - lo)).clamp(0.0, 1.0) if hi > lo else (i >= hi).double()
         f = f * (1 - ramp) + f / factor * ramp
         amplitude = 0.1 * math.log(factor) + 1.0
     else:
