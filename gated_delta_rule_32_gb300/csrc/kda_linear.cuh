@@ -48,6 +48,11 @@ __device__ __forceinline__ bool span(const LinearArgs& p, int n, int64_t& row, i
 // A log-decay as the operator takes it: at most 0 (a NaN stays one).
 __device__ __forceinline__ float clamp_decay(float a) { return a > 0.0f ? 0.0f : a; }
 
+// Whether a token forgets what is before it: e^-104 is below half of the least fp32 number, so
+// the factor is 0.  The state is then dropped, not multiplied: it may hold anything.  (Factors
+// that only come to 0 together, over many tokens, are products: a NaN stays.)
+__device__ __forceinline__ bool forgets(float a) { return a < -104.0f; }
+
 }  // namespace kda_linear
 
 kda_status kda_launch_linear_rec(const kda_linear::LinearArgs& p, kda_dtype dtype,

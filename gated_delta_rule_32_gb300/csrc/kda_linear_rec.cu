@@ -105,13 +105,17 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
     if (tid < nt) {
       const float x = clamp_decay(fa);
       const float m = expm1f(x), e = 1.0f + m;
-      s_e[tid] = x > -0.5f ? e : expf(x);
+      s_e[tid] = forgets(x) ? -1.0f : x > -0.5f ? e : expf(x);
       s_l[tid] = x > -0.5f ? m - (e - 1.0f) : 0.0f;
     }
     if (t0 + TB < len) fetch(t0 + TB);
     __syncthreads();
     for (int t = 0; t < nt; ++t) {
       const float e = s_e[t], l = s_l[t];
+      if (e < 0.0f) {  // (the same for all: what it is multiplied by next is finite)
+#pragma unroll
+        for (int r = 0; r < L::R; ++r) S[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
       const float4 vv = *reinterpret_cast<const float4*>(&s_v[t][cl]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

@@ -65,7 +65,7 @@ struct TileArgs {
   int cols;        // (sequence, segment) columns; packed: the most there can be
   int halves;      // dv / NV
   float* states;   // [cols, H, dk, dv]: what segments end with (first pass), then start from
-  float2* gammas;  // [cols, H] a segment's decay factor, in two parts
+  float2* gammas;  // [cols, H] a segment's decay factor, in two parts (-1, 0: it forgets)
 };
 
 struct alignas(16) Gate {
@@ -74,7 +74,9 @@ struct alignas(16) Gate {
   float row[C];    // scale * 2^G_i
   float v[C];      // 2^(E - G_j)
   int2 end[4];     // G of the last token of each 32, in units of 2^-16 and 2^-40
-  float2 gamma;    // 2^E in two parts
+  float gamma[2];  // 2^E in two parts
+  int first;       // the first token that forgets, C if there is none
+  int unused;
 };
 
 struct Bars {
@@ -540,12 +542,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int L = w.rows();
       // fixed point, exact in its sums: 2^-16 and 2^-40 a unit
       int hi[4], lo[4], sum_hi = 0, sum_lo = 0;
-      uint32_t nan = 0;
+      uint32_t nan = 0, cut = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         // 2^-160 vanishes in 32 bits: what decays more than that decays so much
         const float c = clamp_decay(y[e]) * 1.4426950408889634f, x = c < -160.0f ? -160.0f : c;
         nan |= (x != x) << e;
+        cut |= forgets(y[e]) << e;
         const int i = __float2int_rn(x * 65536.0f);
         hi[e] = sum_hi += i;
         lo[e] = sum_lo += __float2int_rn(fmaf((float)i, -1.0f / 65536.0f, x) * 1099511627776.0f);
@@ -563,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int blk_hi = __shfl_sync(~0u, sum_hi, lane | 7), blk_lo = __shfl_sync(~0u, sum_lo, lane | 7);
       const int pre_hi = sum_hi - hi[3], pre_lo = sum_lo - lo[3];
       // a NaN makes what follows it NaN
-      const uint32_t bad = __ballot_sync(~0u, nan != 0);
+      const uint32_t bad = __ballot_sync(~0u, nan != 0), cuts = __ballot_sync(~0u, cut != 0);
+      const int at = __ffs(cuts) - 1, first = cuts ? 4 * at + __ffs(__shfl_sync(~0u, cut, at)) - 1 : C;
       if (use > 0 && !wait(&bars.gate_empty[slot], use - 1)) break;
       Gate& gt = gates[slot];
       float back[4], col[4], row[4], v[4];
@@ -590,9 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // close to 1, as 1 + (2^E - 1) and what that lost (see the kernel for single tokens)
         const float x = fixed(end_hi, end_lo) * 0.6931471805599453f;
         const float m = expm1f(x), f = 1.0f + m;
-        gt.gamma = bad ? make_float2(none, none)
-                   : x > -0.5f ? make_float2(f, m - (f - 1.0f))
-                               : make_float2(expf(x), 0.0f);
+        const float2 g2 = bad         ? make_float2(none, none)
+                          : x > -0.5f ? make_float2(f, m - (f - 1.0f))
+                                      : make_float2(expf(x), 0.0f);
+        *reinterpret_cast<float4*>(gt.gamma) = make_float4(g2.x, g2.y, __int_as_float(first), 0.0f);
       }
       // In the full pass this warp's chunks are those of one stage, and it sees each of its copies
       // land.  In the first it only looks at a chunk that ends inside: there it may be ahead of the
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool whole = (reinterpret_cast<uint64_t>(p.a.out) & 31) == 0;
     f32x2 S[8];
     float* to = nullptr;  // where the item's state goes
-    double all = 1.0;     // a segment's decay
+    double all = 1.0;     // a segment's decay, -1 where it forgets
     Item it{};
     int id = blockIdx.x, t = 0;
     auto leave = [&]() {
@@ -745,15 +750,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t from = tm + (!OUT && s ? TM_S : TM_DS) + c0;
         sm100::tmem_ld16(from, x);
         sm100::tmem_ld16(from + NV, y);
-        const float2 f = gates[slot].gamma;
+        const float4 f = *reinterpret_cast<const float4*>(gates[slot].gamma);
+        const bool forget = __float_as_int(f.z) < C;
         const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
         sm100::tmem_wait_ld();
         sm100::tc_fence_before();
+        if (forget) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) S[e] = pair(0.0f, 0.0f);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           S[e] = fma2(hi, S[e], fma2(lo, S[e], add2(pair(x[2 * e], x[2 * e + 1]),
                                                     pair(y[2 * e], y[2 * e + 1]))));
-        if (!OUT) all *= (double)f.x + (double)f.y;
+        if (!OUT) all = forget || all < 0.0 ? -1.0 : all * ((double)f.x + (double)f.y);
         t += C;
         if (t >= it.len) {
           leave();
@@ -776,6 +786,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm100::tmem_ld16(tm + TM_O2 + c0, y);
         sm100::tmem_wait_ld();
         sm100::tc_fence_before();
+        const int first = gates[slot].first;
+        if (first < C) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = row >= first ? 0.0f : x[e];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           rows[e] = bf16x2(fma2(ff, pair(x[2 * e], x[2 * e + 1]),
@@ -898,6 +913,7 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Til
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (s0 + k < segs - 1) {
+        if (f[k].x < 0.0f) x = make_float4(0.f, 0.f, 0.f, 0.f);
         x.x = fmaf(f[k].x, x.x, fmaf(f[k].y, x.x, y[k].x));
         x.y = fmaf(f[k].x, x.y, fmaf(f[k].y, x.y, y[k].y));
         x.z = fmaf(f[k].x, x.z, fmaf(f[k].y, x.z, y[k].z));

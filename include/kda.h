@@ -552,8 +552,9 @@ size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv
  *   S_t = exp(a_t) S_{t-1} + k_t v_t^T          (S: dk x dv)
  *   o_t = scale * S_t^T q_t
  *
- * A log-decay of -infinity forgets everything before its token; one above 0
- * counts as 0, a NaN makes what follows it NaN.
+ * A log-decay below -104, -infinity among them, has a factor of 0 in 32 bits: its
+ * token forgets the state before it, whatever that holds (an infinity, a NaN, what
+ * nobody wrote).  One above 0 counts as 0, a NaN makes what follows it NaN.
  *
  *   q, k       [rows, Hk, dk]   rows q_stride, k_stride elements apart
  *   v          [rows, H, dv]    v_stride; out [rows, H, dv] contiguous
@@ -569,7 +570,9 @@ size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv
  * Sums and states are fp32.  What lies outside the rows of a sequence never
  * reaches its results, whatever it is.  Inside one, prompts on the tensor cores
  * multiply values by weights that are 0 for the tokens before them: a NaN or an
- * infinity in v reaches all rows of its 128 tokens, not only those behind it.
+ * infinity in v reaches all rows of its 128 tokens, not only those behind it, and
+ * one in k, v or log_decay goes on into the state unless a token of a later 128
+ * forgets it.
  */
 
 /*
