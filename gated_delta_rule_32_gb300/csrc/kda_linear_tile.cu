@@ -401,8 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (the whole of tensor memory is this CTA's: its columns count from 0)
   const uint32_t tmem = 0;
 
-  auto wait = [&](uint64_t* bar, uint32_t n) -> bool {  // the barrier's phase n
-    return bounded_wait(bar, n & 1, s_abort);
+  // The barrier's phase n.  The warp's threads leave together and with one answer: what comes
+  // next (loads and stores of tensor memory, shuffles, products) is for whole warps, and a wait
+  // that gives up ends the role for all of them.
+  auto wait = [&](uint64_t* bar, uint32_t n) -> bool {
+    return __all_sync(~0u, bounded_wait(bar, n & 1, s_abort));
   };
   // a warp's arrival, after all of its threads' work before it
   auto arrive = [&](uint64_t* bar) {
@@ -472,14 +475,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk<OUT> w(p, order);
     bool more = all(w.valid);
     if (OUT && more) {
-      more = all(wait(&bars.qk_full[0], 0));
+      more = wait(&bars.qk_full[0], 0);
       sm100::tc_fence_after();
       if (more) scores(0);
     }
     // chunk g; false: the last one, or a wait gave up
     auto chunk = [&]() -> bool {
       const uint32_t s = g % NS, odd = g & 1;
-      if (!all((OUT || wait(&bars.qk_full[s], g / NS)) && wait(&bars.ready[odd], g >> 1))) return false;
+      if (!OUT && !wait(&bars.qk_full[s], g / NS)) return false;
+      if (!wait(&bars.ready[odd], g >> 1)) return false;
       sm100::tc_fence_after();
       if (OUT) {
 #pragma unroll
@@ -495,14 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.next();
       const bool next = all(w.valid);
       if (OUT) {
-        if (!all(wait(&bars.p_full, g))) return false;
+        if (!wait(&bars.p_full, g)) return false;
         sm100::tc_fence_after();
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k)
           mma4_ts<128>(TM_O2, TM_P + 32 * k, dv + s * kBox16 + 512 * k, hi, id_q, k, one);
         commit(&bars.o_done[s], one);
         if (next) {
-          if (!all(wait(&bars.qk_full[s ^ 1], (g + 1) >> 1))) return false;
+          if (!wait(&bars.qk_full[s ^ 1], (g + 1) >> 1)) return false;
           sm100::tc_fence_after();
           scores(s ^ 1);
         }
