@@ -16,7 +16,7 @@
 // A decode step is bound by the states' bytes: 64 sequences, 32 heads of 128 x
 // 128 take 43 us, 6.3 TB/s (inputs fetched after the states: 50 us).  Long runs
 // are bound by the chain of tokens, some 180 ns each: 2 rows of 333 tokens, 4
-// heads of 64 x 32, fp32, 59 us.
+// heads of 64 x 32, fp32, 62 us.
 //
 // A slow decay's factor is close to 1, and its rounding to 24 bits would be the
 // same at every token: 2^-25 times 10 000 tokens is more than the sums' own
@@ -35,8 +35,9 @@ struct Rec {
   static constexpr int R = DK / RG;             // rows of a thread: RG apart
   static constexpr int kWarps = kThreads / 32;
   // tokens at a time, as many as static shared memory has room for (8 instead of 16: 61 us
-  // where 16 take 59)
+  // where 16 took 59)
   static constexpr int TB = DVB <= 32 ? 16 : 8;
+  static constexpr bool kAsk = DVB <= 32;       // a block asks first whether a token forgets
 };
 
 template <typename Tin, int DK, int DVB>
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
   using L = Rec<Tin, DK, DVB>;
   constexpr int TB = L::TB;
   __shared__ float s_k[TB][DK], s_q[TB][DK], s_e[TB], s_l[TB];
+  __shared__ bool s_some;  // a token of the block forgets
   __shared__ __align__(16) float s_v[TB][DVB], s_o[TB][L::kWarps][DVB];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cb = p.dv / DVB;
@@ -102,20 +104,22 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
       const int e = tid + x * L::kThreads, t = e / DVB, c = e - t * DVB;
       if (t < nt) s_v[t][c] = fv[x];
     }
+    bool cut = false;
     if (tid < nt) {
       const float x = clamp_decay(fa);
       const float m = expm1f(x), e = 1.0f + m;
-      s_e[tid] = forgets(x) ? -1.0f : x > -0.5f ? e : expf(x);
+      cut = forgets(x);
+      s_e[tid] = cut ? -1.0f : x > -0.5f ? e : expf(x);
       s_l[tid] = x > -0.5f ? m - (e - 1.0f) : 0.0f;
+    }
+    if (L::kAsk && warp == 0) {
+      cut = __any_sync(0xffffffffu, cut);
+      if (lane == 0) s_some = cut;
     }
     if (t0 + TB < len) fetch(t0 + TB);
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
-      const float e = s_e[t], l = s_l[t];
-      if (e < 0.0f) {  // (the same for all: what it is multiplied by next is finite)
-#pragma unroll
-        for (int r = 0; r < L::R; ++r) S[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+    auto step = [&](int t, float e) {
+      const float l = s_l[t];
       const float4 vv = *reinterpret_cast<const float4*>(&s_v[t][cl]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -138,6 +142,21 @@ __global__ void __launch_bounds__(Rec<Tin, DK, DVB>::kThreads)
         o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
       }
       if (lane < L::CL) *reinterpret_cast<float4*>(&s_o[t][warp][cl]) = o;
+    };
+    // Narrow blocks are bound by the chain of tokens, where a branch on the token's factor takes
+    // time (the case of 62 us above 64): they have it only if one of the block's tokens forgets.
+    // Wide ones have it at each token (the decode step takes 2 % more with two loops).
+    if (L::kAsk && !s_some) {
+      for (int t = 0; t < nt; ++t) step(t, s_e[t]);
+    } else {
+      for (int t = 0; t < nt; ++t) {
+        const float e = s_e[t];
+        if (e < 0.0f) {  // (the same for all: what it is multiplied by next is finite)
+#pragma unroll
+          for (int r = 0; r < L::R; ++r) S[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        step(t, e);
+      }
     }
     __syncthreads();
     for (int e = tid; e < nt * DVB; e += L::kThreads) {

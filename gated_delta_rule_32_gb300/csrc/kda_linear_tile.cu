@@ -286,7 +286,7 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __noinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   const uint64_t t0 = sm100::globaltimer_ns();
   while (!poll(bar, parity))
     if (*abort || sm100::globaltimer_ns() - t0 > 2000000000ull) {
@@ -294,11 +294,6 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
       return false;
     }
   return true;
-}
-__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
-                                             volatile int* abort) {
-  const uint32_t at = sm100::smem_u32(bar);
-  return poll(at, parity) || wait_on(at, parity, abort);
 }
 
 // Two fp32 at a time.
@@ -403,9 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // The barrier's phase n.  The warp's threads leave together and with one answer: what comes
   // next (loads and stores of tensor memory, shuffles, products) is for whole warps, and a wait
-  // that gives up ends the role for all of them.
+  // that gives up ends the role for all of them.  (One vote where the phase is over, on which all
+  // then branch: with the vote behind both ways the two rows took 464 us, with none 453.)
   auto wait = [&](uint64_t* bar, uint32_t n) -> bool {
-    return __all_sync(~0u, bounded_wait(bar, n & 1, s_abort));
+    const uint32_t at = sm100::smem_u32(bar);
+    if (__all_sync(~0u, poll(at, n & 1))) return true;
+    return __all_sync(~0u, bounded_wait(at, n & 1, s_abort));
   };
   // a warp's arrival, after all of its threads' work before it
   auto arrive = [&](uint64_t* bar) {
@@ -637,7 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool whole = (reinterpret_cast<uint64_t>(p.a.out) & 31) == 0;
     f32x2 S[8];
     float* to = nullptr;  // where the item's state goes
-    double all = 1.0;     // a segment's decay, -1 where it forgets
+    double all = 1.0;     // a segment's decay
+    bool gone = false;    // it forgets
     Item it{};
     int id = blockIdx.x, t = 0;
     auto leave = [&]() {
@@ -651,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       if (!OUT && it.half == 0 && tid == 128) {
         const float hi = (float)all;
-        p.gammas[(int64_t)it.col * p.a.H + it.h] = make_float2(hi, (float)(all - (double)hi));
+        p.gammas[(int64_t)it.col * p.a.H + it.h] =
+            gone ? make_float2(-1.0f, 0.0f) : make_float2(hi, (float)(all - (double)hi));
       }
     };
     // the next item with tokens, from id on: its entry state (an empty sequence's state passes)
@@ -684,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         t = 0;
         all = 1.0;
+        gone = false;
         if (it.len > 0) return true;
         leave();
       }
@@ -767,7 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 8; ++e)
           S[e] = fma2(hi, S[e], fma2(lo, S[e], add2(pair(x[2 * e], x[2 * e + 1]),
                                                     pair(y[2 * e], y[2 * e + 1]))));
-        if (!OUT) all = forget || all < 0.0 ? -1.0 : all * ((double)f.x + (double)f.y);
+        if (!OUT) {
+          all *= (double)f.x + (double)f.y;
+          gone |= forget;
+        }
         t += C;
         if (t >= it.len) {
           leave();
