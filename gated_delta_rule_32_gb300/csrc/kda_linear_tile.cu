@@ -601,26 +601,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       : make_float2(expf(x), 0.0f);
         *reinterpret_cast<float4*>(gt.gamma) = make_float4(g2.x, g2.y, __int_as_float(first), 0.0f);
       }
-      // In the full pass this warp's chunks are those of one stage, and it sees each of its copies
-      // land.  In the first it only looks at a chunk that ends inside: there it may be ahead of the
-      // copy before in the same place, whose chunk has to be over, as a wait tells a phase only
-      // from the one before.
-      const uint32_t s = g % NS;
-      if (OUT || L < C) {
-        if (!OUT && g >= NS && !wait(&bars.gate_empty[(g - NS) % kGates], (g - NS) / kGates)) break;
+      // Rows past a sequence's end belong to others: zeros, whatever they hold.  (This warp's
+      // chunks are those of one stage, and it sees each of its copies land: no phase is missed.
+      // Segments of the first pass are whole chunks.)
+      if (OUT) {
+        const uint32_t s = g % NS;
         if (!wait(&bars.qk_full[s], g / NS) || !wait(&bars.v_full[s], g / NS)) break;
-      }
-      if (L < C) {
-        // rows past the end, which belong to others: zeros, whatever they hold
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if (L < C) {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-        for (int e = L * 8 + lane; e < C * 8; e += 32) {
+          for (int e = L * 8 + lane; e < C * 8; e += 32) {
 #pragma unroll
-          for (int b = 0; b < DK / 64; ++b)
-            reinterpret_cast<uint4*>(smem + M::kK + s * M::kTile + b * M::kBox)[e] = zero;
-          reinterpret_cast<uint4*>(smem + M::kV + s * M::kBox)[e] = zero;
+            for (int b = 0; b < DK / 64; ++b)
+              reinterpret_cast<uint4*>(smem + M::kK + s * M::kTile + b * M::kBox)[e] = zero;
+            reinterpret_cast<uint4*>(smem + M::kV + s * M::kBox)[e] = zero;
+          }
+          sm100::fence_async_smem();
         }
-        sm100::fence_async_smem();
       }
       arrive(&bars.gate_full[slot]);
     }
