@@ -79,14 +79,23 @@ struct alignas(16) Gate {
   int unused;
 };
 
+// A wait tells a phase only from its neighbours, so every waiter takes every phase of its
+// barrier in turn, and none can end before all have passed the one before it; why, beside each.
 struct Bars {
-  uint64_t qk_full[3], v_full[3];    // copies have landed
+  uint64_t qk_full[3], v_full[3];    // copies have landed (the next into the same place waits for
+                                     // ds_done or o_done, so for V' and P: made by all behind their
+                                     // waits for it)
   uint64_t ds_done[3];               // K^T V' and Q S are there: V', K, Q and S's operand are free
-  uint64_t o_done[2];                // P V is there: V and P are free
-  uint64_t s_done;                   // the scores are there
+                                     // (the next of a place needs its K, so the copies' warp, and
+                                     // `ready`, which the sixteen give behind theirs)
+  uint64_t o_done[2];                // P V is there: V and P are free (likewise, by V and p_full)
+  uint64_t s_done;                   // the scores are there (the next ones come behind p_full)
   uint64_t ready[2];                 // V' and S's operand are made, K^T V' and Q S's places read
-  uint64_t p_full;                   // P is made, the scores and P V's place read
-  uint64_t gate_full[kGates], gate_empty[kGates], drain;
+                                     // (given again behind ds_done of a chunk that it let begin)
+  uint64_t p_full;                   // P is made, the scores and P V's place read (given again
+                                     // behind s_done, which follows the wait for it)
+  uint64_t gate_full[kGates], gate_empty[kGates];  // (each needs the other's last one)
+  uint64_t drain;
 };
 
 // The full pass: Q, K and V in two stages, V' and S's operand.  The first pass: K
@@ -943,10 +952,15 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How the token axis is cut.  Times in chunks of one CTA: a chunk of the first
-// pass costs 0.4 of one of the full pass, and a second and third launch
-// some six.  Packed lengths are not known here: the longest is taken for twice
-// the mean.
+// How the token axis is cut.  Times in chunks of one CTA (1.7 us): segments cost 0.4 of
+// their chunks and six more.  Both numbers are what the choices went best with; a chunk of
+// the first pass alone takes 0.52 of one of the full pass, but a rule with that number and no
+// price for an item of its own takes many short segments: 4096 tokens of 32 heads go from 64 us
+// (two segments; 67 whole) to 112 (sixteen).  Cut against whole: 4096 tokens of 4 heads 27
+// and 64 us, 32 768 of 4 heads 64 and 451, 131 072 of 16 heads 640 and 1753.  Packed lengths are
+// not known here: the longest is taken for twice the mean.  Where they are all alike that is too
+// long (4 sequences of 4096 tokens, 8 heads: cut, 115 us; whole they would take 67), where one
+// is much longer too short.
 struct Cut {
   int seg, segs, cols;
 };
