@@ -16,13 +16,16 @@ of a projection's output: any distance between tokens, the same for all rows.
 Nothing here computes: tensors are checked, outputs allocated and the library
 called, on the current stream of the tensors' device, or on `stream`, which
 then also owns the outputs' memory.  Errors that the host can see raise
-ValueError or KdaError before anything is queued.
+ValueError or KdaError before anything is queued.  No call has a gradient: where
+one would be lost (gradients are enabled and a tensor wants one) it is refused,
+and autograd learns which tensors have changed in place.
 """
 from __future__ import annotations
 
 import functools
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import kda
 from .cache import _call, _index, _need
@@ -65,6 +68,14 @@ def _decay(a, B, T, H, dev):
     return t if T > 1 else b if B > 1 else H
 
 
+def _forward_only(name, *tensors):
+    if torch.is_grad_enabled():
+        for x in tensors:
+            if x is not None and x.requires_grad:
+                raise ValueError("%s has no gradient, and a tensor wants one: call it under "
+                                 "torch.no_grad(), or detach the tensor" % name)
+
+
 def _state(x, name, shape, dev):
     if x.dtype is not torch.float32 or x.shape != shape or not x.is_contiguous() or \
             x.get_device() != dev:
@@ -100,6 +111,7 @@ def linear_attend(q, k, v, log_decay, init_state=None, cu_seqlens=None, scale=1.
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear_attend(q, k, v, log_decay, init_state, cu_seqlens, scale, dev_status)
+    _forward_only("linear_attend", q, k, v, log_decay, init_state)
     dev, code, qs, ks, vs, ds, B, T, H, Hk, dk, dv = _shapes(q, k, v, log_decay)
     N = B
     if cu_seqlens is not None:
@@ -130,12 +142,14 @@ def linear_decode(q, k, v, log_decay, state, scale=1.0, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear_decode(q, k, v, log_decay, state, scale)
+    _forward_only("linear_decode", q, k, v, log_decay, state)
     dev, code, qs, ks, vs, ds, N, T, H, Hk, dk, dv = _shapes(q, k, v, log_decay)
     _state(state, "state", (N, H, dk, dv), dev)
     out = torch.empty((N, T, H, dv), dtype=q.dtype, device=q.device)
     _launch(dev, "kda_linear_decode", q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
            log_decay.data_ptr(), ds, state.data_ptr(), out.data_ptr(), N, T, H, Hk, dk, dv, code,
            scale)
+    increment_version(state)
     return out
 
 

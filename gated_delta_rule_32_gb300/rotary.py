@@ -12,9 +12,10 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.graph import increment_version
 
 from .cache import _index, _need
-from .linear import _DTYPES, _launch
+from .linear import _DTYPES, _forward_only, _launch
 
 
 def rotary_frequencies(part, base=10000.0, scaling=None, factor=1.0, trained=4096, fast=32.0,
@@ -76,11 +77,13 @@ def rotary_embed(q, k, positions, frequencies, interleaved=False, amplitude=1.0,
     negative position are left as they were (allocated).  frequencies: float64
     [part / 2], radians a token; part <= d channels of each head are turned, in
     pairs (i, i + part / 2) or, interleaved, (2 i, 2 i + 1).  `inverse` turns
-    back, which is also the gradient's map."""
+    back, which is also the gradient's map: autograd has none of its own here, and
+    tensors that want a gradient are refused where gradients are enabled."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return rotary_embed(q, k, positions, frequencies, interleaved, amplitude, inverse,
                                 inplace)
+    _forward_only("rotary_embed", q, k, frequencies)
     dev = _index(q, "q")
     code = _DTYPES.get(q.dtype)
     _need(code is not None and q.dim() == 3, "q must be [T, heads, d], bfloat16 or float32")
@@ -105,4 +108,8 @@ def rotary_embed(q, k, positions, frequencies, interleaved=False, amplitude=1.0,
            None if ko is None else ko.data_ptr(), kos, positions.data_ptr(),
            frequencies.data_ptr(), T, Hq, Hk, d, 2 * frequencies.numel(), amplitude, interleaved,
            inverse, code)
+    if inplace:
+        increment_version(q)
+        if k is not None:
+            increment_version(k)
     return qo, ko
