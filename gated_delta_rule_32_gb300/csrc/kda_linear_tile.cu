@@ -18,10 +18,15 @@
 // V' and O the same work took 1.5 to 2 times as long: four kinds of loops on
 // each scheduler do not fit its instruction caches.)
 //
-// Rounding: P and the state as an operand enter as bf16; rows of Q keep their
-// bits, e^G being applied to the product.  The state itself is summed from V'
-// in two bf16 parts (16 bits), so what is carried and returned is fp32 to
-// about 2^-17.  Sums of log-decays are exact, in fixed point, as their
+// Rounding: P and the state as an operand enter as bf16, as the tensor cores multiply
+// V's 16 bits by nothing wider, and tensor memory and shared memory are full without
+// second parts of them: each is one rounding of 2^-9 beside the output's own
+// (outputs err by 2.3e-3 of their norm, the roundings of the outputs alone are
+// 1.7e-3).  Rows of Q keep their bits, e^G being applied to the product.  The state
+// itself is summed from V' in three bf16 parts, which hold all of its 24 bits: what is
+// carried and returned is fp32 (1.2e-7 of its norm from 64 bits, as plain 32-bit
+// operations; two parts left 2.4e-6, and took 0.9 of the time of a full chip's prompts
+// and 0.85 of a first pass).  Sums of log-decays are exact, in fixed point, as their
 // differences are what counts.  Where a tile lies below the diagonal
 // of 32-token blocks, e^(G_i - G_j) is e^(G_i - G_b) e^(G_b - G_j) with b the
 // last token of j's block: both factors are at most 1, so neither overflows
@@ -52,10 +57,11 @@ using kda_cache::wait_for_kernel_before;
 constexpr int C = 128;          // tokens of a chunk
 constexpr int NV = 64;          // value columns of a CTA
 constexpr int kThreads = 640;
-constexpr int kGates = 4;
-constexpr int kOrdered = 1024;  // most sequences of a packed batch that are put in order
-// tensor memory: scores, P, Q S by stage, P V, K^T V' of V's two parts
+constexpr int kOrdered = 320;   // most sequences of a packed batch that are put in order
+// tensor memory: scores, P, Q S by stage, P V, K^T V' of the first part of V' and of the others
 constexpr uint32_t TM_S = 0, TM_P = 128, TM_O1 = 192, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
+// in the first pass: K^T V' of V's three parts, of even and of odd chunks
+constexpr uint32_t TM_D0 = 0, TM_D1 = 192;
 constexpr int kWorkers = kThreads / 32 - 4;
 
 struct TileArgs {
@@ -68,23 +74,26 @@ struct TileArgs {
   float2* gammas;  // [cols, H] a segment's decay factor, in two parts (-1, 0: it forgets)
 };
 
+// What a chunk's decays come to (G: sums of log2-decays).
 struct alignas(16) Gate {
-  float back[C];   // G_b - G_j, b the last token of j's 32 (sums of log2-decays)
+  float back[C];   // G_b - G_j, b the last token of j's 32
   float col[C];    // 2^(G_b - G_j)
-  float row[C];    // scale * 2^G_i
-  float v[C];      // 2^(E - G_j)
-  int2 end[4];     // G of the last token of each 32, in units of 2^-16 and 2^-40
+  float tail[4];   // 2^(E - G_b) of each 32
+  int2 end[4];     // G_b of each 32, in units of 2^-16 and 2^-40
+};
+struct alignas(16) Total {
   float gamma[2];  // 2^E in two parts
   int first;       // the first token that forgets, C if there is none
   int unused;
 };
+constexpr int kTotals = 4;  // (read until the chunk's rows go out; the next but three comes later)
 
 // A wait tells a phase only from its neighbours, so every waiter takes every phase of its
 // barrier in turn, and none can end before all have passed the one before it; why, beside each.
 struct Bars {
-  uint64_t qk_full[3], v_full[3];    // copies have landed (the next into the same place waits for
-                                     // ds_done or o_done, so for V' and P: made by all behind their
-                                     // waits for it)
+  uint64_t qk_full[3], v_full[2];    // copies have landed (the next into the same place waits for
+                                     // ds_done, o_done or, V in the first pass, ready: so for V'
+                                     // and P, made by all behind their waits for it)
   uint64_t ds_done[3];               // K^T V' and Q S are there: V', K, Q and S's operand are free
                                      // (the next of a place needs its K, so the copies' warp, and
                                      // `ready`, which the sixteen give behind theirs)
@@ -94,25 +103,28 @@ struct Bars {
                                      // (given again behind ds_done of a chunk that it let begin)
   uint64_t p_full;                   // P is made, the scores and P V's place read (given again
                                      // behind s_done, which follows the wait for it)
-  uint64_t gate_full[kGates], gate_empty[kGates];  // (each needs the other's last one)
+  uint64_t gate_full[2], gate_empty[2];  // (each needs the other's last one)
   uint64_t drain;
 };
 
-// The full pass: Q, K and V in two stages, V' and S's operand.  The first pass: K
-// and V in three, V' in two places.
+// The full pass: Q, K and V in two stages, V' and S's operand.  The first pass: K in three
+// stages, V in two (free as soon as V' is made), V' in two places.  At 128 channels each takes
+// all that a CTA can have but 250 bytes.
 template <int DK, bool OUT>
 struct Smem {
   static constexpr int kStages = OUT ? 2 : 3;
   static constexpr int kTile = C * DK * 2;                 // Q or K of a chunk
   static constexpr int kBox = C * 128;                     // 64 channels of it
   static constexpr int kQ = 0, kK = OUT ? 2 * kTile : 0, kV = kK + kStages * kTile;
-  static constexpr int kVP = kV + kStages * kBox;          // V' in two parts
-  static constexpr int kVP1 = OUT ? kVP : kVP + 2 * kBox;  // the same of odd chunks
-  static constexpr int kS = kVP1 + 2 * kBox;               // S as an operand
+  static constexpr int kVP = kV + 2 * kBox;                // V' in three parts
+  static constexpr int kVP1 = OUT ? kVP : kVP + 3 * kBox;  // the same of odd chunks
+  static constexpr int kS = kVP1 + 3 * kBox;               // S as an operand
   static constexpr int kGate = kS + (OUT ? DK * NV * 2 : 0);
-  static constexpr int kBars = kGate + kGates * (int)sizeof(Gate);
+  static constexpr int kTotal = kGate + 2 * (int)sizeof(Gate);
+  static constexpr int kBars = kTotal + kTotals * (int)sizeof(Total);
   static constexpr int kOrder = kBars + (int)sizeof(Bars) + 16;
-  static constexpr int kBytes = kOrder + 2 * kOrdered + 1024;  // (and the alignment)
+  static constexpr int kBytes = kOrder + 2 * kOrdered;
+  static_assert(kBytes <= 232448, "more than a CTA can have");
 };
 
 // Items go to the CTAs there and back: round by round, every other one from the
@@ -344,9 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ TileArgs p) {
   using M = Smem<DK, OUT>;
   constexpr uint32_t NS = M::kStages;
-  extern __shared__ unsigned char raw[];
-  unsigned char* smem = raw + ((1024u - (sm100::smem_u32(raw) & 1023u)) & 1023u);
+  // (the copies' swizzle goes by addresses of 1024 bytes)
+  extern __shared__ __align__(1024) unsigned char smem[];
   Gate* gates = reinterpret_cast<Gate*>(smem + M::kGate);
+  Total* totals = reinterpret_cast<Total*>(smem + M::kTotal);
   Bars& bars = *reinterpret_cast<Bars*>(smem + M::kBars);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::kBars + sizeof(Bars));
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
@@ -360,19 +373,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
       sm100::mbar_init(&bars.qk_full[i], 1);
-      sm100::mbar_init(&bars.v_full[i], 1);
       sm100::mbar_init(&bars.ds_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&bars.v_full[i], 1);
+      sm100::mbar_init(&bars.gate_full[i], 1);
+      sm100::mbar_init(&bars.gate_empty[i], kWorkers);
       sm100::mbar_init(&bars.o_done[i], 1);
       sm100::mbar_init(&bars.ready[i], kWorkers);
     }
     sm100::mbar_init(&bars.s_done, 1);
     sm100::mbar_init(&bars.p_full, kWorkers);
-    for (int i = 0; i < kGates; ++i) {
-      sm100::mbar_init(&bars.gate_full[i], 1);
-      sm100::mbar_init(&bars.gate_empty[i], kWorkers);
-    }
     sm100::mbar_init(&bars.drain, 1);
     sm100::fence_mbar_init();
     *s_abort = 0;
@@ -423,11 +434,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------ Q, K and V come
     uint32_t g = 0;
+    auto load_v = [&](const Item& it, int row, uint32_t g) {
+      sm100::mbar_arrive_expect_tx(&bars.v_full[g & 1], M::kBox);
+      sm100::tma_load_3d(smem + M::kV + (g & 1) * M::kBox, &map_v, &bars.v_full[g & 1], NV * it.half,
+                         it.h, row);
+    };
     for (Walk<OUT> w(p, order); w.valid; w.next(), ++g) {
       const uint32_t s = g % NS, use = g / NS;
       const int row = (int)(w.it.row + w.t), hk = w.it.hk;
-      // (in the order in which the products let go of them)
-      if (use > 0 && !wait(&bars.ds_done[s], use - 1)) break;
+      // (in the order in which their places become free)
+      if (!OUT && g > 1 && !wait(&bars.ready[g & 1], (g >> 1) - 1)) break;
+      if (!OUT && lane == 0) load_v(w.it, row, g);
+      if (use > 0 && !wait(&bars.ds_done[s], use - 1)) {
+        if (!OUT) ++g;
+        break;
+      }
       if (lane == 0) {
         sm100::mbar_arrive_expect_tx(&bars.qk_full[s], (OUT ? 2 : 1) * M::kTile);
 #pragma unroll
@@ -438,28 +459,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      // (a give-up leaves the chunk's V out: nobody gets beyond its barrier)
+      // (a give-up leaves one of the chunk's copies out: nobody gets beyond its barrier)
       if (OUT && use > 0 && !wait(&bars.o_done[s], use - 1)) {
         ++g;
         break;
       }
-      if (lane == 0) {
-        sm100::mbar_arrive_expect_tx(&bars.v_full[s], M::kBox);
-        sm100::tma_load_3d(smem + M::kV + s * M::kBox, &map_v, &bars.v_full[s], NV * w.it.half,
-                           w.it.h, row);
-      }
+      if (OUT && lane == 0) load_v(w.it, row, g);
       __syncwarp();
     }
     // copies in flight end before the CTA does
-    for (uint32_t i = g < NS ? 0 : g - NS; i < g; ++i) {
+    for (uint32_t i = g < NS ? 0 : g - NS; i < g; ++i)
       sm100::mbar_wait(&bars.qk_full[i % NS], (i / NS) & 1, 200000000ull);
-      sm100::mbar_wait(&bars.v_full[i % NS], (i / NS) & 1, 200000000ull);
-    }
+    for (uint32_t i = g < 2 ? 0 : g - 2; i < g; ++i)
+      sm100::mbar_wait(&bars.v_full[i & 1], (i >> 1) & 1, 200000000ull);
   } else if (warp == 1) {
     // ----------------------------------------------------------- products
     const uint32_t one = elect_one();
     constexpr uint32_t id_s = sm100::idesc_bf16(C, C, 0, 0), id_q = sm100::idesc_bf16(C, NV, 0, 1);
-    constexpr uint32_t id_d = sm100::idesc_bf16(DK, 2 * NV, 1, 1);
+    constexpr uint32_t id_d = sm100::idesc_bf16(DK, (OUT ? 2 : 3) * NV, 1, 1);
+    constexpr uint32_t id_d2 = sm100::idesc_bf16(DK, NV, 1, 1);
     // (addresses in a descriptor count 16 bytes; a box of 64 channels is one span along M or N)
     constexpr uint32_t kTile16 = M::kTile / 16, kBox16 = M::kBox / 16;
     const uint32_t at = (uint32_t)sm100::smem_desc(sm100::smem_u32(smem), M::kBox, 1024);
@@ -498,10 +516,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma4_ss<2, 128>(TM_O1 + NV * s, dq + s * kTile16 + b * kBox16, dst + 512 * b, hi, st_hi,
                           id_q, b, one);
       }
+      // (in the full pass V's third part is added to what the second gives: tensor memory is full)
+      const uint32_t to = OUT ? TM_DS : odd ? TM_D1 : TM_D0, from = odd ? dvp1 : dvp;
 #pragma unroll
       for (uint32_t k = 0; k < 2; ++k)
-        mma4_ss<128, 128>(!OUT && odd ? TM_S : TM_DS, dk + s * kTile16 + 512 * k,
-                          (odd ? dvp1 : dvp) + 512 * k, hi, hi, id_d, k, one);
+        mma4_ss<128, 128>(to, dk + s * kTile16 + 512 * k, from + 512 * k, hi, hi, id_d, k, one);
+#pragma unroll
+      for (uint32_t k = 0; OUT && k < 2; ++k)
+        mma4_ss<128, 128>(to + NV, dk + s * kTile16 + 512 * k, from + 2 * kBox16 + 512 * k, hi, hi,
+                          id_d2, 1, one);
       commit(&bars.ds_done[s], one);
       w.next();
       const bool next = all(w.valid);
@@ -549,7 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float y[4];
     if (w.valid) fetch(w, y);
     for (uint32_t g = turn; w.valid; g += 2) {
-      const uint32_t slot = g % kGates, use = g / kGates;
       const int L = w.rows();
       // fixed point, exact in its sums: 2^-16 and 2^-40 a unit
       int hi[4], lo[4], sum_hi = 0, sum_lo = 0;
@@ -579,43 +601,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a NaN makes what follows it NaN
       const uint32_t bad = __ballot_sync(~0u, nan != 0), cuts = __ballot_sync(~0u, cut != 0);
       const int at = __ffs(cuts) - 1, first = cuts ? 4 * at + __ffs(__shfl_sync(~0u, cut, at)) - 1 : C;
-      if (use > 0 && !wait(&bars.gate_empty[slot], use - 1)) break;
-      Gate& gt = gates[slot];
-      float back[4], col[4], row[4], v[4];
+      float back[4], col[4];
       const float none = __int_as_float(0x7fffffff);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int h = pre_hi + hi[e], l = pre_lo + lo[e];
         back[e] = fixed(blk_hi - h, blk_lo - l);
         col[e] = ex2(back[e]);
-        row[e] = p.a.scale * ex2(fixed(h, l));
-        v[e] = ex2(fixed(end_hi - h, end_lo - l));
-        if (bad) {
-          // (rare) no sum for tokens from the first NaN on, and no weight to the chunk's end
-          if ((bad & ((1u << lane) - 1)) || (nan & ((2u << e) - 1))) back[e] = row[e] = none;
-          v[e] = none;
-        }
+        // (rare) no sum for tokens from the first NaN on
+        if (bad && ((bad & ((1u << lane) - 1)) || (nan & ((2u << e) - 1)))) back[e] = none;
       }
-      reinterpret_cast<float4*>(gt.back)[lane] = make_float4(back[0], back[1], back[2], back[3]);
-      reinterpret_cast<float4*>(gt.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
-      reinterpret_cast<float4*>(gt.row)[lane] = make_float4(row[0], row[1], row[2], row[3]);
-      reinterpret_cast<float4*>(gt.v)[lane] = make_float4(v[0], v[1], v[2], v[3]);
-      if ((lane & 7) == 7) gt.end[lane >> 3] = make_int2(blk_hi, blk_lo);
-      if (lane == 0) {
-        // close to 1, as 1 + (2^E - 1) and what that lost (see the kernel for single tokens)
-        const float x = fixed(end_hi, end_lo) * 0.6931471805599453f;
-        const float m = expm1f(x), f = 1.0f + m;
-        const float2 g2 = bad         ? make_float2(none, none)
-                          : x > -0.5f ? make_float2(f, m - (f - 1.0f))
-                                      : make_float2(expf(x), 0.0f);
-        *reinterpret_cast<float4*>(gt.gamma) = make_float4(g2.x, g2.y, __int_as_float(first), 0.0f);
+      // (and no weight to the chunk's end)
+      const float tail = bad ? none : ex2(fixed(end_hi - blk_hi, end_lo - blk_lo));
+      // close to 1, as 1 + (2^E - 1) and what that lost (see the kernel for single tokens)
+      const float x = fixed(end_hi, end_lo) * 0.6931471805599453f;
+      const float m = expm1f(x), f = 1.0f + m;
+      const float2 gamma = bad         ? make_float2(none, none)
+                           : x > -0.5f ? make_float2(f, m - (f - 1.0f))
+                                       : make_float2(expf(x), 0.0f);
+      if (g > 1 && !wait(&bars.gate_empty[turn], (g >> 1) - 1)) break;
+      Gate& gate = gates[turn];
+      reinterpret_cast<float4*>(gate.back)[lane] = make_float4(back[0], back[1], back[2], back[3]);
+      reinterpret_cast<float4*>(gate.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
+      if ((lane & 7) == 7) {
+        gate.end[lane >> 3] = make_int2(blk_hi, blk_lo);
+        gate.tail[lane >> 3] = tail;
       }
+      if (lane == 0)
+        *reinterpret_cast<float4*>(&totals[g % kTotals]) =
+            make_float4(gamma.x, gamma.y, __int_as_float(first), 0.0f);
       // Rows past a sequence's end belong to others: zeros, whatever they hold.  (This warp's
       // chunks are those of one stage, and it sees each of its copies land: no phase is missed.
       // Segments of the first pass are whole chunks.)
       if (OUT) {
-        const uint32_t s = g % NS;
-        if (!wait(&bars.qk_full[s], g / NS) || !wait(&bars.v_full[s], g / NS)) break;
+        const uint32_t s = g & 1;
+        if (!wait(&bars.qk_full[s], g >> 1) || !wait(&bars.v_full[s], g >> 1)) break;
         if (L < C) {
           const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
@@ -628,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm100::fence_async_smem();
         }
       }
-      arrive(&bars.gate_full[slot]);
+      arrive(&bars.gate_full[turn]);
     }
   } else {
     // ------ sixteen warps that all do a quarter's fourth of V', S, P and O in turn
@@ -698,30 +718,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // V' of chunk g, 16 bytes a thread at a time (rows of V past the end are zeros by then).
     auto weigh = [&](uint32_t g) -> bool {
-      const uint32_t s = g % NS, slot = g % kGates;
-      if (!wait(&bars.gate_full[slot], g / kGates)) return false;  // (in the full pass V is there)
-      if (!OUT && !wait(&bars.v_full[s], g / NS)) return false;
-      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + s * M::kBox);
+      if (!wait(&bars.gate_full[g & 1], g >> 1)) return false;  // (in the full pass V is there)
+      const Gate& gate = gates[g & 1];
+      if (!OUT && !wait(&bars.v_full[g & 1], g >> 1)) return false;
+      const uint4* v = reinterpret_cast<const uint4*>(smem + M::kV + (g & 1) * M::kBox);
       uint4* to = reinterpret_cast<uint4*>(smem + (g & 1 ? M::kVP1 : M::kVP));
       const f32x2 minus = pair(-1.0f, -1.0f);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int e = 512 * k + tid - 128;
         const uint4 x = v[e];
-        const float f = gates[slot].v[e >> 3];
+        const float f = gate.col[e >> 3] * gate.tail[e >> 8];
         const f32x2 ff = pair(f, f);
         const uint32_t r[4] = {x.x, x.y, x.z, x.w};
-        uint32_t a[4], b[4];
+        uint32_t a[4], b[4], d[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const f32x2 y = mul2(ff, pair(__uint_as_float(r[c] << 16),
-                                        __uint_as_float(r[c] & 0xffff0000u)));
+          auto two = [](uint32_t w) {
+            return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+          };
+          f32x2 y = mul2(ff, two(r[c]));
           a[c] = bf16x2(y);
-          b[c] = bf16x2(fma2(minus, pair(__uint_as_float(a[c] << 16),
-                                         __uint_as_float(a[c] & 0xffff0000u)), y));
+          y = fma2(minus, two(a[c]), y);
+          b[c] = bf16x2(y);
+          d[c] = bf16x2(fma2(minus, two(b[c]), y));
         }
         to[e] = make_uint4(a[0], a[1], a[2], a[3]);
         to[e + M::kBox / 16] = make_uint4(b[0], b[1], b[2], b[3]);
+        to[e + 2 * M::kBox / 16] = make_uint4(d[0], d[1], d[2], d[3]);
       }
       return true;
     };
@@ -734,6 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        bf16x2(S[j / 2 + 1]), bf16x2(S[j / 2 + 2]), bf16x2(S[j / 2 + 3]));
       sm100::fence_async_smem();
       arrive(&bars.ready[g & 1]);
+      if (!OUT) arrive(&bars.gate_empty[g & 1]);
     };
     // The full pass begins and ends a chunk by the same code, one chunk apart: chunk g's K^T V' and
     // O (`old`), chunk g + 1's V', operand of S and P (`more`).  The first pass, whose V' and
@@ -742,9 +767,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // there before the first pass, and the states are what it waits for here)
     if (OUT && p.states) wait_for_kernel_before();
     bool more = enter(), old = false;
+    float factor = 0.0f;  // scale * 2^G of this thread's row
     Walk<OUT> ahead(p, order, !OUT);
     for (uint32_t g = ~0u; more || old; ++g) {
-      const uint32_t s = g & 1, slot = g % kGates, next = (g + 1) % kGates;
+      const uint32_t s = g & 1;
       const int64_t at = it.row + t + row;  // this chunk's rows go out last
       const bool live = row < it.len - t;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) +
@@ -757,15 +783,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (old) {
         if (!wait(&bars.ds_done[g % NS], g / NS)) break;
         sm100::tc_fence_after();
-        float x[16], y[16];
-        const uint32_t from = tm + (!OUT && s ? TM_S : TM_DS) + c0;
+        float x[16], y[16], z[16];
+        const uint32_t from = tm + (OUT ? TM_DS : s ? TM_D1 : TM_D0) + c0;
         sm100::tmem_ld16(from, x);
         sm100::tmem_ld16(from + NV, y);
-        const float4 f = *reinterpret_cast<const float4*>(gates[slot].gamma);
+        if (!OUT) sm100::tmem_ld16(from + 2 * NV, z);
+        const float4 f = *reinterpret_cast<const float4*>(&totals[g % kTotals]);
         const bool forget = __float_as_int(f.z) < C;
         const f32x2 hi = pair(f.x, f.x), lo = pair(f.y, f.y);
         sm100::tmem_wait_ld();
         sm100::tc_fence_before();
+        if (!OUT) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] += z[e];
+        }
         if (forget) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) S[e] = pair(0.0f, 0.0f);
@@ -791,8 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint32_t rows[8];  // O of chunk g, 16 columns
       if (OUT && old) {
-        const float f = gates[slot].row[row];
-        const f32x2 ff = pair(f, f), scale = pair(p.a.scale, p.a.scale);
+        const f32x2 ff = pair(factor, factor), scale = pair(p.a.scale, p.a.scale);
         if (!wait(&bars.o_done[s], g >> 1)) break;
         sm100::tc_fence_after();
         float x[16], y[16];
@@ -800,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm100::tmem_ld16(tm + TM_O2 + c0, y);
         sm100::tmem_wait_ld();
         sm100::tc_fence_before();
-        const int first = gates[slot].first;
+        const int first = totals[g % kTotals].first;
         if (first < C) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = row >= first ? 0.0f : x[e];
@@ -810,14 +840,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           rows[e] = bf16x2(fma2(ff, pair(x[2 * e], x[2 * e + 1]),
                                 mul2(scale, pair(y[2 * e], y[2 * e + 1]))));
       }
-      if (old) arrive(&bars.gate_empty[slot]);
       if (OUT && more) {
         // P, 16 columns at a time
         if (!wait(&bars.s_done, g + 1)) break;
         sm100::tc_fence_after();
-        const Gate& gt = gates[next];
-        const float own = gt.back[row];
-        const int2 e = gt.end[q];
+        const Gate& gate = gates[s ^ 1];
+        const float own = gate.back[row];
+        const int2 e = gate.end[q];
+        // (where the difference is of two large numbers, what lies between them has forgotten
+        // the row's own token: 2^-14 of the factor at 10 tokens of a block that forget)
+        factor = p.a.scale * ex2(fixed(e.x, e.y) - own);
 #pragma unroll 1
         for (int b = part; b < 8; b += 4) {
           uint32_t out[8] = {};
@@ -826,11 +858,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             f32x2 w[8];
             sm100::tmem_ld16(tm + TM_S + 16 * b, x);
             const bool below = b < 2 * q;  // (of the diagonal's 32 columns)
-            const int2 o = gt.end[b >> 1];
+            const int2 o = gate.end[b >> 1];
             float f = fixed(e.x - o.x, e.y - o.y) - own;
             if (below) f = ex2(f);
             const f32x2 ff = pair(f, f);
-            const float4* c = reinterpret_cast<const float4*>((below ? gt.col : gt.back) + 16 * b);
+            const float4* c = reinterpret_cast<const float4*>((below ? gate.col : gate.back) + 16 * b);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float4 y = c[j];
@@ -869,6 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
         arrive(&bars.p_full);
+        arrive(&bars.gate_empty[(g + 1) & 1]);
       }
       // (the stores come last: an arrival right behind them would wait for them, some 750 cycles.
       // 32 rows' sectors are what a warp stores: once each, where out is aligned to them)

@@ -586,8 +586,8 @@ size_t kda_cache_attn_workspace_bytes(int R, int T, int max_new, int Hq, int Hkv
  * unspecified.
  * bf16 with dk and dv 64 or 128 runs on the tensor cores in chunks of 128
  * tokens: weights within a chunk and the state that queries read are rounded
- * to bf16, the state that is carried and returned is summed from 16 bits of each
- * weighted value (2.5e-6 of its norm against 64 bits).  Other types and sizes run
+ * to bf16, the state that is carried and returned is summed in fp32 from all bits of
+ * each weighted value (1.2e-7 of its norm against 64 bits).  Other types and sizes run
  * token by token in fp32.  Few heads with long rows are cut into segments of the
  * token axis; where, and so the last bits, goes by B, T, H, dv and the device's
  * SM count.  The same call gives the same bits each time.
