@@ -57,7 +57,6 @@ using kda_cache::wait_for_kernel_before;
 constexpr int C = 128;          // tokens of a chunk
 constexpr int NV = 64;          // value columns of a CTA
 constexpr int kThreads = 640;
-constexpr int kOrdered = 320;   // most sequences of a packed batch that are put in order
 // tensor memory: scores, P, Q S by stage, P V, K^T V' of the first part of V' and of the others
 constexpr uint32_t TM_S = 0, TM_P = 128, TM_O1 = 192, TM_O2 = 320, TM_DS = 384, kTmemCols = 512;
 // in the first pass: K^T V' of V's three parts, of even and of odd chunks
@@ -123,6 +122,8 @@ struct Smem {
   static constexpr int kTotal = kGate + 2 * (int)sizeof(Gate);
   static constexpr int kBars = kTotal + kTotals * (int)sizeof(Total);
   static constexpr int kOrder = kBars + (int)sizeof(Bars) + 16;
+  // most sequences of a packed batch that are put in order
+  static constexpr int kOrdered = DK == 64 ? 1024 : 320;
   static constexpr int kBytes = kOrder + 2 * kOrdered;
   static_assert(kBytes <= 232448, "more than a CTA can have");
 };
@@ -160,7 +161,7 @@ __device__ __noinline__ bool locate(const TileArgs& p, const uint16_t* order, in
     // segments, and at most one more
     int lo = 0, hi = p.a.N - 1;
     if (p.seg > p.a.T) {
-      lo = p.a.N <= kOrdered ? order[it.col] : it.col;
+      lo = order ? order[it.col] : it.col;
     } else {
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -390,8 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // whole sequences of a packed batch: the longest first, equal ones in order.  (Lengths of
   // malformed offsets are some numbers too: every sequence gets a place of its own.)
-  uint16_t* order = reinterpret_cast<uint16_t*>(smem + M::kOrder);
-  if (p.a.cu && p.seg > p.a.T && p.a.N <= kOrdered) {
+  uint16_t* order = nullptr;
+  if (p.a.cu && p.seg > p.a.T && p.a.N <= M::kOrdered) {
+    order = reinterpret_cast<uint16_t*>(smem + M::kOrder);
     int* lens = reinterpret_cast<int*>(smem + M::kVP);  // (where V' comes later)
     const int N4 = (p.a.N + 3) / 4;
     for (int n = tid; n < 4 * N4; n += kThreads)
