@@ -37,10 +37,10 @@
 // output), a scan composes the states that segments start from, and the full
 // pass runs every segment at once.
 //
-// Measured: two rows of 32 768 tokens, 32 heads of 128 channels, 460 us, 4.7 TB/s
-// (0.70 of a copy's); 17 ragged prompts, 16 heads, 145 us; one row of 131 072
-// tokens, 16 heads, 627 us (213 of them the first pass; with two stages 260).  A chunk takes some 3700
-// cycles, the products 1700 of them; without V', P and the stores it is 2500.
+// Measured: two rows of 32 768 tokens, 32 heads of 128 channels, 502 us, 4.3 TB/s
+// (0.64 of a copy's); 17 ragged prompts, 16 heads, 156 us; one row of 131 072
+// tokens, 16 heads, 726 us (250 of them the first pass).  A chunk takes some 3900
+// cycles, the products 2000 of them.
 #include <cudaTypedefs.h>
 
 #include "kda_cache_attn.cuh"
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The barrier's phase n.  The warp's threads leave together and with one answer: what comes
   // next (loads and stores of tensor memory, shuffles, products) is for whole warps, and a wait
   // that gives up ends the role for all of them.  (One vote where the phase is over, on which all
-  // then branch: with the vote behind both ways the two rows took 464 us, with none 453.)
+  // then branch: with the vote behind both ways the two rows took 464 us, so 456, with none 453.)
   auto wait = [&](uint64_t* bar, uint32_t n) -> bool {
     const uint32_t at = sm100::smem_u32(bar);
     if (__all_sync(~0u, poll(at, n & 1))) return true;
@@ -987,15 +987,16 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How the token axis is cut.  Times in chunks of one CTA (1.7 us): segments cost 0.4 of
+// How the token axis is cut.  Times in chunks of one CTA (1.9 us): segments cost 0.4 of
 // their chunks and six more.  Both numbers are what the choices went best with; a chunk of
-// the first pass alone takes 0.52 of one of the full pass, but a rule with that number and no
-// price for an item of its own takes many short segments: 4096 tokens of 32 heads go from 64 us
-// (two segments; 67 whole) to 112 (sixteen).  Cut against whole: 4096 tokens of 4 heads 27
-// and 64 us, 32 768 of 4 heads 64 and 451, 131 072 of 16 heads 640 and 1753.  Packed lengths are
-// not known here: the longest is taken for twice the mean.  Where they are all alike that is too
-// long (4 sequences of 4096 tokens, 8 heads: cut, 115 us; whole they would take 67), where one
-// is much longer too short.
+// the first pass alone takes 0.55 of one of the full pass, but a rule with that number and no
+// price for an item of its own takes many short segments: 8192 tokens of 16 heads go from 71 us
+// (four segments; 133 whole) to 119 (32).  Cut against whole: 4096 tokens of 4 heads 27
+// and 69 us, 32 768 of 4 heads 69 and 492, 131 072 of 16 heads 750 and 1958; 4096 tokens of 32
+// heads 72 both ways.  Packed lengths are not known here: the longest is taken for twice the
+// mean.  Where they are all alike that is too long (4 sequences of 4096 tokens, 8 heads: cut,
+// 130 us; whole they would take 72), where one is much longer too short (32 000 tokens among 31
+// sequences of 10, 8 heads: whole, 497 us).
 struct Cut {
   int seg, segs, cols;
 };

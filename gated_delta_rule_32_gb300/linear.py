@@ -4,6 +4,9 @@ computes.
 
     S_t = exp(a_t) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,   a_t = min(log_decay_t, 0)
 
+A token with a log_decay below -104 (-inf, say) forgets the state before it,
+whatever that holds.
+
 A prompt, then tokens::
 
     out, state = linear_attend(q, k, v, log_decay, scale=scale)
@@ -107,7 +110,11 @@ def linear_attend(q, k, v, log_decay, init_state=None, cu_seqlens=None, scale=1.
     """Whole prompts: (out [B, T, H, dv], final_state [N, H, dk, dv] float32).
     Packed batches: cu_seqlens (int32 [N + 1], a plan's is one) with B = 1; rows
     past the last sequence are left as they were allocated.  init_state
-    [N, H, dk, dv] defaults to zero."""
+    [N, H, dk, dv] defaults to zero.  bfloat16 with heads of 64 and 128 runs on
+    the tensor cores in chunks of 128 tokens of a sequence, where weights and what
+    queries read of the state are rounded to bfloat16, and where a NaN or an
+    infinity in v reaches all rows of its chunk, those before it too; other types
+    and sizes run token by token in float32."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear_attend(q, k, v, log_decay, init_state, cu_seqlens, scale, dev_status)
